@@ -48,7 +48,8 @@ EXPORTS = ("gemm_sgemm", "gemm_bf16", "gemm_bf16_batched", "gemm_bf16_nt", "gemm
            "gemm_bf16_tn_affine", "gemm_run", "gemm_run_noalloc", "gemm_workspace_size",
            "gemm_status_string",
            "gemm_plan_query", "gemm_plan_query_ex", "gemm_model_local_bytes", "gemm_model_traffic_bytes", "gemm_model_quant_traffic", "gemm_model_act_chain_bytes",
-           "gemm_tile_map")
+           "gemm_tile_map",
+           "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size")
 
 
 class GemmPlan(ctypes.Structure):
@@ -154,6 +155,12 @@ def lib():
     L.gemm_tile_map.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(i64), ctypes.POINTER(i64),
                                 ctypes.POINTER(i64)]
     L.gemm_tile_map.restype = i32
+    L.gemm_rms_norm.argtypes = [i64, i64, p, i64, p, i64, p, i64, p, f32, p, i64, i32, p, p, p]
+    L.gemm_rms_norm.restype = i32
+    L.gemm_rms_norm_backward.argtypes = [i64, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, p, u64, p]
+    L.gemm_rms_norm_backward.restype = i32
+    L.gemm_rms_norm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(u64)]
+    L.gemm_rms_norm_workspace_size.restype = i32
     _lib = L
     return L
 

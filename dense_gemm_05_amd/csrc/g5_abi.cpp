@@ -1207,6 +1207,124 @@ int gemm_bf16_nt_affine(int64_t batch, int64_t M, int64_t N, int64_t K, const ui
     return g5::run(p, stream);
 }
 
+// ---- RMS norm: the arguments' checks, shared shape of the entries below
+// [lo, hi) of a vector of n elements of esz bytes (empty for NULL).
+static g5::Range vec_range(const void *v, int64_t n, int esz)
+{
+    if (!v) return g5::Range{0, 0};
+    return g5::Range{(__int128)(uint64_t)v, (__int128)(uint64_t)v + (__int128)esz * n};
+}
+// Whether any output range overlaps an input or another output.
+static bool outputs_overlap(const g5::Range *out, int n_out, const g5::Range *in, int n_in)
+{
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (g5::overlap(out[i], in[j])) return true;
+        for (int j = i + 1; j < n_out; ++j)
+            if (g5::overlap(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+int gemm_rms_norm(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, const uint16_t *R, int64_t ldr,
+                  uint16_t *H, int64_t ldh, const uint16_t *W, float eps, void *Y, int64_t ldy, int y_type,
+                  float *scale, float *rstd, void *stream)
+{
+    using g5::Range;
+    const bool codes = y_type == GEMM_OUT_E4M3;
+    if (rows < 0 || cols < 0 || rows > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    if ((y_type != GEMM_OUT_BF16 && !codes) || !std::isfinite(eps) || eps < 0.0f) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    if (!X || !Y || (codes && !scale) || (H && !R)) return GEMM_ERR_INVALID_ARG;
+    if (ldx < cols || ldy < cols || (R && ldr < cols) || (H && ldh < cols)) return GEMM_ERR_INVALID_ARG;
+    const int ey = codes ? 1 : 2;
+    if (((uint64_t)X % 2) || ((uint64_t)R % 2) || ((uint64_t)H % 2) || ((uint64_t)W % 2) || ((uint64_t)Y % ey) ||
+        (codes && ((uint64_t)scale % 4)) || ((uint64_t)rstd % 4))
+        return GEMM_ERR_INVALID_ARG;
+    const Range none{0, 0};
+    const Range rx = g5::extent((uint64_t)X, 1, rows, cols, ldx, 0, 2);
+    const Range rr = R ? g5::extent((uint64_t)R, 1, rows, cols, ldr, 0, 2) : none;
+    const Range rh = H ? g5::extent((uint64_t)H, 1, rows, cols, ldh, 0, 2) : none;
+    const Range ry = g5::extent((uint64_t)Y, 1, rows, cols, ldy, 0, ey);
+    const Range rw = vec_range(W, cols, 2);
+    const __int128 top = (__int128)1 << 63;
+    if (rx.hi > top || rr.hi > top || rh.hi > top || ry.hi > top || rw.hi > top) return GEMM_ERR_INVALID_ARG;
+    // H may be X or R itself (the sum in place): then the two ranges are one
+    const bool h_is_x = H && H == X && ldh == ldx, h_is_r = H && H == R && ldh == ldr;
+    const Range in[] = {h_is_x ? none : rx, h_is_r ? none : rr, rw};
+    const Range out[] = {rh, ry, codes ? vec_range(scale, rows, 4) : none, vec_range(rstd, rows, 4)};
+    if (outputs_overlap(out, 4, in, 3)) return GEMM_ERR_INVALID_ARG;
+    const int st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    g5::NormArgs a{X, R, W, H, Y, codes ? scale : nullptr, rstd, rows, cols, ldx, R ? ldr : cols, H ? ldh : cols, ldy,
+                   eps, g5::row_alignment((uint64_t)X, ldx, 0, 1, 2),
+                   R ? g5::row_alignment((uint64_t)R, ldr, 0, 1, 2) : 16,
+                   W ? g5::row_alignment((uint64_t)W, 0, 0, 1, 2) : 16,
+                   H ? g5::row_alignment((uint64_t)H, ldh, 0, 1, 2) : 16,
+                   g5::row_alignment((uint64_t)Y, ldy, 0, 1, ey)};
+    const bool vec = cols % 8 == 0 && a.align_x >= 16 && a.align_r >= 16 && a.align_w >= 16 && a.align_h >= 16 &&
+                     a.align_y >= 8 * ey;
+    const hipError_t e = g5::launch_rms_norm(a, codes, vec, (hipStream_t)stream);
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes)
+{
+    if (bytes) *bytes = 0;
+    if (rows < 0 || cols < 0 || rows > 0x7fffffff || cols > ((int64_t)1 << 40)) return GEMM_ERR_INVALID_ARG;
+    if (bytes && rows > 0 && cols > 0)
+        *bytes = g5::kCounterBytes + g5::round256((size_t)g5::norm_grad_parts(rows) * (size_t)cols * 4);
+    return GEMM_OK;
+}
+
+int gemm_rms_norm_backward(int64_t rows, int64_t cols, const uint16_t *dY, int64_t lddy, const uint16_t *H,
+                           int64_t ldh, const uint16_t *W, const float *rstd, const uint16_t *dH, int64_t lddh,
+                           uint16_t *dX, int64_t lddx, float *dW, void *workspace, uint64_t workspace_bytes,
+                           void *stream)
+{
+    using g5::Range;
+    if (rows < 0 || cols < 0 || rows > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    if (cols == 0 || (rows == 0 && !dW)) return GEMM_OK;
+    if (rows == 0) {          // dW := 0, the empty sum
+        if ((uint64_t)dW % 4 || vec_range(dW, cols, 4).hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
+        const int st = g5::check_device();
+        if (st != GEMM_OK) return st;
+        return g5::launch_norm_dw(nullptr, 0, cols, dW, (hipStream_t)stream) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    }
+    if (!dY || !H || !rstd || !dX || lddy < cols || ldh < cols || lddx < cols || (dH && lddh < cols))
+        return GEMM_ERR_INVALID_ARG;
+    if (((uint64_t)dY % 2) || ((uint64_t)H % 2) || ((uint64_t)W % 2) || ((uint64_t)dH % 2) || ((uint64_t)dX % 2) ||
+        ((uint64_t)rstd % 4) || ((uint64_t)dW % 4))
+        return GEMM_ERR_INVALID_ARG;
+    const Range none{0, 0};
+    const Range rdy = g5::extent((uint64_t)dY, 1, rows, cols, lddy, 0, 2);
+    const Range rh = g5::extent((uint64_t)H, 1, rows, cols, ldh, 0, 2);
+    const Range rdh = dH ? g5::extent((uint64_t)dH, 1, rows, cols, lddh, 0, 2) : none;
+    const Range rdx = g5::extent((uint64_t)dX, 1, rows, cols, lddx, 0, 2);
+    const __int128 top = (__int128)1 << 63;
+    if (rdy.hi > top || rh.hi > top || rdh.hi > top || rdx.hi > top) return GEMM_ERR_INVALID_ARG;
+    const Range in[] = {rdy, rh, rdh, vec_range(W, cols, 2), vec_range(rstd, rows, 4)};
+    uint64_t need = 0;
+    if (dW && gemm_rms_norm_workspace_size(rows, cols, &need) != GEMM_OK) return GEMM_ERR_INVALID_ARG;
+    const Range rws = dW && workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + need} : none;
+    const Range out[] = {rdx, vec_range(dW, cols, 4), rws};
+    if (outputs_overlap(out, 3, in, 5)) return GEMM_ERR_INVALID_ARG;
+    if (dW && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
+    if (dW && ((uint64_t)workspace % 256)) return GEMM_ERR_INVALID_ARG;
+    const int st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    g5::NormGradArgs a{dY, H, W, dH, rstd, dX, dW ? (float *)((char *)workspace + g5::kCounterBytes) : nullptr, dW,
+                       rows, cols, lddy, ldh, dH ? lddh : cols, lddx,
+                       g5::row_alignment((uint64_t)dY, lddy, 0, 1, 2), g5::row_alignment((uint64_t)H, ldh, 0, 1, 2),
+                       W ? g5::row_alignment((uint64_t)W, 0, 0, 1, 2) : 16,
+                       dH ? g5::row_alignment((uint64_t)dH, lddh, 0, 1, 2) : 16,
+                       g5::row_alignment((uint64_t)dX, lddx, 0, 1, 2)};
+    const bool vec = cols % 8 == 0 && a.align_dy >= 16 && a.align_h >= 16 && a.align_w >= 16 && a.align_dh >= 16 &&
+                     a.align_dx >= 16;
+    const hipError_t e = g5::launch_rms_norm_grad(a, vec, (hipStream_t)stream);
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
 const char *gemm_status_string(int status)
 {
     switch (status) {

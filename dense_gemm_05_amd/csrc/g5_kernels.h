@@ -116,4 +116,33 @@ struct ActArgs {
 // ld == N.  Else one element per thread.
 hipError_t launch_act_chain(int step, const ActArgs &a, bool vec, bool contig, hipStream_t s);
 
+// The RMS norm with the residual's addition (g5_norm.hip).  Strides in
+// elements (Y: bytes for codes); align_*: byte alignment of the row starts.
+struct NormArgs {
+    const uint16_t *X, *R, *W;   // R (residual) and W (weight) or NULL
+    uint16_t *H;                 // bf16(X + R), or NULL
+    void *Y;                     // bf16, or E4M3FN codes with factors scale[rows]
+    float *scale, *rstd;         // rstd or NULL
+    int64_t rows, cols, ldx, ldr, ldh, ldy;
+    float eps;
+    int align_x, align_r, align_w, align_h, align_y;
+};
+// vec: cols % 8 == 0 and every row start 16-byte aligned (codes: 8-byte).
+hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t s);
+
+// Its gradient: dX and, when dW is given, the weight's through `part`
+// (norm_grad_parts(rows) rows of cols floats, written before they are read).
+struct NormGradArgs {
+    const uint16_t *dY, *H, *W, *dH;   // W and dH (the residual branch's gradient) or NULL
+    const float *rstd;
+    uint16_t *dX;
+    float *part, *dW;
+    int64_t rows, cols, lddy, ldh, lddh, lddx;
+    int align_dy, align_h, align_w, align_dh, align_dx;
+};
+int norm_grad_parts(int64_t rows);
+// dW[n] := the sum of `parts` rows of `part` (0: zeros, `part` not read).
+hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s);
+hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s);
+
 }  // namespace g5

@@ -1,0 +1,451 @@
+// g5_norm.hip -- the RMS norm that stands before a projection, with the
+// residual's addition and a bf16 or E4M3FN output, and its gradient.
+//
+//   h = bf16(x + r)                       (or h = x without a residual)
+//   rstd = 1 / sqrt(sum_j h_j^2 / cols + eps)
+//   y_j = bf16(h_j rstd w_j)              (codes: y's row quantized as
+//                                          k_quant_rows_e4m3 quantizes it)
+//
+// Sums and rstd are FP32.  h is rounded once because it is stored as the
+// residual stream, and the norm reads what is stored; y is rounded to bf16
+// before it is quantized, so the codes are those of the unfused program.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "g5_device.h"
+#include "g5_kernels.h"
+
+namespace g5 {
+
+namespace {
+
+// Chunk c (8 elements) of a row: one 16-byte load when VEC (every row
+// 16-byte aligned and a whole number of chunks), else by alignment.
+template <bool VEC>
+__device__ __forceinline__ u32x4 norm_load(const uint16_t *row, int64_t col, int64_t cols, int align)
+{
+    if constexpr (VEC) return *(const u32x4 *)(row + col);
+    else return load_chunk8_bf16(row, col, cols, true, align);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void norm_store(uint16_t *row, int64_t col, int64_t cols, int align, u32x4 v)
+{
+    if (VEC || (col + 8 <= cols && align >= 16)) {
+        *(u32x4 *)(row + col) = v;
+    } else if (col + 8 <= cols && align >= 8) {
+        *(u32x2 *)(row + col) = u32x2{v[0], v[1]};
+        *(u32x2 *)(row + col + 4) = u32x2{v[2], v[3]};
+    } else {
+        for (int i = 0; i < 8 && col + i < cols; ++i) row[col + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void norm_store_codes(uint8_t *row, int64_t col, int64_t cols, int align, uint32_t w0,
+                                                 uint32_t w1)
+{
+    if (VEC || (col + 8 <= cols && align >= 8)) {
+        *(u32x2 *)(row + col) = u32x2{w0, w1};
+    } else {
+        const uint32_t w[2] = {w0, w1};
+        for (int i = 0; i < 8 && col + i < cols; ++i) row[col + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+}
+
+__device__ __forceinline__ u32x4 add8_bf16(u32x4 x, u32x4 r)
+{
+    u32x4 h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = pack_bf16x2(bf16_lo(x[i]) + bf16_lo(r[i]), bf16_hi(x[i]) + bf16_hi(r[i]));
+    return h;
+}
+
+__device__ __forceinline__ float sumsq8(float s, u32x4 h)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = __builtin_fmaf(bf16_lo(h[i]), bf16_lo(h[i]), s);
+        s = __builtin_fmaf(bf16_hi(h[i]), bf16_hi(h[i]), s);
+    }
+    return s;
+}
+
+__device__ __forceinline__ u32x4 scale8(u32x4 h, float rstd, u32x4 w, bool has_w)
+{
+    u32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float lo = bf16_lo(h[i]) * rstd, hi = bf16_hi(h[i]) * rstd;
+        y[i] = has_w ? pack_bf16x2(lo * bf16_lo(w[i]), hi * bf16_hi(w[i])) : pack_bf16x2(lo, hi);
+    }
+    return y;
+}
+
+__device__ __forceinline__ float absmax8(float m, u32x4 c)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(c[i])), fabsf(bf16_hi(c[i]))));
+    return m;
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+__device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps)
+{
+    return 1.0f / sqrtf(ss / (float)cols + eps);
+}
+
+}  // namespace
+
+// Rows of up to WPR * NCH * 512 elements, held in registers between the
+// passes: WPR of the workgroup's four waves share a row (part p holds its
+// chunks p, p + WPR, ... of 512 elements), 4 / WPR rows per workgroup.  Each
+// wave sums in a fixed order (chunk, element, butterfly), the parts are
+// added in order, so a row's result does not depend on the others.
+template <int WPR, int NCH, bool CODES, bool VEC>
+__global__ void __launch_bounds__(256) k_rms_norm(NormArgs a)
+{
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, part = wv % WPR, w0 = wv - part;
+    const int64_t r = (int64_t)blockIdx.x * (4 / WPR) + wv / WPR;
+    const bool r_ok = r < a.rows;
+    if (WPR == 1 && !r_ok) return;        // a whole wave; nothing below joins waves
+    const int64_t rr = r_ok ? r : 0;
+    auto col_of = [&](int j) { return (int64_t)lane * 8 + (int64_t)(j * WPR + part) * 512; };
+    u32x4 h[NCH], w[NCH];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        h[j] = w[j] = u32x4{0u, 0u, 0u, 0u};
+        if (r_ok && col_of(j) < a.cols) h[j] = norm_load<VEC>(a.X + rr * a.ldx, col_of(j), a.cols, a.align_x);
+    }
+    if (a.R) {
+        u32x4 q[NCH];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            q[j] = u32x4{0u, 0u, 0u, 0u};
+            if (r_ok && col_of(j) < a.cols) q[j] = norm_load<VEC>(a.R + rr * a.ldr, col_of(j), a.cols, a.align_r);
+        }
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) h[j] = add8_bf16(h[j], q[j]);
+        if (a.H) {
+#pragma unroll
+            for (int j = 0; j < NCH; ++j)
+                if (r_ok && col_of(j) < a.cols) norm_store<VEC>(a.H + rr * a.ldh, col_of(j), a.cols, a.align_h, h[j]);
+        }
+    }
+    if (a.W) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+            if (col_of(j) < a.cols) w[j] = norm_load<VEC>(a.W, col_of(j), a.cols, a.align_w);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) ss = sumsq8(ss, h[j]);
+    ss = wave_sum(ss);
+    if constexpr (WPR > 1) {
+        if (lane == 0) red[0][wv] = ss;
+        __syncthreads();
+        ss = red[0][w0];
+#pragma unroll
+        for (int k = 1; k < WPR; ++k) ss += red[0][w0 + k];
+    }
+    const float rstd = rstd_of(ss, a.cols, a.eps);
+    if (a.rstd && r_ok && part == 0 && lane == 0) a.rstd[r] = rstd;
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) h[j] = scale8(h[j], rstd, w[j], a.W != nullptr);
+    if constexpr (!CODES) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+            if (r_ok && col_of(j) < a.cols)
+                norm_store<VEC>((uint16_t *)a.Y + rr * a.ldy, col_of(j), a.cols, a.align_y, h[j]);
+    } else {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) amax = absmax8(amax, h[j]);
+        amax = wave_max(amax);
+        if constexpr (WPR > 1) {
+            if (lane == 0) red[1][wv] = amax;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < WPR; ++k) amax = fmaxf(amax, red[1][w0 + k]);
+        }
+        if (!r_ok) return;
+        if (part == 0 && lane == 0) a.scale[r] = amax / 448.0f;
+        const E4m3Quot qz(amax);
+        auto emit = [&](auto fast) {
+            constexpr bool F = decltype(fast)::value;
+#pragma unroll
+            for (int j = 0; j < NCH; ++j)
+                if (col_of(j) < a.cols)
+                    norm_store_codes<VEC>((uint8_t *)a.Y + rr * a.ldy, col_of(j), a.cols, a.align_y,
+                                          qz.code4<F>(h[j][0], h[j][1]), qz.code4<F>(h[j][2], h[j][3]));
+        };
+        if (qz.fast) emit(std::true_type{});
+        else emit(std::false_type{});
+    }
+}
+
+// Longer rows: a workgroup per row reads it again in each pass.  Each thread
+// reads back only elements of H that it stored itself.
+template <bool CODES>
+__global__ void __launch_bounds__(256) k_rms_norm_long(NormArgs a)
+{
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int64_t r = blockIdx.x;
+    const uint16_t *x = a.X + r * a.ldx, *q = a.R ? a.R + r * a.ldr : nullptr;
+    uint16_t *hrow = a.R && a.H ? a.H + r * a.ldh : nullptr;
+    float ss = 0.f;
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048) {
+        u32x4 h = load_chunk8_bf16(x, c, a.cols, true, a.align_x);
+        if (q) h = add8_bf16(h, load_chunk8_bf16(q, c, a.cols, true, a.align_r));
+        if (hrow) norm_store<false>(hrow, c, a.cols, a.align_h, h);
+        ss = sumsq8(ss, h);
+    }
+    ss = wave_sum(ss);
+    if (lane == 0) red[0][wv] = ss;
+    __syncthreads();
+    const float rstd = rstd_of(((red[0][0] + red[0][1]) + red[0][2]) + red[0][3], a.cols, a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+    auto y_of = [&](int64_t c) {
+        u32x4 h;
+        if (hrow) {
+            h = load_chunk8_bf16(hrow, c, a.cols, true, a.align_h);
+        } else {
+            h = load_chunk8_bf16(x, c, a.cols, true, a.align_x);
+            if (q) h = add8_bf16(h, load_chunk8_bf16(q, c, a.cols, true, a.align_r));
+        }
+        const u32x4 w = a.W ? load_chunk8_bf16(a.W, c, a.cols, true, a.align_w) : u32x4{0u, 0u, 0u, 0u};
+        return scale8(h, rstd, w, a.W != nullptr);
+    };
+    if constexpr (!CODES) {
+        for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048)
+            norm_store<false>((uint16_t *)a.Y + r * a.ldy, c, a.cols, a.align_y, y_of(c));
+    } else {
+        float amax = 0.f;
+        for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048) amax = absmax8(amax, y_of(c));
+        amax = wave_max(amax);
+        if (lane == 0) red[1][wv] = amax;
+        __syncthreads();
+        amax = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+        if (threadIdx.x == 0) a.scale[r] = amax / 448.0f;
+        const E4m3Quot qz(amax);
+        for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048) {
+            const u32x4 y = y_of(c);
+            const uint32_t w0 = qz.fast ? qz.code4<true>(y[0], y[1]) : qz.code4<false>(y[0], y[1]);
+            const uint32_t w1 = qz.fast ? qz.code4<true>(y[2], y[3]) : qz.code4<false>(y[2], y[3]);
+            norm_store_codes<false>((uint8_t *)a.Y + r * a.ldy, c, a.cols, a.align_y, w0, w1);
+        }
+    }
+}
+
+template <int WPR, int NCH>
+static hipError_t launch_norm_held(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+{
+    const dim3 g((unsigned)((a.rows + 4 / WPR - 1) / (4 / WPR))), b(256);
+    if (codes) {
+        if (vec) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, true, true>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((k_rms_norm<WPR, NCH, true, false>), g, b, 0, s, a);
+    } else {
+        if (vec) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, false, true>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((k_rms_norm<WPR, NCH, false, false>), g, b, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+static hipError_t launch_norm_rows(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+{
+    if (a.cols <= 512) return launch_norm_held<1, 1>(a, codes, vec, s);
+    if (a.cols <= 2048) return launch_norm_held<4, 1>(a, codes, vec, s);
+    if (a.cols <= 4096) return launch_norm_held<4, 2>(a, codes, vec, s);
+    if (a.cols <= 8192) return launch_norm_held<4, 4>(a, codes, vec, s);
+    if (a.cols <= 16384) return launch_norm_held<4, 8>(a, codes, vec, s);
+    if (codes) hipLaunchKernelGGL((k_rms_norm_long<true>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm_long<false>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+// (a launch holds fewer than 2^32 threads: 2^22 rows at a time)
+hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+{
+    constexpr int64_t kRows = (int64_t)1 << 22;
+    for (int64_t r = 0; r < a.rows; r += kRows) {
+        NormArgs b = a;
+        b.X += r * a.ldx;
+        if (b.R) b.R += r * a.ldr;
+        if (b.H) b.H += r * a.ldh;
+        b.Y = (char *)a.Y + r * a.ldy * (codes ? 1 : 2);
+        if (b.scale) b.scale += r;
+        if (b.rstd) b.rstd += r;
+        b.rows = a.rows - r < kRows ? a.rows - r : kRows;
+        const hipError_t e = launch_norm_rows(b, codes, vec, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// ------------------------------------------------------------- the gradient
+//
+// With xh = h rstd and g = dy w, element by element:
+//   dX_j = rstd (g_j - xh_j * sum_i(g_i xh_i) / cols) + dH_j
+//   dW_j = sum over rows of dy_j xh_j
+// One pass: workgroup b takes rows b, b + gridDim.x, ...; a thread owns the
+// same columns in every row, so dW's sums over the workgroup's rows stay in
+// its registers (NCH > 0) and go out once, as row b of `part`; a second
+// kernel adds the workgroups' rows in order.
+template <int NCH, bool VEC>
+__global__ void __launch_bounds__(256) k_rms_norm_grad(NormGradArgs a)
+{
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    auto col_of = [&](int j) { return (int64_t)threadIdx.x * 8 + (int64_t)j * 2048; };
+    u32x4 w[NCH];
+    float dw[NCH][8];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        w[j] = u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};   // ones
+        if (a.W && col_of(j) < a.cols) w[j] = norm_load<VEC>(a.W, col_of(j), a.cols, a.align_w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+    }
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+        u32x4 dy[NCH], h[NCH], dh[NCH];
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            dy[j] = h[j] = dh[j] = u32x4{0u, 0u, 0u, 0u};
+            if (col_of(j) < a.cols) {
+                dy[j] = norm_load<VEC>(a.dY + r * a.lddy, col_of(j), a.cols, a.align_dy);
+                h[j] = norm_load<VEC>(a.H + r * a.ldh, col_of(j), a.cols, a.align_h);
+                if (a.dH) dh[j] = norm_load<VEC>(a.dH + r * a.lddh, col_of(j), a.cols, a.align_dh);
+            }
+        }
+        const float rstd = a.rstd[r];
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float plo = bf16_lo(dy[j][i]) * (bf16_lo(h[j][i]) * rstd);
+                const float phi = bf16_hi(dy[j][i]) * (bf16_hi(h[j][i]) * rstd);
+                dw[j][2 * i] += plo;
+                dw[j][2 * i + 1] += phi;
+                dot = __builtin_fmaf(plo, bf16_lo(w[j][i]), dot);
+                dot = __builtin_fmaf(phi, bf16_hi(w[j][i]), dot);
+            }
+        dot = wave_sum(dot);
+        // (two sets of slots in turn: one barrier per row)
+        if (lane == 0) red[turn][wv] = dot;
+        __syncthreads();
+        const float c = (((red[turn][0] + red[turn][1]) + red[turn][2]) + red[turn][3]) / (float)a.cols;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            u32x4 dx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float glo = bf16_lo(dy[j][i]) * bf16_lo(w[j][i]), ghi = bf16_hi(dy[j][i]) * bf16_hi(w[j][i]);
+                const float xlo = bf16_lo(h[j][i]) * rstd, xhi = bf16_hi(h[j][i]) * rstd;
+                dx[i] = pack_bf16x2(__builtin_fmaf(rstd, glo - xlo * c, bf16_lo(dh[j][i])),
+                                    __builtin_fmaf(rstd, ghi - xhi * c, bf16_hi(dh[j][i])));
+            }
+            if (col_of(j) < a.cols) norm_store<VEC>(a.dX + r * a.lddx, col_of(j), a.cols, a.align_dx, dx);
+        }
+    }
+    if (a.part) {
+#pragma unroll
+        for (int j = 0; j < NCH; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col_of(j) + i < a.cols) a.part[(int64_t)blockIdx.x * a.cols + col_of(j) + i] = dw[j][i];
+    }
+}
+
+// Rows past 16384 elements: each is read twice, and a workgroup's row of
+// `part` holds its running sums (each element read and written by one
+// thread only).
+__global__ void __launch_bounds__(256) k_rms_norm_grad_long(NormGradArgs a)
+{
+    __shared__ float red[2][4];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    float *part = a.part ? a.part + (int64_t)blockIdx.x * a.cols : nullptr;
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+        const uint16_t *dyr = a.dY + r * a.lddy, *hr = a.H + r * a.ldh;
+        const float rstd = a.rstd[r];
+        float dot = 0.f;
+        for (int64_t col = threadIdx.x; col < a.cols; col += 256) {
+            const float p = __uint_as_float((uint32_t)dyr[col] << 16) * (__uint_as_float((uint32_t)hr[col] << 16) * rstd);
+            const float w = a.W ? __uint_as_float((uint32_t)a.W[col] << 16) : 1.0f;
+            dot = __builtin_fmaf(p, w, dot);
+            if (part) part[col] = r == (int64_t)blockIdx.x ? p : part[col] + p;
+        }
+        dot = wave_sum(dot);
+        if (lane == 0) red[turn][wv] = dot;
+        __syncthreads();
+        const float c = (((red[turn][0] + red[turn][1]) + red[turn][2]) + red[turn][3]) / (float)a.cols;
+        for (int64_t col = threadIdx.x; col < a.cols; col += 256) {
+            const float w = a.W ? __uint_as_float((uint32_t)a.W[col] << 16) : 1.0f;
+            const float g = __uint_as_float((uint32_t)dyr[col] << 16) * w;
+            const float xh = __uint_as_float((uint32_t)hr[col] << 16) * rstd;
+            const float dh = a.dH ? __uint_as_float((uint32_t)a.dH[r * a.lddh + col] << 16) : 0.f;
+            a.dX[r * a.lddx + col] = (uint16_t)bf16_rne(__builtin_fmaf(rstd, g - xh * c, dh));
+        }
+    }
+}
+
+// dW[n] = sum of rows 0 .. parts - 1 of `part`: a workgroup owns 64
+// columns, its four waves add every fourth row each, joined in order.
+__global__ void __launch_bounds__(256) k_norm_dw(const float *part, int parts, int64_t cols, float *dW)
+{
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (n < cols)
+        for (int p = wv; p < parts; p += 4) s += part[(int64_t)p * cols + n];
+    red[wv][lane] = s;
+    __syncthreads();
+    if (wv == 0 && n < cols) dW[n] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+}
+
+template <int NCH>
+static void launch_norm_grad_held(const NormGradArgs &a, int grid, bool vec, hipStream_t s)
+{
+    if (vec) hipLaunchKernelGGL((k_rms_norm_grad<NCH, true>), dim3(grid), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm_grad<NCH, false>), dim3(grid), dim3(256), 0, s, a);
+}
+
+hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, s, part, parts, cols, dW);
+    return hipGetLastError();
+}
+
+int norm_grad_parts(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+
+hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s)
+{
+    const int grid = norm_grad_parts(a.rows);
+    if (a.cols <= 2048) launch_norm_grad_held<1>(a, grid, vec, s);
+    else if (a.cols <= 4096) launch_norm_grad_held<2>(a, grid, vec, s);
+    else if (a.cols <= 8192) launch_norm_grad_held<4>(a, grid, vec, s);
+    else if (a.cols <= 16384) launch_norm_grad_held<8>(a, grid, vec, s);
+    else hipLaunchKernelGGL(k_rms_norm_grad_long, dim3(grid), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !a.dW ? e : launch_norm_dw(a.part, grid, a.cols, a.dW, s);
+}
+
+}  // namespace g5

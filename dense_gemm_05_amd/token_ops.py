@@ -1,0 +1,137 @@
+"""Binding of the operators around a projection: the RMS norm with the
+residual's addition and its gradient.  As gemm.py: argument marshalling only;
+the arithmetic runs in the gfx950 kernels of libgemm05.so.
+"""
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import GemmError, lib
+from .gemm import Workspace, _check_dev, _launch, _ld
+
+__all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward"]
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _vector(t, n, dtype, name):
+    """A contiguous vector of n elements, or None."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1)):
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements")
+    return t
+
+
+def _rows(t, shape, dtype, name):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
+    return t
+
+
+def _scratch(workspace, dev, need):
+    """The memory of a Workspace (grown to `need` bytes) or of a uint8 tensor."""
+    if workspace is None:
+        workspace = Workspace(dev)
+    if isinstance(workspace, Workspace):
+        if workspace.device != dev:
+            raise ValueError("the workspace must be on the operands' GPU")
+        return workspace.reserve(need)
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.dim() != 1:
+        raise ValueError("a workspace tensor must be a 1-D uint8 tensor")
+    if workspace.device != dev:
+        raise ValueError("the workspace must be on the operands' GPU")
+    return workspace
+
+
+def _rms_norm(what, X, W, residual, eps, Y, H, rstd, codes, scale):
+    if X.dtype != torch.bfloat16 or X.dim() != 2:
+        raise TypeError(f"{what} takes a 2-D bfloat16 X")
+    rows, cols = X.shape
+    _rows(residual, (rows, cols), torch.bfloat16, "residual")
+    _vector(W, cols, torch.bfloat16, "W")
+    _vector(rstd, rows, torch.float32, "rstd")
+    if H is not None and residual is None:
+        raise ValueError("H is the sum with a residual: none was given")
+    dev = _check_dev(X, W, residual, Y, H, rstd, scale)
+    ydt = torch.uint8 if codes else torch.bfloat16
+    if Y is None:
+        Y = torch.empty((rows, cols), dtype=ydt, device=dev)
+    if codes and str(Y.dtype) == "torch.float8_e4m3fn":
+        Y = Y.view(torch.uint8)
+    _rows(Y, (rows, cols), ydt, "Q" if codes else "Y")
+    if codes and scale is None:
+        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if codes:
+        _vector(scale, rows, torch.float32, "scale")
+    if residual is not None and H is None:
+        H = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    _rows(H, (rows, cols), torch.bfloat16, "H")
+    st = _launch(lib().gemm_rms_norm, dev, rows, cols, X.data_ptr(), _ld(X, cols), _ptr(residual),
+                 cols if residual is None else _ld(residual, cols), _ptr(H), cols if H is None else _ld(H, cols),
+                 _ptr(W), float(eps), Y.data_ptr(), _ld(Y, cols), _lib.GEMM_OUT_E4M3 if codes else _lib.GEMM_OUT_BF16,
+                 _ptr(scale) if codes else None, _ptr(rstd))
+    if st != 0:
+        raise GemmError(st, "gemm_rms_norm")
+    return Y, scale, H
+
+
+def rms_norm(X, W=None, residual=None, eps=1e-6, Y=None, H=None, rstd=None):
+    """Y = bf16(h * rstd * W) per row of a bfloat16 [rows, cols] tensor, with
+    h = bf16(X + residual) (h = X without a residual) and
+    rstd = 1 / sqrt(mean(h^2) + eps) (gemm_rms_norm).  W: a bfloat16 vector
+    of cols elements or None (ones).  Returns Y, or (Y, H) with a residual:
+    H, the sum, may be X or residual itself.  rstd: a float32 vector of rows
+    elements to be filled for rms_norm_backward."""
+    Y, _, H = _rms_norm("rms_norm", X, W, residual, eps, Y, H, rstd, False, None)
+    return Y if residual is None else (Y, H)
+
+
+def rms_norm_e4m3(X, W=None, residual=None, eps=1e-6, Q=None, scale=None, H=None, rstd=None):
+    """The rows of rms_norm as E4M3FN codes (uint8 [rows, cols]) with
+    float32 factors scale[rows]: those of gemm_fp8_quantize_rows on rms_norm's
+    bf16 output, and the first operand of gemm_fp8_nt.  Returns (Q, scale),
+    or (Q, scale, H) with a residual."""
+    Q, scale, H = _rms_norm("rms_norm_e4m3", X, W, residual, eps, Q, H, rstd, True, scale)
+    return (Q, scale) if residual is None else (Q, scale, H)
+
+
+def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, need_dw=True, workspace=None):
+    """The gradient of rms_norm (gemm_rms_norm_backward): from dY [rows, cols]
+    (bfloat16), H what was normed, W and the forward call's rstd, and dH the
+    gradient that reaches H from the residual stream (or None), returns
+    (dX bfloat16 [rows, cols], dW float32 [cols]; None without need_dw).
+    dX is the gradient of X and of the residual.  workspace: as for the
+    products (one is created for the call when None is given)."""
+    if dY.dtype != torch.bfloat16 or dY.dim() != 2:
+        raise TypeError("rms_norm_backward takes a 2-D bfloat16 dY")
+    rows, cols = dY.shape
+    _rows(H, (rows, cols), torch.bfloat16, "H")
+    _rows(dH, (rows, cols), torch.bfloat16, "dH")
+    _vector(W, cols, torch.bfloat16, "W")
+    if rstd is None:
+        raise ValueError("rstd: the vector the forward call filled")
+    _vector(rstd, rows, torch.float32, "rstd")
+    dev = _check_dev(dY, H, W, rstd, dH, dX, dW)
+    if dX is None:
+        dX = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    _rows(dX, (rows, cols), torch.bfloat16, "dX")
+    buf = None
+    if need_dw:
+        if dW is None:
+            dW = torch.empty((cols,), dtype=torch.float32, device=dev)
+        _vector(dW, cols, torch.float32, "dW")
+        n = ctypes.c_uint64(0)
+        st = lib().gemm_rms_norm_workspace_size(rows, cols, ctypes.byref(n))
+        if st != 0:
+            raise GemmError(st, "gemm_rms_norm_workspace_size")
+        buf = _scratch(workspace, dev, n.value)
+    else:
+        dW = None
+    st = _launch(lib().gemm_rms_norm_backward, dev, rows, cols, dY.data_ptr(), _ld(dY, cols), H.data_ptr(),
+                 _ld(H, cols), _ptr(W), rstd.data_ptr(), _ptr(dH), cols if dH is None else _ld(dH, cols),
+                 dX.data_ptr(), _ld(dX, cols), _ptr(dW), _ptr(buf), 0 if buf is None else buf.numel())
+    if st != 0:
+        raise GemmError(st, "gemm_rms_norm_backward")
+    return dX, dW

@@ -516,6 +516,72 @@ int gemm_workspace_size(int op, int64_t batch, int64_t M, int64_t N, int64_t K,
                         uint64_t c_addr, int64_t ldc, int64_t strideC,
                         int c_type, uint64_t *bytes);
 
+/* ---- RMS norm ---------------------------------------------------------------
+ *
+ * The norm that stands before a projection, with the residual's addition and
+ * an output in bf16 or in the codes an FP8 projection reads:
+ *
+ *     h    = bf16(x + r)                      (h = x when R is NULL)
+ *     rstd = 1 / sqrt(sum_j h_j^2 / cols + eps)
+ *     y_j  = bf16(h_j * rstd * w_j)           (w = 1 when W is NULL)
+ *
+ * per row of X [rows, cols] (bf16 bit patterns, row stride ldx); R [rows,
+ * cols] the residual stream or NULL, H [rows, cols] where the sum is stored
+ * or NULL (requires R), W a bf16 vector of cols elements or NULL.  y_type
+ * GEMM_OUT_BF16: Y [rows, cols] bf16.  GEMM_OUT_E4M3: Y holds E4M3FN codes
+ * (bytes) and scale[rows] their factors, those that gemm_fp8_quantize_rows
+ * gives for the bf16 y (the A operand of gemm_fp8_nt); scale is not touched
+ * otherwise.  rstd[rows] (float) or NULL receives each row's rstd, which the
+ * gradient reads.  The sums, rstd and the products are FP32 (a row's sum of
+ * squares must stay below 3.4e38); a row's result does not depend on the
+ * other rows.  A row of zeros with eps == 0 gives NaN, as the formula does;
+ * an infinite or NaN element spreads over its row only.
+ *
+ * H may be X or R itself (same pointer and stride: the sum is formed in
+ * place); no other output may overlap an input or another output.  Rows of
+ * whole 16-byte chunks at 16-byte aligned starts (codes: 8-byte) run
+ * fastest; rows past 16384 elements are read more than once.  rows == 0 or
+ * cols == 0: nothing is done.  Errors, nothing enqueued:
+ * GEMM_ERR_INVALID_ARG for negative sizes, rows > 2^31 - 1, another y_type,
+ * a negative or non-finite eps, strides below cols, missing or misaligned
+ * pointers (bf16 2 bytes, float 4), H without R, or an overlap. */
+int gemm_rms_norm(int64_t rows, int64_t cols,
+                  const uint16_t *X, int64_t ldx,
+                  const uint16_t *R, int64_t ldr,
+                  uint16_t *H, int64_t ldh,
+                  const uint16_t *W, float eps,
+                  void *Y, int64_t ldy, int y_type,
+                  float *scale, float *rstd,
+                  void *stream);
+
+/* The gradient of gemm_rms_norm's bf16 output: dY [rows, cols] the gradient
+ * of y, H [rows, cols] what was normed (X without a residual), W and rstd
+ * as in the forward call, dH [rows, cols] the gradient that reaches h from
+ * the residual stream or NULL (all bf16 but rstd).  With xh = h * rstd and
+ * g = dy * w,
+ *
+ *     dX_j = bf16(rstd * (g_j - xh_j * sum_i(g_i * xh_i) / cols) + dH_j)
+ *     dW_j = sum over the rows of dy_j * xh_j          (float [cols], or NULL)
+ *
+ * dX is the gradient of both X and R.  dW goes through the workspace
+ * (gemm_rms_norm_workspace_size bytes, 256-byte aligned; its first
+ * GEMM_WORKSPACE_COUNTER_BYTES are left untouched, so gemm_run's workspace
+ * serves), summed in a fixed order: the same call gives the same bits.
+ * Without dW no workspace is needed.  cols == 0: nothing is done; rows == 0:
+ * dW := 0, the empty sum (no workspace needed).  Errors as gemm_rms_norm, and GEMM_ERR_WORKSPACE
+ * for a missing or small workspace with dW. */
+int gemm_rms_norm_backward(int64_t rows, int64_t cols,
+                           const uint16_t *dY, int64_t lddy,
+                           const uint16_t *H, int64_t ldh,
+                           const uint16_t *W, const float *rstd,
+                           const uint16_t *dH, int64_t lddh,
+                           uint16_t *dX, int64_t lddx, float *dW,
+                           void *workspace, uint64_t workspace_bytes,
+                           void *stream);
+
+/* Workspace bytes of gemm_rms_norm_backward with dW (host only). */
+int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
+
 /* Static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 

@@ -1,0 +1,124 @@
+"""Host-only checks of the operators around a projection: arguments refused
+before anything is enqueued (no GPU), and the sizes their workspaces need."""
+import ctypes
+
+import pytest
+import torch
+
+import dense_gemm_05_amd as g5
+from dense_gemm_05_amd import token_ops as ops
+from test_binding_host import FakeGpuTensor
+
+P = 0x7F0000000000     # fake, aligned addresses 16 GiB apart, never dereferenced
+X, R, H, W, Y, S, T = (P + (i << 34) for i in range(7))
+INV, WS, OK = g5.GEMM_ERR_INVALID_ARG, g5.GEMM_ERR_WORKSPACE, g5.GEMM_OK
+CR = g5.GEMM_WORKSPACE_COUNTER_BYTES
+
+
+def norm(**kw):
+    a = dict(rows=4, cols=64, X=X, ldx=64, R=R, ldr=64, H=H, ldh=64, W=W, eps=1e-6, Y=Y, ldy=64, t=0, scale=None,
+             rstd=None)
+    a.update(kw)
+    return g5.lib().gemm_rms_norm(a["rows"], a["cols"], a["X"], a["ldx"], a["R"], a["ldr"], a["H"], a["ldh"], a["W"],
+                                  a["eps"], a["Y"], a["ldy"], a["t"], a["scale"], a["rstd"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=-1), dict(cols=-1), dict(rows=1 << 31), dict(X=None), dict(Y=None), dict(ldx=63), dict(ldr=63),
+    dict(ldh=63), dict(ldy=63), dict(t=1), dict(t=3), dict(t=2), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(eps=float("inf")), dict(R=None), dict(X=X + 1), dict(R=R + 1), dict(H=H + 1), dict(W=W + 1), dict(Y=Y + 1),
+    dict(rstd=T + 2), dict(t=2, scale=S + 2),
+    dict(Y=X), dict(Y=R), dict(Y=H), dict(Y=W), dict(H=X + 128), dict(H=X, ldh=128), dict(H=R, ldh=72),
+    dict(rstd=X), dict(rstd=Y), dict(t=2, scale=Y), dict(t=2, scale=S, rstd=S), dict(H=W),
+    dict(Y=X + 2 * 3 * 64 + 126)])
+def test_norm_refuses(bad):
+    assert norm(**bad) == INV
+
+
+def grad(**kw):
+    a = dict(rows=4, cols=64, dY=X, lddy=64, H=H, ldh=64, W=W, rstd=S, dH=R, lddh=64, dX=Y, lddx=64, dW=T, ws=P + (8 << 34),
+             n=CR + 4096)
+    a.update(kw)
+    return g5.lib().gemm_rms_norm_backward(a["rows"], a["cols"], a["dY"], a["lddy"], a["H"], a["ldh"], a["W"], a["rstd"],
+                                           a["dH"], a["lddh"], a["dX"], a["lddx"], a["dW"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(rows=-1), INV), (dict(cols=-2), INV), (dict(rows=1 << 31), INV), (dict(dY=None), INV), (dict(H=None), INV),
+    (dict(rstd=None), INV), (dict(dX=None), INV), (dict(lddy=63), INV), (dict(ldh=63), INV), (dict(lddh=63), INV),
+    (dict(lddx=63), INV), (dict(dY=X + 1), INV), (dict(H=H + 1), INV), (dict(W=W + 1), INV), (dict(dH=R + 1), INV),
+    (dict(dX=Y + 1), INV), (dict(rstd=S + 2), INV), (dict(dW=T + 2), INV), (dict(dX=X), INV), (dict(dX=H), INV),
+    (dict(dX=R), INV), (dict(dW=S), INV), (dict(dW=Y), INV), (dict(ws=None), WS), (dict(n=CR + 1023), WS),
+    (dict(ws=P + (8 << 34) + 128), INV), (dict(ws=H), INV), (dict(rows=0, dW=T + 2), INV)])
+def test_norm_gradient_refuses(bad, status):
+    assert grad(**bad) == status
+
+
+def test_norm_empty_calls_do_nothing():
+    assert norm(rows=0, X=None, Y=None) == OK and norm(cols=0, X=None, Y=None) == OK
+    assert grad(cols=0, dY=None) == OK and grad(rows=0, dW=None, dY=None) == OK
+
+
+def test_norm_workspace_size():
+    n = ctypes.c_uint64(1)
+    f = g5.lib().gemm_rms_norm_workspace_size
+    assert f(0, 64, ctypes.byref(n)) == OK and n.value == 0
+    assert f(3, 64, ctypes.byref(n)) == OK and n.value == CR + 3 * 64 * 4
+    big = n.value
+    assert f(1 << 20, 4096, ctypes.byref(n)) == OK and n.value > big
+    assert f(-1, 64, ctypes.byref(n)) == INV and f(4, -1, ctypes.byref(n)) == INV
+    assert f(4, 64, None) == OK
+
+
+@pytest.fixture
+def no_lib(monkeypatch):
+    def boom():
+        raise AssertionError("the library was called")
+    monkeypatch.setattr(ops, "lib", boom)
+
+
+def _bf(*shape):
+    return FakeGpuTensor(shape, torch.bfloat16)
+
+
+def _f32(*shape):
+    return FakeGpuTensor(shape, torch.float32)
+
+
+def test_norm_binding_refuses(no_lib):
+    x = _bf(4, 64)
+    for fn in (g5.rms_norm, g5.rms_norm_e4m3):
+        with pytest.raises(TypeError):
+            fn(_f32(4, 64))
+        with pytest.raises(TypeError):
+            fn(_bf(4, 2, 32))
+        with pytest.raises(ValueError):
+            fn(x, _bf(65))
+        with pytest.raises(ValueError):
+            fn(x, _f32(64))
+        with pytest.raises(ValueError):
+            fn(x, residual=_bf(4, 65))
+        with pytest.raises(ValueError):
+            fn(x, H=_bf(4, 64))
+        with pytest.raises(ValueError):
+            fn(x, rstd=_f32(5))
+        with pytest.raises(ValueError):
+            fn(x, residual=torch.empty((4, 64), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        g5.rms_norm(x, Y=_f32(4, 64))
+    with pytest.raises(ValueError):
+        g5.rms_norm_e4m3(x, Q=_bf(4, 64))
+    with pytest.raises(ValueError):
+        g5.rms_norm_e4m3(x, Q=FakeGpuTensor((4, 64), torch.uint8), scale=_f32(3))
+
+
+def test_norm_gradient_binding_refuses(no_lib):
+    x, s = _bf(4, 64), _f32(4)
+    with pytest.raises(TypeError):
+        g5.rms_norm_backward(_f32(4, 64), x, None, s)
+    for bad in (dict(H=_bf(4, 65)), dict(W=_bf(63)), dict(rstd=_f32(3)), dict(rstd=None), dict(dH=_bf(3, 64)),
+                dict(dX=_f32(4, 64)), dict(dX=torch.empty((4, 64), dtype=torch.bfloat16))):
+        a = dict(H=x, W=None, rstd=s)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            g5.rms_norm_backward(x, a.pop("H"), a.pop("W"), a.pop("rstd"), **a)
