@@ -49,7 +49,8 @@ EXPORTS = ("gemm_sgemm", "gemm_bf16", "gemm_bf16_batched", "gemm_bf16_nt", "gemm
            "gemm_status_string",
            "gemm_plan_query", "gemm_plan_query_ex", "gemm_model_local_bytes", "gemm_model_traffic_bytes", "gemm_model_quant_traffic", "gemm_model_act_chain_bytes",
            "gemm_tile_map",
-           "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size")
+           "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size",
+           "gemm_moe_swiglu", "gemm_moe_workspace_size")
 
 
 class GemmPlan(ctypes.Structure):
@@ -161,6 +162,11 @@ def lib():
     L.gemm_rms_norm_backward.restype = i32
     L.gemm_rms_norm_workspace_size.argtypes = [i64, i64, ctypes.POINTER(u64)]
     L.gemm_rms_norm_workspace_size.restype = i32
+    L.gemm_moe_swiglu.argtypes = [i64, i64, i64, i64, i64, i32, p, i64, p, i64, i32, p, i64, i64, p, p, i64, i64, p,
+                                  p, i64, i32, p, p, p, u64, p]
+    L.gemm_moe_swiglu.restype = i32
+    L.gemm_moe_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(u64)]
+    L.gemm_moe_workspace_size.restype = i32
     _lib = L
     return L
 

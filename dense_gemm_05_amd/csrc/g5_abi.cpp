@@ -1325,6 +1325,118 @@ int gemm_rms_norm_backward(int64_t rows, int64_t cols, const uint16_t *dY, int64
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+// ---- mixture-of-experts layer for a few tokens
+// Scratch after the counter region, each part 256-byte aligned.
+struct MoeLayout {
+    size_t ids, gates, z, part, total;
+    int64_t ldz, zplane;
+};
+static MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t topk)
+{
+    MoeLayout L;
+    const size_t pairs = (size_t)T * topk;
+    L.ldz = (I + 7) / 8 * 8;
+    L.zplane = (int64_t)pairs * L.ldz;
+    L.ids = g5::kCounterBytes;
+    L.gates = L.ids + g5::round256(pairs * 4);
+    L.z = L.gates + g5::round256(pairs * 4);
+    L.part = L.z + g5::round256((size_t)L.zplane * 4);
+    L.total = L.part + g5::round256(pairs * (size_t)H * 4);
+    return L;
+}
+static bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk)
+{
+    return T >= 0 && T <= g5::kMoeMaxTokens && H >= 0 && H <= g5::kMoeMaxWidth && I >= 0 && I <= g5::kMoeMaxWidth &&
+           E >= 1 && E <= g5::kMoeMaxExperts && topk >= 1 && topk <= g5::kMoeMaxTopk && topk <= E;
+}
+
+int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, uint64_t *bytes)
+{
+    if (bytes) *bytes = 0;
+    if (!moe_sizes_ok(T, H, I, E, topk)) return GEMM_ERR_INVALID_ARG;
+    if (bytes && T > 0) *bytes = moe_layout(T, H, I, topk).total;
+    return GEMM_OK;
+}
+
+int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, int renormalize, const uint16_t *X,
+                    int64_t ldx, const float *logits, int64_t ldl, int w_type, const void *Wgu, int64_t ldgu,
+                    int64_t strideGu, const float *scale_gu, const void *Wd, int64_t ldd, int64_t strideD,
+                    const float *scale_d, void *Y, int64_t ldy, int c_type, int32_t *ids, float *gates,
+                    void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    using g5::Range;
+    const bool codes = w_type == GEMM_OUT_E4M3;
+    if (!moe_sizes_ok(T, H, I, E, topk)) return GEMM_ERR_INVALID_ARG;
+    if ((w_type != GEMM_OUT_BF16 && !codes) || (c_type != GEMM_OUT_BF16 && c_type != GEMM_OUT_F32))
+        return GEMM_ERR_INVALID_ARG;
+    if (T == 0) return GEMM_OK;
+    const int ew = codes ? 1 : 2, ec = c_type == GEMM_OUT_F32 ? 4 : 2;
+    if (!logits || ldl < E || ((uint64_t)logits % 4) || ((uint64_t)ids % 4) || ((uint64_t)gates % 4))
+        return GEMM_ERR_INVALID_ARG;
+    if (H > 0 && (!X || !Y || ldx < H || ldy < H || ((uint64_t)X % 2) || ((uint64_t)Y % ec))) return GEMM_ERR_INVALID_ARG;
+    if (((uint64_t)scale_gu % 4) || ((uint64_t)scale_d % 4) || (!codes && (scale_gu || scale_d)))
+        return GEMM_ERR_INVALID_ARG;
+    const bool weights = H > 0 && I > 0;
+    if (weights && (!Wgu || !Wd || ldgu < H || ldd < I || strideGu < 0 || strideD < 0 || ((uint64_t)Wgu % ew) ||
+                    ((uint64_t)Wd % ew)))
+        return GEMM_ERR_INVALID_ARG;
+    const Range none{0, 0};
+    const Range in[] = {H > 0 ? g5::extent((uint64_t)X, 1, T, H, ldx, 0, 2) : none,
+                        g5::extent((uint64_t)logits, 1, T, E, ldl, 0, 4),
+                        weights ? g5::extent((uint64_t)Wgu, E, 2 * I, H, ldgu, strideGu, ew) : none,
+                        weights ? g5::extent((uint64_t)Wd, E, H, I, ldd, strideD, ew) : none,
+                        vec_range(scale_gu, E * 2 * I, 4), vec_range(scale_d, E * H, 4)};
+    const MoeLayout L = moe_layout(T, H, I, topk);
+    const Range out[] = {H > 0 ? g5::extent((uint64_t)Y, 1, T, H, ldy, 0, ec) : none, vec_range(ids, T * topk, 4),
+                         vec_range(gates, T * topk, 4),
+                         workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)L.total}
+                                   : none};
+    for (const Range &r : in)
+        if (r.hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
+    if (out[0].hi > ((__int128)1 << 63) || outputs_overlap(out, 4, in, 6)) return GEMM_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < L.total) return GEMM_ERR_WORKSPACE;
+    if ((uint64_t)workspace % 256) return GEMM_ERR_INVALID_ARG;
+    const int st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    char *ws = (char *)workspace;
+    g5::MoeArgs a{};
+    a.X = X;
+    a.logits = logits;
+    a.Wgu = Wgu;
+    a.Wd = Wd;
+    a.scale_gu = scale_gu;
+    a.scale_d = scale_d;
+    a.Y = Y;
+    a.ids = ids;
+    a.gates = gates;
+    a.T = T;
+    a.H = H;
+    a.I = I;
+    a.E = E;
+    a.ldx = ldx;
+    a.ldl = ldl;
+    a.ldgu = ldgu;
+    a.strideGu = strideGu;
+    a.ldd = ldd;
+    a.strideD = strideD;
+    a.ldy = ldy;
+    a.topk = (int)topk;
+    a.renormalize = renormalize != 0;
+    a.out_f32 = ec == 4;
+    a.align_x = g5::row_alignment((uint64_t)X, ldx, 0, 1, 2);
+    a.align_gu = g5::row_alignment((uint64_t)Wgu, ldgu, strideGu, E, ew);
+    a.align_d = g5::row_alignment((uint64_t)Wd, ldd, strideD, E, ew);
+    a.w_ids = (int32_t *)(ws + L.ids);
+    a.w_gates = (float *)(ws + L.gates);
+    a.z = (uint16_t *)(ws + L.z);
+    a.ldz = L.ldz;
+    a.zplane = L.zplane;
+    a.part = (float *)(ws + L.part);
+    const hipError_t e = g5::launch_moe(a, codes, a.align_x >= 16 && a.align_gu >= 16, a.align_d >= 16,
+                                        (hipStream_t)stream);
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
 const char *gemm_status_string(int status)
 {
     switch (status) {

@@ -145,4 +145,28 @@ int norm_grad_parts(int64_t rows);
 hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s);
 hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s);
 
+// The mixture-of-experts SwiGLU layer for a few tokens (g5_moe.hip).
+// Weights bf16, or E4M3FN codes with factors per row; strides in elements.
+constexpr int kMoeMaxTokens = 256, kMoeMaxExperts = 1024, kMoeMaxTopk = 32, kMoeMaxWidth = 65536;
+struct MoeArgs {
+    const uint16_t *X;
+    const float *logits;
+    const void *Wgu, *Wd;
+    const float *scale_gu, *scale_d;   // [E, 2I], [E, H] or NULL
+    void *Y;
+    int32_t *ids;                      // [T, topk] or NULL
+    float *gates;
+    int64_t T, H, I, E, ldx, ldl, ldgu, strideGu, ldd, strideD, ldy;
+    int topk, renormalize, out_f32, align_x, align_gu, align_d;
+    // scratch: the routing [T * topk]; z as two bf16 planes of rows of ldz;
+    // each pair's gated output, rows of H floats
+    int32_t *w_ids;
+    float *w_gates;
+    uint16_t *z;
+    int64_t ldz, zplane;
+    float *part;
+};
+// vec_gu, vec_d: the rows of X and Wgu (of Wd) start 16-byte aligned.
+hipError_t launch_moe(const MoeArgs &a, bool codes, bool vec_gu, bool vec_d, hipStream_t s);
+
 }  // namespace g5

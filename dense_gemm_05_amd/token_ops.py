@@ -1,5 +1,6 @@
 """Binding of the operators around a projection: the RMS norm with the
-residual's addition and its gradient.  As gemm.py: argument marshalling only;
+residual's addition and its gradient, and the mixture-of-experts layer for a
+few tokens.  As gemm.py: argument marshalling only;
 the arithmetic runs in the gfx950 kernels of libgemm05.so.
 """
 import ctypes
@@ -8,9 +9,9 @@ import torch
 
 from . import _lib
 from ._lib import GemmError, lib
-from .gemm import Workspace, _check_dev, _launch, _ld
+from .gemm import Workspace, _bstride, _check_dev, _codes, _launch, _ld, _out_code
 
-__all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward"]
+__all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward", "moe_swiglu"]
 
 
 def _ptr(t):
@@ -135,3 +136,60 @@ def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, need_dw=True, w
     if st != 0:
         raise GemmError(st, "gemm_rms_norm_backward")
     return dX, dW
+
+
+def moe_swiglu(X, logits, topk, Wgu, Wd, scale_gu=None, scale_d=None, renormalize=True, Y=None,
+               out_dtype=torch.bfloat16, ids=None, gates=None, workspace=None):
+    """A mixture-of-experts SwiGLU layer for up to 256 tokens, behind the
+    router's product (gemm_moe_swiglu): X [T, H] bfloat16, logits [T, E]
+    float32, Wgu [E, 2I, H] (gate rows, then up rows) and Wd [E, H, I] in
+    bfloat16, or as E4M3FN codes with float32 factors scale_gu [E, 2I] and
+    scale_d [E, H].  Each token's topk experts (ties to the lowest index; -inf
+    and NaN never) are weighted by the softmax of their logits, over the
+    chosen ones (renormalize) or over all.  Returns (Y [T, H] in out_dtype,
+    ids int32 [T, topk], gates float32 [T, topk])."""
+    if X.dtype != torch.bfloat16 or X.dim() != 2 or logits.dtype != torch.float32 or logits.dim() != 2:
+        raise TypeError("moe_swiglu takes a 2-D bfloat16 X and 2-D float32 logits")
+    if Wgu.dim() != 3 or Wd.dim() != 3:
+        raise ValueError("Wgu must be [E, 2I, H] and Wd [E, H, I]")
+    coded = Wgu.dtype != torch.bfloat16
+    if coded:
+        Wgu, Wd = _codes(Wgu), _codes(Wd)
+    elif Wd.dtype != torch.bfloat16:
+        raise TypeError("Wgu and Wd must both be bfloat16 or both codes")
+    T, H = X.shape
+    E, I2, H2 = Wgu.shape
+    I = I2 // 2
+    topk = int(topk)
+    if I2 % 2 or H2 != H or tuple(Wd.shape) != (E, H, I) or tuple(logits.shape) != (T, E):
+        raise ValueError("expected X [T, H], logits [T, E], Wgu [E, 2I, H] and Wd [E, H, I]")
+    if not coded and (scale_gu is not None or scale_d is not None):
+        raise ValueError("factors belong to E4M3FN weights")
+    for s, shape, name in ((scale_gu, (E, I2), "scale_gu"), (scale_d, (E, H), "scale_d")):
+        if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != shape or not s.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous float32 {list(shape)}")
+    dev = _check_dev(X, logits, Wgu, Wd, scale_gu, scale_d, Y, ids, gates)
+    n = ctypes.c_uint64(0)
+    st = lib().gemm_moe_workspace_size(T, H, I, E, topk, ctypes.byref(n))
+    if st != 0:
+        raise GemmError(st, "gemm_moe_swiglu")
+    if Y is None:
+        Y = torch.empty((T, H), dtype=out_dtype, device=dev)
+    if ids is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    if gates is None:
+        gates = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    if tuple(Y.shape) != (T, H):
+        raise ValueError("Y must be [T, H]")
+    for t, dt, name in ((ids, torch.int32, "ids"), (gates, torch.float32, "gates")):
+        if tuple(t.shape) != (T, topk) or t.dtype != dt or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dt} [T, topk]")
+    buf = _scratch(workspace, dev, n.value)
+    st = _launch(lib().gemm_moe_swiglu, dev, T, H, I, E, topk, 1 if renormalize else 0, X.data_ptr(), _ld(X, H),
+                 logits.data_ptr(), _ld(logits, E), _lib.GEMM_OUT_E4M3 if coded else _lib.GEMM_OUT_BF16,
+                 Wgu.data_ptr(), _ld(Wgu, H), _bstride(Wgu), _ptr(scale_gu), Wd.data_ptr(), _ld(Wd, I), _bstride(Wd),
+                 _ptr(scale_d), Y.data_ptr(), _ld(Y, H), _out_code(Y.dtype), ids.data_ptr(), gates.data_ptr(),
+                 _ptr(buf), 0 if buf is None else buf.numel())
+    if st != 0:
+        raise GemmError(st, "gemm_moe_swiglu")
+    return Y, ids, gates

@@ -582,6 +582,60 @@ int gemm_rms_norm_backward(int64_t rows, int64_t cols,
 /* Workspace bytes of gemm_rms_norm_backward with dW (host only). */
 int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
 
+/* ---- mixture-of-experts layer for a few tokens --------------------------------
+ *
+ * Everything behind the router's product, for T tokens (0 <= T <= 256;
+ * larger batches: gemm_bf16_nt_batched or gemm_fp8_nt_batched per expert and
+ * gemm_act_chain).  Per token t, with l = logits[t] (float [T, E], e.g.
+ * gemm_bf16_nt with a float output):
+ *
+ *     ids[t]   = the topk largest of l, in falling order, ties to the lowest
+ *                index; an expert whose logit is -inf or NaN is never chosen
+ *     gates[t] = exp(l - max) / sum over the chosen experts (renormalize), or
+ *                over all experts (renormalize == 0)
+ *     z_s      = silu(x Wg_e^T) (.) (x Wu_e^T),   e = ids[t][s]
+ *     y        = sum_s gates[t][s] * (z_s Wd_e^T)
+ *
+ * A token with fewer than topk experts to choose from has id -1 and gate 0
+ * in the rest; one with none gets zeros.  A logit of +inf gives NaN gates.
+ * Weights in the [out, in] layout of a linear layer, one per expert: Wgu
+ * [E, 2I, H] the gate rows 0 .. I-1 and the up rows I .. 2I-1 (row stride
+ * ldgu, expert stride strideGu), Wd [E, H, I] (ldd, strideD); w_type
+ * GEMM_OUT_BF16 (scale_gu and scale_d NULL) or GEMM_OUT_E4M3: codes (bytes)
+ * with factors per row scale_gu [E, 2I] and scale_d [E, H] (float,
+ * contiguous; NULL: 1), as gemm_fp8_quantize_rows gives them.  X [T, H]
+ * bf16; Y [T, H] bf16 or float by c_type.  ids [T, topk] (int32) and gates
+ * [T, topk] (float), contiguous, or NULL.
+ *
+ * Products are summed in FP32, z is kept as the sum of two bf16 values (to
+ * 2^-16 of it) and y rounded once: unlike the fused epilogues above, no
+ * intermediate is rounded to bf16.  Only the chosen experts' weights are
+ * read.  Deterministic, and a token's result does not depend on the others
+ * in the call.  1 <= topk <= min(E, 32), E <= 1024, H and I <= 65536.
+ * 16-byte aligned rows run fastest; any other alignment is taken.
+ * workspace: gemm_moe_workspace_size bytes, 256-byte aligned, its first
+ * GEMM_WORKSPACE_COUNTER_BYTES zero before and after the call (gemm_run's
+ * workspace serves); calls that may overlap in time need workspaces of their
+ * own.  T == 0: nothing is done.  I == 0 gives zeros.  Errors, nothing
+ * enqueued: GEMM_ERR_INVALID_ARG for sizes outside these ranges, another
+ * w_type or c_type, factors with bf16 weights, strides below the row
+ * lengths, negative expert strides, missing or misaligned pointers, an
+ * output or the workspace overlapping an input or another output;
+ * GEMM_ERR_WORKSPACE for a missing or small workspace. */
+int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, int renormalize,
+                    const uint16_t *X, int64_t ldx,
+                    const float *logits, int64_t ldl,
+                    int w_type,
+                    const void *Wgu, int64_t ldgu, int64_t strideGu, const float *scale_gu,
+                    const void *Wd, int64_t ldd, int64_t strideD, const float *scale_d,
+                    void *Y, int64_t ldy, int c_type,
+                    int32_t *ids, float *gates,
+                    void *workspace, uint64_t workspace_bytes,
+                    void *stream);
+
+/* Workspace bytes of gemm_moe_swiglu (host only). */
+int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, uint64_t *bytes);
+
 /* Static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 

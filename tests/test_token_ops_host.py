@@ -122,3 +122,58 @@ def test_norm_gradient_binding_refuses(no_lib):
         a.update(bad)
         with pytest.raises(ValueError):
             g5.rms_norm_backward(x, a.pop("H"), a.pop("W"), a.pop("rstd"), **a)
+
+
+def moe(**kw):
+    a = dict(T=4, H=64, I=32, E=8, k=2, renorm=1, X=X, ldx=64, L=S, ldl=8, wt=0, Wgu=W, ldgu=64, sgu=64 * 64, fgu=None,
+             Wd=H, ldd=32, sd=64 * 32, fd=None, Y=Y, ldy=64, ct=0, ids=T, gates=T + 4096, ws=P + (8 << 34), n=CR + (1 << 20))
+    a.update(kw)
+    return g5.lib().gemm_moe_swiglu(a["T"], a["H"], a["I"], a["E"], a["k"], a["renorm"], a["X"], a["ldx"], a["L"],
+                                    a["ldl"], a["wt"], a["Wgu"], a["ldgu"], a["sgu"], a["fgu"], a["Wd"], a["ldd"],
+                                    a["sd"], a["fd"], a["Y"], a["ldy"], a["ct"], a["ids"], a["gates"], a["ws"], a["n"],
+                                    None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(T=-1), INV), (dict(T=257), INV), (dict(H=-1), INV), (dict(H=65537), INV), (dict(I=-1), INV),
+    (dict(I=65537), INV), (dict(E=0), INV), (dict(E=1025), INV), (dict(k=0), INV), (dict(k=9), INV),
+    (dict(E=64, ldl=64, k=33), INV), (dict(wt=1), INV), (dict(ct=2), INV), (dict(X=None), INV), (dict(L=None), INV),
+    (dict(Wgu=None), INV), (dict(Wd=None), INV), (dict(Y=None), INV), (dict(ldx=63), INV), (dict(ldl=7), INV),
+    (dict(ldgu=63), INV), (dict(ldd=31), INV), (dict(ldy=63), INV), (dict(sgu=-1), INV), (dict(sd=-1), INV),
+    (dict(X=X + 1), INV), (dict(L=S + 2), INV), (dict(Wgu=W + 1), INV), (dict(Wd=H + 1), INV), (dict(Y=Y + 1), INV),
+    (dict(ct=1, Y=Y + 2), INV), (dict(ids=T + 2), INV), (dict(gates=T + 4098), INV), (dict(fgu=R), INV),
+    (dict(wt=2, fgu=R + 2), INV), (dict(wt=2, fd=R + 1), INV), (dict(Y=X), INV), (dict(Y=W), INV), (dict(ids=S), INV),
+    (dict(gates=T), INV), (dict(ids=Y), INV), (dict(ws=None), WS), (dict(n=CR), WS), (dict(ws=P + (8 << 34) + 64), INV),
+    (dict(ws=H), INV), (dict(ws=Y - CR), INV)])
+def test_moe_refuses(bad, status):
+    assert moe(**bad) == status
+
+
+def test_moe_workspace_size():
+    n = ctypes.c_uint64(1)
+    f = g5.lib().gemm_moe_workspace_size
+    assert f(0, 64, 32, 8, 2, ctypes.byref(n)) == OK and n.value == 0
+    assert f(4, 64, 32, 8, 2, ctypes.byref(n)) == OK
+    # routing (2 x 8 words), z in two planes of 8 x 32 bf16, 8 rows of 64 floats
+    assert n.value == CR + 256 + 256 + 1024 + 2048
+    assert f(257, 64, 32, 8, 2, ctypes.byref(n)) == INV and f(4, 64, 32, 8, 9, ctypes.byref(n)) == INV
+    assert moe(T=0, X=None, L=None) == OK
+
+
+def test_moe_binding_refuses(no_lib):
+    x, l, w, d = _bf(4, 64), _f32(4, 8), _bf(8, 64, 64), _bf(8, 64, 32)
+    with pytest.raises(TypeError):
+        g5.moe_swiglu(_f32(4, 64), l, 2, w, d)
+    with pytest.raises(TypeError):
+        g5.moe_swiglu(x, _bf(4, 8), 2, w, d)
+    with pytest.raises(TypeError):
+        g5.moe_swiglu(x, l, 2, w, FakeGpuTensor((8, 64, 32), torch.uint8))
+    with pytest.raises(TypeError):
+        g5.moe_swiglu(x, l, 2, _f32(8, 64, 64), d)
+    for bad in (dict(X=_bf(4, 63)), dict(logits=_f32(4, 9)), dict(Wgu=_bf(8, 63, 64)), dict(Wd=_bf(8, 64, 33)),
+                dict(Wgu=_bf(64, 64)), dict(scale_gu=_f32(8, 64)),
+                dict(logits=torch.empty((4, 8)))):
+        a = dict(X=x, logits=l, topk=2, Wgu=w, Wd=d)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            g5.moe_swiglu(**a)
