@@ -20,4 +20,4 @@ from .gemm import (  # noqa: F401
     act_chain, act_silu, act_mul, act_swiglu, act_quantize_e4m3, act_swiglu_e4m3,
     gemm_bf16_nt_affine, gemm_bf16_tn_affine, plan_query, workspace_size, Workspace,
 )
-from .token_ops import rms_norm, rms_norm_e4m3, rms_norm_backward, moe_swiglu  # noqa: F401
+from .token_ops import rms_norm, rms_norm_e4m3, rms_norm_backward, moe_swiglu, gemm_bf16_nt_lora  # noqa: F401

@@ -50,7 +50,8 @@ EXPORTS = ("gemm_sgemm", "gemm_bf16", "gemm_bf16_batched", "gemm_bf16_nt", "gemm
            "gemm_plan_query", "gemm_plan_query_ex", "gemm_model_local_bytes", "gemm_model_traffic_bytes", "gemm_model_quant_traffic", "gemm_model_act_chain_bytes",
            "gemm_tile_map",
            "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size",
-           "gemm_moe_swiglu", "gemm_moe_workspace_size")
+           "gemm_moe_swiglu", "gemm_moe_workspace_size",
+           "gemm_bf16_nt_lora", "gemm_lora_workspace_size")
 
 
 class GemmPlan(ctypes.Structure):
@@ -167,6 +168,12 @@ def lib():
     L.gemm_moe_swiglu.restype = i32
     L.gemm_moe_workspace_size.argtypes = [i64, i64, i64, i64, i64, ctypes.POINTER(u64)]
     L.gemm_moe_workspace_size.restype = i32
+    L.gemm_bf16_nt_lora.argtypes = [i64, i64, i64, p, i64, p, i64, i64, i64, p, i64, i64, p, i64, i64, p, p, p, i64,
+                                    i32, p, u64, p]
+    L.gemm_bf16_nt_lora.restype = i32
+    L.gemm_lora_workspace_size.argtypes = [i64, i64, i64, i64, i64, u64, i64, u64, i64, u64, i64, i32,
+                                           ctypes.POINTER(u64)]
+    L.gemm_lora_workspace_size.restype = i32
     _lib = L
     return L
 

@@ -55,6 +55,8 @@ struct Problem {
     uint64_t bias = 0;                   // bf16 [N], 0 = none
     // SwiGLU with c_type GEMM_OUT_E4M3: the fixed range that maps to 448
     float out_amax = 0.0f;
+    // GEMM_OP_BF16_NT with low-rank adapters joined to its sums (NULL: none)
+    const LoraArgs *lora = nullptr;
 };
 
 struct Plan {
@@ -270,6 +272,7 @@ bool config_fits(const Problem &p, int id)
         if (b_trans(p)) return id == CFG_DECODE_NT && p.M <= 16 && p.batch <= 65535;   // (affine only)
         return (id == CFG_DECODE_64 || id == CFG_DECODE_SPLIT) && p.M <= 16 && p.batch <= 65535;
     }
+    if (p.lora) return has_epilogues(id) || (id == CFG_DECODE_NT && p.M <= 16);   // g5_lora.hip's kernels
     if (epi_of(p) != EPI_NONE) return has_epilogues(id);
     if (p.op == GEMM_OP_FP8_NT && id == CFG_DECODE_NT) return p.M <= 16 && p.batch <= 65535;   // k_decode_nt_f8
     if (p.op == GEMM_OP_FP8_NT) return has_epilogues(id);         // fp8 ring kernels: 256x192, 256x256, 128x128
@@ -572,7 +575,8 @@ int select_plan(const Problem &p, Plan &pl, bool ws)
     }
     if (ws && kConfigs[pl.config].family == GEMM_FAMILY_BF16_MFMA && !is_fp8(p) &&
         (pl.align_a < 16 || (a_trans(p) && p.M % 8 != 0)) &&
-        ((double)p.batch * p.M * p.N * p.K >= (double)(1 << 30) || (ring_only(p) && pl.variant == 0))) {
+        ((double)p.batch * p.M * p.N * p.K >= (double)(1 << 30) || (ring_only(p) && pl.variant == 0) ||
+         (p.lora && pl.variant == 3))) {
         Problem q = p;
         if (pl.realign_b) {
             q.ldb = pl.ldb2;
@@ -595,6 +599,7 @@ int select_plan(const Problem &p, Plan &pl, bool ws)
     }
     // fused epilogues and a transposed B exist in the ring kernels only (variants 1-3)
     if (ring_only(p) && tiled(pl.config) && pl.variant == 0) return GEMM_ERR_UNSUPPORTED;
+    if (p.lora && tiled(pl.config) && pl.variant == 3) return GEMM_ERR_UNSUPPORTED;   // (16-byte copies only)
     if (const char *fs = std::getenv("GEMM_FORCE_STREAMK")) {
         // diagnostic: the persistent stream-K schedule for the chosen tile
         if (*fs == '1') {
@@ -755,6 +760,28 @@ int plan_for_call(const Problem &p, const void *ws, size_t ws_bytes, Plan &pl, W
     return GEMM_OK;
 }
 
+// The adapters' values v [splits, M, ranks] follow the product's own scratch.
+// K is cut into up to 4 slices of at least 512 (for M <= 16 by K alone, so a
+// row's result does not depend on the other rows; for more rows while the
+// grid stays within one workgroup per CU), and the adapters of a row block
+// are shared out while that grid has room.
+size_t lora_layout(const Problem &p, const WsLayout &L, LoraArgs &q, size_t *total)
+{
+    const int64_t wgs = cdiv(p.M, 16) * cdiv(q.R, 16);
+    const int64_t room = kNumCU / wgs > 1 ? kNumCU / wgs : 1;
+    int64_t splits = p.K / 512 < 4 ? p.K / 512 : 4;
+    if (p.M > 16 && splits > room) splits = room;
+    q.splits = splits < 1 ? 1 : (int)splits;
+    int64_t turns = p.M < 16 ? p.M : 16;
+    if (turns > q.L) turns = q.L;
+    if (turns > room) turns = room;
+    q.turns = turns < 1 ? 1 : (int)turns;
+    q.ranks = (int)((q.R + 7) / 8 * 8);
+    const size_t at = L.total > kCounterBytes ? L.total : kCounterBytes;
+    *total = at + round256((size_t)q.splits * p.M * q.ranks * 4);
+    return at;
+}
+
 // Validate, plan and enqueue one call.  `ws`: the caller's workspace (NULL:
 // none); no memory is allocated, freed, copied or waited for here.
 int run(const Problem &p, void *stream, void *ws = nullptr, size_t ws_bytes = 0)
@@ -766,6 +793,14 @@ int run(const Problem &p, void *stream, void *ws = nullptr, size_t ws_bytes = 0)
     st = plan_for_call(p, ws, ws_bytes, pl, L);
     if (st != GEMM_OK) return st;
     if (pl.config == CFG_NONE) return GEMM_OK;
+    LoraArgs lora{};
+    if (p.lora && pl.config != CFG_ZERO) {
+        lora = *p.lora;
+        size_t need = 0;
+        const size_t at = lora_layout(p, L, lora, &need);
+        if (!ws || need > ws_bytes) return GEMM_ERR_WORKSPACE;
+        lora.V = (float *)((char *)ws + at);
+    }
     st = check_device();
     if (st != GEMM_OK) return st;
     char *wsb = (char *)ws;
@@ -846,6 +881,11 @@ int run(const Problem &p, void *stream, void *ws = nullptr, size_t ws_bytes = 0)
         a.lda = pl.lda2;
         a.sA = a_rows(p) * pl.lda2;
         a.align_a = 16;
+    }
+    if (p.lora && pl.config != CFG_ZERO) {
+        hipError_t e = launch_lora_shrink(a, lora, (hipStream_t)stream);
+        if (e == hipSuccess) e = launch_lora(pl.config, a, lora, pl.variant, pl.grid, (hipStream_t)stream);
+        return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
     }
     if (pl.config == CFG_DECODE_SPLIT) {
         const bool pair = decode_split_pair(p, pl);
@@ -1435,6 +1475,76 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     const hipError_t e = g5::launch_moe(a, codes, a.align_x >= 16 && a.align_gu >= 16, a.align_d >= 16,
                                         (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+// ---- low-rank adapters beside a projection
+static int lora_sizes_ok(int64_t L, int64_t R) { return L >= 0 && L <= 0x7fffffff && R >= 0 && R <= 4096; }
+
+int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R, uint64_t x_addr, int64_t ldx,
+                             uint64_t w_addr, int64_t ldw, uint64_t c_addr, int64_t ldc, int c_type, uint64_t *bytes)
+{
+    if (bytes) *bytes = 0;
+    if (!lora_sizes_ok(L, R)) return GEMM_ERR_INVALID_ARG;
+    g5::LoraArgs q{};
+    q.L = L;
+    q.R = R;
+    Problem p{GEMM_OP_BF16_NT, 1, M, N, K, x_addr, w_addr, c_addr, ldx, ldw, ldc, 0, 0, 0, c_type};
+    if (L > 0 && R > 0) p.lora = &q;
+    int st = g5::validate(p);
+    if (st != GEMM_OK) return st;
+    g5::Plan pl;
+    st = g5::select_plan(p, pl, true);
+    if (st != GEMM_OK || !bytes || pl.config == g5::CFG_NONE || pl.config == g5::CFG_ZERO) return st;
+    const g5::WsLayout W = g5::ws_layout(p, pl);
+    size_t need = W.total;
+    if (p.lora) g5::lora_layout(p, W, q, &need);
+    *bytes = need;
+    return GEMM_OK;
+}
+
+int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_t ldx, const uint16_t *Wt, int64_t ldw,
+                      int64_t L, int64_t R, const uint16_t *A, int64_t lda, int64_t strideA, const uint16_t *B,
+                      int64_t ldb, int64_t strideB, const float *scale, const int32_t *idx, void *C, int64_t ldc,
+                      int c_type, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    using g5::Range;
+    if (!lora_sizes_ok(L, R)) return GEMM_ERR_INVALID_ARG;
+    Problem p{GEMM_OP_BF16_NT, 1, M, N, K, (uint64_t)X, (uint64_t)Wt, (uint64_t)C, ldx, ldw, ldc, 0, 0, 0, c_type};
+    const int st = g5::validate(p);
+    if (st != GEMM_OK) return st;
+    const bool some = M > 0 && N > 0 && K > 0;
+    g5::LoraArgs q{};
+    Range in[7] = {};
+    if (some) {
+        in[0] = g5::extent((uint64_t)X, 1, M, K, ldx, 0, 2);
+        in[1] = g5::extent((uint64_t)Wt, 1, N, K, ldw, 0, 2);
+    }
+    if (some && L > 0 && R > 0) {
+        if (!A || !B || !idx || lda < K || ldb < R || strideA < 0 || strideB < 0) return GEMM_ERR_INVALID_ARG;
+        if (((uint64_t)A % 2) || ((uint64_t)B % 2) || ((uint64_t)scale % 4) || ((uint64_t)idx % 4))
+            return GEMM_ERR_INVALID_ARG;
+        in[2] = g5::extent((uint64_t)A, L, R, K, lda, strideA, 2);
+        in[3] = g5::extent((uint64_t)B, L, N, R, ldb, strideB, 2);
+        in[4] = vec_range(scale, L, 4);
+        in[5] = vec_range(idx, M, 4);
+        if (in[2].hi > ((__int128)1 << 63) || in[3].hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
+        q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB,
+                         g5::row_alignment((uint64_t)A, lda, strideA, L, 2),
+                         g5::row_alignment((uint64_t)B, ldb, strideB, L, 2), 0, 0, 0, nullptr};
+        p.lora = &q;
+    }
+    if (some) {
+        uint64_t need = 0;
+        const int ws = gemm_lora_workspace_size(M, N, K, L, R, p.a, ldx, p.b, ldw, p.c, ldc, c_type, &need);
+        if (ws != GEMM_OK) return ws;
+        const Range out[] = {g5::extent((uint64_t)C, 1, M, N, ldc, 0, g5::elem_c(p)),
+                             workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + need}
+                                       : Range{0, 0}};
+        if (outputs_overlap(out, 2, in, 6)) return GEMM_ERR_INVALID_ARG;
+        if (need > 0 && (!workspace || workspace_bytes < need)) return GEMM_ERR_WORKSPACE;
+        if ((uint64_t)workspace % 256) return GEMM_ERR_INVALID_ARG;
+    }
+    return g5::run(p, stream, workspace, (size_t)workspace_bytes);
 }
 
 const char *gemm_status_string(int status)

@@ -1103,6 +1103,62 @@ struct RingTile {
 
     }
 
+    // K split over workgroups: hand in this slice's sums of tile `wg`; true
+    // in the workgroup that arrives last, which then holds the whole sums.
+    __device__ static __forceinline__ bool join_slices(const GemmArgs &p, int64_t wg, int slice, Acc &acc)
+    {
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = tid >> 6;
+    // Publish this slice's FP32 tile in register order (block, wave,
+    // lane: each wave writes 1 KiB runs) with device-scope (sc1) stores,
+    // wait for them, then count the arrival.  The workgroup that brings
+    // the tile's counter to ksplit adds the slices 0, 1, ... in order
+    // (its own from registers, bit-identical to what it stored), resets
+    // the counter for the next call and stores the tile.  No fence: the
+    // sc1 (device-scope) stores and loads of the partial tiles complete
+    // at the device's coherence point, never in an XCD's private L2,
+    // the wait and barrier retire every store before the counter
+    // atomic (performed at that point) is issued, and the last arriver
+    // loads only after reading the atomic's result.
+    __shared__ unsigned sk_arrived;
+    constexpr int TILE_F = BM * BN;
+    float *tile_ws = p.ws_part + wg * p.ksplit * (int64_t)TILE_F;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        tile_ws + (int64_t)slice * TILE_F, 0, TILE_F * 4, 0x00020000);
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+            const int off = (((fn * FM + fm) * NWAVE + wave) * 64 + lane) * 16;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[fn][fm]), wr, off, 0, 16);
+        }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tid == 0) sk_arrived = __hip_atomic_fetch_add(p.ws_cnt + wg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (sk_arrived != (unsigned)(p.ksplit - 1)) return false;
+    f32x4 tot[FN][FM];
+    for (int s2 = 0; s2 < p.ksplit; ++s2) {
+        const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
+            tile_ws + (int64_t)s2 * TILE_F, 0, TILE_F * 4, 0x00020000);
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                const int off = (((fn * FM + fm) * NWAVE + wave) * 64 + lane) * 16;
+                const f32x4 v = s2 == slice ? acc[fn][fm]
+                                            : __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, off, 0, 16));
+                tot[fn][fm] = s2 == 0 ? v : tot[fn][fm] + v;
+            }
+    }
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) acc[fn][fm] = tot[fn][fm];
+    if (tid == 0) __hip_atomic_store(p.ws_cnt + wg, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+    }
+
     __device__ static __forceinline__ void store(const GemmArgs &p, uint16_t *smem, const TileCoord &tc, Acc &acc)
     {
     int tid = threadIdx.x;
@@ -1176,10 +1232,8 @@ template <int BM, int BN, int WGM, int WGN, int NSA, int NSB, int AV, bool MASKE
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_bf16_ms(GemmArgs p)
 {
     using R = RingTile<BM, BN, WGM, WGN, NSA, NSB, AV, MASKED, EPI, BT, F8, AT>;
-    constexpr int FM = R::FM, FN = R::FN, NWAVE = R::NWAVE, KS = R::KS;
+    constexpr int FM = R::FM, FN = R::FN, KS = R::KS;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
-    const int tid = threadIdx.x;
-    const int lane = tid & 63, wave = tid >> 6;
     const int64_t ntiles = p.batch * p.tiles_m * p.tiles_n;
     const int64_t wg = SK ? (int64_t)blockIdx.x % ntiles : (int64_t)blockIdx.x;
     const int slice = SK ? (int)((int64_t)blockIdx.x / ntiles) : 0;
@@ -1193,53 +1247,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_bf16_ms(GemmArgs p)
     R::accumulate(p, smem, tc, kbase, Kpart, acc);
 
     if constexpr (SK) {
-        // Publish this slice's FP32 tile in register order (block, wave,
-        // lane: each wave writes 1 KiB runs) with device-scope (sc1) stores,
-        // wait for them, then count the arrival.  The workgroup that brings
-        // the tile's counter to ksplit adds the slices 0, 1, ... in order
-        // (its own from registers, bit-identical to what it stored), resets
-        // the counter for the next call and stores the tile.  No fence: the
-        // sc1 (device-scope) stores and loads of the partial tiles complete
-        // at the device's coherence point, never in an XCD's private L2,
-        // the wait and barrier retire every store before the counter
-        // atomic (performed at that point) is issued, and the last arriver
-        // loads only after reading the atomic's result.
-        __shared__ unsigned sk_arrived;
-        constexpr int TILE_F = BM * BN;
-        float *tile_ws = p.ws_part + wg * p.ksplit * (int64_t)TILE_F;
-        const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
-            tile_ws + (int64_t)slice * TILE_F, 0, TILE_F * 4, 0x00020000);
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-                const int off = (((fn * FM + fm) * NWAVE + wave) * 64 + lane) * 16;
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[fn][fm]), wr, off, 0, 16);
-            }
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (tid == 0) sk_arrived = __hip_atomic_fetch_add(p.ws_cnt + wg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (sk_arrived != (unsigned)(p.ksplit - 1)) return;
-        f32x4 tot[FN][FM];
-        for (int s2 = 0; s2 < p.ksplit; ++s2) {
-            const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
-                tile_ws + (int64_t)s2 * TILE_F, 0, TILE_F * 4, 0x00020000);
-#pragma unroll
-            for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-                for (int fm = 0; fm < FM; ++fm) {
-                    const int off = (((fn * FM + fm) * NWAVE + wave) * 64 + lane) * 16;
-                    const f32x4 v = s2 == slice ? acc[fn][fm]
-                                                : __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rr, off, 0, 16));
-                    tot[fn][fm] = s2 == 0 ? v : tot[fn][fm] + v;
-                }
-        }
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) acc[fn][fm] = tot[fn][fm];
-        if (tid == 0) __hip_atomic_store(p.ws_cnt + wg, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (!R::join_slices(p, wg, slice, acc)) return;
     }
 
     R::store(p, smem, tc, acc);

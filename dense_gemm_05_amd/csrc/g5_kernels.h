@@ -169,4 +169,23 @@ struct MoeArgs {
 // vec_gu, vec_d: the rows of X and Wgu (of Wd) start 16-byte aligned.
 hipError_t launch_moe(const MoeArgs &a, bool codes, bool vec_gu, bool vec_d, hipStream_t s);
 
+// The low-rank adapters beside a bf16 product with B given transposed
+// (g5_lora.hip): adapter a has A at A + a strideA [R, K] and B at
+// B + a strideB [N, R]; row m of the product uses adapter idx[m] (none when
+// outside [0, L)).
+struct LoraArgs {
+    const uint16_t *A, *B;
+    const float *scale;          // [L] or NULL
+    const int32_t *idx;          // [M]
+    int64_t L, R, lda, strideA, ldb, strideB;
+    int align_a, align_b;        // byte alignments of the row starts
+    int ranks;                   // R rounded up to 8: the row length of V
+    int splits, turns;           // K slices of V; workgroups sharing a row block's adapters
+    float *V;                    // [splits, M, ranks] floats of scratch (rows without an adapter unused)
+};
+hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s);
+// The product with v B^T joined: configs 256x192, 256x256, 128x128 (also
+// with K split; variants 1 and 2) and the small-M CFG_DECODE_NT.
+hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s);
+
 }  // namespace g5

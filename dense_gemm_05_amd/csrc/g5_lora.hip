@@ -1,0 +1,339 @@
+// g5_lora.hip -- a shared projection with low-rank adapters of many requests:
+//
+//   C[m] = X[m] Wt^T + s_a (X[m] A_a^T) B_a^T,   a = idx[m]
+//
+// in two launches: the low-rank values v[m] = s_a X[m] A_a^T (FP32, R per
+// row) into the workspace, then the product, whose kernels add v B_a^T to the
+// FP32 sums before they are rounded once.  An adapter adds 2 R (K + N) flops
+// and R (K + N) elements to a row's 2 N K: both are small beside the
+// projection, so the product's kernels stay as they are (the weight stream of
+// the small-M kernel, the ring kernel's tiles) and the adapters join at their
+// ends, where rows of different adapters may stand next to each other in any
+// order.
+#include <hip/hip_runtime.h>
+
+#include "g5_device.h"
+#include "g5_kernels.h"
+
+namespace g5 {
+
+namespace {
+
+constexpr int kShrinkWaves = 8;
+
+// The adapter of row m, or -1: rows without one, past M, or whose index
+// names no adapter.
+__device__ __forceinline__ int lora_adapter(const LoraArgs &q, int64_t m, int64_t M)
+{
+    const int a = m < M ? q.idx[m] : -1;
+    return a >= 0 && a < q.L ? a : -1;
+}
+
+// Calls f(a, mine) for every adapter among 16 rows, in the order of their
+// first rows; the lane's row is lane % 16 and its adapter `a_row`.
+template <class F>
+__device__ __forceinline__ void each_adapter(int a_row, F f)
+{
+    uint64_t todo = __ballot(a_row >= 0) & 0xffffull;
+    for (int ordinal = 0; todo; ++ordinal) {
+        const int a = __builtin_amdgcn_readlane(a_row, __builtin_ctzll(todo));
+        f(a, a_row == a, ordinal);
+        todo &= ~__ballot(a_row == a);
+    }
+}
+
+}  // namespace
+
+// v of 16 rows and 16 ranks over one of q.splits slices of K.  Workgroup
+// (x: row block, y: rank group, z: adapter turn * splits + slice) takes every
+// q.turns-th adapter of its rows; its eight waves divide the slice, their sums
+// are added in wave order.  The adapter's rows of A are the matrix core's
+// 16-row operand, X's rows the other: a row's sums are its own whatever
+// stands in the other rows, and only rows of this adapter keep them.
+__global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, LoraArgs q)
+{
+    __shared__ f32x4 red[kShrinkWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int64_t m = (int64_t)blockIdx.x * 16 + li;
+    const int r0 = blockIdx.y * 16, rank = r0 + li;
+    const int slice = blockIdx.z % q.splits, turn = blockIdx.z / q.splits;
+    const int a_row = lora_adapter(q, m, p.M);
+    const int64_t steps = (p.K + 31) / 32;
+    const int64_t b0 = steps * slice / q.splits, b1 = steps * (slice + 1) / q.splits;
+    const int64_t s0 = b0 + (b1 - b0) * wave / kShrinkWaves, s1 = b0 + (b1 - b0) * (wave + 1) / kShrinkWaves;
+    const uint16_t *xrow = (const uint16_t *)p.A + (a_row >= 0 ? m : 0) * p.lda;
+    const bool r_ok = rank < q.R;
+    each_adapter(a_row, [&](int a, bool mine, int ordinal) {
+        if (ordinal % q.turns != turn) return;        // uniform over the workgroup
+        const uint16_t *arow = q.A + (int64_t)a * q.strideA + (int64_t)(r_ok ? rank : 0) * q.lda;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        constexpr int D = 4;
+        for (int64_t s = s0; s < s1; s += D) {
+            u32x4 w[D], x[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j) {
+                const bool in = s + j < s1;
+                w[j] = load_chunk8_bf16(arow, (s + j) * 32 + g * 8, p.K, in && r_ok, q.align_a);
+                x[j] = load_chunk8_bf16(xrow, (s + j) * 32 + g * 8, p.K, in && a_row >= 0, p.align_a);
+            }
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j]),
+                                                              __builtin_bit_cast(bf16x8, x[j]), acc, 0, 0, 0);
+        }
+        __syncthreads();                              // (the adapter before has been read)
+        red[wave][lane] = acc;
+        __syncthreads();
+        if (wave == 0 && mine && r0 + 4 * g < q.ranks) {
+            f32x4 v = red[0][lane];
+#pragma unroll
+            for (int w2 = 1; w2 < kShrinkWaves; ++w2) v += red[w2][lane];
+            const float sc = q.scale ? q.scale[a] : 1.0f;
+            *(f32x4 *)(q.V + ((int64_t)slice * p.M + m) * q.ranks + r0 + 4 * g) = v * sc;
+        }
+    });
+}
+
+namespace {
+
+// Ranks 8 c .. 8 c + 7 of v[m], the slices added in order.
+__device__ __forceinline__ void lora_v8(const LoraArgs &q, int64_t M, int64_t m, int c, f32x4 (&v)[2])
+{
+    const float *src = q.V + m * q.ranks + 8 * c;
+    v[0] = *(const f32x4 *)src;
+    v[1] = *(const f32x4 *)(src + 4);
+    for (int s = 1; s < q.splits; ++s) {
+        src += M * q.ranks;
+        v[0] += *(const f32x4 *)src;
+        v[1] += *(const f32x4 *)(src + 4);
+    }
+}
+
+// acc += v B^T for the rows and columns of a ring tile.  The FP32 values v
+// go through the matrix core as two bf16 parts, v = hi + lo to 2^-16 of it:
+// 2 R products deep, the first R with hi and the next R with lo against the
+// same rows of B.  16 rows at a time, one adapter of theirs after the other;
+// each row keeps the sums of its own.
+template <class RT>
+__device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q, const TileCoord &tc,
+                                            typename RT::Acc &acc, int wave, int WGN, int64_t m0, int64_t n0)
+{
+    const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+    const int64_t mw = m0 + (wave / WGN) * RT::TM, nw = n0 + (wave % WGN) * RT::TN;
+    const int chunks = q.ranks / 8, depth = (2 * chunks + 3) / 4;     // 8-rank chunks; 32-deep steps
+#pragma unroll
+    for (int fm = 0; fm < RT::FM; ++fm) {
+        const int64_t m = mw + fm * 16 + li;
+        const int a_row = lora_adapter(q, m, p.M);
+        each_adapter(a_row, [&](int a, bool mine, int) {
+            f32x4 d[RT::FN];
+#pragma unroll
+            for (int fn = 0; fn < RT::FN; ++fn) d[fn] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const uint16_t *Ba = q.B + (int64_t)a * q.strideB;
+            for (int k = 0; k < depth; ++k) {
+                const int kc = 4 * k + g, c = kc < chunks ? kc : kc - chunks;
+                u32x4 x = {0u, 0u, 0u, 0u};
+                if (mine && c < chunks) {
+                    f32x4 v[2];
+                    lora_v8(q, p.M, m, c, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float lo = v[i >> 1][2 * (i & 1)], hi = v[i >> 1][2 * (i & 1) + 1];
+                        x[i] = pack_bf16x2(lo, hi);
+                        if (kc >= chunks) {
+                            // (an infinite value has no rest)
+                            lo = (x[i] & 0x7f80u) == 0x7f80u ? 0.f : lo - bf16_lo(x[i]);
+                            hi = (x[i] & 0x7f800000u) == 0x7f800000u ? 0.f : hi - bf16_hi(x[i]);
+                            x[i] = pack_bf16x2(lo, hi);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int fn = 0; fn < RT::FN; ++fn) {
+                    const int64_t n = nw + fn * 16 + li;
+                    const u32x4 b = load_chunk8_bf16(Ba + (n < p.N ? n : 0) * q.ldb, 8 * c, q.R,
+                                                     n < p.N && c < chunks, q.align_b);
+                    d[fn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
+                                                                    __builtin_bit_cast(bf16x8, x), d[fn], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int fn = 0; fn < RT::FN; ++fn)
+                if (mine) acc[fn][fm] += d[fn];
+        });
+    }
+}
+
+}  // namespace
+
+// The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
+// sums.
+template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_lora_ms(GemmArgs p, LoraArgs q)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, MASKED, EPI_NONE, true, false, false>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    const int64_t ntiles = p.tiles_m * p.tiles_n;
+    const int64_t wg = SK ? (int64_t)blockIdx.x % ntiles : (int64_t)blockIdx.x;
+    const int slice = SK ? (int)((int64_t)blockIdx.x / ntiles) : 0;
+    const TileCoord tc = tile_map(wg, 1, p.tiles_m, p.tiles_n, p.group_m);
+    const int64_t kbase = SK ? (int64_t)slice * p.kt_per * R::KS : 0;
+    const int64_t Kpart = SK && slice < p.ksplit - 1 ? (int64_t)p.kt_per * R::KS : p.K - kbase;
+    typename R::Acc acc;
+    R::zero(acc);
+    R::accumulate(p, smem, tc, kbase, Kpart, acc);
+    if constexpr (SK) {
+        if (!R::join_slices(p, wg, slice, acc)) return;
+    }
+    lora_expand<R>(p, q, tc, acc, threadIdx.x >> 6, WGN, tc.tm * BM, tc.tn * BN);
+    R::store(p, smem, tc, acc);
+}
+
+// M <= 16: k_decode_nt's weight stream on NW waves, and four more waves that
+// form v B^T of the workgroup's 16 RB columns meanwhile, an output at a time
+// per thread (R products in rank order); the last pass adds both.
+template <int NW, int RB>
+__global__ void __launch_bounds__((NW + 4) * 64) k_lora_decode(GemmArgs p, LoraArgs q)
+{
+    constexpr int NX = 4 * 64;                            // the extra waves' threads
+    __shared__ f32x4 red[NW][RB][64];
+    __shared__ float extra[16][16 * RB];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = lane >> 4, li = lane & 15;
+    const int64_t M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
+    const int64_t n0 = (int64_t)blockIdx.x * 16 * RB;
+    if (wave >= NW) {
+        const int chunks = q.ranks / 8;
+        for (int o = tid - NW * 64; o < (int)M * 16 * RB; o += NX) {
+            const int m = o / (16 * RB), c0 = o - m * (16 * RB);
+            const int64_t n = n0 + c0;
+            const int a = lora_adapter(q, m, M);
+            float d = 0.f;
+            if (a >= 0 && n < N) {
+                const uint16_t *brow = q.B + (int64_t)a * q.strideB + n * q.ldb;
+                for (int c = 0; c < chunks; ++c) {
+                    const u32x4 b = load_chunk8_bf16(brow, 8 * c, q.R, true, q.align_b);
+                    f32x4 v[2];
+                    lora_v8(q, M, m, c, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d = __builtin_fmaf(v[i >> 1][2 * (i & 1)], bf16_lo(b[i]), d);
+                        d = __builtin_fmaf(v[i >> 1][2 * (i & 1) + 1], bf16_hi(b[i]), d);
+                    }
+                }
+            }
+            extra[m][c0] = d;
+        }
+    } else {
+        const uint16_t *X = (const uint16_t *)p.A, *Bt = (const uint16_t *)p.B;
+        const bool m_ok = li < M;
+        bool n_ok[RB];
+        const uint16_t *brow[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            n_ok[r] = n0 + 16 * r + li < N;
+            brow[r] = Bt + (n_ok[r] ? n0 + 16 * r + li : 0) * ldb;
+        }
+        const uint16_t *xrow = X + (m_ok ? li : 0) * lda;
+        const int64_t whole = K / 32;
+        const int64_t s_begin = whole * wave / NW, s_end = whole * (wave + 1) / NW;
+        f32x4 acc[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto load_b = [&](int r, int64_t s) -> u32x4 {
+            return n_ok[r] ? __builtin_nontemporal_load((const u32x4 *)(brow[r] + s * 32 + g * 8))
+                           : u32x4{0u, 0u, 0u, 0u};
+        };
+        auto load_x = [&](int64_t s) -> u32x4 { return load_chunk8_bf16(xrow, s * 32 + g * 8, K, m_ok, p.align_a); };
+        auto mma = [&](int r, u32x4 b, u32x4 x) {
+            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
+                                                             __builtin_bit_cast(bf16x8, x), acc[r], 0, 0, 0);
+        };
+        constexpr int D = RB == 1 ? 4 : 2;
+        int64_t s = s_begin;
+        for (; s + D <= s_end; s += D) {
+            u32x4 b[D][RB], x[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) b[j][r] = load_b(r, s + j);
+#pragma unroll
+            for (int j = 0; j < D; ++j) x[j] = load_x(s + j);
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) mma(r, b[j][r], x[j]);
+        }
+        for (; s < s_end; ++s) {
+            const u32x4 x = load_x(s);
+#pragma unroll
+            for (int r = 0; r < RB; ++r) mma(r, load_b(r, s), x);
+        }
+        if (wave == NW - 1 && K % 32 != 0) {
+            const u32x4 x = load_x(whole);
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                mma(r, load_chunk8_bf16(brow[r], whole * 32 + g * 8, K, n_ok[r], p.align_b), x);
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) red[wave][r][lane] = acc[r];
+    }
+    __syncthreads();
+    if (tid < 64 * RB) {
+        const int r = tid >> 6, t = tid & 63;
+        f32x4 sum = red[0][r][t];
+#pragma unroll
+        for (int w2 = 1; w2 < NW; ++w2) sum += red[w2][r][t];
+        const int m = t & 15, gg = t >> 4;
+        if (m < M) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t n = n0 + 16 * r + 4 * gg + i;
+                if (n >= N) continue;
+                store_out(p, 0, m, n, sum[i] + extra[m][16 * r + 4 * gg + i]);
+            }
+        }
+    }
+}
+
+hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s)
+{
+    const dim3 g((unsigned)((a.M + 15) / 16), (unsigned)((q.ranks + 15) / 16), (unsigned)(q.turns * q.splits));
+    hipLaunchKernelGGL(k_lora_shrink, g, dim3(kShrinkWaves * 64), 0, s, a, q);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WGM, int WGN>
+static hipError_t launch_lora_ring(const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s)
+{
+    const dim3 g((unsigned)grid), b(WGM * WGN * 64);
+    if constexpr (BM == 128 && BN == 128) {
+        if (a.ksplit > 1) {
+            if (variant == 1) hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, false, true>), g, b, 0, s, a, q);
+            else hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, true, true>), g, b, 0, s, a, q);
+            return hipGetLastError();
+        }
+    }
+    if (variant == 1) hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, false, false>), g, b, 0, s, a, q);
+    else hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, true, false>), g, b, 0, s, a, q);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s)
+{
+    if (config_id == CFG_DECODE_NT) {
+        // (fill_grid: three 16-row blocks of Wt per workgroup when M > 1)
+        if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 3>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
+        else hipLaunchKernelGGL((k_lora_decode<8, 1>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
+        return hipGetLastError();
+    }
+    if (variant != 1 && variant != 2) return hipErrorInvalidValue;
+    switch (config_id) {
+    case CFG_BF16_256x192: return launch_lora_ring<256, 192, 2, 4>(a, q, variant, grid, s);
+    case CFG_BF16_256x256: return launch_lora_ring<256, 256, 2, 4>(a, q, variant, grid, s);
+    case CFG_BF16_128x128: return launch_lora_ring<128, 128, 4, 2>(a, q, variant, grid, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace g5

@@ -1,6 +1,6 @@
 """Binding of the operators around a projection: the RMS norm with the
-residual's addition and its gradient, and the mixture-of-experts layer for a
-few tokens.  As gemm.py: argument marshalling only;
+residual's addition and its gradient, the projection with low-rank adapters
+and the mixture-of-experts layer for a few tokens.  As gemm.py: argument marshalling only;
 the arithmetic runs in the gfx950 kernels of libgemm05.so.
 """
 import ctypes
@@ -11,7 +11,7 @@ from . import _lib
 from ._lib import GemmError, lib
 from .gemm import Workspace, _bstride, _check_dev, _codes, _launch, _ld, _out_code
 
-__all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward", "moe_swiglu"]
+__all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward", "moe_swiglu", "gemm_bf16_nt_lora"]
 
 
 def _ptr(t):
@@ -193,3 +193,43 @@ def moe_swiglu(X, logits, topk, Wgu, Wd, scale_gu=None, scale_d=None, renormaliz
     if st != 0:
         raise GemmError(st, "gemm_moe_swiglu")
     return Y, ids, gates
+
+
+def gemm_bf16_nt_lora(X, Wt, A, B, idx, scale=None, C=None, out_dtype=torch.bfloat16, workspace=None):
+    """C[m] = X[m] . Wt^T + scale[a] * (X[m] . A[a]^T) . B[a]^T with
+    a = idx[m] (gemm_bf16_nt_lora): a projection Wt [N, K] shared by the rows
+    of X [M, K], and low-rank adapters A [L, R, K], B [L, N, R] (bfloat16),
+    scale float32 [L] or None (1).  idx: int32 [M]; rows whose index is not
+    in [0, L) (e.g. -1) have no adapter."""
+    if any(t.dtype != torch.bfloat16 for t in (X, Wt, A, B)) or idx.dtype != torch.int32:
+        raise TypeError("gemm_bf16_nt_lora takes bfloat16 operands and an int32 idx")
+    if X.dim() != 2 or Wt.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("expected X [M, K], Wt [N, K], A [L, R, K] and B [L, N, R]")
+    M, K = X.shape
+    N, K2 = Wt.shape
+    L, R, K3 = A.shape
+    if K2 != K or K3 != K or tuple(B.shape) != (L, N, R):
+        raise ValueError("expected X [M, K], Wt [N, K], A [L, R, K] and B [L, N, R]")
+    _vector(idx, M, torch.int32, "idx")
+    _vector(scale, L, torch.float32, "scale")
+    dev = _check_dev(X, Wt, A, B, idx, scale, C)
+    if C is None:
+        C = torch.empty((M, N), dtype=out_dtype, device=dev)
+    if tuple(C.shape) != (M, N):
+        raise ValueError("C must be [M, N]")
+    code = _out_code(C.dtype)
+    ldx, ldw, ldc = _ld(X, K), _ld(Wt, K), _ld(C, N)
+    px, pw, pc = X.data_ptr(), Wt.data_ptr(), C.data_ptr()
+    if workspace is None:
+        workspace = Workspace(dev)
+    n = ctypes.c_uint64(0)
+    st = lib().gemm_lora_workspace_size(M, N, K, L, R, px, ldx, pw, ldw, pc, ldc, code, ctypes.byref(n))
+    if st != 0:
+        raise GemmError(st, "gemm_bf16_nt_lora")
+    buf = _scratch(workspace, dev, n.value)
+    st = _launch(lib().gemm_bf16_nt_lora, dev, M, N, K, px, ldx, pw, ldw, L, R, A.data_ptr(), _ld(A, K), _bstride(A),
+                 B.data_ptr(), _ld(B, R), _bstride(B), _ptr(scale), idx.data_ptr(), pc, ldc, code, buf.data_ptr(),
+                 buf.numel())
+    if st != 0:
+        raise GemmError(st, "gemm_bf16_nt_lora")
+    return C

@@ -636,6 +636,51 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
 /* Workspace bytes of gemm_moe_swiglu (host only). */
 int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, uint64_t *bytes);
 
+/* ---- low-rank adapters beside a projection -------------------------------------
+ *
+ * A linear layer shared by many requests, each row of which may carry a
+ * low-rank adapter of its own:
+ *
+ *     C[m] = X[m] . Wt^T + scale[a] * (X[m] . A_a^T) . B_a^T,   a = idx[m]
+ *
+ * X [M, K], Wt [N, K], C [M, N] as gemm_bf16_nt; adapter a of L has A_a
+ * [R, K] at A + a*strideA (row stride lda) and B_a [N, R] at B + a*strideB
+ * (row stride ldb), bf16; scale[L] (float) or NULL for 1.  idx[M] (int32,
+ * device memory): rows whose index lies outside [0, L) -- by convention -1 --
+ * have no adapter.  Rows of different adapters may stand in any order.  The
+ * adapter's R values per row are kept in FP32 (as two bf16 parts, to 2^-16,
+ * in the products of M > 16) and joined to the FP32 sums of the projection,
+ * which are rounded once to C's type.  A row depends on its own adapter
+ * only: values of other rows and adapters, NaN and infinities among them,
+ * do not reach it.  Deterministic; for M <= 16 a row's result does not
+ * depend on the others.
+ *
+ * L == 0 or R == 0: the plain product.  K == 0: C := 0.  R <= 4096.  Any
+ * alignment is taken; rows of X or Wt that are not 16-byte aligned are
+ * copied first as gemm_run does.  workspace: at least
+ * gemm_lora_workspace_size bytes, 256-byte aligned, as gemm_run's (its
+ * counter region zero before and after the call).  Errors as gemm_bf16_nt,
+ * and GEMM_ERR_INVALID_ARG for L or R out of range, short or negative
+ * strides, missing or misaligned pointers of the adapters, C or the
+ * workspace overlapping any of them; GEMM_ERR_WORKSPACE for a missing or
+ * small workspace. */
+int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K,
+                      const uint16_t *X, int64_t ldx,
+                      const uint16_t *Wt, int64_t ldw,
+                      int64_t L, int64_t R,
+                      const uint16_t *A, int64_t lda, int64_t strideA,
+                      const uint16_t *B, int64_t ldb, int64_t strideB,
+                      const float *scale, const int32_t *idx,
+                      void *C, int64_t ldc, int c_type,
+                      void *workspace, uint64_t workspace_bytes,
+                      void *stream);
+
+/* Workspace bytes of gemm_bf16_nt_lora (host only; pointers as integers,
+ * their alignment decides as in gemm_workspace_size). */
+int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t R,
+                             uint64_t x_addr, int64_t ldx, uint64_t w_addr, int64_t ldw,
+                             uint64_t c_addr, int64_t ldc, int c_type, uint64_t *bytes);
+
 /* Static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 

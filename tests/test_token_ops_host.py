@@ -177,3 +177,61 @@ def test_moe_binding_refuses(no_lib):
         a.update(bad)
         with pytest.raises(ValueError):
             g5.moe_swiglu(**a)
+
+
+def lora(**kw):
+    a = dict(M=4, N=64, K=32, X=X, ldx=32, Wt=W, ldw=32, L=2, R=8, A=R, lda=32, sA=256, B=H, ldb=8, sB=512, scale=S,
+             idx=S + 4096, C=Y, ldc=64, ct=0, ws=T, n=CR + 4096)
+    a.update(kw)
+    return g5.lib().gemm_bf16_nt_lora(a["M"], a["N"], a["K"], a["X"], a["ldx"], a["Wt"], a["ldw"], a["L"], a["R"], a["A"],
+                                      a["lda"], a["sA"], a["B"], a["ldb"], a["sB"], a["scale"], a["idx"], a["C"],
+                                      a["ldc"], a["ct"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(M=-1), INV), (dict(N=-1), INV), (dict(K=-1), INV), (dict(L=-1), INV), (dict(L=1 << 31), INV),
+    (dict(R=-1), INV), (dict(R=4097, ldb=4097), INV), (dict(X=None), INV), (dict(Wt=None), INV), (dict(C=None), INV),
+    (dict(A=None), INV), (dict(B=None), INV), (dict(idx=None), INV), (dict(ldx=31), INV), (dict(ldw=31), INV),
+    (dict(lda=31), INV), (dict(ldb=7), INV), (dict(ldc=63), INV), (dict(sA=-1), INV), (dict(sB=-1), INV),
+    (dict(ct=2), INV), (dict(A=R + 1), INV), (dict(B=H + 1), INV), (dict(scale=S + 2), INV), (dict(idx=S + 4097), INV),
+    (dict(C=X), INV), (dict(C=W), INV), (dict(C=R), INV), (dict(C=H), INV), (dict(C=S), INV), (dict(ws=None), WS),
+    (dict(n=CR), WS), (dict(ws=T + 128), INV), (dict(ws=H), INV), (dict(ws=Y), INV), (dict(ws=S), INV)])
+def test_lora_refuses(bad, status):
+    assert lora(**bad) == status
+
+
+def lora_size(M, N, K, L, R, ldx=None):
+    n = ctypes.c_uint64(1)
+    st = g5.lib().gemm_lora_workspace_size(M, N, K, L, R, X, ldx or K, W, K, Y, N, 0, ctypes.byref(n))
+    return st, n.value
+
+
+def test_lora_workspace_size():
+    # one slice of 4 rows of 8 floats; four slices of 16 rows of 24
+    assert lora_size(4, 64, 32, 2, 8) == (OK, CR + 256)
+    assert lora_size(16, 64, 2048, 2, 17) == (OK, CR + 4 * 16 * 24 * 4)
+    # the product's own scratch comes first
+    st, own = g5.plan_query(g5.GEMM_OP_BF16_NT, 128, 1536, 4096)[0], g5.plan_query(g5.GEMM_OP_BF16_NT, 128, 1536, 4096)[1]
+    st2, n = lora_size(128, 1536, 4096, 2, 16)
+    assert st == st2 == OK and n > own.workspace_bytes >= CR
+    assert lora_size(0, 64, 32, 2, 8) == (OK, 0) and lora_size(4, 64, 0, 2, 8)[1] == 0
+    assert lora_size(4, 64, 32, -1, 8)[0] == INV and lora_size(-4, 64, 32, 1, 8)[0] == INV
+    # rows that only 4-byte copies could read are realigned: their copy is counted
+    assert lora_size(200, 640, 1024, 2, 8, ldx=1026)[1] >= CR + 200 * 1024 * 2
+
+
+def test_lora_empty_calls_do_nothing():
+    assert lora(M=0, X=None, ws=None) == OK and lora(N=0, ldc=0, ws=None) == OK
+
+
+def test_lora_binding_refuses(no_lib):
+    good = dict(X=_bf(4, 32), Wt=_bf(64, 32), A=_bf(2, 8, 32), B=_bf(2, 64, 8), idx=FakeGpuTensor((4,), torch.int32))
+    for bad in (dict(X=_f32(4, 32)), dict(Wt=_f32(64, 32)), dict(A=_f32(2, 8, 32)), dict(B=_f32(2, 64, 8)),
+                dict(idx=FakeGpuTensor((4,), torch.int64))):
+        with pytest.raises(TypeError):
+            g5.gemm_bf16_nt_lora(**{**good, **bad})
+    for bad in (dict(X=_bf(4, 33)), dict(A=_bf(8, 32)), dict(B=_bf(2, 64, 9)), dict(B=_bf(3, 64, 8)),
+                dict(idx=FakeGpuTensor((5,), torch.int32)), dict(scale=_f32(3)), dict(C=_bf(4, 63)),
+                dict(idx=torch.zeros(4, dtype=torch.int32)), dict(C=torch.empty((4, 64), dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            g5.gemm_bf16_nt_lora(**{**good, **bad})
