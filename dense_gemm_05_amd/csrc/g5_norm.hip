@@ -77,8 +77,10 @@ __device__ __forceinline__ u32x4 scale8(u32x4 h, float rstd, u32x4 w, bool has_w
     u32x4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = bf16_lo(h[i]) * rstd, hi = bf16_hi(h[i]) * rstd;
-        y[i] = has_w ? pack_bf16x2(lo * bf16_lo(w[i]), hi * bf16_hi(w[i])) : pack_bf16x2(lo, hi);
+        // (h w is exact in FP32)
+        const float lo = has_w ? bf16_lo(h[i]) * bf16_lo(w[i]) : bf16_lo(h[i]);
+        const float hi = has_w ? bf16_hi(h[i]) * bf16_hi(w[i]) : bf16_hi(h[i]);
+        y[i] = pack_bf16x2(lo * rstd, hi * rstd);
     }
     return y;
 }
@@ -406,19 +408,33 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad_long(NormGradArgs a)
     }
 }
 
-// dW[n] = sum of rows 0 .. parts - 1 of `part`: a workgroup owns 64
-// columns, its four waves add every fourth row each, joined in order.
-__global__ void __launch_bounds__(256) k_norm_dw(const float *part, int parts, int64_t cols, float *dW)
+// dW[n] = sum of rows 0 .. parts - 1 of `part`: a workgroup owns 16 columns
+// (64 bytes of a row), 64 rows in flight at once; thread (row r, column c)
+// adds rows r, r + 64, ..., and the 64 sums are joined in order of a tree.
+__global__ void __launch_bounds__(1024) k_norm_dw(const float *part, int parts, int64_t cols, float *dW)
 {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float red[64][17];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t n = (int64_t)blockIdx.x * 16 + c;
     float s = 0.f;
-    if (n < cols)
-        for (int p = wv; p < parts; p += 4) s += part[(int64_t)p * cols + n];
-    red[wv][lane] = s;
+    if (n < cols) {
+#pragma unroll 8
+        for (int p = r; p < parts; p += 64) s += part[(int64_t)p * cols + n];
+    }
+    red[r][c] = s;
     __syncthreads();
-    if (wv == 0 && n < cols) dW[n] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        if (r < o) red[r][c] += red[r + o][c];
+        __syncthreads();
+    }
+    if (r == 0 && n < cols) dW[n] = red[0][c];
+}
+
+hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, s, part, parts, cols, dW);
+    return hipGetLastError();
 }
 
 template <int NCH>
@@ -426,12 +442,6 @@ static void launch_norm_grad_held(const NormGradArgs &a, int grid, bool vec, hip
 {
     if (vec) hipLaunchKernelGGL((k_rms_norm_grad<NCH, true>), dim3(grid), dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_rms_norm_grad<NCH, false>), dim3(grid), dim3(256), 0, s, a);
-}
-
-hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s)
-{
-    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, s, part, parts, cols, dW);
-    return hipGetLastError();
 }
 
 int norm_grad_parts(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
