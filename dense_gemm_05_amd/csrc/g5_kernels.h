@@ -148,6 +148,9 @@ hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s);
 // The mixture-of-experts SwiGLU layer for a few tokens (g5_moe.hip).
 // Weights bf16, or E4M3FN codes with factors per row; strides in elements.
 constexpr int kMoeMaxTokens = 256, kMoeMaxExperts = 1024, kMoeMaxTopk = 32, kMoeMaxWidth = 65536;
+struct MoeItem {
+    int expert, first, count, pad;   // its pairs: first .. first + count - 1 of the sorted list
+};
 struct MoeArgs {
     const uint16_t *X;
     const float *logits;
@@ -158,8 +161,14 @@ struct MoeArgs {
     float *gates;
     int64_t T, H, I, E, ldx, ldl, ldgu, strideGu, ldd, strideD, ldy;
     int topk, renormalize, out_f32, align_x, align_gu, align_d;
-    // scratch: the routing [T * topk]; z as two bf16 planes of rows of ldz;
-    // each pair's gated output, rows of H floats
+    // scratch: counters (zero before and after: 1 + one per strip of the down
+    // kernel); the routing [T * topk], the number of chosen experts, the
+    // experts in order and the pairs sorted by them; z as two bf16 planes of
+    // rows of ldz; each pair's gated output, rows of H floats
+    unsigned *counter;
+    int *chosen;
+    MoeItem *items;
+    int32_t *pairs;
     int32_t *w_ids;
     float *w_gates;
     uint16_t *z;

@@ -154,8 +154,9 @@ def test_moe_workspace_size():
     f = g5.lib().gemm_moe_workspace_size
     assert f(0, 64, 32, 8, 2, ctypes.byref(n)) == OK and n.value == 0
     assert f(4, 64, 32, 8, 2, ctypes.byref(n)) == OK
-    # routing (2 x 8 words), z in two planes of 8 x 32 bf16, 8 rows of 64 floats
-    assert n.value == CR + 256 + 256 + 1024 + 2048
+    # routing (2 x 8 words), the number of experts, 8 of them, 8 pairs, z in
+    # two planes of 8 x 32 bf16, 8 rows of 64 floats
+    assert n.value == CR + 256 + 256 + 256 + 256 + 256 + 1024 + 2048
     assert f(257, 64, 32, 8, 2, ctypes.byref(n)) == INV and f(4, 64, 32, 8, 9, ctypes.byref(n)) == INV
     assert moe(T=0, X=None, L=None) == OK
 
