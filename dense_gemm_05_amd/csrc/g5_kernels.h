@@ -147,7 +147,8 @@ hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s);
 
 // The mixture-of-experts SwiGLU layer for a few tokens (g5_moe.hip).
 // Weights bf16, or E4M3FN codes with factors per row; strides in elements.
-constexpr int kMoeMaxTokens = 256, kMoeMaxExperts = 1024, kMoeMaxTopk = 32, kMoeMaxWidth = 65536;
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopk = 16, kMoeMaxWidth = 65536;
+constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
 struct MoeItem {
     int expert, first, count, pad;   // its pairs: first .. first + count - 1 of the sorted list
 };
@@ -161,11 +162,10 @@ struct MoeArgs {
     float *gates;
     int64_t T, H, I, E, ldx, ldl, ldgu, strideGu, ldd, strideD, ldy;
     int topk, renormalize, out_f32, align_x, align_gu, align_d;
-    // scratch: counters (zero before and after: 1 + one per strip of the down
-    // kernel); the routing [T * topk], the number of chosen experts, the
+    int cols;                          // hidden columns per workgroup of the down kernel
+    // scratch: the routing [T * topk], the number of chosen experts, the
     // experts in order and the pairs sorted by them; z as two bf16 planes of
-    // rows of ldz; each pair's gated output, rows of H floats
-    unsigned *counter;
+    // rows of ldz
     int *chosen;
     MoeItem *items;
     int32_t *pairs;
@@ -173,7 +173,6 @@ struct MoeArgs {
     float *w_gates;
     uint16_t *z;
     int64_t ldz, zplane;
-    float *part;
 };
 // vec_gu, vec_d: the rows of X and Wgu (of Wd) start 16-byte aligned.
 hipError_t launch_moe(const MoeArgs &a, bool codes, bool vec_gu, bool vec_d, hipStream_t s);

@@ -28,11 +28,39 @@ namespace {
 constexpr int kMoeWaves = 8;
 constexpr int kMoeThreads = kMoeWaves * 64;
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float max_dpp(float v)
+{
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xf,
+                                                               false)));
+}
+// The largest of the wave's values, in every lane.
+__device__ __forceinline__ float wave_max_dpp(float v)
+{
+    // lane i takes the maximum with lanes i - 1, i - 2, i - 4, i - 8 of its
+    // row of 16, then with the rows before: lane 63 has all
+    v = max_dpp<0x111, 0xf>(v);
+    v = max_dpp<0x112, 0xf>(v);
+    v = max_dpp<0x114, 0xf>(v);
+    v = max_dpp<0x118, 0xf>(v);
+    v = max_dpp<0x142, 0xa>(v);
+    v = max_dpp<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
 // One token's routing, by one wave: lane l holds logits l, l + 64, ...
 // (NV of them).  Each of the topk turns takes the largest remaining one, the
-// lowest index among equals.
+// lowest index among equals; lane s ends up with slot s: its expert (-1:
+// none) and gate.
 template <int NV>
-__device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lane)
+__device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lane, int &id, float &gate)
 {
     const float *lg = a.logits + t * a.ldl;
     const float ninf = -__builtin_inff();
@@ -43,140 +71,110 @@ __device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lan
         const float x = e < a.E ? lg[e] : ninf;
         v[j] = x == x ? x : ninf;
     }
-    float m = v[0];
-#pragma unroll
-    for (int j = 1; j < NV; ++j) m = fmaxf(m, v[j]);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    float all = 0.f;
-    if (!a.renormalize) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) all += v[j] > ninf ? expf(v[j] - m) : 0.f;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, 64);
-    }
-    // lane s ends up with slot s
-    float my = ninf, sum = 0.f;
-    int my_id = -1;
+    float m = 0.f, all = 0.f, my = ninf;
+    id = -1;
     for (int s = 0; s < a.topk; ++s) {
         float best = v[0];
-        int at = lane;
 #pragma unroll
-        for (int j = 1; j < NV; ++j)
-            if (v[j] > best) {
-                best = v[j];
-                at = lane + 64 * j;
-            }
+        for (int j = 1; j < NV; ++j) best = fmaxf(best, v[j]);
+        best = wave_max_dpp(best);
+        if (!(best > ninf)) break;          // nothing left to choose
+        if (s == 0) {
+            m = best;
+            if (!a.renormalize) {
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const float ov = __shfl_xor(best, o, 64);
-            const int oi = __shfl_xor(at, o, 64);
-            if (ov > best || (ov == best && oi < at)) {
-                best = ov;
-                at = oi;
+                for (int j = 0; j < NV; ++j) all += v[j] > ninf ? expf(v[j] - m) : 0.f;
             }
         }
-        if (!(best > ninf)) break;          // uniform: nothing left to choose
+        int at = -1;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const uint64_t eq = __ballot(v[j] == best);
+            if (at < 0 && eq) at = 64 * j + __builtin_ctzll(eq);
+        }
         if (lane == s) {
             my = best;
-            my_id = at;
+            id = at;
         }
-        sum += expf(best - m);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (at == lane + 64 * j) v[j] = ninf;
     }
-    if (lane < a.topk) {
-        const float gate = my_id >= 0 ? expf(my - m) / (a.renormalize ? sum : all) : 0.f;
-        const int64_t p = t * a.topk + lane;
-        __hip_atomic_store(a.w_ids + p, my_id, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.w_gates[p] = gate;
-        if (a.ids) a.ids[p] = my_id;
-        if (a.gates) a.gates[p] = gate;
-    }
+    const float p = id >= 0 ? expf(my - m) : 0.f;
+    const float sum = wave_sum(a.renormalize ? p : all);
+    gate = id >= 0 ? p / sum : 0.f;
 }
 
-// Routing: four waves, a token each.  The workgroup that arrives last then
-// sorts the pairs (token * topk + slot) by expert, tokens in order: a bit per
-// token and expert (OR-ed in any order), the experts' counts added up, and
-// each pair's place is its expert's first place plus the bits below its own.
-// Other workgroups' ids are read at the device's coherence point: written and
-// read with device-scope accesses, the writes complete (the wait) before the
-// arrival is counted.
-constexpr int kMaskWords = kMoeMaxTokens / 32;
+// Routing, by one workgroup: a wave per token (and every 16th after), then
+// the pairs (token * topk + slot) sorted by expert, tokens in order: a bit
+// per token and expert, the experts' counts added up, and each pair's place
+// is its expert's first place plus the bits below its own.
 template <int NV>
-__global__ void __launch_bounds__(256) k_moe_route(MoeArgs a)
+__global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
 {
-    __shared__ unsigned mask[NV * 64][kMaskWords + 1];      // [expert][token / 32]; the last word: first place
-    __shared__ unsigned arrived, sums[2][4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    if (t < a.T) route_token<NV>(a, t, lane);
-    __builtin_amdgcn_s_waitcnt(0);
+    __shared__ unsigned long long mask[NV * 64];             // tokens of each expert
+    __shared__ int first[NV * 64], ids[kMoeMaxPairs];
+    __shared__ int sums[2][16];
+    static_assert(kMoeMaxTokens == 64 && NV * 64 <= 1024, "a word of bits per expert, a thread per expert");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
+    for (int i = tid; i < NV * 64; i += threads) mask[i] = 0ull;
     __syncthreads();
-    if (tid == 0) arrived = __hip_atomic_fetch_add(a.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int i = tid; i < NV * 64 * (kMaskWords + 1); i += 256) (&mask[0][0])[i] = 0u;
-    __syncthreads();
-    if (arrived != gridDim.x - 1) return;
-    const int pairs = (int)a.T * a.topk;
-    for (int p = tid; p < pairs; p += 256) {
-        const int e = __hip_atomic_load(a.w_ids + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int tok = p / a.topk;
-        if (e >= 0) atomicOr(&mask[e][tok >> 5], 1u << (tok & 31));
-    }
-    __syncthreads();
-    // thread i sums experts NV / 4 i ..: pairs before, chosen experts before
-    constexpr int EPT = NV * 64 / 256 > 0 ? NV * 64 / 256 : 1;
-    unsigned cnt[EPT], pr = 0, ch = 0;
-#pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        const int e = tid * EPT + j;
-        cnt[j] = 0;
-        if (e < NV * 64)
-            for (int w = 0; w < kMaskWords; ++w) cnt[j] += __builtin_popcount(mask[e][w]);
-        pr += cnt[j];
-        ch += cnt[j] > 0;
-    }
-    unsigned pr_to = pr, ch_to = ch;         // inclusive over the wave
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const unsigned x = __shfl_up(pr_to, o, 64), y = __shfl_up(ch_to, o, 64);
-        if (lane >= o) {
-            pr_to += x;
-            ch_to += y;
+    for (int t = wave; t < (int)a.T; t += threads / 64) {
+        int id;
+        float gate;
+        route_token<NV>(a, t, lane, id, gate);
+        if (lane < a.topk) {
+            const int p = t * a.topk + lane;
+            ids[p] = id;
+            a.w_ids[p] = id;
+            a.w_gates[p] = gate;
+            if (a.ids) a.ids[p] = id;
+            if (a.gates) a.gates[p] = gate;
+            if (id >= 0) atomicOr(&mask[id], 1ull << t);
         }
     }
-    if (lane == 63) {
-        sums[0][wave] = pr_to;
-        sums[1][wave] = ch_to;
-    }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) {
-        pr_to += sums[0][w];
-        ch_to += sums[1][w];
-    }
-    unsigned first = pr_to - pr, ordinal = ch_to - ch;
+    // experts in turns of one per thread: pairs before, chosen experts before
+    int pr0 = 0, ch0 = 0;
+    for (int e0 = 0; e0 < NV * 64; e0 += threads) {
+        const int e = e0 + tid;
+        const int cnt = e < NV * 64 ? __builtin_popcountll(mask[e]) : 0;
+        int pr = cnt, ch = cnt > 0;
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-        const int e = tid * EPT + j;
-        if (cnt[j] > 0) {
-            a.items[ordinal] = MoeItem{e, (int)first, (int)cnt[j], 0};
-            mask[e][kMaskWords] = first;
-            ++ordinal;
-            first += cnt[j];
+        for (int o = 1; o < 64; o <<= 1) {
+            const int x = __shfl_up(pr, o, 64), y = __shfl_up(ch, o, 64);
+            if (lane >= o) {
+                pr += x;
+                ch += y;
+            }
         }
+        if (lane == 63) {
+            sums[0][wave] = pr;
+            sums[1][wave] = ch;
+        }
+        __syncthreads();
+        int pr_all = pr0, ch_all = ch0;
+        for (int w = 0; w < threads / 64; ++w) {
+            if (w == wave) {
+                pr += pr_all;
+                ch += ch_all;
+            }
+            pr_all += sums[0][w];
+            ch_all += sums[1][w];
+        }
+        if (cnt > 0) {
+            first[e] = pr - cnt;
+            a.items[ch - 1] = MoeItem{e, pr - cnt, cnt, 0};
+        }
+        pr0 = pr_all;
+        ch0 = ch_all;
+        __syncthreads();
     }
-    if (tid == 255) *a.chosen = (int)ch_to;
-    __syncthreads();
-    for (int p = tid; p < pairs; p += 256) {
-        const int e = __hip_atomic_load(a.w_ids + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (e < 0) continue;
-        const int tok = p / a.topk;
-        unsigned at = mask[e][kMaskWords] + __builtin_popcount(mask[e][tok >> 5] & ((1u << (tok & 31)) - 1u));
-        for (int w = 0; w < (tok >> 5); ++w) at += __builtin_popcount(mask[e][w]);
-        a.pairs[at] = p;
+    if (tid == 0) *a.chosen = ch0;
+    for (int p = tid; p < (int)a.T * a.topk; p += threads) {
+        const int e = ids[p];
+        if (e >= 0) a.pairs[first[e] + __builtin_popcountll(mask[e] & ((1ull << (p / a.topk)) - 1))] = p;
     }
-    if (tid == 0) __hip_atomic_store(a.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // 16 E4M3FN codes as 16 bf16 values (each exact), in order.
@@ -196,23 +194,22 @@ __device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
 // tokens (80 registers), two for the others, whose larger steps need 128.
 constexpr int moe_occupancy(bool codes, bool many) { return codes || many ? 4 : 6; }
 
-// acc[r][c] += rows of W block r (two blocks of 16 rows) times the token
+// acc[r][c] += rows of W block r (RB blocks of 16 rows) times the token
 // rows of chunk c (16 of them), over slice ks of KW of K.  wrow[r]: the
 // lane's row (li) of block r; xrow[c]: the lane's row of chunk c in plane 0,
 // plane 1 at + xplane (PL == 2).  A step is 64 bytes of every row: lane
 // group g takes bytes 16 g .. 16 g + 15; D steps' loads are issued before the
 // first is used.
-template <bool CODES, int PL, int NC, int KW, bool VEC, bool MANY>
-__device__ __forceinline__ void moe_stream(const void *const (&wrow)[2], const bool (&wok)[2], int align_w,
+template <bool CODES, int PL, int RB, int NC, int KW, int REGS, bool VEC>
+__device__ __forceinline__ void moe_stream(const void *const (&wrow)[RB], const bool (&wok)[RB], int align_w,
                                            const uint16_t *const (&xrow)[NC], const bool (&xok)[NC], int64_t xplane,
-                                           int align_x, int64_t K, int ks, int g, f32x4 (&acc)[2][NC])
+                                           int align_x, int64_t K, int ks, int g, f32x4 (&acc)[RB][NC])
 {
     constexpr int KS = CODES ? 64 : 32;
     constexpr int XQ = CODES ? 2 : 1;              // 8-element pieces of x per lane and step
-    // as many steps as the kernel's registers hold (8 words of W and 4 per
-    // piece of x each): moe_occupancy leaves 80 or 128 registers per lane
-    constexpr int fit = (moe_occupancy(CODES, MANY) == 6 ? 48 : CODES ? 72 : 80) / (8 + 4 * NC * PL * XQ);
-    constexpr int D = fit < 1 ? 1 : fit < 4 ? fit : 4;
+    // as many steps as REGS registers hold (4 per piece of W and of x)
+    constexpr int fit = REGS / (4 * RB + 4 * NC * PL * XQ);
+    constexpr int D = fit < 1 ? 1 : fit < 8 ? fit : 8;
     const int whole = (int)(K / KS);
     const int s0 = whole * ks / KW, s1 = whole * (ks + 1) / KW;
     auto load_w = [&](int r, int s, bool in) -> u32x4 {
@@ -227,9 +224,9 @@ __device__ __forceinline__ void moe_stream(const void *const (&wrow)[2], const b
         if constexpr (VEC) return xok[c] && in ? *(const u32x4 *)(row + col) : u32x4{0u, 0u, 0u, 0u};
         return load_chunk8_bf16(row, col, K, xok[c] && in, align_x);
     };
-    auto mma = [&](const u32x4 (&w)[2], const u32x4 (&x)[NC][PL][XQ]) {
+    auto mma = [&](const u32x4 (&w)[RB], const u32x4 (&x)[NC][PL][XQ]) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RB; ++r) {
             u32x4 b[2] = {w[r], w[r]};
             if constexpr (CODES) codes16_to_bf16(w[r], b[0], b[1]);
 #pragma unroll
@@ -244,11 +241,11 @@ __device__ __forceinline__ void moe_stream(const void *const (&wrow)[2], const b
         }
     };
     for (int s = s0; s < s1; s += D) {
-        u32x4 w[D][2], x[D][NC][PL][XQ];
+        u32x4 w[D][RB], x[D][NC][PL][XQ];
 #pragma unroll
         for (int j = 0; j < D; ++j)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) w[j][r] = load_w(r, s + j, s + j < s1);
+            for (int r = 0; r < RB; ++r) w[j][r] = load_w(r, s + j, s + j < s1);
 #pragma unroll
         for (int j = 0; j < D; ++j)
 #pragma unroll
@@ -262,9 +259,9 @@ __device__ __forceinline__ void moe_stream(const void *const (&wrow)[2], const b
     }
     if (ks == KW - 1 && K % KS != 0) {
         // the rest of K, zero-filled past it
-        u32x4 w[2], x[NC][PL][XQ];
+        u32x4 w[RB], x[NC][PL][XQ];
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RB; ++r)
             w[r] = CODES ? load_chunk16_u8((const uint8_t *)wrow[r], whole * KS + g * 16, K, wok[r], align_w)
                          : load_chunk8_bf16((const uint16_t *)wrow[r], whole * KS + g * 8, K, wok[r], align_w);
 #pragma unroll
@@ -279,10 +276,9 @@ __device__ __forceinline__ void moe_stream(const void *const (&wrow)[2], const b
     }
 }
 
-// The KW slices' partial sums of chunk c, added in order by the first
-// 64 * 8 / KW threads (64 per group of rows): s[r] is block r's sum of rows
-// 4 (t % 64 / 16) .. + 3, token t % 16.
-template <int NC, int KW>
+// The waves' partial sums of chunk c, added in order by the first 64 threads:
+// s[r] is block r's sum of rows 4 (t / 16) .. + 3, token t % 16.
+template <int NC>
 __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f32x4 (&acc)[2][NC], int c,
                                          f32x4 (&s)[2])
 {
@@ -291,12 +287,12 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
     red[wave][0][lane] = acc[0][c];
     red[wave][1][lane] = acc[1][c];
     __syncthreads();
-    if (wave < kMoeWaves / KW) {
+    if (wave == 0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            s[r] = red[wave * KW][r][lane];
+            s[r] = red[0][r][lane];
 #pragma unroll
-            for (int w = 1; w < KW; ++w) s[r] += red[wave * KW + w][r][lane];
+            for (int w = 1; w < kMoeWaves; ++w) s[r] += red[w][r][lane];
         }
     }
 }
@@ -325,12 +321,12 @@ __device__ __forceinline__ void moe_gate_up_tokens(const MoeArgs &a, const MoeIt
     f32x4 acc[2][NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_stream<CODES, 1, NC, kMoeWaves, VEC, MANY>(wrow, wok, a.align_gu, xrow, xok, 0, a.align_x, a.H, wave, g, acc);
+    moe_stream<CODES, 1, 2, NC, kMoeWaves, moe_occupancy(CODES, MANY) == 6 ? 48 : 64, VEC>(wrow, wok, a.align_gu, xrow, xok, 0, a.align_x, a.H, wave, g, acc);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         if (base + 16 * c >= it.count) break;       // uniform
         f32x4 s[2];
-        moe_join<NC, kMoeWaves>(red, acc, c, s);
+        moe_join<NC>(red, acc, c, s);
         if (wave == 0 && xok[c]) {
             const int64_t p = pair[c], i = i0 + 4 * g;
 #pragma unroll
@@ -373,21 +369,22 @@ __global__ void __launch_bounds__(kMoeThreads, moe_occupancy(CODES, MANY)) k_moe
     }
 }
 
-constexpr int kDownK = 4;                                  // K slices of the down kernel's waves
-constexpr int kDownCols = 32 * (kMoeWaves / kDownK);       // hidden columns per workgroup
-
-// gate * (z Wd^T) of the workgroup's hidden columns for the expert's tokens,
-// each pair's into its own row of `part`.
+// The down rows.  A workgroup owns `cols` (at most 16) hidden columns for
+// every expert, so a token's slots meet in its LDS and nothing else is joined:
+// its sixteen waves take pieces (expert, half of K) one after the other, the
+// next free one each, and leave each pair's sums in the piece's own places.
+// The order in which pieces are taken does not matter; the halves and the
+// slots are added in order.
+constexpr int kDownWaves = 16, kDownSlices = 2;
 template <bool CODES, bool VEC, int NC, bool MANY>
-__device__ __forceinline__ void moe_down_tokens(const MoeArgs &a, const MoeItem &it, int n0, int base,
-                                                f32x4 (&red)[kMoeWaves][2][64])
+__device__ __forceinline__ void moe_down_tokens(const MoeArgs &a, const MoeItem &it, int n0, int slice, int base,
+                                                float (&part)[kDownSlices][kMoeMaxPairs][16])
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
     constexpr int EB = CODES ? 1 : 2;
     const char *W = (const char *)a.Wd + (int64_t)it.expert * a.strideD * EB;
-    const int nw = n0 + 32 * (wave / kDownK);
-    const bool wok[2] = {nw + li < a.H, nw + 16 + li < a.H};
-    const void *const wrow[2] = {W + (wok[0] ? nw + li : 0) * a.ldd * EB, W + (wok[1] ? nw + 16 + li : 0) * a.ldd * EB};
+    const bool wok[1] = {li < a.cols && n0 + li < a.H};
+    const void *const wrow[1] = {W + (wok[0] ? n0 + li : 0) * a.ldd * EB};
     const uint16_t *zrow[NC];
     bool zok[NC];
     int pair[NC];
@@ -397,75 +394,55 @@ __device__ __forceinline__ void moe_down_tokens(const MoeArgs &a, const MoeItem 
         pair[c] = zok[c] ? a.pairs[it.first + base + 16 * c + li] : 0;
         zrow[c] = a.z + (int64_t)pair[c] * a.ldz;
     }
-    f32x4 acc[2][NC];
+    f32x4 acc[1][NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_stream<CODES, 2, NC, kDownK, VEC, MANY>(wrow, wok, a.align_d, zrow, zok, a.zplane, 16, a.I, wave % kDownK, g, acc);
+    for (int c = 0; c < NC; ++c) acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    moe_stream<CODES, 2, 1, NC, kDownSlices, MANY ? 64 : CODES ? 80 : 96, VEC>(wrow, wok, a.align_d, zrow, zok, a.zplane, 16, a.I,
+                                                                  slice, g, acc);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        if (base + 16 * c >= it.count) break;       // uniform
-        f32x4 s[2];
-        moe_join<NC, kDownK>(red, acc, c, s);
-        if (wave < kMoeWaves / kDownK && zok[c]) {
-            const int64_t p = pair[c];
-            const float gate = a.w_gates[p];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t n = n0 + 32 * wave + 16 * r + 4 * g + q;
-                    if (n >= a.H) break;
-                    const float sc = a.scale_d ? a.scale_d[(int64_t)it.expert * a.H + n] : 1.0f;
-                    __hip_atomic_store(a.part + p * a.H + n, gate * (s[r][q] * sc), __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-                }
-        }
-    }
+    for (int c = 0; c < NC; ++c)
+        if (zok[c]) *(f32x4 *)&part[slice][pair[c]][4 * g] = acc[0][c];
 }
 
-// The last of a column strip's workgroups (one per chosen expert) adds each
-// token's pairs in slot order: the parts are written and read at the device's
-// coherence point, complete before the arrival is counted.
 template <bool CODES, bool VEC, bool MANY>
-__global__ void __launch_bounds__(kMoeThreads, moe_occupancy(CODES, MANY)) k_moe_down(MoeArgs a)
+__global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 {
-    __shared__ f32x4 red[kMoeWaves][2][64];
-    __shared__ unsigned arrived;
-    const int strips = (int)((a.H + kDownCols - 1) / kDownCols), ordinal = blockIdx.x / strips;
-    const int strip = blockIdx.x - ordinal * strips, n0 = strip * kDownCols;
-    const int chosen = *a.chosen;
-    if (ordinal >= chosen && !(chosen == 0 && ordinal == 0)) return;
-    if (chosen > 0) {
-        const MoeItem it = a.items[ordinal];
+    __shared__ __attribute__((aligned(16))) float part[kDownSlices][kMoeMaxPairs][16];
+    __shared__ int next;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = blockIdx.x * a.cols;
+    if (threadIdx.x == 0) next = kDownWaves;
+    __syncthreads();
+    const int pieces = *a.chosen * kDownSlices;
+    for (int piece = wave; piece < pieces;) {
+        const MoeItem it = a.items[piece / kDownSlices];
+        const int slice = piece % kDownSlices;
         if constexpr (!MANY) {
-            moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, 0, red);
+            moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, slice, 0, part);
         } else {
             for (int base = 0; base < it.count; base += 32) {
-                if (it.count - base <= 16) moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, base, red);
-                else moe_down_tokens<CODES, VEC, 2, MANY>(a, it, n0, base, red);
+                if (it.count - base <= 16) moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, slice, base, part);
+                else moe_down_tokens<CODES, VEC, 2, MANY>(a, it, n0, slice, base, part);
             }
         }
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        unsigned *c = a.counter + 1 + strip;
-        if (threadIdx.x == 0) arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __syncthreads();
-        if (arrived != (unsigned)(chosen - 1)) return;
-        if (threadIdx.x == 0) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        int p = 0;
+        if (lane == 0) p = atomicAdd(&next, 1);
+        piece = __builtin_amdgcn_readfirstlane(p);
     }
-    for (int o = threadIdx.x; o < (int)a.T * kDownCols; o += kMoeThreads) {
-        const int64_t t = o / kDownCols, n = n0 + o % kDownCols;
-        if (n >= a.H) continue;
-        float y = 0.f;
+    __syncthreads();
+    // a thread per token and column
+    const int t = threadIdx.x >> 4, c = threadIdx.x & 15, n = n0 + c;
+    if (t >= (int)a.T || c >= a.cols || n >= (int)a.H) return;
+    float y = 0.f;
 #pragma unroll 4
-        for (int s = 0; s < a.topk; ++s) {
-            const int64_t p = t * a.topk + s;
-            if (a.w_ids[p] >= 0)
-                y += __hip_atomic_load(a.part + p * a.H + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        if (a.out_f32) ((float *)a.Y)[t * a.ldy + n] = y;
-        else ((uint16_t *)a.Y)[t * a.ldy + n] = (uint16_t)bf16_rne(y);
+    for (int s = 0; s < a.topk; ++s) {
+        const int p = t * a.topk + s, e = a.w_ids[p];
+        if (e < 0) continue;
+        float v = part[0][p][c] + part[1][p][c];
+        if (a.scale_d) v *= a.scale_d[(int64_t)e * a.H + n];
+        y = __builtin_fmaf(a.w_gates[p], v, y);
     }
+    if (a.out_f32) ((float *)a.Y)[t * a.ldy + n] = y;
+    else ((uint16_t *)a.Y)[t * a.ldy + n] = (uint16_t)bf16_rne(y);
 }
 
 }  // namespace
@@ -474,22 +451,26 @@ template <bool CODES, bool MANY>
 static hipError_t launch_moe_weights(const MoeArgs &a, bool vec_gu, bool vec_d, hipStream_t s)
 {
     const int64_t chosen = a.E < a.T * a.topk ? a.E : a.T * a.topk;   // experts at most
-    const dim3 gg((unsigned)(chosen * ((a.I + 15) / 16))), gd((unsigned)(chosen * ((a.H + kDownCols - 1) / kDownCols)));
-    const dim3 b(kMoeThreads);
+    const dim3 gg((unsigned)(chosen * ((a.I + 15) / 16))), gd((unsigned)((a.H + a.cols - 1) / a.cols));
+    const dim3 b(kMoeThreads), bd(kDownWaves * 64);
     if (a.I > 0) {      // (no inner columns: the down kernel's sums are empty)
         if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, MANY>), gg, b, 0, s, a);
         else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, MANY>), gg, b, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, MANY>), gd, b, 0, s, a);
-    else hipLaunchKernelGGL((k_moe_down<CODES, false, MANY>), gd, b, 0, s, a);
+    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, MANY>), gd, bd, 0, s, a);
+    else hipLaunchKernelGGL((k_moe_down<CODES, false, MANY>), gd, bd, 0, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_moe(const MoeArgs &a, bool codes, bool vec_gu, bool vec_d, hipStream_t s)
+hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, hipStream_t s)
 {
-    const dim3 rg((unsigned)((a.T + 3) / 4)), rb(256);
+    MoeArgs a = args;
+    // hidden columns per workgroup of the down kernel: as many workgroups as
+    // the 256 CUs, 16 columns at most and 4 at least
+    a.cols = a.H > 2048 ? 16 : a.H > 1024 ? 8 : 4;
+    const dim3 rg(1), rb((unsigned)(a.T < 16 ? a.T * 64 : 1024));
     if (a.E <= 64) hipLaunchKernelGGL((k_moe_route<1>), rg, rb, 0, s, a);
     else if (a.E <= 128) hipLaunchKernelGGL((k_moe_route<2>), rg, rb, 0, s, a);
     else if (a.E <= 256) hipLaunchKernelGGL((k_moe_route<4>), rg, rb, 0, s, a);

@@ -140,7 +140,7 @@ def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, need_dw=True, w
 
 def moe_swiglu(X, logits, topk, Wgu, Wd, scale_gu=None, scale_d=None, renormalize=True, Y=None,
                out_dtype=torch.bfloat16, ids=None, gates=None, workspace=None):
-    """A mixture-of-experts SwiGLU layer for up to 256 tokens, behind the
+    """A mixture-of-experts SwiGLU layer for up to 64 tokens, behind the
     router's product (gemm_moe_swiglu): X [T, H] bfloat16, logits [T, E]
     float32, Wgu [E, 2I, H] (gate rows, then up rows) and Wd [E, H, I] in
     bfloat16, or as E4M3FN codes with float32 factors scale_gu [E, 2I] and

@@ -584,7 +584,7 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
 
 /* ---- mixture-of-experts layer for a few tokens --------------------------------
  *
- * Everything behind the router's product, for T tokens (0 <= T <= 256;
+ * Everything behind the router's product, for T tokens (0 <= T <= 64;
  * larger batches: gemm_bf16_nt_batched or gemm_fp8_nt_batched per expert and
  * gemm_act_chain).  Per token t, with l = logits[t] (float [T, E], e.g.
  * gemm_bf16_nt with a float output):
@@ -611,11 +611,11 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
  * 2^-16 of it) and y rounded once: unlike the fused epilogues above, no
  * intermediate is rounded to bf16.  Only the chosen experts' weights are
  * read.  Deterministic, and a token's result does not depend on the others
- * in the call.  1 <= topk <= min(E, 32), E <= 1024, H and I <= 65536.
+ * in the call.  1 <= topk <= min(E, 16), E <= 1024, H and I <= 65536.
  * 16-byte aligned rows run fastest; any other alignment is taken.
  * workspace: gemm_moe_workspace_size bytes, 256-byte aligned, its first
- * GEMM_WORKSPACE_COUNTER_BYTES zero before and after the call (gemm_run's
- * workspace serves); calls that may overlap in time need workspaces of their
+ * GEMM_WORKSPACE_COUNTER_BYTES left untouched (gemm_run's workspace serves);
+ * calls that may overlap in time need workspaces of their
  * own.  T == 0: nothing is done.  I == 0 gives zeros.  Errors, nothing
  * enqueued: GEMM_ERR_INVALID_ARG for sizes outside these ranges, another
  * w_type or c_type, factors with bf16 weights, strides below the row

@@ -111,12 +111,14 @@ CASES = [  # T, H, I, E, topk, codes, renormalize, layout
     (1, 256, 64, 8, 2, False, True, "contig"), (1, 520, 72, 4, 4, False, False, "contig"),
     (5, 264, 40, 16, 3, False, True, "padded"), (7, 100, 33, 5, 2, False, False, "odd"),
     (17, 512, 130, 3, 2, False, True, "contig"), (40, 192, 48, 2, 1, False, True, "contig"),
-    (70, 128, 64, 4, 3, False, False, "padded"), (64, 128, 32, 130, 8, False, True, "contig"),
-    (256, 64, 32, 3, 2, False, True, "contig"), (3, 1, 1, 1, 1, False, True, "contig"),
-    (9, 96, 24, 300, 32, False, False, "contig"), (2, 64, 16, 1024, 5, False, True, "contig"),
+    (50, 128, 64, 4, 3, False, False, "padded"), (64, 128, 32, 130, 8, False, True, "contig"),
+    (64, 64, 32, 3, 2, False, True, "contig"), (3, 1, 1, 1, 1, False, True, "contig"),
+    (9, 96, 24, 300, 16, False, False, "contig"), (2, 64, 16, 1024, 5, False, True, "contig"),
     (1, 256, 64, 8, 2, True, True, "contig"), (6, 320, 96, 6, 2, True, False, "padded"),
     (7, 100, 33, 5, 2, True, True, "odd"), (33, 528, 80, 3, 2, True, False, "contig"),
-    (70, 128, 64, 2, 1, True, True, "contig"), (1, 2048, 512, 4, 2, False, True, "contig"),
+    (64, 128, 64, 2, 1, True, True, "contig"), (1, 2048, 512, 4, 2, False, True, "contig"),
+    (2, 1100, 64, 3, 2, False, True, "contig"), (2, 2304, 64, 3, 2, True, True, "contig"),
+    (64, 40, 24, 16, 16, False, True, "contig"),
 ]
 
 
