@@ -1368,20 +1368,20 @@ int gemm_rms_norm_backward(int64_t rows, int64_t cols, const uint16_t *dY, int64
 // ---- mixture-of-experts layer for a few tokens
 // Scratch after the counter region, each part 256-byte aligned.
 struct MoeLayout {
-    size_t ids, gates, chosen, items, pairs, z, total;
+    size_t ids, gates, n_items, items, pairs, z, total;
     int64_t ldz, zplane;
 };
 static MoeLayout moe_layout(int64_t T, int64_t I, int64_t E, int64_t topk)
 {
     MoeLayout L;
     const size_t pairs = (size_t)T * topk;
-    L.ldz = (I + 7) / 8 * 8;
+    L.ldz = (I + 127) / 128 * 128;      // whole steps of the down kernel, the rest zeros
     L.zplane = (int64_t)pairs * L.ldz;
     L.ids = g5::kCounterBytes;
     L.gates = L.ids + g5::round256(pairs * 4);
-    L.chosen = L.gates + g5::round256(pairs * 4);
-    L.items = L.chosen + 256;
-    L.pairs = L.items + g5::round256((size_t)E * sizeof(g5::MoeItem));
+    L.n_items = L.gates + g5::round256(pairs * 4);
+    L.items = L.n_items + 256;
+    L.pairs = L.items + g5::round256((size_t)g5::moe_items(T, E, topk) * sizeof(g5::MoeItem));
     L.z = L.pairs + g5::round256(pairs * 4);
     L.total = L.z + g5::round256((size_t)L.zplane * 4);
     return L;
@@ -1468,7 +1468,7 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     a.align_x = g5::row_alignment((uint64_t)X, ldx, 0, 1, 2);
     a.align_gu = g5::row_alignment((uint64_t)Wgu, ldgu, strideGu, E, ew);
     a.align_d = g5::row_alignment((uint64_t)Wd, ldd, strideD, E, ew);
-    a.chosen = (int *)(ws + L.chosen);
+    a.n_items = (int *)(ws + L.n_items);
     a.items = (g5::MoeItem *)(ws + L.items);
     a.pairs = (int32_t *)(ws + L.pairs);
     a.w_ids = (int32_t *)(ws + L.ids);
@@ -1476,8 +1476,12 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     a.z = (uint16_t *)(ws + L.z);
     a.ldz = L.ldz;
     a.zplane = L.zplane;
-    const hipError_t e = g5::launch_moe(a, codes, a.align_x >= 16 && a.align_gu >= 16, a.align_d >= 16,
-                                        (hipStream_t)stream);
+    // (the fast kernels add 32-bit byte offsets of up to 16 weight rows and 64
+    // token rows, and read whole 16-byte pieces)
+    constexpr int64_t kFar = (int64_t)1 << 31;
+    const bool vec_gu = a.align_x >= 16 && a.align_gu >= 16 && H % (16 / ew) == 0 && ldgu * ew < kFar / 16 && ldx * 2 < kFar / 64;
+    const bool vec_d = a.align_d >= 16 && I % (16 / ew) == 0 && ldd * ew < kFar / 16;
+    const hipError_t e = g5::launch_moe(a, codes, vec_gu, vec_d, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 

@@ -152,6 +152,15 @@ constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
 struct MoeItem {
     int expert, first, count, pad;   // its pairs: first .. first + count - 1 of the sorted list
 };
+// Tokens per work item (the matrix core's 16 columns once or twice), and the
+// most items a call can have: one per chosen expert and one more per whole
+// chunk, never more than pairs.
+inline int moe_chunk(int64_t T) { return T > 16 ? 32 : 16; }
+inline int64_t moe_items(int64_t T, int64_t E, int64_t topk)
+{
+    const int64_t pairs = T * topk, most = E + pairs / moe_chunk(T);
+    return most < pairs ? most : pairs;
+}
 struct MoeArgs {
     const uint16_t *X;
     const float *logits;
@@ -163,10 +172,11 @@ struct MoeArgs {
     int64_t T, H, I, E, ldx, ldl, ldgu, strideGu, ldd, strideD, ldy;
     int topk, renormalize, out_f32, align_x, align_gu, align_d;
     int cols;                          // hidden columns per workgroup of the down kernel
-    // scratch: the routing [T * topk], the number of chosen experts, the
-    // experts in order and the pairs sorted by them; z as two bf16 planes of
+    int chunk;                         // moe_chunk(T)
+    // scratch: the routing [T * topk], the number of work items, the items by
+    // expert and the pairs sorted by expert; z as two bf16 planes of
     // rows of ldz
-    int *chosen;
+    int *n_items;
     MoeItem *items;
     int32_t *pairs;
     int32_t *w_ids;

@@ -108,7 +108,8 @@ __device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lan
 // Routing, by one workgroup: a wave per token (and every 16th after), then
 // the pairs (token * topk + slot) sorted by expert, tokens in order: a bit
 // per token and expert, the experts' counts added up, and each pair's place
-// is its expert's first place plus the bits below its own.
+// is its expert's first place plus the bits below its own.  The work items of
+// the kernels below are runs of at most a.chunk pairs of one expert.
 template <int NV>
 __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
 {
@@ -134,12 +135,13 @@ __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
         }
     }
     __syncthreads();
-    // experts in turns of one per thread: pairs before, chosen experts before
+    // experts in turns of one per thread: pairs before, items before
     int pr0 = 0, ch0 = 0;
     for (int e0 = 0; e0 < NV * 64; e0 += threads) {
         const int e = e0 + tid;
         const int cnt = e < NV * 64 ? __builtin_popcountll(mask[e]) : 0;
-        int pr = cnt, ch = cnt > 0;
+        int pr = cnt, ch = (cnt + a.chunk - 1) / a.chunk;
+        const int mine = ch;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const int x = __shfl_up(pr, o, 64), y = __shfl_up(ch, o, 64);
@@ -164,13 +166,16 @@ __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
         }
         if (cnt > 0) {
             first[e] = pr - cnt;
-            a.items[ch - 1] = MoeItem{e, pr - cnt, cnt, 0};
+            for (int i = 0; i < mine; ++i) {
+                const int left = cnt - i * a.chunk;
+                a.items[ch - mine + i] = MoeItem{e, pr - cnt + i * a.chunk, left < a.chunk ? left : a.chunk, 0};
+            }
         }
         pr0 = pr_all;
         ch0 = ch_all;
         __syncthreads();
     }
-    if (tid == 0) *a.chosen = ch0;
+    if (tid == 0) *a.n_items = ch0;
     for (int p = tid; p < (int)a.T * a.topk; p += threads) {
         const int e = ids[p];
         if (e >= 0) a.pairs[first[e] + __builtin_popcountll(mask[e] & ((1ull << (p / a.topk)) - 1))] = p;
@@ -190,90 +195,184 @@ __device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
     }
 }
 
-// Waves per SIMD: three workgroups per CU for bf16 weights and at most 16
-// tokens (80 registers), two for the others, whose larger steps need 128.
-constexpr int moe_occupancy(bool codes, bool many) { return codes || many ? 4 : 6; }
+// A step is a 128-byte line of every weight row, read in two pieces: lane
+// group g (of four) takes bytes 16 g .. 16 g + 15 of each half.  The halves
+// are loaded one right after the other: the bytes in flight exceed an XCD's
+// L2, so a line whose second half is asked for later is fetched again
+// (measured: 1.6 times the bytes with the halves a batch apart, 1.5 times
+// with a lane's 32 bytes next to each other).  Piece h meets the same elements
+// of the token's row (8 of bf16, or 16 codes in two products).
+template <bool CODES>
+constexpr int kStep = CODES ? 128 : 64;       // elements
+template <bool CODES>
+constexpr int kPieces = CODES ? 4 : 2;        // 8-element pieces of a token row per lane and step
 
-// acc[r][c] += rows of W block r (RB blocks of 16 rows) times the token
-// rows of chunk c (16 of them), over slice ks of KW of K.  wrow[r]: the
-// lane's row (li) of block r; xrow[c]: the lane's row of chunk c in plane 0,
-// plane 1 at + xplane (PL == 2).  A step is 64 bytes of every row: lane
-// group g takes bytes 16 g .. 16 g + 15; D steps' loads are issued before the
-// first is used.
-template <bool CODES, int PL, int RB, int NC, int KW, int REGS, bool VEC>
-__device__ __forceinline__ void moe_stream(const void *const (&wrow)[RB], const bool (&wok)[RB], int align_w,
-                                           const uint16_t *const (&xrow)[NC], const bool (&xok)[NC], int64_t xplane,
-                                           int align_x, int64_t K, int ks, int g, f32x4 (&acc)[RB][NC])
+// Where piece q of a token's row starts in a step, for lane group g: bf16 has
+// one per half, codes two.
+template <bool CODES>
+__device__ __forceinline__ int x_piece(int q, int g)
 {
-    constexpr int KS = CODES ? 64 : 32;
-    constexpr int XQ = CODES ? 2 : 1;              // 8-element pieces of x per lane and step
-    // as many steps as REGS registers hold (4 per piece of W and of x)
-    constexpr int fit = REGS / (4 * RB + 4 * NC * PL * XQ);
-    constexpr int D = fit < 1 ? 1 : fit < 8 ? fit : 8;
-    const int whole = (int)(K / KS);
-    const int s0 = whole * ks / KW, s1 = whole * (ks + 1) / KW;
-    auto load_w = [&](int r, int s, bool in) -> u32x4 {
-        if (!wok[r] || !in) return u32x4{0u, 0u, 0u, 0u};
-        if constexpr (VEC) return __builtin_nontemporal_load((const u32x4 *)((const char *)wrow[r] + s * 64 + g * 16));
-        if constexpr (CODES) return load_chunk16_u8((const uint8_t *)wrow[r], s * KS + g * 16, K, true, align_w);
-        else return load_chunk8_bf16((const uint16_t *)wrow[r], s * KS + g * 8, K, true, align_w);
-    };
-    auto load_x = [&](int c, int pl, int q, int s, bool in) -> u32x4 {
-        const int col = s * KS + (CODES ? g * 16 + q * 8 : g * 8);
-        const uint16_t *row = xrow[c] + pl * xplane;
-        if constexpr (VEC) return xok[c] && in ? *(const u32x4 *)(row + col) : u32x4{0u, 0u, 0u, 0u};
-        return load_chunk8_bf16(row, col, K, xok[c] && in, align_x);
-    };
-    auto mma = [&](const u32x4 (&w)[RB], const u32x4 (&x)[NC][PL][XQ]) {
+    return CODES ? 64 * (q >> 1) + 16 * g + 8 * (q & 1) : 32 * q + 8 * g;
+}
+
+// The lane group's part of that, in bytes.
+template <bool CODES>
+__device__ __forceinline__ uint32_t x_lane(int g)
+{
+    return (CODES ? 32u : 16u) * g;
+}
+
+// D steps of RB weight rows and of NC token rows in PL planes in registers,
+// and their products: step s in place j is multiplied and step s + D loaded
+// over it, so D steps stay in flight.
+template <bool CODES, int RB, int NC, int PL, int D>
+struct MoeStream {
+    static constexpr int XP = kPieces<CODES>, KS = kStep<CODES>;
+    u32x4 w[D][RB][2], x[D][NC][PL][XP];
+
+    // Whole step s of 16-byte aligned rows: wave-uniform bases and the lane's
+    // byte offsets (its row and 16 g).  A lane without a token leaves its x
+    // as it is (its column of the product is never read).
+    __device__ __forceinline__ void load(int j, const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
+                                         const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s)
+    {
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            u32x4 b[2] = {w[r], w[r]};
-            if constexpr (CODES) codes16_to_bf16(w[r], b[0], b[1]);
+        for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int q = 0; q < XQ; ++q)
+            for (int h = 0; h < 2; ++h)
+                w[j][r][h] = __builtin_nontemporal_load((const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff));
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int pl = 0; pl < PL; ++pl)
-                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[q]),
-                                                                            __builtin_bit_cast(bf16x8, x[c][pl][q]),
-                                                                            acc[r][c], 0, 0, 0);
-        }
-    };
-    for (int s = s0; s < s1; s += D) {
-        u32x4 w[D][RB], x[D][NC][PL][XQ];
-#pragma unroll
-        for (int j = 0; j < D; ++j)
-#pragma unroll
-            for (int r = 0; r < RB; ++r) w[j][r] = load_w(r, s + j, s + j < s1);
-#pragma unroll
-        for (int j = 0; j < D; ++j)
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
+            if (xok[c]) {
 #pragma unroll
                 for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-                    for (int q = 0; q < XQ; ++q) x[j][c][pl][q] = load_x(c, pl, q, s + j, s + j < s1);
-#pragma unroll
-        for (int j = 0; j < D; ++j) mma(w[j], x[j]);
+                    for (int q = 0; q < XP; ++q)
+                        x[j][c][pl][q] =
+                            *(const u32x4 *)((xbase + (pl * xplane + (int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
+            }
     }
-    if (ks == KW - 1 && K % KS != 0) {
-        // the rest of K, zero-filled past it
-        u32x4 w[RB], x[NC][PL][XQ];
+
+    // The last, partial step (K a whole number of 16-byte pieces): pieces
+    // past K are zeros.
+    __device__ __forceinline__ void load_tail(const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
+                                              const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s,
+                                              int K, int g)
+    {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-            w[r] = CODES ? load_chunk16_u8((const uint8_t *)wrow[r], whole * KS + g * 16, K, wok[r], align_w)
-                         : load_chunk8_bf16((const uint16_t *)wrow[r], whole * KS + g * 8, K, wok[r], align_w);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = s * 128 + 64 * h;                     // + 16 g, in woff
+            const bool in = (int)(at + 16 * g) < (CODES ? K : 2 * K);
+#pragma unroll
+            for (int r = 0; r < RB; ++r) w[0][r][h] = in ? *(const u32x4 *)(wbase[r] + (woff + at)) : zero;
+        }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-                for (int q = 0; q < XQ; ++q)
-                    x[c][pl][q] = load_chunk8_bf16(xrow[c] + pl * xplane,
-                                                   whole * KS + (CODES ? g * 16 + q * 8 : g * 8), K, xok[c], align_x);
-        mma(w, x);
+                for (int q = 0; q < XP; ++q) {
+                    const int col = s * KS + x_piece<CODES>(q, g);
+                    x[0][c][pl][q] = xok[c] && col < K
+                                         ? *(const u32x4 *)((xbase + pl * xplane * 2) +
+                                                            (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0))))
+                                         : zero;
+                }
     }
+
+    // Step s of rows of any alignment, zero-filled past K.
+    __device__ __forceinline__ void load_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
+                                             const bool (&xok)[NC], int64_t xplane, int align_x, int s, int K, int g)
+    {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (CODES)
+                    w[0][r][h] = load_chunk16_u8((const uint8_t *)wrow[r], s * 128 + 64 * h + 16 * g, K, true, align_w);
+                else
+                    w[0][r][h] = load_chunk8_bf16((const uint16_t *)wrow[r], s * 64 + 32 * h + 8 * g, K, true, align_w);
+            }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+                for (int q = 0; q < XP; ++q)
+                    x[0][c][pl][q] = load_chunk8_bf16(xrow[c] + pl * xplane, s * KS + x_piece<CODES>(q, g), K, xok[c], align_x);
+    }
+
+    __device__ __forceinline__ void mma(int j, f32x4 (&acc)[RB][NC]) const
+    {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 b[2] = {w[j][r][h], w[j][r][h]};
+                if constexpr (CODES) codes16_to_bf16(w[j][r][h], b[0], b[1]);
+#pragma unroll
+                for (int q = 0; q < XP / 2; ++q)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int pl = 0; pl < PL; ++pl)
+                            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, b[q]),
+                                __builtin_bit_cast(bf16x8, x[j][c][pl][h * (XP / 2) + q]), acc[r][c], 0, 0, 0);
+            }
+    }
+
+    // Steps s0 .. s1 - 1 of K (the last may be partial), 16-byte aligned.
+    __device__ __forceinline__ void run(const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
+                                        const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s0, int s1,
+                                        int K, int g, f32x4 (&acc)[RB][NC])
+    {
+        const int whole = K / KS, sw = s1 < whole ? s1 : whole;
+        int s = s0;
+        if (s + D <= sw) {
+#pragma unroll
+            for (int j = 0; j < D; ++j) load(j, wbase, woff, xbase, xoff, xok, xplane, s + j);
+            for (; s + 2 * D <= sw; s += D) {
+#pragma unroll
+                for (int j = 0; j < D; ++j) {
+                    mma(j, acc);
+                    load(j, wbase, woff, xbase, xoff, xok, xplane, s + D + j);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < D; ++j) mma(j, acc);
+            s += D;
+        }
+        // (fewer than D whole steps left: the clamped ones are loaded for nothing)
+        if (s < sw) {
+#pragma unroll
+            for (int j = 0; j < D - 1; ++j) load(j, wbase, woff, xbase, xoff, xok, xplane, s + j < sw ? s + j : sw - 1);
+#pragma unroll
+            for (int j = 0; j < D - 1; ++j)
+                if (s + j < sw) mma(j, acc);
+        }
+        if (s0 < s1 && s1 > whole) {
+            load_tail(wbase, woff, xbase, xoff, xok, xplane, whole, K, g);
+            mma(0, acc);
+        }
+    }
+    __device__ __forceinline__ void run_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
+                                            const bool (&xok)[NC], int64_t xplane, int align_x, int s0, int s1, int K,
+                                            int g, f32x4 (&acc)[RB][NC])
+    {
+        for (int s = s0; s < s1; ++s) {
+            load_any(wrow, align_w, xrow, xok, xplane, align_x, s, K, g);
+            mma(0, acc);
+        }
+    }
+};
+
+// (the same item in every lane)
+__device__ __forceinline__ MoeItem uniform_item(const MoeItem &it)
+{
+    return MoeItem{__builtin_amdgcn_readfirstlane(it.expert), __builtin_amdgcn_readfirstlane(it.first),
+                   __builtin_amdgcn_readfirstlane(it.count), 0};
 }
 
 // The waves' partial sums of chunk c, added in order by the first 64 threads:
@@ -297,43 +396,63 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
     }
 }
 
-// z of 16 inner columns: gate rows i0 .. i0 + 15 and the up rows of the same
-// columns, for tokens base .. base + 16 NC - 1 of the expert's pairs.
-template <bool CODES, bool VEC, int NC, bool MANY>
-__device__ __forceinline__ void moe_gate_up_tokens(const MoeArgs &a, const MoeItem &it, int i0, int base,
-                                                   f32x4 (&red)[kMoeWaves][2][64])
+// z of 16 inner columns for the tokens of one work item (at most 16 NC): gate
+// rows i0 .. i0 + 15 and the up rows of the same columns.  Up to 80 registers
+// per lane let three workgroups share a CU; codes (whose steps are twice as
+// deep) and two chunks of tokens need 128, for two.
+constexpr int gate_up_occupancy(bool codes, int nc) { return codes || nc > 1 ? 4 : 6; }
+template <bool CODES, bool VEC, int NC>
+__global__ void __launch_bounds__(kMoeThreads, gate_up_occupancy(CODES, NC)) k_moe_gate_up(MoeArgs a)
 {
+    __shared__ f32x4 red[kMoeWaves][2][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int strips = (int)(a.ldz / 16), ordinal = blockIdx.x / strips;
+    if (ordinal >= *a.n_items) return;
+    const MoeItem it = uniform_item(a.items[ordinal]);
+    const int i0 = (blockIdx.x - ordinal * strips) * 16;
     constexpr int EB = CODES ? 1 : 2;
     const char *W = (const char *)a.Wgu + (int64_t)it.expert * a.strideGu * EB;
-    const bool wok[2] = {i0 + li < a.I, i0 + li < a.I};
-    const int64_t row = wok[0] ? i0 + li : 0;
-    const void *const wrow[2] = {W + row * a.ldgu * EB, W + (a.I + row) * a.ldgu * EB};
+    const bool wok = i0 + li < a.I;
+    const int64_t row = wok ? i0 + li : 0;
+    const char *const wrow[2] = {W + row * a.ldgu * EB, W + (a.I + row) * a.ldgu * EB};
     const uint16_t *xrow[NC];
     bool xok[NC];
     int pair[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        xok[c] = base + 16 * c + li < it.count;
-        pair[c] = xok[c] ? a.pairs[it.first + base + 16 * c + li] : 0;
+        xok[c] = 16 * c + li < it.count;
+        pair[c] = xok[c] ? a.pairs[it.first + 16 * c + li] : 0;
         xrow[c] = a.X + (int64_t)(pair[c] / a.topk) * a.ldx;
     }
     f32x4 acc[2][NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_stream<CODES, 1, 2, NC, kMoeWaves, moe_occupancy(CODES, MANY) == 6 ? 48 : 64, VEC>(wrow, wok, a.align_gu, xrow, xok, 0, a.align_x, a.H, wave, g, acc);
+    constexpr int KS = kStep<CODES>, D = CODES && NC > 1 ? 1 : 2;        // steps in flight
+    const int K = (int)a.H, steps = (K + KS - 1) / KS;
+    const int s0 = steps * wave / kMoeWaves, s1 = steps * (wave + 1) / kMoeWaves;
+    MoeStream<CODES, 2, NC, 1, D> b;
+    if constexpr (VEC) {
+        // (a block's rows, and all token rows, lie within 2 GiB of their first)
+        const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
+        const uint32_t woff = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g;
+        uint32_t xoff[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) xoff[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
+        b.run(wbase, woff, (const char *)a.X, xoff, xok, 0, s0, s1, K, g, acc);
+    } else {
+        b.run_any(wrow, a.align_gu, xrow, xok, 0, a.align_x, s0, s1, K, g, acc);
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        if (base + 16 * c >= it.count) break;       // uniform
+        if (16 * c >= it.count) break;       // uniform
         f32x4 s[2];
         moe_join<NC>(red, acc, c, s);
         if (wave == 0 && xok[c]) {
             const int64_t p = pair[c], i = i0 + 4 * g;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (i + q >= a.I) break;
-                float gt = s[0][q], up = s[1][q];
-                if (a.scale_gu) {
+                float gt = s[0][q], up = s[1][q];       // (past I: zeros, so z's rows end in zeros)
+                if (a.scale_gu && i + q < a.I) {
                     const float *sc = a.scale_gu + (int64_t)it.expert * 2 * a.I;
                     gt *= sc[i + q];
                     up *= sc[a.I + i + q];
@@ -349,81 +468,53 @@ __device__ __forceinline__ void moe_gate_up_tokens(const MoeArgs &a, const MoeIt
     }
 }
 
-// MANY: an expert may have more than 16 tokens (T > 16), taken 32 at a time
-// (the weights come from the caches after the first).
-template <bool CODES, bool VEC, bool MANY>
-__global__ void __launch_bounds__(kMoeThreads, moe_occupancy(CODES, MANY)) k_moe_gate_up(MoeArgs a)
-{
-    __shared__ f32x4 red[kMoeWaves][2][64];
-    const int strips = (int)((a.I + 15) / 16), ordinal = blockIdx.x / strips;
-    if (ordinal >= *a.chosen) return;
-    const MoeItem it = a.items[ordinal];
-    const int i0 = (blockIdx.x - ordinal * strips) * 16;
-    if constexpr (!MANY) {
-        moe_gate_up_tokens<CODES, VEC, 1, MANY>(a, it, i0, 0, red);
-    } else {
-        for (int base = 0; base < it.count; base += 32) {
-            if (it.count - base <= 16) moe_gate_up_tokens<CODES, VEC, 1, MANY>(a, it, i0, base, red);
-            else moe_gate_up_tokens<CODES, VEC, 2, MANY>(a, it, i0, base, red);
-        }
-    }
-}
-
 // The down rows.  A workgroup owns `cols` (at most 16) hidden columns for
 // every expert, so a token's slots meet in its LDS and nothing else is joined:
-// its sixteen waves take pieces (expert, half of K) one after the other, the
-// next free one each, and leave each pair's sums in the piece's own places.
-// The order in which pieces are taken does not matter; the halves and the
-// slots are added in order.
-constexpr int kDownWaves = 16, kDownSlices = 2;
-template <bool CODES, bool VEC, int NC, bool MANY>
-__device__ __forceinline__ void moe_down_tokens(const MoeArgs &a, const MoeItem &it, int n0, int slice, int base,
-                                                float (&part)[kDownSlices][kMoeMaxPairs][16])
-{
-    const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
-    constexpr int EB = CODES ? 1 : 2;
-    const char *W = (const char *)a.Wd + (int64_t)it.expert * a.strideD * EB;
-    const bool wok[1] = {li < a.cols && n0 + li < a.H};
-    const void *const wrow[1] = {W + (wok[0] ? n0 + li : 0) * a.ldd * EB};
-    const uint16_t *zrow[NC];
-    bool zok[NC];
-    int pair[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        zok[c] = base + 16 * c + li < it.count;
-        pair[c] = zok[c] ? a.pairs[it.first + base + 16 * c + li] : 0;
-        zrow[c] = a.z + (int64_t)pair[c] * a.ldz;
-    }
-    f32x4 acc[1][NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    moe_stream<CODES, 2, 1, NC, kDownSlices, MANY ? 64 : CODES ? 80 : 96, VEC>(wrow, wok, a.align_d, zrow, zok, a.zplane, 16, a.I,
-                                                                  slice, g, acc);
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-        if (zok[c]) *(f32x4 *)&part[slice][pair[c]][4 * g] = acc[0][c];
-}
-
-template <bool CODES, bool VEC, bool MANY>
+// its sixteen waves take pieces (work item, half of K) one after the other,
+// the next free one each, and leave each pair's sums in the piece's own
+// places.  The order in which pieces are taken does not matter; the halves and
+// the slots are added in order.
+constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
+// A piece has 16 tokens at most: a work item's SUB chunks are pieces of their
+// own (z's two planes leave no registers for more).
+template <bool CODES, bool VEC, int SUB>
 __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 {
+    constexpr int EB = CODES ? 1 : 2, KS = kStep<CODES>;
+    constexpr int D = CODES ? 2 : 3;       // steps in flight
     __shared__ __attribute__((aligned(16))) float part[kDownSlices][kMoeMaxPairs][16];
-    __shared__ int next;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = blockIdx.x * a.cols;
+    __shared__ MoeItem items[kMoeMaxItems];
+    __shared__ int pairs[kMoeMaxPairs], next;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int n0 = blockIdx.x * a.cols, K = (int)a.I;
+    const int n_items = *a.n_items;
+    for (int i = threadIdx.x; i < n_items; i += kDownWaves * 64) items[i] = a.items[i];
+    for (int i = threadIdx.x; i < (int)a.T * a.topk; i += kDownWaves * 64) pairs[i] = a.pairs[i];
     if (threadIdx.x == 0) next = kDownWaves;
     __syncthreads();
-    const int pieces = *a.chosen * kDownSlices;
+
+    const int pieces = n_items * (kDownSlices * SUB), steps = (K + KS - 1) / KS;
+    const bool wok = li < a.cols && n0 + li < (int)a.H;
+    const int64_t wlane = (int64_t)(wok ? li : 0) * a.ldd * EB;
+    const uint32_t woff = (uint32_t)wlane + 16 * g;
+    MoeStream<CODES, 1, 1, 2, D> b;
     for (int piece = wave; piece < pieces;) {
-        const MoeItem it = a.items[piece / kDownSlices];
-        const int slice = piece % kDownSlices;
-        if constexpr (!MANY) {
-            moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, slice, 0, part);
+        const MoeItem it = uniform_item(items[piece / (kDownSlices * SUB)]);
+        const int slice = piece % kDownSlices, from = piece / kDownSlices % SUB * 16;
+        const int s0 = steps * slice / kDownSlices, s1 = from < it.count ? steps * (slice + 1) / kDownSlices : s0;
+        const char *const wbase[1] = {(const char *)a.Wd + ((int64_t)it.expert * a.strideD + (int64_t)n0 * a.ldd) * EB};
+        const bool zok[1] = {from + li < it.count};
+        const int pair = zok[0] ? pairs[it.first + from + li] : 0;
+        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+        if constexpr (VEC) {
+            const uint32_t zoff[1] = {(uint32_t)pair * (uint32_t)(a.ldz * 2) + x_lane<CODES>(g)};
+            b.run(wbase, woff, (const char *)a.z, zoff, zok, a.zplane, s0, s1, K, g, acc);
         } else {
-            for (int base = 0; base < it.count; base += 32) {
-                if (it.count - base <= 16) moe_down_tokens<CODES, VEC, 1, MANY>(a, it, n0, slice, base, part);
-                else moe_down_tokens<CODES, VEC, 2, MANY>(a, it, n0, slice, base, part);
-            }
+            const char *const wrow[1] = {wbase[0] + wlane};
+            const uint16_t *const zrow[1] = {a.z + (int64_t)pair * a.ldz};
+            b.run_any(wrow, a.align_d, zrow, zok, a.zplane, 16, s0, s1, K, g, acc);
         }
+        if (zok[0]) *(f32x4 *)&part[slice][pair][4 * g] = acc[0][0];
         int p = 0;
         if (lane == 0) p = atomicAdd(&next, 1);
         piece = __builtin_amdgcn_readfirstlane(p);
@@ -447,26 +538,26 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 
 }  // namespace
 
-template <bool CODES, bool MANY>
+template <bool CODES, int NC>
 static hipError_t launch_moe_weights(const MoeArgs &a, bool vec_gu, bool vec_d, hipStream_t s)
 {
-    const int64_t chosen = a.E < a.T * a.topk ? a.E : a.T * a.topk;   // experts at most
-    const dim3 gg((unsigned)(chosen * ((a.I + 15) / 16))), gd((unsigned)((a.H + a.cols - 1) / a.cols));
-    const dim3 b(kMoeThreads), bd(kDownWaves * 64);
+    const dim3 gg((unsigned)(moe_items(a.T, a.E, a.topk) * (a.ldz / 16)));
+    const dim3 gd((unsigned)((a.H + a.cols - 1) / a.cols)), bg(kMoeThreads), bd(kDownWaves * 64);
     if (a.I > 0) {      // (no inner columns: the down kernel's sums are empty)
-        if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, MANY>), gg, b, 0, s, a);
-        else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, MANY>), gg, b, 0, s, a);
+        if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, NC>), gg, bg, 0, s, a);
+        else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, NC>), gg, bg, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, MANY>), gd, bd, 0, s, a);
-    else hipLaunchKernelGGL((k_moe_down<CODES, false, MANY>), gd, bd, 0, s, a);
+    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, NC>), gd, bd, 0, s, a);
+    else hipLaunchKernelGGL((k_moe_down<CODES, false, NC>), gd, bd, 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, hipStream_t s)
 {
     MoeArgs a = args;
+    a.chunk = moe_chunk(a.T);
     // hidden columns per workgroup of the down kernel: as many workgroups as
     // the 256 CUs, 16 columns at most and 4 at least
     a.cols = a.H > 2048 ? 16 : a.H > 1024 ? 8 : 4;
@@ -477,11 +568,9 @@ hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, 
     else hipLaunchKernelGGL((k_moe_route<kMoeMaxExperts / 64>), rg, rb, 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.H == 0) return e;
-    if (a.T > 16)
-        return codes ? launch_moe_weights<true, true>(a, vec_gu, vec_d, s)
-                     : launch_moe_weights<false, true>(a, vec_gu, vec_d, s);
-    return codes ? launch_moe_weights<true, false>(a, vec_gu, vec_d, s)
-                 : launch_moe_weights<false, false>(a, vec_gu, vec_d, s);
+    if (a.chunk > 16)
+        return codes ? launch_moe_weights<true, 2>(a, vec_gu, vec_d, s) : launch_moe_weights<false, 2>(a, vec_gu, vec_d, s);
+    return codes ? launch_moe_weights<true, 1>(a, vec_gu, vec_d, s) : launch_moe_weights<false, 1>(a, vec_gu, vec_d, s);
 }
 
 }  // namespace g5

@@ -155,8 +155,8 @@ def test_moe_workspace_size():
     assert f(0, 64, 32, 8, 2, ctypes.byref(n)) == OK and n.value == 0
     assert f(4, 64, 32, 8, 2, ctypes.byref(n)) == OK
     # routing (2 x 8 words), the number of experts, 8 of them, 8 pairs, z in
-    # two planes of 8 x 32 bf16
-    assert n.value == CR + 256 + 256 + 256 + 256 + 256 + 1024
+    # two planes of 8 x 128 bf16
+    assert n.value == CR + 256 + 256 + 256 + 256 + 256 + 4096
     assert f(65, 64, 32, 8, 2, ctypes.byref(n)) == INV and f(4, 64, 32, 8, 9, ctypes.byref(n)) == INV
     assert moe(T=0, X=None, L=None) == OK
 
