@@ -25,7 +25,7 @@ namespace g5 {
 
 namespace {
 
-constexpr int kMoeWaves = 8;
+constexpr int kMoeWaves = 4;
 constexpr int kMoeThreads = kMoeWaves * 64;
 
 template <int CTRL, int ROWS>
@@ -222,42 +222,40 @@ __device__ __forceinline__ uint32_t x_lane(int g)
     return (CODES ? 32u : 16u) * g;
 }
 
-// D steps of RB weight rows and of NC token rows in PL planes in registers,
-// and their products: step s in place j is multiplied and step s + D loaded
+// D steps of RB weight rows and of NC token rows in registers, and their
+// products: step s in place j is multiplied and step s + D loaded
 // over it, so D steps stay in flight.
-template <bool CODES, int RB, int NC, int PL, int D>
+template <bool CODES, int RB, int NC, int D>
 struct MoeStream {
     static constexpr int XP = kPieces<CODES>, KS = kStep<CODES>;
-    u32x4 w[D][RB][2], x[D][NC][PL][XP];
+    u32x4 w[D][RB][2], x[D][NC][XP];
 
     // Whole step s of 16-byte aligned rows: wave-uniform bases and the lane's
     // byte offsets (its row and 16 g).  A lane without a token leaves its x
     // as it is (its column of the product is never read).
-    __device__ __forceinline__ void load(int j, const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
-                                         const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s)
+    __device__ __forceinline__ void load_w(int j, const char *const (&wbase)[RB], uint32_t woff, int s)
     {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 w[j][r][h] = __builtin_nontemporal_load((const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff));
+    }
+    __device__ __forceinline__ void load_x(int j, const char *xbase, const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s)
+    {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (xok[c]) {
 #pragma unroll
-                for (int pl = 0; pl < PL; ++pl)
-#pragma unroll
-                    for (int q = 0; q < XP; ++q)
-                        x[j][c][pl][q] =
-                            *(const u32x4 *)((xbase + (pl * xplane + (int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
+                for (int q = 0; q < XP; ++q)
+                    x[j][c][q] = *(const u32x4 *)((xbase + ((int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
             }
     }
 
     // The last, partial step (K a whole number of 16-byte pieces): pieces
     // past K are zeros.
     __device__ __forceinline__ void load_tail(const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
-                                              const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s,
-                                              int K, int g)
+                                              const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s, int K, int g)
     {
         const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -270,20 +268,15 @@ struct MoeStream {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int pl = 0; pl < PL; ++pl)
-#pragma unroll
-                for (int q = 0; q < XP; ++q) {
-                    const int col = s * KS + x_piece<CODES>(q, g);
-                    x[0][c][pl][q] = xok[c] && col < K
-                                         ? *(const u32x4 *)((xbase + pl * xplane * 2) +
-                                                            (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0))))
-                                         : zero;
-                }
+            for (int q = 0; q < XP; ++q)
+                x[0][c][q] = xok[c] && s * KS + x_piece<CODES>(q, g) < K
+                                 ? *(const u32x4 *)(xbase + (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0))))
+                                 : zero;
     }
 
     // Step s of rows of any alignment, zero-filled past K.
     __device__ __forceinline__ void load_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                             const bool (&xok)[NC], int64_t xplane, int align_x, int s, int K, int g)
+                                             const bool (&xok)[NC], int align_x, int s, int K, int g)
     {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
@@ -297,10 +290,8 @@ struct MoeStream {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int pl = 0; pl < PL; ++pl)
-#pragma unroll
-                for (int q = 0; q < XP; ++q)
-                    x[0][c][pl][q] = load_chunk8_bf16(xrow[c] + pl * xplane, s * KS + x_piece<CODES>(q, g), K, xok[c], align_x);
+            for (int q = 0; q < XP; ++q)
+                x[0][c][q] = load_chunk8_bf16(xrow[c], s * KS + x_piece<CODES>(q, g), K, xok[c], align_x);
     }
 
     __device__ __forceinline__ void mma(int j, f32x4 (&acc)[RB][NC]) const
@@ -315,54 +306,70 @@ struct MoeStream {
                 for (int q = 0; q < XP / 2; ++q)
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int pl = 0; pl < PL; ++pl)
-                            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, b[q]),
-                                __builtin_bit_cast(bf16x8, x[j][c][pl][h * (XP / 2) + q]), acc[r][c], 0, 0, 0);
+                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8, b[q]), __builtin_bit_cast(bf16x8, x[j][c][h * (XP / 2) + q]),
+                            acc[r][c], 0, 0, 0);
             }
     }
 
     // Steps s0 .. s1 - 1 of K (the last may be partial), 16-byte aligned.
-    __device__ __forceinline__ void run(const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
-                                        const uint32_t (&xoff)[NC], const bool (&xok)[NC], int64_t xplane, int s0, int s1,
-                                        int K, int g, f32x4 (&acc)[RB][NC])
+    // tokens(xoff, xok) gives the lane's token rows, asked for when the first
+    // weights are on their way.
+    template <class F>
+    __device__ __forceinline__ void run(const char *const (&wbase)[RB], uint32_t woff, const char *xbase, F tokens, int s0,
+                                        int s1, int K, int g, f32x4 (&acc)[RB][NC])
     {
         const int whole = K / KS, sw = s1 < whole ? s1 : whole;
+        uint32_t xoff[NC];
+        bool xok[NC];
         int s = s0;
         if (s + D <= sw) {
 #pragma unroll
-            for (int j = 0; j < D; ++j) load(j, wbase, woff, xbase, xoff, xok, xplane, s + j);
+            for (int j = 0; j < D; ++j) load_w(j, wbase, woff, s + j);
+            tokens(xoff, xok);
+#pragma unroll
+            for (int j = 0; j < D; ++j) load_x(j, xbase, xoff, xok, s + j);
             for (; s + 2 * D <= sw; s += D) {
 #pragma unroll
                 for (int j = 0; j < D; ++j) {
                     mma(j, acc);
-                    load(j, wbase, woff, xbase, xoff, xok, xplane, s + D + j);
+                    load_w(j, wbase, woff, s + D + j);
+                    load_x(j, xbase, xoff, xok, s + D + j);
                 }
             }
+            // the last whole group, and behind it the fewer than D steps left
 #pragma unroll
-            for (int j = 0; j < D; ++j) mma(j, acc);
+            for (int j = 0; j < D; ++j) {
+                mma(j, acc);
+                if (j < D - 1 && s + D + j < sw) {
+                    load_w(j, wbase, woff, s + D + j);
+                    load_x(j, xbase, xoff, xok, s + D + j);
+                }
+            }
             s += D;
-        }
-        // (fewer than D whole steps left: the clamped ones are loaded for nothing)
-        if (s < sw) {
-#pragma unroll
-            for (int j = 0; j < D - 1; ++j) load(j, wbase, woff, xbase, xoff, xok, xplane, s + j < sw ? s + j : sw - 1);
+        } else {
+            tokens(xoff, xok);
 #pragma unroll
             for (int j = 0; j < D - 1; ++j)
-                if (s + j < sw) mma(j, acc);
+                if (s + j < sw) {
+                    load_w(j, wbase, woff, s + j);
+                    load_x(j, xbase, xoff, xok, s + j);
+                }
         }
+#pragma unroll
+        for (int j = 0; j < D - 1; ++j)
+            if (s + j < sw) mma(j, acc);
         if (s0 < s1 && s1 > whole) {
-            load_tail(wbase, woff, xbase, xoff, xok, xplane, whole, K, g);
+            load_tail(wbase, woff, xbase, xoff, xok, whole, K, g);
             mma(0, acc);
         }
     }
     __device__ __forceinline__ void run_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                            const bool (&xok)[NC], int64_t xplane, int align_x, int s0, int s1, int K,
-                                            int g, f32x4 (&acc)[RB][NC])
+                                            const bool (&xok)[NC], int align_x, int s0, int s1, int K, int g,
+                                            f32x4 (&acc)[RB][NC])
     {
         for (int s = s0; s < s1; ++s) {
-            load_any(wrow, align_w, xrow, xok, xplane, align_x, s, K, g);
+            load_any(wrow, align_w, xrow, xok, align_x, s, K, g);
             mma(0, acc);
         }
     }
@@ -397,50 +404,50 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
 }
 
 // z of 16 inner columns for the tokens of one work item (at most 16 NC): gate
-// rows i0 .. i0 + 15 and the up rows of the same columns.  Up to 80 registers
-// per lane let three workgroups share a CU; codes (whose steps are twice as
-// deep) and two chunks of tokens need 128, for two.
-constexpr int gate_up_occupancy(bool codes, int nc) { return codes || nc > 1 ? 4 : 6; }
-template <bool CODES, bool VEC, int NC>
-__global__ void __launch_bounds__(kMoeThreads, gate_up_occupancy(CODES, NC)) k_moe_gate_up(MoeArgs a)
+// rows i0 .. i0 + 15 and the up rows of the same columns.
+template <bool CODES, bool VEC, int NC, int D>
+__device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it, int i0,
+                                            f32x4 (&red)[kMoeWaves][2][64])
 {
-    __shared__ f32x4 red[kMoeWaves][2][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
-    const int strips = (int)(a.ldz / 16), ordinal = blockIdx.x / strips;
-    if (ordinal >= *a.n_items) return;
-    const MoeItem it = uniform_item(a.items[ordinal]);
-    const int i0 = (blockIdx.x - ordinal * strips) * 16;
-    constexpr int EB = CODES ? 1 : 2;
+    constexpr int EB = CODES ? 1 : 2, KS = kStep<CODES>;
     const char *W = (const char *)a.Wgu + (int64_t)it.expert * a.strideGu * EB;
     const bool wok = i0 + li < a.I;
-    const int64_t row = wok ? i0 + li : 0;
-    const char *const wrow[2] = {W + row * a.ldgu * EB, W + (a.I + row) * a.ldgu * EB};
-    const uint16_t *xrow[NC];
     bool xok[NC];
     int pair[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         xok[c] = 16 * c + li < it.count;
         pair[c] = xok[c] ? a.pairs[it.first + 16 * c + li] : 0;
-        xrow[c] = a.X + (int64_t)(pair[c] / a.topk) * a.ldx;
     }
     f32x4 acc[2][NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int KS = kStep<CODES>, D = CODES && NC > 1 ? 1 : 2;        // steps in flight
     const int K = (int)a.H, steps = (K + KS - 1) / KS;
     const int s0 = steps * wave / kMoeWaves, s1 = steps * (wave + 1) / kMoeWaves;
-    MoeStream<CODES, 2, NC, 1, D> b;
-    if constexpr (VEC) {
+    MoeStream<CODES, 2, NC, D> b;
+    // (a row past I repeats the block's first and is not stored; whole blocks
+    // past I only fill z's rows with zeros)
+    if (i0 >= a.I) {
+    } else if constexpr (VEC) {
         // (a block's rows, and all token rows, lie within 2 GiB of their first)
         const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
         const uint32_t woff = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g;
-        uint32_t xoff[NC];
+        auto tokens = [&](uint32_t (&off)[NC], bool (&ok)[NC]) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) xoff[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
-        b.run(wbase, woff, (const char *)a.X, xoff, xok, 0, s0, s1, K, g, acc);
+            for (int c = 0; c < NC; ++c) {
+                ok[c] = xok[c];
+                off[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
+            }
+        };
+        b.run(wbase, woff, (const char *)a.X, tokens, s0, s1, K, g, acc);
     } else {
-        b.run_any(wrow, a.align_gu, xrow, xok, 0, a.align_x, s0, s1, K, g, acc);
+        const int64_t row = wok ? i0 + li : i0;
+        const char *const wrow[2] = {W + row * a.ldgu * EB, W + (a.I + row) * a.ldgu * EB};
+        const uint16_t *xrow[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) xrow[c] = a.X + (int64_t)(pair[c] / a.topk) * a.ldx;
+        b.run_any(wrow, a.align_gu, xrow, xok, a.align_x, s0, s1, K, g, acc);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -451,8 +458,9 @@ __global__ void __launch_bounds__(kMoeThreads, gate_up_occupancy(CODES, NC)) k_m
             const int64_t p = pair[c], i = i0 + 4 * g;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                float gt = s[0][q], up = s[1][q];       // (past I: zeros, so z's rows end in zeros)
-                if (a.scale_gu && i + q < a.I) {
+                float gt = s[0][q], up = s[1][q];
+                if (i + q >= a.I) gt = up = 0.f;        // z's rows end in zeros
+                else if (a.scale_gu) {
                     const float *sc = a.scale_gu + (int64_t)it.expert * 2 * a.I;
                     gt *= sc[i + q];
                     up *= sc[a.I + i + q];
@@ -468,6 +476,20 @@ __global__ void __launch_bounds__(kMoeThreads, gate_up_occupancy(CODES, NC)) k_m
     }
 }
 
+// (128 registers per lane: four workgroups per CU; MANY: items of up to 32
+// tokens)
+template <bool CODES, bool VEC, bool MANY>
+__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
+{
+    __shared__ f32x4 red[kMoeWaves][2][64];
+    const int strips = (int)(a.ldz / 16), ordinal = blockIdx.x / strips;
+    if (ordinal >= *a.n_items) return;
+    const MoeItem it = uniform_item(a.items[ordinal]);
+    const int i0 = (blockIdx.x - ordinal * strips) * 16;
+    if (MANY && it.count > 16) moe_gate_up<CODES, VEC, 2, CODES ? 1 : 2>(a, it, i0, red);
+    else moe_gate_up<CODES, VEC, 1, CODES ? 2 : 3>(a, it, i0, red);
+}
+
 // The down rows.  A workgroup owns `cols` (at most 16) hidden columns for
 // every expert, so a token's slots meet in its LDS and nothing else is joined:
 // its sixteen waves take pieces (work item, half of K) one after the other,
@@ -475,46 +497,74 @@ __global__ void __launch_bounds__(kMoeThreads, gate_up_occupancy(CODES, NC)) k_m
 // places.  The order in which pieces are taken does not matter; the halves and
 // the slots are added in order.
 constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
+// A piece's products for its tokens, 8 to a block of the matrix core's 16
+// columns: columns 0 .. 7 take z's hi parts, 8 .. 15 the lo parts, and the two
+// sums are added at the end.
+template <bool CODES, bool VEC, int NB, int D>
+__device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, int from, int slice, int n0,
+                                         const int *pairs, float (&part)[kDownSlices][kMoeMaxPairs][16])
+{
+    constexpr int EB = CODES ? 1 : 2, KS = kStep<CODES>;
+    const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+    const int K = (int)a.I, steps = (K + KS - 1) / KS;
+    const int s0 = steps * slice / kDownSlices, s1 = steps * (slice + 1) / kDownSlices;
+    const char *const wbase[1] = {(const char *)a.Wd + ((int64_t)it.expert * a.strideD + (int64_t)n0 * a.ldd) * EB};
+    const int wrow = li < a.cols && n0 + li < (int)a.H ? li : 0;
+    bool zok[NB];
+    int pair[NB];
+    f32x4 acc[1][NB];
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        const int i = from + 8 * c + (li & 7);
+        zok[c] = i < it.count;
+        pair[c] = zok[c] ? pairs[it.first + i] : 0;
+        acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    MoeStream<CODES, 1, NB, D> b;
+    if constexpr (VEC) {
+        auto tokens = [&](uint32_t (&off)[NB], bool (&ok)[NB]) {
+#pragma unroll
+            for (int c = 0; c < NB; ++c) {
+                ok[c] = zok[c];
+                off[c] = 2 * ((uint32_t)pair[c] * (uint32_t)a.ldz + (li < 8 ? 0u : (uint32_t)a.zplane)) + x_lane<CODES>(g);
+            }
+        };
+        b.run(wbase, (uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g, (const char *)a.z, tokens, s0, s1, K, g, acc);
+    } else {
+        const char *const wlane[1] = {wbase[0] + (int64_t)wrow * a.ldd * EB};
+        const uint16_t *zrow[NB];
+#pragma unroll
+        for (int c = 0; c < NB; ++c) zrow[c] = a.z + (int64_t)pair[c] * a.ldz + (li < 8 ? 0 : a.zplane);
+        b.run_any(wlane, a.align_d, zrow, zok, 16, s0, s1, K, g, acc);
+    }
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        f32x4 v = acc[0][c];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8, 64);
+        if (zok[c] && li < 8) *(f32x4 *)&part[slice][pair[c]][4 * g] = v;
+    }
+}
+
 // A piece has 16 tokens at most: a work item's SUB chunks are pieces of their
-// own (z's two planes leave no registers for more).
+// own.
 template <bool CODES, bool VEC, int SUB>
 __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 {
-    constexpr int EB = CODES ? 1 : 2, KS = kStep<CODES>;
-    constexpr int D = CODES ? 2 : 3;       // steps in flight
     __shared__ __attribute__((aligned(16))) float part[kDownSlices][kMoeMaxPairs][16];
     __shared__ MoeItem items[kMoeMaxItems];
     __shared__ int pairs[kMoeMaxPairs], next;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
-    const int n0 = blockIdx.x * a.cols, K = (int)a.I;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = blockIdx.x * a.cols;
     const int n_items = *a.n_items;
     for (int i = threadIdx.x; i < n_items; i += kDownWaves * 64) items[i] = a.items[i];
     for (int i = threadIdx.x; i < (int)a.T * a.topk; i += kDownWaves * 64) pairs[i] = a.pairs[i];
     if (threadIdx.x == 0) next = kDownWaves;
     __syncthreads();
-
-    const int pieces = n_items * (kDownSlices * SUB), steps = (K + KS - 1) / KS;
-    const bool wok = li < a.cols && n0 + li < (int)a.H;
-    const int64_t wlane = (int64_t)(wok ? li : 0) * a.ldd * EB;
-    const uint32_t woff = (uint32_t)wlane + 16 * g;
-    MoeStream<CODES, 1, 1, 2, D> b;
-    for (int piece = wave; piece < pieces;) {
+    for (int piece = wave; piece < n_items * (kDownSlices * SUB);) {
         const MoeItem it = uniform_item(items[piece / (kDownSlices * SUB)]);
         const int slice = piece % kDownSlices, from = piece / kDownSlices % SUB * 16;
-        const int s0 = steps * slice / kDownSlices, s1 = from < it.count ? steps * (slice + 1) / kDownSlices : s0;
-        const char *const wbase[1] = {(const char *)a.Wd + ((int64_t)it.expert * a.strideD + (int64_t)n0 * a.ldd) * EB};
-        const bool zok[1] = {from + li < it.count};
-        const int pair = zok[0] ? pairs[it.first + from + li] : 0;
-        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
-        if constexpr (VEC) {
-            const uint32_t zoff[1] = {(uint32_t)pair * (uint32_t)(a.ldz * 2) + x_lane<CODES>(g)};
-            b.run(wbase, woff, (const char *)a.z, zoff, zok, a.zplane, s0, s1, K, g, acc);
-        } else {
-            const char *const wrow[1] = {wbase[0] + wlane};
-            const uint16_t *const zrow[1] = {a.z + (int64_t)pair * a.ldz};
-            b.run_any(wrow, a.align_d, zrow, zok, a.zplane, 16, s0, s1, K, g, acc);
-        }
-        if (zok[0]) *(f32x4 *)&part[slice][pair][4 * g] = acc[0][0];
+        if (it.count - from > 8) moe_down<CODES, VEC, 2, CODES ? 2 : 3>(a, it, from, slice, n0, pairs, part);
+        else if (it.count > from) moe_down<CODES, VEC, 1, CODES ? 3 : 5>(a, it, from, slice, n0, pairs, part);
         int p = 0;
         if (lane == 0) p = atomicAdd(&next, 1);
         piece = __builtin_amdgcn_readfirstlane(p);
@@ -538,19 +588,19 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 
 }  // namespace
 
-template <bool CODES, int NC>
+template <bool CODES, bool MANY>
 static hipError_t launch_moe_weights(const MoeArgs &a, bool vec_gu, bool vec_d, hipStream_t s)
 {
     const dim3 gg((unsigned)(moe_items(a.T, a.E, a.topk) * (a.ldz / 16)));
     const dim3 gd((unsigned)((a.H + a.cols - 1) / a.cols)), bg(kMoeThreads), bd(kDownWaves * 64);
     if (a.I > 0) {      // (no inner columns: the down kernel's sums are empty)
-        if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, NC>), gg, bg, 0, s, a);
-        else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, NC>), gg, bg, 0, s, a);
+        if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, MANY>), gg, bg, 0, s, a);
+        else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, MANY>), gg, bg, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, NC>), gd, bd, 0, s, a);
-    else hipLaunchKernelGGL((k_moe_down<CODES, false, NC>), gd, bd, 0, s, a);
+    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, MANY ? 2 : 1>), gd, bd, 0, s, a);
+    else hipLaunchKernelGGL((k_moe_down<CODES, false, MANY ? 2 : 1>), gd, bd, 0, s, a);
     return hipGetLastError();
 }
 
@@ -569,8 +619,10 @@ hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.H == 0) return e;
     if (a.chunk > 16)
-        return codes ? launch_moe_weights<true, 2>(a, vec_gu, vec_d, s) : launch_moe_weights<false, 2>(a, vec_gu, vec_d, s);
-    return codes ? launch_moe_weights<true, 1>(a, vec_gu, vec_d, s) : launch_moe_weights<false, 1>(a, vec_gu, vec_d, s);
+        return codes ? launch_moe_weights<true, true>(a, vec_gu, vec_d, s)
+                     : launch_moe_weights<false, true>(a, vec_gu, vec_d, s);
+    return codes ? launch_moe_weights<true, false>(a, vec_gu, vec_d, s)
+                 : launch_moe_weights<false, false>(a, vec_gu, vec_d, s);
 }
 
 }  // namespace g5
