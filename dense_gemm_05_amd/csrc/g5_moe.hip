@@ -197,10 +197,11 @@ __device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
 
 // A step is a 128-byte line of every weight row, read in two pieces: lane
 // group g (of four) takes bytes 16 g .. 16 g + 15 of each half.  The halves
-// are loaded one right after the other: the bytes in flight exceed an XCD's
-// L2, so a line whose second half is asked for later is fetched again
-// (measured: 1.6 times the bytes with the halves a batch apart, 1.5 times
-// with a lane's 32 bytes next to each other).  Piece h meets the same elements
+// are loaded one right after the other and with ordinary loads: the bytes in
+// flight exceed an XCD's L2, so a line whose second half is asked for later
+// is fetched again (measured: 1.6 times the bytes with the halves a batch
+// apart), and loads marked non-temporal give it up sooner (16 tokens, down
+// rows: 170 us against 132).  Piece h meets the same elements
 // of the token's row (8 of bf16, or 16 codes in two products).
 template <bool CODES>
 constexpr int kStep = CODES ? 128 : 64;       // elements
@@ -239,7 +240,7 @@ struct MoeStream {
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[j][r][h] = __builtin_nontemporal_load((const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff));
+                w[j][r][h] = *(const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff);
     }
     __device__ __forceinline__ void load_x(int j, const char *xbase, const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s)
     {
