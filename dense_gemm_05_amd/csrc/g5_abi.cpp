@@ -760,21 +760,19 @@ int plan_for_call(const Problem &p, const void *ws, size_t ws_bytes, Plan &pl, W
     return GEMM_OK;
 }
 
-// The adapters' values v [splits, M, ranks] follow the product's own scratch.
-// K is cut into up to 4 slices of at least 512 (for M <= 16 by K alone, so a
-// row's result does not depend on the other rows; for more rows while the
-// grid stays within one workgroup per CU), and the adapters of a row block
-// are shared out while that grid has room.
-size_t lora_layout(const Problem &p, const WsLayout &L, LoraArgs &q, size_t *total)
+// The adapters' values v follow the product's own scratch.  For the small-M
+// kernel K is cut into up to 4 slices of at least 512 (by K alone, so a row's
+// result does not depend on the other rows); the adapters of a row block are
+// shared out while the grid stays within one workgroup per CU.
+size_t lora_layout(const Problem &p, const Plan &pl, const WsLayout &L, LoraArgs &q, size_t *total)
 {
-    const int64_t wgs = cdiv(p.M, 16) * cdiv(q.R, 16);
-    const int64_t room = kNumCU / wgs > 1 ? kNumCU / wgs : 1;
-    int64_t splits = p.K / 512 < 4 ? p.K / 512 : 4;
-    if (p.M > 16 && splits > room) splits = room;
-    q.splits = splits < 1 ? 1 : (int)splits;
+    const bool small = pl.config == CFG_DECODE_NT;
+    const int64_t room = kNumCU / (cdiv(p.M, 16) * cdiv(q.R, 16));
+    const int64_t splits = p.K / 512 < 4 ? p.K / 512 : 4;
+    q.splits = small && splits > 1 ? (int)splits : 1;
     int64_t turns = p.M < 16 ? p.M : 16;
     if (turns > q.L) turns = q.L;
-    if (turns > room) turns = room;
+    if (!small && turns > room) turns = room;
     q.turns = turns < 1 ? 1 : (int)turns;
     q.ranks = (int)((q.R + 7) / 8 * 8);
     const size_t at = L.total > kCounterBytes ? L.total : kCounterBytes;
@@ -797,9 +795,10 @@ int run(const Problem &p, void *stream, void *ws = nullptr, size_t ws_bytes = 0)
     if (p.lora && pl.config != CFG_ZERO) {
         lora = *p.lora;
         size_t need = 0;
-        const size_t at = lora_layout(p, L, lora, &need);
+        const size_t at = lora_layout(p, pl, L, lora, &need);
         if (!ws || need > ws_bytes) return GEMM_ERR_WORKSPACE;
-        lora.V = (float *)((char *)ws + at);
+        if (pl.config == CFG_DECODE_NT) lora.V = (float *)((char *)ws + at);
+        else lora.V2 = (uint16_t *)((char *)ws + at);
     }
     st = check_device();
     if (st != GEMM_OK) return st;
@@ -1505,7 +1504,7 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t
     if (st != GEMM_OK || !bytes || pl.config == g5::CFG_NONE || pl.config == g5::CFG_ZERO) return st;
     const g5::WsLayout W = g5::ws_layout(p, pl);
     size_t need = W.total;
-    if (p.lora) g5::lora_layout(p, W, q, &need);
+    if (p.lora) g5::lora_layout(p, pl, W, q, &need);
     *bytes = need;
     return GEMM_OK;
 }
@@ -1538,7 +1537,7 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
         if (in[2].hi > ((__int128)1 << 63) || in[3].hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
         q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB,
                          g5::row_alignment((uint64_t)A, lda, strideA, L, 2),
-                         g5::row_alignment((uint64_t)B, ldb, strideB, L, 2), 0, 0, 0, nullptr};
+                         g5::row_alignment((uint64_t)B, ldb, strideB, L, 2), 0, 0, 0, nullptr, nullptr};
         p.lora = &q;
     }
     if (some) {

@@ -199,7 +199,11 @@ struct LoraArgs {
     int align_a, align_b;        // byte alignments of the row starts
     int ranks;                   // R rounded up to 8: the row length of V
     int splits, turns;           // K slices of V; workgroups sharing a row block's adapters
-    float *V;                    // [splits, M, ranks] floats of scratch (rows without an adapter unused)
+    // scratch for the values v (rows without an adapter unused): FP32
+    // [splits, M, ranks] for the small-M kernel, else (V NULL, splits 1) two
+    // bf16 parts per row, [M, 2, ranks]
+    float *V;
+    uint16_t *V2;
 };
 hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s);
 // The product with v B^T joined: configs 256x192, 256x256, 128x128 (also

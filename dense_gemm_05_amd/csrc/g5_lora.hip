@@ -2,8 +2,8 @@
 //
 //   C[m] = X[m] Wt^T + s_a (X[m] A_a^T) B_a^T,   a = idx[m]
 //
-// in two launches: the low-rank values v[m] = s_a X[m] A_a^T (FP32, R per
-// row) into the workspace, then the product, whose kernels add v B_a^T to the
+// in two launches: the low-rank values v[m] = s_a X[m] A_a^T (R per row, in
+// FP32 or as two bf16 parts) into the workspace, then the product, whose kernels add v B_a^T to the
 // FP32 sums before they are rounded once.  An adapter adds 2 R (K + N) flops
 // and R (K + N) elements to a row's 2 N K: both are small beside the
 // projection, so the product's kernels stay as they are (the weight stream of
@@ -49,7 +49,14 @@ __device__ __forceinline__ void each_adapter(int a_row, F f)
 // q.turns-th adapter of its rows; its eight waves divide the slice, their sums
 // are added in wave order.  The adapter's rows of A are the matrix core's
 // 16-row operand, X's rows the other: a row's sums are its own whatever
-// stands in the other rows, and only rows of this adapter keep them.
+// stands in the other rows, and only rows of this adapter keep them.  Bound by
+// what one CU reads (about 35 GB/s beside the latency): with K = 4096 in four
+// slices 3.8 us for one row and 5.8 us for 16 rows of 16 adapters, in one
+// slice 11 us for 1024 rows.  The ring kernels take one slice all the same:
+// adding four at their ends cost them 10 us and saved 3 here.  Sixteen waves,
+// or eight steps in flight, measured no faster.  VEC: 16-byte aligned rows of
+// A and X, K a multiple of 8.
+template <bool VEC>
 __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, LoraArgs q)
 {
     __shared__ f32x4 red[kShrinkWaves][64];
@@ -58,23 +65,34 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, L
     const int r0 = blockIdx.y * 16, rank = r0 + li;
     const int slice = blockIdx.z % q.splits, turn = blockIdx.z / q.splits;
     const int a_row = lora_adapter(q, m, p.M);
-    const int64_t steps = (p.K + 31) / 32;
-    const int64_t b0 = steps * slice / q.splits, b1 = steps * (slice + 1) / q.splits;
-    const int64_t s0 = b0 + (b1 - b0) * wave / kShrinkWaves, s1 = b0 + (b1 - b0) * (wave + 1) / kShrinkWaves;
+    const int K = (int)p.K, steps = (K + 31) / 32;
+    const int b0 = steps / q.splits * slice, b1 = slice + 1 < q.splits ? b0 + steps / q.splits : steps;
+    const int s0 = b0 + (int)((unsigned)((b1 - b0) * wave) / kShrinkWaves);
+    const int s1 = b0 + (int)((unsigned)((b1 - b0) * (wave + 1)) / kShrinkWaves);
+    // (rows without an adapter and ranks past R read row 0: not kept)
     const uint16_t *xrow = (const uint16_t *)p.A + (a_row >= 0 ? m : 0) * p.lda;
-    const bool r_ok = rank < q.R;
+    const int64_t ra = (int64_t)(rank < q.R ? rank : 0) * q.lda;
     each_adapter(a_row, [&](int a, bool mine, int ordinal) {
         if (ordinal % q.turns != turn) return;        // uniform over the workgroup
-        const uint16_t *arow = q.A + (int64_t)a * q.strideA + (int64_t)(r_ok ? rank : 0) * q.lda;
+        const uint16_t *arow = q.A + (int64_t)a * q.strideA + ra;
+        const float sc = q.scale ? q.scale[a] : 1.0f;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         constexpr int D = 4;
-        for (int64_t s = s0; s < s1; s += D) {
+        for (int s = s0; s < s1; s += D) {
             u32x4 w[D], x[D];
 #pragma unroll
             for (int j = 0; j < D; ++j) {
-                const bool in = s + j < s1;
-                w[j] = load_chunk8_bf16(arow, (s + j) * 32 + g * 8, p.K, in && r_ok, q.align_a);
-                x[j] = load_chunk8_bf16(xrow, (s + j) * 32 + g * 8, p.K, in && a_row >= 0, p.align_a);
+                const int col = (s + j) * 32 + g * 8;
+                const bool in = s + j < s1 && col < K;
+                if constexpr (VEC) {
+                    const uint32_t at = in ? col : s0 * 32;     // (a step of its own, again)
+                    w[j] = *(const u32x4 *)(arow + at);
+                    x[j] = *(const u32x4 *)(xrow + at);
+                    if (!in) w[j] = x[j] = u32x4{0u, 0u, 0u, 0u};
+                } else {
+                    w[j] = load_chunk8_bf16(arow, col, K, in, q.align_a);
+                    x[j] = load_chunk8_bf16(xrow, col, K, in, p.align_a);
+                }
             }
 #pragma unroll
             for (int j = 0; j < D; ++j)
@@ -88,8 +106,25 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, L
             f32x4 v = red[0][lane];
 #pragma unroll
             for (int w2 = 1; w2 < kShrinkWaves; ++w2) v += red[w2][lane];
-            const float sc = q.scale ? q.scale[a] : 1.0f;
-            *(f32x4 *)(q.V + ((int64_t)slice * p.M + m) * q.ranks + r0 + 4 * g) = v * sc;
+            v = v * sc;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r0 + 4 * g + i >= q.R) v[i] = 0.f;
+            if (q.V) {
+                *(f32x4 *)(q.V + ((int64_t)slice * p.M + m) * q.ranks + r0 + 4 * g) = v;
+            } else {
+                // two bf16 parts (an infinite value has no rest)
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+                    lo[i] = pack_bf16x2((hi[i] & 0x7f80u) == 0x7f80u ? 0.f : v[2 * i] - bf16_lo(hi[i]),
+                                        (hi[i] & 0x7f800000u) == 0x7f800000u ? 0.f : v[2 * i + 1] - bf16_hi(hi[i]));
+                }
+                uint16_t *dst = q.V2 + m * 2 * q.ranks + r0 + 4 * g;
+                *(u32x2 *)dst = u32x2{hi[0], hi[1]};
+                *(u32x2 *)(dst + q.ranks) = u32x2{lo[0], lo[1]};
+            }
         }
     });
 }
@@ -109,58 +144,116 @@ __device__ __forceinline__ void lora_v8(const LoraArgs &q, int64_t M, int64_t m,
     }
 }
 
-// acc += v B^T for the rows and columns of a ring tile.  The FP32 values v
-// go through the matrix core as two bf16 parts, v = hi + lo to 2^-16 of it:
-// 2 R products deep, the first R with hi and the next R with lo against the
-// same rows of B.  16 rows at a time, one adapter of theirs after the other;
-// each row keeps the sums of its own.
-template <class RT>
-__device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q, const TileCoord &tc,
-                                            typename RT::Acc &acc, int wave, int WGN, int64_t m0, int64_t n0)
+// Ranks 8 c .. 8 c + 7 of a row of B (zeros past R).  BVEC: 16-byte aligned
+// rows of whole chunks; else element by element.  No branches: the loads of
+// several rows go out together.
+template <bool BVEC>
+__device__ __forceinline__ u32x4 lora_b8(const LoraArgs &q, const uint16_t *row, int c)
+{
+    if constexpr (BVEC) return *(const u32x4 *)(row + 8 * c);
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = 8 * c + 2 * i, last = q.R - 1;
+        const uint32_t lo = row[r < last ? r : last], hi = row[r + 1 < last ? r + 1 : last];
+        v[i] = (r < q.R ? lo : 0u) | (r + 1 < q.R ? hi << 16 : 0u);
+    }
+    return v;
+}
+
+// acc += v B^T for the rows and columns of a ring tile, 16 rows at a time.
+//  - Sixteen rows of one adapter: matrix-core products of the adapter's rows
+//    of B with the rows' values, which are stored as two bf16 parts behind
+//    each other (v = hi + lo to 2^-16 of it): 2 R deep, both parts against
+//    the same rows of B.  Rows of B stay in registers while the adapter stays.
+//  - Any other sixteen rows: each lane forms its own outputs from its row's
+//    values and its adapter's rows of B, R products each.  Every load is
+//    independent, so rows of sixteen adapters cost little more than the
+//    latency of one (a loop over the adapters measured 85 us at
+//    77 x 4104 x 4100 with 16 of them).
+template <class RT, int WGN, bool BVEC>
+__device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q, typename RT::Acc &acc, int wave,
+                                            int64_t m0, int64_t n0)
 {
     const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
     const int64_t mw = m0 + (wave / WGN) * RT::TM, nw = n0 + (wave % WGN) * RT::TN;
     const int chunks = q.ranks / 8, depth = (2 * chunks + 3) / 4;     // 8-rank chunks; 32-deep steps
+    int a_row[RT::FM], one[RT::FM];      // the lane's adapter; all sixteen rows' or -1
+#pragma unroll
+    for (int fm = 0; fm < RT::FM; ++fm) a_row[fm] = lora_adapter(q, mw + fm * 16 + li, p.M);
 #pragma unroll
     for (int fm = 0; fm < RT::FM; ++fm) {
-        const int64_t m = mw + fm * 16 + li;
-        const int a_row = lora_adapter(q, m, p.M);
-        each_adapter(a_row, [&](int a, bool mine, int) {
-            f32x4 d[RT::FN];
+        const int a = __builtin_amdgcn_readfirstlane(a_row[fm]);
+        one[fm] = __ballot(a_row[fm] != a) ? -1 : a;
+    }
+    for (int k = 0; k < depth; ++k) {
+        const int kc = 4 * k + g, c = kc < chunks ? kc : kc - chunks;
+        u32x4 x[RT::FM], b[RT::FN];
 #pragma unroll
-            for (int fn = 0; fn < RT::FN; ++fn) d[fn] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const uint16_t *Ba = q.B + (int64_t)a * q.strideB;
-            for (int k = 0; k < depth; ++k) {
-                const int kc = 4 * k + g, c = kc < chunks ? kc : kc - chunks;
-                u32x4 x = {0u, 0u, 0u, 0u};
-                if (mine && c < chunks) {
-                    f32x4 v[2];
-                    lora_v8(q, p.M, m, c, v);
+        for (int fm = 0; fm < RT::FM; ++fm) {
+            x[fm] = u32x4{0u, 0u, 0u, 0u};
+            if (one[fm] >= 0 && c < chunks)
+                x[fm] = *(const u32x4 *)(q.V2 + (mw + fm * 16 + li) * 2 * q.ranks + 8 * kc);
+        }
+        int held = -1;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo = v[i >> 1][2 * (i & 1)], hi = v[i >> 1][2 * (i & 1) + 1];
-                        x[i] = pack_bf16x2(lo, hi);
-                        if (kc >= chunks) {
-                            // (an infinite value has no rest)
-                            lo = (x[i] & 0x7f80u) == 0x7f80u ? 0.f : lo - bf16_lo(x[i]);
-                            hi = (x[i] & 0x7f800000u) == 0x7f800000u ? 0.f : hi - bf16_hi(x[i]);
-                            x[i] = pack_bf16x2(lo, hi);
-                        }
-                    }
-                }
+        for (int fm = 0; fm < RT::FM; ++fm) {
+            if (one[fm] < 0) continue;
+            if (one[fm] != held) {
+                held = one[fm];
 #pragma unroll
                 for (int fn = 0; fn < RT::FN; ++fn) {
+                    // (a column past N reads another, c past the chunks the
+                    // first, which meets zeros of x: but not if it is NaN)
                     const int64_t n = nw + fn * 16 + li;
-                    const u32x4 b = load_chunk8_bf16(Ba + (n < p.N ? n : 0) * q.ldb, 8 * c, q.R,
-                                                     n < p.N && c < chunks, q.align_b);
-                    d[fn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
-                                                                    __builtin_bit_cast(bf16x8, x), d[fn], 0, 0, 0);
+                    b[fn] = lora_b8<BVEC>(q, q.B + (int64_t)held * q.strideB + (n < p.N ? n : 0) * q.ldb,
+                                          c < chunks ? c : 0);
+                    if (c >= chunks) b[fn] = u32x4{0u, 0u, 0u, 0u};
                 }
             }
 #pragma unroll
             for (int fn = 0; fn < RT::FN; ++fn)
-                if (mine) acc[fn][fm] += d[fn];
-        });
+                acc[fn][fm] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[fn]),
+                                                                      __builtin_bit_cast(bf16x8, x[fm]), acc[fn][fm], 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int fm = 0; fm < RT::FM; ++fm) {
+        if (one[fm] >= 0 || a_row[fm] < 0) continue;
+        // (addresses formed anew for each sixteen rows: kept for all of them
+        // they would not fit beside the sums)
+        int lane_g = g;
+        asm volatile("" : "+v"(lane_g));
+        const uint16_t *Ba = q.B + (int64_t)a_row[fm] * q.strideB;
+        for (int c = 0; c < chunks; ++c) {
+            const uint16_t *src = q.V2 + (mw + fm * 16 + li) * 2 * q.ranks + 8 * c;
+            const u32x4 hi = *(const u32x4 *)src, lo = *(const u32x4 *)(src + q.ranks);
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bf16_lo(hi[i]) + bf16_lo(lo[i]);
+                v[2 * i + 1] = bf16_hi(hi[i]) + bf16_hi(lo[i]);
+            }
+#pragma unroll
+            for (int fn = 0; fn < RT::FN; ++fn) {
+                u32x4 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t n = nw + fn * 16 + 4 * lane_g + i;
+                    b[i] = lora_b8<BVEC>(q, Ba + (n < p.N ? n : 0) * q.ldb, c);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        d = __builtin_fmaf(v[2 * j], bf16_lo(b[i][j]), d);
+                        d = __builtin_fmaf(v[2 * j + 1], bf16_hi(b[i][j]), d);
+                    }
+                    acc[fn][fm][i] += d;
+                }
+            }
+        }
     }
 }
 
@@ -168,8 +261,8 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 
 // The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
 // sums.
-template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK>
-__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_lora_ms(GemmArgs p, LoraArgs q)
+template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool BVEC>
+__global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(GemmArgs p, LoraArgs q)
 {
     using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, MASKED, EPI_NONE, true, false, false>;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
@@ -185,17 +278,16 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_lora_ms(GemmArgs p, LoraAr
     if constexpr (SK) {
         if (!R::join_slices(p, wg, slice, acc)) return;
     }
-    lora_expand<R>(p, q, tc, acc, threadIdx.x >> 6, WGN, tc.tm * BM, tc.tn * BN);
+    lora_expand<R, WGN, BVEC>(p, q, acc, threadIdx.x >> 6, tc.tm * BM, tc.tn * BN);
     R::store(p, smem, tc, acc);
 }
 
-// M <= 16: k_decode_nt's weight stream on NW waves, and four more waves that
+// M <= 16: k_decode_nt's weight stream on NW waves, and NX more waves that
 // form v B^T of the workgroup's 16 RB columns meanwhile, an output at a time
 // per thread (R products in rank order); the last pass adds both.
-template <int NW, int RB>
-__global__ void __launch_bounds__((NW + 4) * 64) k_lora_decode(GemmArgs p, LoraArgs q)
+template <int NW, int NX, int RB>
+__global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, LoraArgs q)
 {
-    constexpr int NX = 4 * 64;                            // the extra waves' threads
     __shared__ f32x4 red[NW][RB][64];
     __shared__ float extra[16][16 * RB];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -204,7 +296,7 @@ __global__ void __launch_bounds__((NW + 4) * 64) k_lora_decode(GemmArgs p, LoraA
     const int64_t n0 = (int64_t)blockIdx.x * 16 * RB;
     if (wave >= NW) {
         const int chunks = q.ranks / 8;
-        for (int o = tid - NW * 64; o < (int)M * 16 * RB; o += NX) {
+        for (int o = tid - NW * 64; o < (int)M * 16 * RB; o += NX * 64) {
             const int m = o / (16 * RB), c0 = o - m * (16 * RB);
             const int64_t n = n0 + c0;
             const int a = lora_adapter(q, m, M);
@@ -299,32 +391,42 @@ __global__ void __launch_bounds__((NW + 4) * 64) k_lora_decode(GemmArgs p, LoraA
 hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s)
 {
     const dim3 g((unsigned)((a.M + 15) / 16), (unsigned)((q.ranks + 15) / 16), (unsigned)(q.turns * q.splits));
-    hipLaunchKernelGGL(k_lora_shrink, g, dim3(kShrinkWaves * 64), 0, s, a, q);
+    if (a.align_a >= 16 && q.align_a >= 16 && a.K % 8 == 0)
+        hipLaunchKernelGGL((k_lora_shrink<true>), g, dim3(kShrinkWaves * 64), 0, s, a, q);
+    else
+        hipLaunchKernelGGL((k_lora_shrink<false>), g, dim3(kShrinkWaves * 64), 0, s, a, q);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK>
+static hipError_t launch_lora_tile(const GemmArgs &a, const LoraArgs &q, int64_t grid, hipStream_t s)
+{
+    const dim3 g((unsigned)grid), b(WGM * WGN * 64);
+    if (q.align_b >= 16 && q.R % 8 == 0)
+        hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, MASKED, SK, true>), g, b, 0, s, a, q);
+    else
+        hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, MASKED, SK, false>), g, b, 0, s, a, q);
     return hipGetLastError();
 }
 
 template <int BM, int BN, int WGM, int WGN>
 static hipError_t launch_lora_ring(const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s)
 {
-    const dim3 g((unsigned)grid), b(WGM * WGN * 64);
     if constexpr (BM == 128 && BN == 128) {
-        if (a.ksplit > 1) {
-            if (variant == 1) hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, false, true>), g, b, 0, s, a, q);
-            else hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, true, true>), g, b, 0, s, a, q);
-            return hipGetLastError();
-        }
+        if (a.ksplit > 1)
+            return variant == 1 ? launch_lora_tile<BM, BN, WGM, WGN, false, true>(a, q, grid, s)
+                                : launch_lora_tile<BM, BN, WGM, WGN, true, true>(a, q, grid, s);
     }
-    if (variant == 1) hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, false, false>), g, b, 0, s, a, q);
-    else hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, true, false>), g, b, 0, s, a, q);
-    return hipGetLastError();
+    return variant == 1 ? launch_lora_tile<BM, BN, WGM, WGN, false, false>(a, q, grid, s)
+                        : launch_lora_tile<BM, BN, WGM, WGN, true, false>(a, q, grid, s);
 }
 
 hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s)
 {
     if (config_id == CFG_DECODE_NT) {
         // (fill_grid: three 16-row blocks of Wt per workgroup when M > 1)
-        if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 3>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
-        else hipLaunchKernelGGL((k_lora_decode<8, 1>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
+        if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 4, 3>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
+        else hipLaunchKernelGGL((k_lora_decode<8, 1, 1>), dim3((unsigned)grid), dim3(9 * 64), 0, s, a, q);
         return hipGetLastError();
     }
     if (variant != 1 && variant != 2) return hipErrorInvalidValue;

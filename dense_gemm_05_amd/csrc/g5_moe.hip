@@ -20,6 +20,7 @@
 
 #include "g5_device.h"
 #include "g5_kernels.h"
+#include "g5_stream.h"
 
 namespace g5 {
 
@@ -182,200 +183,6 @@ __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
     }
 }
 
-// 16 E4M3FN codes as 16 bf16 values (each exact), in order.
-__device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], false);
-        const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i], true);
-        u32x4 &d = i < 2 ? lo : hi;
-        d[2 * (i & 1)] = pack_bf16x2(a[0], a[1]);
-        d[2 * (i & 1) + 1] = pack_bf16x2(b[0], b[1]);
-    }
-}
-
-// A step is a 128-byte line of every weight row, read in two pieces: lane
-// group g (of four) takes bytes 16 g .. 16 g + 15 of each half.  The halves
-// are loaded one right after the other and with ordinary loads: the bytes in
-// flight exceed an XCD's L2, so a line whose second half is asked for later
-// is fetched again (measured: 1.6 times the bytes with the halves a batch
-// apart), and loads marked non-temporal give it up sooner (16 tokens, down
-// rows: 170 us against 132).  Piece h meets the same elements
-// of the token's row (8 of bf16, or 16 codes in two products).
-template <bool CODES>
-constexpr int kStep = CODES ? 128 : 64;       // elements
-template <bool CODES>
-constexpr int kPieces = CODES ? 4 : 2;        // 8-element pieces of a token row per lane and step
-
-// Where piece q of a token's row starts in a step, for lane group g: bf16 has
-// one per half, codes two.
-template <bool CODES>
-__device__ __forceinline__ int x_piece(int q, int g)
-{
-    return CODES ? 64 * (q >> 1) + 16 * g + 8 * (q & 1) : 32 * q + 8 * g;
-}
-
-// The lane group's part of that, in bytes.
-template <bool CODES>
-__device__ __forceinline__ uint32_t x_lane(int g)
-{
-    return (CODES ? 32u : 16u) * g;
-}
-
-// D steps of RB weight rows and of NC token rows in registers, and their
-// products: step s in place j is multiplied and step s + D loaded
-// over it, so D steps stay in flight.
-template <bool CODES, int RB, int NC, int D>
-struct MoeStream {
-    static constexpr int XP = kPieces<CODES>, KS = kStep<CODES>;
-    u32x4 w[D][RB][2], x[D][NC][XP];
-
-    // Whole step s of 16-byte aligned rows: wave-uniform bases and the lane's
-    // byte offsets (its row and 16 g).  A lane without a token leaves its x
-    // as it is (its column of the product is never read).
-    __device__ __forceinline__ void load_w(int j, const char *const (&wbase)[RB], uint32_t woff, int s)
-    {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[j][r][h] = *(const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff);
-    }
-    __device__ __forceinline__ void load_x(int j, const char *xbase, const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s)
-    {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (xok[c]) {
-#pragma unroll
-                for (int q = 0; q < XP; ++q)
-                    x[j][c][q] = *(const u32x4 *)((xbase + ((int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
-            }
-    }
-
-    // The last, partial step (K a whole number of 16-byte pieces): pieces
-    // past K are zeros.
-    __device__ __forceinline__ void load_tail(const char *const (&wbase)[RB], uint32_t woff, const char *xbase,
-                                              const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s, int K, int g)
-    {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t at = s * 128 + 64 * h;                     // + 16 g, in woff
-            const bool in = (int)(at + 16 * g) < (CODES ? K : 2 * K);
-#pragma unroll
-            for (int r = 0; r < RB; ++r) w[0][r][h] = in ? *(const u32x4 *)(wbase[r] + (woff + at)) : zero;
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int q = 0; q < XP; ++q)
-                x[0][c][q] = xok[c] && s * KS + x_piece<CODES>(q, g) < K
-                                 ? *(const u32x4 *)(xbase + (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0))))
-                                 : zero;
-    }
-
-    // Step s of rows of any alignment, zero-filled past K.
-    __device__ __forceinline__ void load_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                             const bool (&xok)[NC], int align_x, int s, int K, int g)
-    {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (CODES)
-                    w[0][r][h] = load_chunk16_u8((const uint8_t *)wrow[r], s * 128 + 64 * h + 16 * g, K, true, align_w);
-                else
-                    w[0][r][h] = load_chunk8_bf16((const uint16_t *)wrow[r], s * 64 + 32 * h + 8 * g, K, true, align_w);
-            }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int q = 0; q < XP; ++q)
-                x[0][c][q] = load_chunk8_bf16(xrow[c], s * KS + x_piece<CODES>(q, g), K, xok[c], align_x);
-    }
-
-    __device__ __forceinline__ void mma(int j, f32x4 (&acc)[RB][NC]) const
-    {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 b[2] = {w[j][r][h], w[j][r][h]};
-                if constexpr (CODES) codes16_to_bf16(w[j][r][h], b[0], b[1]);
-#pragma unroll
-                for (int q = 0; q < XP / 2; ++q)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, b[q]), __builtin_bit_cast(bf16x8, x[j][c][h * (XP / 2) + q]),
-                            acc[r][c], 0, 0, 0);
-            }
-    }
-
-    // Steps s0 .. s1 - 1 of K (the last may be partial), 16-byte aligned.
-    // tokens(xoff, xok) gives the lane's token rows, asked for when the first
-    // weights are on their way.
-    template <class F>
-    __device__ __forceinline__ void run(const char *const (&wbase)[RB], uint32_t woff, const char *xbase, F tokens, int s0,
-                                        int s1, int K, int g, f32x4 (&acc)[RB][NC])
-    {
-        const int whole = K / KS, sw = s1 < whole ? s1 : whole;
-        uint32_t xoff[NC];
-        bool xok[NC];
-        int s = s0;
-        if (s + D <= sw) {
-#pragma unroll
-            for (int j = 0; j < D; ++j) load_w(j, wbase, woff, s + j);
-            tokens(xoff, xok);
-#pragma unroll
-            for (int j = 0; j < D; ++j) load_x(j, xbase, xoff, xok, s + j);
-            for (; s + 2 * D <= sw; s += D) {
-#pragma unroll
-                for (int j = 0; j < D; ++j) {
-                    mma(j, acc);
-                    load_w(j, wbase, woff, s + D + j);
-                    load_x(j, xbase, xoff, xok, s + D + j);
-                }
-            }
-            // the last whole group, and behind it the fewer than D steps left
-#pragma unroll
-            for (int j = 0; j < D; ++j) {
-                mma(j, acc);
-                if (j < D - 1 && s + D + j < sw) {
-                    load_w(j, wbase, woff, s + D + j);
-                    load_x(j, xbase, xoff, xok, s + D + j);
-                }
-            }
-            s += D;
-        } else {
-            tokens(xoff, xok);
-#pragma unroll
-            for (int j = 0; j < D - 1; ++j)
-                if (s + j < sw) {
-                    load_w(j, wbase, woff, s + j);
-                    load_x(j, xbase, xoff, xok, s + j);
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < D - 1; ++j)
-            if (s + j < sw) mma(j, acc);
-        if (s0 < s1 && s1 > whole) {
-            load_tail(wbase, woff, xbase, xoff, xok, whole, K, g);
-            mma(0, acc);
-        }
-    }
-    __device__ __forceinline__ void run_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                            const bool (&xok)[NC], int align_x, int s0, int s1, int K, int g,
-                                            f32x4 (&acc)[RB][NC])
-    {
-        for (int s = s0; s < s1; ++s) {
-            load_any(wrow, align_w, xrow, xok, align_x, s, K, g);
-            mma(0, acc);
-        }
-    }
-};
-
 // (the same item in every lane)
 __device__ __forceinline__ MoeItem uniform_item(const MoeItem &it)
 {
@@ -426,14 +233,14 @@ __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it,
     for (int c = 0; c < NC; ++c) acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int K = (int)a.H, steps = (K + KS - 1) / KS;
     const int s0 = steps * wave / kMoeWaves, s1 = steps * (wave + 1) / kMoeWaves;
-    MoeStream<CODES, 2, NC, D> b;
+    RowStream<CODES, 2, NC, D> b;
     // (a row past I repeats the block's first and is not stored; whole blocks
     // past I only fill z's rows with zeros)
     if (i0 >= a.I) {
     } else if constexpr (VEC) {
         // (a block's rows, and all token rows, lie within 2 GiB of their first)
         const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
-        const uint32_t woff = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g;
+        const uint32_t off = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g, woff[2] = {off, off};
         auto tokens = [&](uint32_t (&off)[NC], bool (&ok)[NC]) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -521,7 +328,7 @@ __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, in
         pair[c] = zok[c] ? pairs[it.first + i] : 0;
         acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    MoeStream<CODES, 1, NB, D> b;
+    RowStream<CODES, 1, NB, D> b;
     if constexpr (VEC) {
         auto tokens = [&](uint32_t (&off)[NB], bool (&ok)[NB]) {
 #pragma unroll
@@ -530,7 +337,8 @@ __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, in
                 off[c] = 2 * ((uint32_t)pair[c] * (uint32_t)a.ldz + (li < 8 ? 0u : (uint32_t)a.zplane)) + x_lane<CODES>(g);
             }
         };
-        b.run(wbase, (uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g, (const char *)a.z, tokens, s0, s1, K, g, acc);
+        const uint32_t woff[1] = {(uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g};
+        b.run(wbase, woff, (const char *)a.z, tokens, s0, s1, K, g, acc);
     } else {
         const char *const wlane[1] = {wbase[0] + (int64_t)wrow * a.ldd * EB};
         const uint16_t *zrow[NB];
