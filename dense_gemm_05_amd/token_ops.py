@@ -8,7 +8,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import GemmError, lib
+from ._lib import GEMM_ERR_WORKSPACE, GemmError, lib
 from .gemm import Workspace, _bstride, _check_dev, _codes, _launch, _ld, _out_code
 
 __all__ = ["rms_norm", "rms_norm_e4m3", "rms_norm_backward", "moe_swiglu", "gemm_bf16_nt_lora"]
@@ -18,17 +18,42 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# (A small norm's kernel takes 3 us: what the binding does per call counts.)
+def _stride(t, cols):
+    """Row stride of a tensor whose last dimension has `cols` elements."""
+    return cols if t.is_contiguous() else _ld(t, cols)
+
+
+def _like(t, dtype):
+    """A new contiguous tensor of t's shape on its device."""
+    return torch.empty_like(t, dtype=dtype) if t.is_contiguous() else torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def _vector(t, n, dtype, name):
     """A contiguous vector of n elements, or None."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1)):
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1)):
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} elements")
-    return t
 
 
 def _rows(t, shape, dtype, name):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} {list(shape)}")
-    return t
+
+
+def _need(workspace, what, *args):
+    """Workspace bytes of a call (`what`: the size query, host only), kept by
+    the workspace: the answer depends on the arguments alone."""
+    if isinstance(workspace, Workspace):
+        n = workspace._need.get((what, args))
+        if n is not None:
+            return n
+    out = ctypes.c_uint64(0)
+    st = getattr(lib(), what)(*args, ctypes.byref(out))
+    if st != 0:
+        raise GemmError(st, what)
+    if isinstance(workspace, Workspace):
+        workspace._need[(what, args)] = out.value
+    return out.value
 
 
 def _scratch(workspace, dev, need):
@@ -47,10 +72,11 @@ def _scratch(workspace, dev, need):
 
 
 def _rms_norm(what, X, W, residual, eps, Y, H, rstd, codes, scale):
-    if X.dtype != torch.bfloat16 or X.dim() != 2:
+    shape = X.shape
+    if X.dtype != torch.bfloat16 or len(shape) != 2:
         raise TypeError(f"{what} takes a 2-D bfloat16 X")
-    rows, cols = X.shape
-    _rows(residual, (rows, cols), torch.bfloat16, "residual")
+    rows, cols = shape
+    _rows(residual, shape, torch.bfloat16, "residual")
     _vector(W, cols, torch.bfloat16, "W")
     _vector(rstd, rows, torch.float32, "rstd")
     if H is not None and residual is None:
@@ -58,21 +84,24 @@ def _rms_norm(what, X, W, residual, eps, Y, H, rstd, codes, scale):
     dev = _check_dev(X, W, residual, Y, H, rstd, scale)
     ydt = torch.uint8 if codes else torch.bfloat16
     if Y is None:
-        Y = torch.empty((rows, cols), dtype=ydt, device=dev)
-    if codes and str(Y.dtype) == "torch.float8_e4m3fn":
-        Y = Y.view(torch.uint8)
-    _rows(Y, (rows, cols), ydt, "Q" if codes else "Y")
-    if codes and scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        Y = _like(X, ydt)
+    else:
+        if codes and str(Y.dtype) == "torch.float8_e4m3fn":
+            Y = Y.view(torch.uint8)
+        _rows(Y, shape, ydt, "Q" if codes else "Y")
     if codes:
-        _vector(scale, rows, torch.float32, "scale")
+        if scale is None:
+            scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        else:
+            _vector(scale, rows, torch.float32, "scale")
     if residual is not None and H is None:
-        H = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    _rows(H, (rows, cols), torch.bfloat16, "H")
-    st = _launch(lib().gemm_rms_norm, dev, rows, cols, X.data_ptr(), _ld(X, cols), _ptr(residual),
-                 cols if residual is None else _ld(residual, cols), _ptr(H), cols if H is None else _ld(H, cols),
-                 _ptr(W), float(eps), Y.data_ptr(), _ld(Y, cols), _lib.GEMM_OUT_E4M3 if codes else _lib.GEMM_OUT_BF16,
-                 _ptr(scale) if codes else None, _ptr(rstd))
+        H = _like(X, torch.bfloat16)
+    else:
+        _rows(H, shape, torch.bfloat16, "H")
+    st = _launch(lib().gemm_rms_norm, dev, rows, cols, X.data_ptr(), _stride(X, cols), _ptr(residual),
+                 cols if residual is None else _stride(residual, cols), _ptr(H), cols if H is None else _stride(H, cols),
+                 _ptr(W), eps, Y.data_ptr(), _stride(Y, cols), _lib.GEMM_OUT_E4M3 if codes else _lib.GEMM_OUT_BF16,
+                 scale.data_ptr() if codes else None, _ptr(rstd))
     if st != 0:
         raise GemmError(st, "gemm_rms_norm")
     return Y, scale, H
@@ -116,23 +145,19 @@ def rms_norm_backward(dY, H, W, rstd, dH=None, dX=None, dW=None, need_dw=True, w
     _vector(rstd, rows, torch.float32, "rstd")
     dev = _check_dev(dY, H, W, rstd, dH, dX, dW)
     if dX is None:
-        dX = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        dX = _like(dY, torch.bfloat16)
     _rows(dX, (rows, cols), torch.bfloat16, "dX")
     buf = None
     if need_dw:
         if dW is None:
             dW = torch.empty((cols,), dtype=torch.float32, device=dev)
         _vector(dW, cols, torch.float32, "dW")
-        n = ctypes.c_uint64(0)
-        st = lib().gemm_rms_norm_workspace_size(rows, cols, ctypes.byref(n))
-        if st != 0:
-            raise GemmError(st, "gemm_rms_norm_workspace_size")
-        buf = _scratch(workspace, dev, n.value)
+        buf = _scratch(workspace, dev, _need(workspace, "gemm_rms_norm_workspace_size", rows, cols))
     else:
         dW = None
-    st = _launch(lib().gemm_rms_norm_backward, dev, rows, cols, dY.data_ptr(), _ld(dY, cols), H.data_ptr(),
-                 _ld(H, cols), _ptr(W), rstd.data_ptr(), _ptr(dH), cols if dH is None else _ld(dH, cols),
-                 dX.data_ptr(), _ld(dX, cols), _ptr(dW), _ptr(buf), 0 if buf is None else buf.numel())
+    st = _launch(lib().gemm_rms_norm_backward, dev, rows, cols, dY.data_ptr(), _stride(dY, cols), H.data_ptr(),
+                 _stride(H, cols), _ptr(W), rstd.data_ptr(), _ptr(dH), cols if dH is None else _stride(dH, cols),
+                 dX.data_ptr(), _stride(dX, cols), _ptr(dW), _ptr(buf), 0 if buf is None else buf.numel())
     if st != 0:
         raise GemmError(st, "gemm_rms_norm_backward")
     return dX, dW
@@ -169,10 +194,7 @@ def moe_swiglu(X, logits, topk, Wgu, Wd, scale_gu=None, scale_d=None, renormaliz
         if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != shape or not s.is_contiguous()):
             raise ValueError(f"{name} must be contiguous float32 {list(shape)}")
     dev = _check_dev(X, logits, Wgu, Wd, scale_gu, scale_d, Y, ids, gates)
-    n = ctypes.c_uint64(0)
-    st = lib().gemm_moe_workspace_size(T, H, I, E, topk, ctypes.byref(n))
-    if st != 0:
-        raise GemmError(st, "gemm_moe_swiglu")
+    need = _need(workspace, "gemm_moe_workspace_size", T, H, I, E, topk)
     if Y is None:
         Y = torch.empty((T, H), dtype=out_dtype, device=dev)
     if ids is None:
@@ -184,11 +206,11 @@ def moe_swiglu(X, logits, topk, Wgu, Wd, scale_gu=None, scale_d=None, renormaliz
     for t, dt, name in ((ids, torch.int32, "ids"), (gates, torch.float32, "gates")):
         if tuple(t.shape) != (T, topk) or t.dtype != dt or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dt} [T, topk]")
-    buf = _scratch(workspace, dev, n.value)
-    st = _launch(lib().gemm_moe_swiglu, dev, T, H, I, E, topk, 1 if renormalize else 0, X.data_ptr(), _ld(X, H),
-                 logits.data_ptr(), _ld(logits, E), _lib.GEMM_OUT_E4M3 if coded else _lib.GEMM_OUT_BF16,
-                 Wgu.data_ptr(), _ld(Wgu, H), _bstride(Wgu), _ptr(scale_gu), Wd.data_ptr(), _ld(Wd, I), _bstride(Wd),
-                 _ptr(scale_d), Y.data_ptr(), _ld(Y, H), _out_code(Y.dtype), ids.data_ptr(), gates.data_ptr(),
+    buf = _scratch(workspace, dev, need)
+    st = _launch(lib().gemm_moe_swiglu, dev, T, H, I, E, topk, 1 if renormalize else 0, X.data_ptr(), _stride(X, H),
+                 logits.data_ptr(), _stride(logits, E), _lib.GEMM_OUT_E4M3 if coded else _lib.GEMM_OUT_BF16,
+                 Wgu.data_ptr(), _stride(Wgu, H), _bstride(Wgu), _ptr(scale_gu), Wd.data_ptr(), _stride(Wd, I), _bstride(Wd),
+                 _ptr(scale_d), Y.data_ptr(), _stride(Y, H), _out_code(Y.dtype), ids.data_ptr(), gates.data_ptr(),
                  _ptr(buf), 0 if buf is None else buf.numel())
     if st != 0:
         raise GemmError(st, "gemm_moe_swiglu")
@@ -218,18 +240,33 @@ def gemm_bf16_nt_lora(X, Wt, A, B, idx, scale=None, C=None, out_dtype=torch.bflo
     if tuple(C.shape) != (M, N):
         raise ValueError("C must be [M, N]")
     code = _out_code(C.dtype)
-    ldx, ldw, ldc = _ld(X, K), _ld(Wt, K), _ld(C, N)
+    ldx, ldw, ldc = _stride(X, K), _stride(Wt, K), _stride(C, N)
     px, pw, pc = X.data_ptr(), Wt.data_ptr(), C.data_ptr()
     if workspace is None:
         workspace = Workspace(dev)
-    n = ctypes.c_uint64(0)
-    st = lib().gemm_lora_workspace_size(M, N, K, L, R, px, ldx, pw, ldw, pc, ldc, code, ctypes.byref(n))
-    if st != 0:
-        raise GemmError(st, "gemm_bf16_nt_lora")
-    buf = _scratch(workspace, dev, n.value)
-    st = _launch(lib().gemm_bf16_nt_lora, dev, M, N, K, px, ldx, pw, ldw, L, R, A.data_ptr(), _ld(A, K), _bstride(A),
-                 B.data_ptr(), _ld(B, R), _bstride(B), _ptr(scale), idx.data_ptr(), pc, ldc, code, buf.data_ptr(),
-                 buf.numel())
+    # the size depends on the pointers only through their alignment
+    key = ("lora", M, N, K, L, R, px % 256, ldx, pw % 256, ldw, pc % 256, ldc, code)
+    held = workspace._need if isinstance(workspace, Workspace) else {}
+
+    def size():
+        n = ctypes.c_uint64(0)
+        st = lib().gemm_lora_workspace_size(M, N, K, L, R, px, ldx, pw, ldw, pc, ldc, code, ctypes.byref(n))
+        if st != 0:
+            raise GemmError(st, "gemm_bf16_nt_lora")
+        held[key] = n.value
+        return n.value
+
+    def run(buf):
+        return _launch(lib().gemm_bf16_nt_lora, dev, M, N, K, px, ldx, pw, ldw, L, R, A.data_ptr(), _stride(A, K),
+                       _bstride(A), B.data_ptr(), _stride(B, R), _bstride(B), _ptr(scale), idx.data_ptr(), pc, ldc, code,
+                       buf.data_ptr(), buf.numel())
+
+    need = held.get(key)
+    st = run(_scratch(workspace, dev, size() if need is None else need))
+    if st == GEMM_ERR_WORKSPACE and need is not None:
+        # the kept size went stale (the plan also follows the library's
+        # environment overrides): nothing was launched, so ask again
+        st = run(_scratch(workspace, dev, size()))
     if st != 0:
         raise GemmError(st, "gemm_bf16_nt_lora")
     return C
