@@ -1295,15 +1295,9 @@ int gemm_rms_norm(int64_t rows, int64_t cols, const uint16_t *X, int64_t ldx, co
     if (outputs_overlap(out, 4, in, 3)) return GEMM_ERR_INVALID_ARG;
     const int st = g5::check_device();
     if (st != GEMM_OK) return st;
-    g5::NormArgs a{X, R, W, H, Y, codes ? scale : nullptr, rstd, rows, cols, ldx, R ? ldr : cols, H ? ldh : cols, ldy,
-                   eps, g5::row_alignment((uint64_t)X, ldx, 0, 1, 2),
-                   R ? g5::row_alignment((uint64_t)R, ldr, 0, 1, 2) : 16,
-                   W ? g5::row_alignment((uint64_t)W, 0, 0, 1, 2) : 16,
-                   H ? g5::row_alignment((uint64_t)H, ldh, 0, 1, 2) : 16,
-                   g5::row_alignment((uint64_t)Y, ldy, 0, 1, ey)};
-    const bool vec = cols % 8 == 0 && a.align_x >= 16 && a.align_r >= 16 && a.align_w >= 16 && a.align_h >= 16 &&
-                     a.align_y >= 8 * ey;
-    const hipError_t e = g5::launch_rms_norm(a, codes, vec, (hipStream_t)stream);
+    const g5::NormArgs a{X, R, W, H, Y, codes ? scale : nullptr, rstd, rows, cols, ldx, R ? ldr : cols, H ? ldh : cols,
+                         ldy, eps};
+    const hipError_t e = g5::launch_rms_norm(a, codes, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -1352,15 +1346,9 @@ int gemm_rms_norm_backward(int64_t rows, int64_t cols, const uint16_t *dY, int64
     if (dW && ((uint64_t)workspace % 256)) return GEMM_ERR_INVALID_ARG;
     const int st = g5::check_device();
     if (st != GEMM_OK) return st;
-    g5::NormGradArgs a{dY, H, W, dH, rstd, dX, dW ? (float *)((char *)workspace + g5::kCounterBytes) : nullptr, dW,
-                       rows, cols, lddy, ldh, dH ? lddh : cols, lddx,
-                       g5::row_alignment((uint64_t)dY, lddy, 0, 1, 2), g5::row_alignment((uint64_t)H, ldh, 0, 1, 2),
-                       W ? g5::row_alignment((uint64_t)W, 0, 0, 1, 2) : 16,
-                       dH ? g5::row_alignment((uint64_t)dH, lddh, 0, 1, 2) : 16,
-                       g5::row_alignment((uint64_t)dX, lddx, 0, 1, 2)};
-    const bool vec = cols % 8 == 0 && a.align_dy >= 16 && a.align_h >= 16 && a.align_w >= 16 && a.align_dh >= 16 &&
-                     a.align_dx >= 16;
-    const hipError_t e = g5::launch_rms_norm_grad(a, vec, (hipStream_t)stream);
+    const g5::NormGradArgs a{dY, H, W, dH, rstd, dX, dW ? (float *)((char *)workspace + g5::kCounterBytes) : nullptr, dW,
+                             rows, cols, lddy, ldh, dH ? lddh : cols, lddx};
+    const hipError_t e = g5::launch_rms_norm_grad(a, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -1437,6 +1425,8 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     if (out[0].hi > ((__int128)1 << 63) || outputs_overlap(out, 4, in, 6)) return GEMM_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < L.total) return GEMM_ERR_WORKSPACE;
     if ((uint64_t)workspace % 256) return GEMM_ERR_INVALID_ARG;
+    // (the kernels add 32-bit byte offsets of 16 weight rows and of the token rows)
+    if (weights && (ldgu * ew >= (1 << 27) || ldd * ew >= (1 << 27) || ldx * 2 >= (1 << 25))) return GEMM_ERR_UNSUPPORTED;
     const int st = g5::check_device();
     if (st != GEMM_OK) return st;
     char *ws = (char *)workspace;
@@ -1464,9 +1454,6 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     a.topk = (int)topk;
     a.renormalize = renormalize != 0;
     a.out_f32 = ec == 4;
-    a.align_x = g5::row_alignment((uint64_t)X, ldx, 0, 1, 2);
-    a.align_gu = g5::row_alignment((uint64_t)Wgu, ldgu, strideGu, E, ew);
-    a.align_d = g5::row_alignment((uint64_t)Wd, ldd, strideD, E, ew);
     a.n_items = (int *)(ws + L.n_items);
     a.items = (g5::MoeItem *)(ws + L.items);
     a.pairs = (int32_t *)(ws + L.pairs);
@@ -1475,12 +1462,7 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     a.z = (uint16_t *)(ws + L.z);
     a.ldz = L.ldz;
     a.zplane = L.zplane;
-    // (the fast kernels add 32-bit byte offsets of up to 16 weight rows and 64
-    // token rows, and read whole 16-byte pieces)
-    constexpr int64_t kFar = (int64_t)1 << 31;
-    const bool vec_gu = a.align_x >= 16 && a.align_gu >= 16 && H % (16 / ew) == 0 && ldgu * ew < kFar / 16 && ldx * 2 < kFar / 64;
-    const bool vec_d = a.align_d >= 16 && I % (16 / ew) == 0 && ldd * ew < kFar / 16;
-    const hipError_t e = g5::launch_moe(a, codes, vec_gu, vec_d, (hipStream_t)stream);
+    const hipError_t e = g5::launch_moe(a, codes, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -1535,9 +1517,7 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
         in[4] = vec_range(scale, L, 4);
         in[5] = vec_range(idx, M, 4);
         if (in[2].hi > ((__int128)1 << 63) || in[3].hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
-        q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB,
-                         g5::row_alignment((uint64_t)A, lda, strideA, L, 2),
-                         g5::row_alignment((uint64_t)B, ldb, strideB, L, 2), 0, 0, 0, nullptr, nullptr};
+        q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB, 0, 0, 0, nullptr, nullptr};
         p.lora = &q;
     }
     if (some) {

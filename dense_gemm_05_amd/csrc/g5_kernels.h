@@ -117,7 +117,7 @@ struct ActArgs {
 hipError_t launch_act_chain(int step, const ActArgs &a, bool vec, bool contig, hipStream_t s);
 
 // The RMS norm with the residual's addition (g5_norm.hip).  Strides in
-// elements (Y: bytes for codes); align_*: byte alignment of the row starts.
+// elements (Y: bytes for codes); rows of any alignment.
 struct NormArgs {
     const uint16_t *X, *R, *W;   // R (residual) and W (weight) or NULL
     uint16_t *H;                 // bf16(X + R), or NULL
@@ -125,10 +125,8 @@ struct NormArgs {
     float *scale, *rstd;         // rstd or NULL
     int64_t rows, cols, ldx, ldr, ldh, ldy;
     float eps;
-    int align_x, align_r, align_w, align_h, align_y;
 };
-// vec: cols % 8 == 0 and every row start 16-byte aligned (codes: 8-byte).
-hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t s);
+hipError_t launch_rms_norm(const NormArgs &a, bool codes, hipStream_t s);
 
 // Its gradient: dX and, when dW is given, the weight's through `part`
 // (norm_grad_parts(rows) rows of cols floats, written before they are read).
@@ -138,12 +136,11 @@ struct NormGradArgs {
     uint16_t *dX;
     float *part, *dW;
     int64_t rows, cols, lddy, ldh, lddh, lddx;
-    int align_dy, align_h, align_w, align_dh, align_dx;
 };
 int norm_grad_parts(int64_t rows);
 // dW[n] := the sum of `parts` rows of `part` (0: zeros, `part` not read).
 hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s);
-hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s);
+hipError_t launch_rms_norm_grad(const NormGradArgs &a, hipStream_t s);
 
 // The mixture-of-experts SwiGLU layer for a few tokens (g5_moe.hip).
 // Weights bf16, or E4M3FN codes with factors per row; strides in elements.
@@ -170,7 +167,7 @@ struct MoeArgs {
     int32_t *ids;                      // [T, topk] or NULL
     float *gates;
     int64_t T, H, I, E, ldx, ldl, ldgu, strideGu, ldd, strideD, ldy;
-    int topk, renormalize, out_f32, align_x, align_gu, align_d;
+    int topk, renormalize, out_f32;
     int cols;                          // hidden columns per workgroup of the down kernel
     int chunk;                         // moe_chunk(T)
     // scratch: the routing [T * topk], the number of work items, the items by
@@ -184,19 +181,19 @@ struct MoeArgs {
     uint16_t *z;
     int64_t ldz, zplane;
 };
-// vec_gu, vec_d: the rows of X and Wgu (of Wd) start 16-byte aligned.
-hipError_t launch_moe(const MoeArgs &a, bool codes, bool vec_gu, bool vec_d, hipStream_t s);
+// Rows of any alignment; 16 rows of Wgu or Wd and the T rows of X span less
+// than 2 GiB.
+hipError_t launch_moe(const MoeArgs &a, bool codes, hipStream_t s);
 
 // The low-rank adapters beside a bf16 product with B given transposed
 // (g5_lora.hip): adapter a has A at A + a strideA [R, K] and B at
 // B + a strideB [N, R]; row m of the product uses adapter idx[m] (none when
-// outside [0, L)).
+// outside [0, L)); rows of any alignment.
 struct LoraArgs {
     const uint16_t *A, *B;
     const float *scale;          // [L] or NULL
     const int32_t *idx;          // [M]
     int64_t L, R, lda, strideA, ldb, strideB;
-    int align_a, align_b;        // byte alignments of the row starts
     int ranks;                   // R rounded up to 8: the row length of V
     int splits, turns;           // K slices of V; workgroups sharing a row block's adapters
     // scratch for the values v (rows without an adapter unused): FP32

@@ -14,6 +14,7 @@
 
 #include "g5_device.h"
 #include "g5_kernels.h"
+#include "g5_stream.h"
 
 namespace g5 {
 
@@ -54,9 +55,9 @@ __device__ __forceinline__ void each_adapter(int a_row, F f)
 // slices 3.8 us for one row and 5.8 us for 16 rows of 16 adapters, in one
 // slice 11 us for 1024 rows.  The ring kernels take one slice all the same:
 // adding four at their ends cost them 10 us and saved 3 here.  Sixteen waves,
-// or eight steps in flight, measured no faster.  VEC: 16-byte aligned rows of
-// A and X, K a multiple of 8.
-template <bool VEC>
+// or eight steps in flight, measured no faster.  WHOLE: K is a
+// multiple of 8.
+template <bool WHOLE>
 __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, LoraArgs q)
 {
     __shared__ f32x4 red[kShrinkWaves][64];
@@ -84,14 +85,21 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, L
             for (int j = 0; j < D; ++j) {
                 const int col = (s + j) * 32 + g * 8;
                 const bool in = s + j < s1 && col < K;
-                if constexpr (VEC) {
-                    const uint32_t at = in ? col : s0 * 32;     // (a step of its own, again)
-                    w[j] = *(const u32x4 *)(arow + at);
-                    x[j] = *(const u32x4 *)(xrow + at);
-                    if (!in) w[j] = x[j] = u32x4{0u, 0u, 0u, 0u};
-                } else {
-                    w[j] = load_chunk8_bf16(arow, col, K, in, q.align_a);
-                    x[j] = load_chunk8_bf16(xrow, col, K, in, p.align_a);
+                w[j] = x[j] = u32x4{0u, 0u, 0u, 0u};
+                if constexpr (WHOLE) {
+                    // (a lane or step past the end reads the wave's first again)
+                    const uint32_t at = in ? col : s0 * 32;
+                    const u32x4 lw = load16(arow + at), lx = load16(xrow + at);
+                    if (in) {
+                        w[j] = lw;
+                        x[j] = lx;
+                    }
+                } else if (in && col + 8 <= K) {
+                    w[j] = load16(arow + col);
+                    x[j] = load16(xrow + col);
+                } else if (in) {
+                    w[j] = load_part8(arow + col, K - col);
+                    x[j] = load_part8(xrow + col, K - col);
                 }
             }
 #pragma unroll
@@ -144,21 +152,13 @@ __device__ __forceinline__ void lora_v8(const LoraArgs &q, int64_t M, int64_t m,
     }
 }
 
-// Ranks 8 c .. 8 c + 7 of a row of B (zeros past R).  BVEC: 16-byte aligned
-// rows of whole chunks; else element by element.  No branches: the loads of
-// several rows go out together.
-template <bool BVEC>
+// Ranks 8 c .. 8 c + 7 of a row of B (zeros past R).  WHOLE: R is a multiple
+// of 8.
+template <bool WHOLE>
 __device__ __forceinline__ u32x4 lora_b8(const LoraArgs &q, const uint16_t *row, int c)
 {
-    if constexpr (BVEC) return *(const u32x4 *)(row + 8 * c);
-    u32x4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = 8 * c + 2 * i, last = q.R - 1;
-        const uint32_t lo = row[r < last ? r : last], hi = row[r + 1 < last ? r + 1 : last];
-        v[i] = (r < q.R ? lo : 0u) | (r + 1 < q.R ? hi << 16 : 0u);
-    }
-    return v;
+    if (WHOLE || 8 * c + 8 <= q.R) return load16(row + 8 * c);
+    return load_part8(row + 8 * c, (int)q.R - 8 * c);
 }
 
 // acc += v B^T for the rows and columns of a ring tile, 16 rows at a time.
@@ -171,7 +171,7 @@ __device__ __forceinline__ u32x4 lora_b8(const LoraArgs &q, const uint16_t *row,
 //    independent, so rows of sixteen adapters cost little more than the
 //    latency of one (a loop over the adapters measured 85 us at
 //    77 x 4104 x 4100 with 16 of them).
-template <class RT, int WGN, bool BVEC>
+template <class RT, int WGN, bool WHOLE>
 __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q, typename RT::Acc &acc, int wave,
                                             int64_t m0, int64_t n0)
 {
@@ -206,7 +206,7 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
                     // (a column past N reads another, c past the chunks the
                     // first, which meets zeros of x: but not if it is NaN)
                     const int64_t n = nw + fn * 16 + li;
-                    b[fn] = lora_b8<BVEC>(q, q.B + (int64_t)held * q.strideB + (n < p.N ? n : 0) * q.ldb,
+                    b[fn] = lora_b8<WHOLE>(q, q.B + (int64_t)held * q.strideB + (n < p.N ? n : 0) * q.ldb,
                                           c < chunks ? c : 0);
                     if (c >= chunks) b[fn] = u32x4{0u, 0u, 0u, 0u};
                 }
@@ -240,7 +240,7 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int64_t n = nw + fn * 16 + 4 * lane_g + i;
-                    b[i] = lora_b8<BVEC>(q, Ba + (n < p.N ? n : 0) * q.ldb, c);
+                    b[i] = lora_b8<WHOLE>(q, Ba + (n < p.N ? n : 0) * q.ldb, c);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -261,7 +261,7 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 
 // The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
 // sums.
-template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool BVEC>
+template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool WHOLE>
 __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(GemmArgs p, LoraArgs q)
 {
     using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, MASKED, EPI_NONE, true, false, false>;
@@ -278,21 +278,21 @@ __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(Ge
     if constexpr (SK) {
         if (!R::join_slices(p, wg, slice, acc)) return;
     }
-    lora_expand<R, WGN, BVEC>(p, q, acc, threadIdx.x >> 6, tc.tm * BM, tc.tn * BN);
+    lora_expand<R, WGN, WHOLE>(p, q, acc, threadIdx.x >> 6, tc.tm * BM, tc.tn * BN);
     R::store(p, smem, tc, acc);
 }
 
 // M <= 16: k_decode_nt's weight stream on NW waves, and NX more waves that
 // form v B^T of the workgroup's 16 RB columns meanwhile, an output at a time
 // per thread (R products in rank order); the last pass adds both.
-template <int NW, int NX, int RB>
+template <int NW, int NX, int RB, int D>
 __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, LoraArgs q)
 {
     __shared__ f32x4 red[NW][RB][64];
     __shared__ float extra[16][16 * RB];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane >> 4, li = lane & 15;
-    const int64_t M = p.M, N = p.N, K = p.K, lda = p.lda, ldb = p.ldb;
+    const int64_t M = p.M, N = p.N;
     const int64_t n0 = (int64_t)blockIdx.x * 16 * RB;
     if (wave >= NW) {
         const int chunks = q.ranks / 8;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
             if (a >= 0 && n < N) {
                 const uint16_t *brow = q.B + (int64_t)a * q.strideB + n * q.ldb;
                 for (int c = 0; c < chunks; ++c) {
-                    const u32x4 b = load_chunk8_bf16(brow, 8 * c, q.R, true, q.align_b);
+                    const u32x4 b = lora_b8<false>(q, brow, c);
                     f32x4 v[2];
                     lora_v8(q, M, m, c, v);
 #pragma unroll
@@ -317,58 +317,28 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
             extra[m][c0] = d;
         }
     } else {
-        const uint16_t *X = (const uint16_t *)p.A, *Bt = (const uint16_t *)p.B;
-        const bool m_ok = li < M;
-        bool n_ok[RB];
-        const uint16_t *brow[RB];
+        // (a block's rows lie within 2 GiB of its first; rows past N read a
+        // row that is there, rows past M the first: not stored)
+        const char *wbase[RB];
+        uint32_t woff[RB];
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-            n_ok[r] = n0 + 16 * r + li < N;
-            brow[r] = Bt + (n_ok[r] ? n0 + 16 * r + li : 0) * ldb;
+            const int64_t n = n0 + 16 * r < N ? n0 + 16 * r : n0;
+            wbase[r] = (const char *)p.B + n * p.ldb * 2;
+            woff[r] = (uint32_t)(n + li < N ? li : 0) * (uint32_t)(p.ldb * 2) + 16 * g;
         }
-        const uint16_t *xrow = X + (m_ok ? li : 0) * lda;
-        const int64_t whole = K / 32;
-        const int64_t s_begin = whole * wave / NW, s_end = whole * (wave + 1) / NW;
-        f32x4 acc[RB];
-#pragma unroll
-        for (int r = 0; r < RB; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-        auto load_b = [&](int r, int64_t s) -> u32x4 {
-            return n_ok[r] ? __builtin_nontemporal_load((const u32x4 *)(brow[r] + s * 32 + g * 8))
-                           : u32x4{0u, 0u, 0u, 0u};
+        auto tokens = [&](uint32_t (&off)[1], bool (&ok)[1]) {
+            ok[0] = true;
+            off[0] = (uint32_t)(li < M ? li : 0) * (uint32_t)(p.lda * 2) + x_lane<false>(g);
         };
-        auto load_x = [&](int64_t s) -> u32x4 { return load_chunk8_bf16(xrow, s * 32 + g * 8, K, m_ok, p.align_a); };
-        auto mma = [&](int r, u32x4 b, u32x4 x) {
-            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b),
-                                                             __builtin_bit_cast(bf16x8, x), acc[r], 0, 0, 0);
-        };
-        constexpr int D = RB == 1 ? 4 : 2;
-        int64_t s = s_begin;
-        for (; s + D <= s_end; s += D) {
-            u32x4 b[D][RB], x[D];
+        const int K = (int)p.K, steps = (K + kStep<false> - 1) / kStep<false>;
+        RowStream<false, RB, 1, D> b;
+        f32x4 acc[RB][1];
 #pragma unroll
-            for (int j = 0; j < D; ++j)
+        for (int r = 0; r < RB; ++r) acc[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+        b.run(wbase, woff, (const char *)p.A, tokens, steps * wave / NW, steps * (wave + 1) / NW, K, g, acc);
 #pragma unroll
-                for (int r = 0; r < RB; ++r) b[j][r] = load_b(r, s + j);
-#pragma unroll
-            for (int j = 0; j < D; ++j) x[j] = load_x(s + j);
-#pragma unroll
-            for (int j = 0; j < D; ++j)
-#pragma unroll
-                for (int r = 0; r < RB; ++r) mma(r, b[j][r], x[j]);
-        }
-        for (; s < s_end; ++s) {
-            const u32x4 x = load_x(s);
-#pragma unroll
-            for (int r = 0; r < RB; ++r) mma(r, load_b(r, s), x);
-        }
-        if (wave == NW - 1 && K % 32 != 0) {
-            const u32x4 x = load_x(whole);
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-                mma(r, load_chunk8_bf16(brow[r], whole * 32 + g * 8, K, n_ok[r], p.align_b), x);
-        }
-#pragma unroll
-        for (int r = 0; r < RB; ++r) red[wave][r][lane] = acc[r];
+        for (int r = 0; r < RB; ++r) red[wave][r][lane] = acc[r][0];
     }
     __syncthreads();
     if (tid < 64 * RB) {
@@ -391,7 +361,7 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
 hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s)
 {
     const dim3 g((unsigned)((a.M + 15) / 16), (unsigned)((q.ranks + 15) / 16), (unsigned)(q.turns * q.splits));
-    if (a.align_a >= 16 && q.align_a >= 16 && a.K % 8 == 0)
+    if (a.K % 8 == 0)
         hipLaunchKernelGGL((k_lora_shrink<true>), g, dim3(kShrinkWaves * 64), 0, s, a, q);
     else
         hipLaunchKernelGGL((k_lora_shrink<false>), g, dim3(kShrinkWaves * 64), 0, s, a, q);
@@ -402,7 +372,7 @@ template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK>
 static hipError_t launch_lora_tile(const GemmArgs &a, const LoraArgs &q, int64_t grid, hipStream_t s)
 {
     const dim3 g((unsigned)grid), b(WGM * WGN * 64);
-    if (q.align_b >= 16 && q.R % 8 == 0)
+    if (q.R % 8 == 0)
         hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, MASKED, SK, true>), g, b, 0, s, a, q);
     else
         hipLaunchKernelGGL((k_lora_ms<BM, BN, WGM, WGN, MASKED, SK, false>), g, b, 0, s, a, q);
@@ -425,8 +395,8 @@ hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int 
 {
     if (config_id == CFG_DECODE_NT) {
         // (fill_grid: three 16-row blocks of Wt per workgroup when M > 1)
-        if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 4, 3>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
-        else hipLaunchKernelGGL((k_lora_decode<8, 1, 1>), dim3((unsigned)grid), dim3(9 * 64), 0, s, a, q);
+        if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 4, 3, 2>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);
+        else hipLaunchKernelGGL((k_lora_decode<8, 1, 1, 4>), dim3((unsigned)grid), dim3(9 * 64), 0, s, a, q);
         return hipGetLastError();
     }
     if (variant != 1 && variant != 2) return hipErrorInvalidValue;

@@ -213,7 +213,7 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
 
 // z of 16 inner columns for the tokens of one work item (at most 16 NC): gate
 // rows i0 .. i0 + 15 and the up rows of the same columns.
-template <bool CODES, bool VEC, int NC, int D>
+template <bool CODES, int NC, int D>
 __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it, int i0,
                                             f32x4 (&red)[kMoeWaves][2][64])
 {
@@ -237,25 +237,18 @@ __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it,
     // (a row past I repeats the block's first and is not stored; whole blocks
     // past I only fill z's rows with zeros)
     if (i0 >= a.I) {
-    } else if constexpr (VEC) {
+    } else {
         // (a block's rows, and all token rows, lie within 2 GiB of their first)
         const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
         const uint32_t off = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g, woff[2] = {off, off};
-        auto tokens = [&](uint32_t (&off)[NC], bool (&ok)[NC]) {
+        auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 ok[c] = xok[c];
-                off[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
+                xoff[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
             }
         };
         b.run(wbase, woff, (const char *)a.X, tokens, s0, s1, K, g, acc);
-    } else {
-        const int64_t row = wok ? i0 + li : i0;
-        const char *const wrow[2] = {W + row * a.ldgu * EB, W + (a.I + row) * a.ldgu * EB};
-        const uint16_t *xrow[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) xrow[c] = a.X + (int64_t)(pair[c] / a.topk) * a.ldx;
-        b.run_any(wrow, a.align_gu, xrow, xok, a.align_x, s0, s1, K, g, acc);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -286,7 +279,7 @@ __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it,
 
 // (128 registers per lane: four workgroups per CU; MANY: items of up to 32
 // tokens)
-template <bool CODES, bool VEC, bool MANY>
+template <bool CODES, bool MANY>
 __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
 {
     __shared__ f32x4 red[kMoeWaves][2][64];
@@ -294,8 +287,8 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
     if (ordinal >= *a.n_items) return;
     const MoeItem it = uniform_item(a.items[ordinal]);
     const int i0 = (blockIdx.x - ordinal * strips) * 16;
-    if (MANY && it.count > 16) moe_gate_up<CODES, VEC, 2, CODES ? 1 : 2>(a, it, i0, red);
-    else moe_gate_up<CODES, VEC, 1, CODES ? 2 : 3>(a, it, i0, red);
+    if (MANY && it.count > 16) moe_gate_up<CODES, 2, CODES ? 1 : 2>(a, it, i0, red);
+    else moe_gate_up<CODES, 1, CODES ? 2 : 3>(a, it, i0, red);
 }
 
 // The down rows.  A workgroup owns `cols` (at most 16) hidden columns for
@@ -308,7 +301,7 @@ constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
 // A piece's products for its tokens, 8 to a block of the matrix core's 16
 // columns: columns 0 .. 7 take z's hi parts, 8 .. 15 the lo parts, and the two
 // sums are added at the end.
-template <bool CODES, bool VEC, int NB, int D>
+template <bool CODES, int NB, int D>
 __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, int from, int slice, int n0,
                                          const int *pairs, float (&part)[kDownSlices][kMoeMaxPairs][16])
 {
@@ -329,23 +322,15 @@ __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, in
         acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     RowStream<CODES, 1, NB, D> b;
-    if constexpr (VEC) {
-        auto tokens = [&](uint32_t (&off)[NB], bool (&ok)[NB]) {
+    auto tokens = [&](uint32_t (&off)[NB], bool (&ok)[NB]) {
 #pragma unroll
-            for (int c = 0; c < NB; ++c) {
-                ok[c] = zok[c];
-                off[c] = 2 * ((uint32_t)pair[c] * (uint32_t)a.ldz + (li < 8 ? 0u : (uint32_t)a.zplane)) + x_lane<CODES>(g);
-            }
-        };
-        const uint32_t woff[1] = {(uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g};
-        b.run(wbase, woff, (const char *)a.z, tokens, s0, s1, K, g, acc);
-    } else {
-        const char *const wlane[1] = {wbase[0] + (int64_t)wrow * a.ldd * EB};
-        const uint16_t *zrow[NB];
-#pragma unroll
-        for (int c = 0; c < NB; ++c) zrow[c] = a.z + (int64_t)pair[c] * a.ldz + (li < 8 ? 0 : a.zplane);
-        b.run_any(wlane, a.align_d, zrow, zok, 16, s0, s1, K, g, acc);
-    }
+        for (int c = 0; c < NB; ++c) {
+            ok[c] = zok[c];
+            off[c] = 2 * ((uint32_t)pair[c] * (uint32_t)a.ldz + (li < 8 ? 0u : (uint32_t)a.zplane)) + x_lane<CODES>(g);
+        }
+    };
+    const uint32_t woff[1] = {(uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g};
+    b.run(wbase, woff, (const char *)a.z, tokens, s0, s1, K, g, acc);
 #pragma unroll
     for (int c = 0; c < NB; ++c) {
         f32x4 v = acc[0][c];
@@ -357,7 +342,7 @@ __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, in
 
 // A piece has 16 tokens at most: a work item's SUB chunks are pieces of their
 // own.
-template <bool CODES, bool VEC, int SUB>
+template <bool CODES, int SUB>
 __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 {
     __shared__ __attribute__((aligned(16))) float part[kDownSlices][kMoeMaxPairs][16];
@@ -372,8 +357,8 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
     for (int piece = wave; piece < n_items * (kDownSlices * SUB);) {
         const MoeItem it = uniform_item(items[piece / (kDownSlices * SUB)]);
         const int slice = piece % kDownSlices, from = piece / kDownSlices % SUB * 16;
-        if (it.count - from > 8) moe_down<CODES, VEC, 2, CODES ? 2 : 3>(a, it, from, slice, n0, pairs, part);
-        else if (it.count > from) moe_down<CODES, VEC, 1, CODES ? 3 : 5>(a, it, from, slice, n0, pairs, part);
+        if (it.count - from > 8) moe_down<CODES, 2, CODES ? 2 : 3>(a, it, from, slice, n0, pairs, part);
+        else if (it.count > from) moe_down<CODES, 1, CODES ? 3 : 5>(a, it, from, slice, n0, pairs, part);
         int p = 0;
         if (lane == 0) p = atomicAdd(&next, 1);
         piece = __builtin_amdgcn_readfirstlane(p);
@@ -398,22 +383,20 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
 }  // namespace
 
 template <bool CODES, bool MANY>
-static hipError_t launch_moe_weights(const MoeArgs &a, bool vec_gu, bool vec_d, hipStream_t s)
+static hipError_t launch_moe_weights(const MoeArgs &a, hipStream_t s)
 {
     const dim3 gg((unsigned)(moe_items(a.T, a.E, a.topk) * (a.ldz / 16)));
     const dim3 gd((unsigned)((a.H + a.cols - 1) / a.cols)), bg(kMoeThreads), bd(kDownWaves * 64);
     if (a.I > 0) {      // (no inner columns: the down kernel's sums are empty)
-        if (vec_gu) hipLaunchKernelGGL((k_moe_gate_up<CODES, true, MANY>), gg, bg, 0, s, a);
-        else hipLaunchKernelGGL((k_moe_gate_up<CODES, false, MANY>), gg, bg, 0, s, a);
+        hipLaunchKernelGGL((k_moe_gate_up<CODES, MANY>), gg, bg, 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (vec_d) hipLaunchKernelGGL((k_moe_down<CODES, true, MANY ? 2 : 1>), gd, bd, 0, s, a);
-    else hipLaunchKernelGGL((k_moe_down<CODES, false, MANY ? 2 : 1>), gd, bd, 0, s, a);
+    hipLaunchKernelGGL((k_moe_down<CODES, MANY ? 2 : 1>), gd, bd, 0, s, a);
     return hipGetLastError();
 }
 
-hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, hipStream_t s)
+hipError_t launch_moe(const MoeArgs &args, bool codes, hipStream_t s)
 {
     MoeArgs a = args;
     a.chunk = moe_chunk(a.T);
@@ -428,10 +411,8 @@ hipError_t launch_moe(const MoeArgs &args, bool codes, bool vec_gu, bool vec_d, 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.H == 0) return e;
     if (a.chunk > 16)
-        return codes ? launch_moe_weights<true, true>(a, vec_gu, vec_d, s)
-                     : launch_moe_weights<false, true>(a, vec_gu, vec_d, s);
-    return codes ? launch_moe_weights<true, false>(a, vec_gu, vec_d, s)
-                 : launch_moe_weights<false, false>(a, vec_gu, vec_d, s);
+        return codes ? launch_moe_weights<true, true>(a, s) : launch_moe_weights<false, true>(a, s);
+    return codes ? launch_moe_weights<true, false>(a, s) : launch_moe_weights<false, false>(a, s);
 }
 
 }  // namespace g5

@@ -15,42 +15,61 @@
 
 #include "g5_device.h"
 #include "g5_kernels.h"
+#include "g5_stream.h"
 
 namespace g5 {
 
 namespace {
 
-// Chunk c (8 elements) of a row: one 16-byte load when VEC (every row
-// 16-byte aligned and a whole number of chunks), else by alignment.
-template <bool VEC>
-__device__ __forceinline__ u32x4 norm_load(const uint16_t *row, int64_t col, int64_t cols, int align)
+// Chunks of 8 elements of rows of any alignment, one instruction each; WHOLE:
+// cols is a multiple of 8.  Else the row's last chunk either ends with the row
+// (`lap`: it repeats `dup` elements of the chunk before, which the row's sums
+// leave out and which are stored twice with the same value), so that no load
+// waits on a condition; or, for rows of less than a chunk and for a sum formed
+// in place (whose elements may be read once only), it goes element by element.
+struct NormCols {
+    int64_t cols;
+    bool lap;
+    __device__ __forceinline__ int64_t at(int64_t col) const { return lap && col + 8 > cols ? cols - 8 : col; }
+    __device__ __forceinline__ int dup(int64_t col) const { return lap && col + 8 > cols ? (int)(col + 8 - cols) : 0; }
+};
+// v without its first n elements.
+__device__ __forceinline__ u32x4 drop_first(u32x4 v, int n)
 {
-    if constexpr (VEC) return *(const u32x4 *)(row + col);
-    else return load_chunk8_bf16(row, col, cols, true, align);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] &= (2 * i < n ? 0u : 0xffffu) | (2 * i + 1 < n ? 0u : 0xffff0000u);
+    return v;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void norm_store(uint16_t *row, int64_t col, int64_t cols, int align, u32x4 v)
+template <bool WHOLE>
+__device__ __forceinline__ u32x4 norm_load(const uint16_t *row, int64_t col, int64_t cols)
 {
-    if (VEC || (col + 8 <= cols && align >= 16)) {
-        *(u32x4 *)(row + col) = v;
-    } else if (col + 8 <= cols && align >= 8) {
-        *(u32x2 *)(row + col) = u32x2{v[0], v[1]};
-        *(u32x2 *)(row + col + 4) = u32x2{v[2], v[3]};
+    if (WHOLE || col + 8 <= cols) return load16(row + col);
+    return load_part8(row + col, (int)(cols - col));
+}
+
+template <bool WHOLE>
+__device__ __forceinline__ void norm_store(uint16_t *row, int64_t col, int64_t cols, u32x4 v)
+{
+    if (WHOLE || col + 8 <= cols) {
+        store16(row + col, v);
     } else {
-        for (int i = 0; i < 8 && col + i < cols; ++i) row[col + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < cols) row[col + i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void norm_store_codes(uint8_t *row, int64_t col, int64_t cols, int align, uint32_t w0,
-                                                 uint32_t w1)
+template <bool WHOLE>
+__device__ __forceinline__ void norm_store_codes(uint8_t *row, int64_t col, int64_t cols, uint32_t w0, uint32_t w1)
 {
-    if (VEC || (col + 8 <= cols && align >= 8)) {
-        *(u32x2 *)(row + col) = u32x2{w0, w1};
+    if (WHOLE || col + 8 <= cols) {
+        const u32x2 v = {w0, w1};
+        __builtin_memcpy(row + col, &v, 8);
     } else {
-        const uint32_t w[2] = {w0, w1};
-        for (int i = 0; i < 8 && col + i < cols; ++i) row[col + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < cols) row[col + i] = (uint8_t)((i < 4 ? w0 : w1) >> (8 * (i & 3)));
     }
 }
 
@@ -113,49 +132,52 @@ __device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps)
 }  // namespace
 
 // Rows of up to WPR * NCH * 512 elements, held in registers between the
-// passes: WPR of the workgroup's four waves share a row (part p holds its
-// chunks p, p + WPR, ... of 512 elements), 4 / WPR rows per workgroup.  Each
+// passes: WPR waves share a row (part p holds its chunks p, p + WPR, ... of
+// 512 elements), in workgroups of four waves, or eight for the longest.  Each
 // wave sums in a fixed order (chunk, element, butterfly), the parts are
 // added in order, so a row's result does not depend on the others.
-template <int WPR, int NCH, bool CODES, bool VEC>
-__global__ void __launch_bounds__(256) k_rms_norm(NormArgs a)
+template <int WPR, int NCH, bool CODES, bool WHOLE>
+__global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256, 4) k_rms_norm(NormArgs a)
 {
-    __shared__ float red[2][4];
+    constexpr int ROWS = WPR > 4 ? 1 : 4 / WPR;              // per workgroup
+    __shared__ float red[2][WPR > 4 ? WPR : 4];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, part = wv % WPR, w0 = wv - part;
-    const int64_t r = (int64_t)blockIdx.x * (4 / WPR) + wv / WPR;
+    const int64_t r = (int64_t)blockIdx.x * ROWS + wv / WPR;
     const bool r_ok = r < a.rows;
     if (WPR == 1 && !r_ok) return;        // a whole wave; nothing below joins waves
     const int64_t rr = r_ok ? r : 0;
     auto col_of = [&](int j) { return (int64_t)lane * 8 + (int64_t)(j * WPR + part) * 512; };
+    const NormCols cc{a.cols, !WHOLE && a.cols >= 8 && a.H != a.X && a.H != a.R};
+    auto at_of = [&](int j) { return WHOLE ? col_of(j) : cc.at(col_of(j)); };
     u32x4 h[NCH], w[NCH];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
         h[j] = w[j] = u32x4{0u, 0u, 0u, 0u};
-        if (r_ok && col_of(j) < a.cols) h[j] = norm_load<VEC>(a.X + rr * a.ldx, col_of(j), a.cols, a.align_x);
+        if (r_ok && col_of(j) < a.cols) h[j] = norm_load<WHOLE>(a.X + rr * a.ldx, at_of(j), a.cols);
     }
     if (a.R) {
         u32x4 q[NCH];
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             q[j] = u32x4{0u, 0u, 0u, 0u};
-            if (r_ok && col_of(j) < a.cols) q[j] = norm_load<VEC>(a.R + rr * a.ldr, col_of(j), a.cols, a.align_r);
+            if (r_ok && col_of(j) < a.cols) q[j] = norm_load<WHOLE>(a.R + rr * a.ldr, at_of(j), a.cols);
         }
 #pragma unroll
         for (int j = 0; j < NCH; ++j) h[j] = add8_bf16(h[j], q[j]);
         if (a.H) {
 #pragma unroll
             for (int j = 0; j < NCH; ++j)
-                if (r_ok && col_of(j) < a.cols) norm_store<VEC>(a.H + rr * a.ldh, col_of(j), a.cols, a.align_h, h[j]);
+                if (r_ok && col_of(j) < a.cols) norm_store<WHOLE>(a.H + rr * a.ldh, at_of(j), a.cols, h[j]);
         }
     }
     if (a.W) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
-            if (col_of(j) < a.cols) w[j] = norm_load<VEC>(a.W, col_of(j), a.cols, a.align_w);
+            if (col_of(j) < a.cols) w[j] = norm_load<WHOLE>(a.W, at_of(j), a.cols);
     }
     float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j) ss = sumsq8(ss, h[j]);
+    for (int j = 0; j < NCH; ++j) ss = sumsq8(ss, WHOLE ? h[j] : drop_first(h[j], cc.dup(col_of(j))));
     ss = wave_sum(ss);
     if constexpr (WPR > 1) {
         if (lane == 0) red[0][wv] = ss;
@@ -172,7 +194,7 @@ __global__ void __launch_bounds__(256) k_rms_norm(NormArgs a)
 #pragma unroll
         for (int j = 0; j < NCH; ++j)
             if (r_ok && col_of(j) < a.cols)
-                norm_store<VEC>((uint16_t *)a.Y + rr * a.ldy, col_of(j), a.cols, a.align_y, h[j]);
+                norm_store<WHOLE>((uint16_t *)a.Y + rr * a.ldy, at_of(j), a.cols, h[j]);
     } else {
         float amax = 0.f;
 #pragma unroll
@@ -192,7 +214,7 @@ __global__ void __launch_bounds__(256) k_rms_norm(NormArgs a)
 #pragma unroll
             for (int j = 0; j < NCH; ++j)
                 if (col_of(j) < a.cols)
-                    norm_store_codes<VEC>((uint8_t *)a.Y + rr * a.ldy, col_of(j), a.cols, a.align_y,
+                    norm_store_codes<WHOLE>((uint8_t *)a.Y + rr * a.ldy, at_of(j), a.cols,
                                           qz.code4<F>(h[j][0], h[j][1]), qz.code4<F>(h[j][2], h[j][3]));
         };
         if (qz.fast) emit(std::true_type{});
@@ -212,9 +234,9 @@ __global__ void __launch_bounds__(256) k_rms_norm_long(NormArgs a)
     uint16_t *hrow = a.R && a.H ? a.H + r * a.ldh : nullptr;
     float ss = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048) {
-        u32x4 h = load_chunk8_bf16(x, c, a.cols, true, a.align_x);
-        if (q) h = add8_bf16(h, load_chunk8_bf16(q, c, a.cols, true, a.align_r));
-        if (hrow) norm_store<false>(hrow, c, a.cols, a.align_h, h);
+        u32x4 h = norm_load<false>(x, c, a.cols);
+        if (q) h = add8_bf16(h, norm_load<false>(q, c, a.cols));
+        if (hrow) norm_store<false>(hrow, c, a.cols, h);
         ss = sumsq8(ss, h);
     }
     ss = wave_sum(ss);
@@ -225,17 +247,17 @@ __global__ void __launch_bounds__(256) k_rms_norm_long(NormArgs a)
     auto y_of = [&](int64_t c) {
         u32x4 h;
         if (hrow) {
-            h = load_chunk8_bf16(hrow, c, a.cols, true, a.align_h);
+            h = norm_load<false>(hrow, c, a.cols);
         } else {
-            h = load_chunk8_bf16(x, c, a.cols, true, a.align_x);
-            if (q) h = add8_bf16(h, load_chunk8_bf16(q, c, a.cols, true, a.align_r));
+            h = norm_load<false>(x, c, a.cols);
+            if (q) h = add8_bf16(h, norm_load<false>(q, c, a.cols));
         }
-        const u32x4 w = a.W ? load_chunk8_bf16(a.W, c, a.cols, true, a.align_w) : u32x4{0u, 0u, 0u, 0u};
+        const u32x4 w = a.W ? norm_load<false>(a.W, c, a.cols) : u32x4{0u, 0u, 0u, 0u};
         return scale8(h, rstd, w, a.W != nullptr);
     };
     if constexpr (!CODES) {
         for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048)
-            norm_store<false>((uint16_t *)a.Y + r * a.ldy, c, a.cols, a.align_y, y_of(c));
+            norm_store<false>((uint16_t *)a.Y + r * a.ldy, c, a.cols, y_of(c));
     } else {
         float amax = 0.f;
         for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 2048) amax = absmax8(amax, y_of(c));
@@ -249,39 +271,41 @@ __global__ void __launch_bounds__(256) k_rms_norm_long(NormArgs a)
             const u32x4 y = y_of(c);
             const uint32_t w0 = qz.fast ? qz.code4<true>(y[0], y[1]) : qz.code4<false>(y[0], y[1]);
             const uint32_t w1 = qz.fast ? qz.code4<true>(y[2], y[3]) : qz.code4<false>(y[2], y[3]);
-            norm_store_codes<false>((uint8_t *)a.Y + r * a.ldy, c, a.cols, a.align_y, w0, w1);
+            norm_store_codes<false>((uint8_t *)a.Y + r * a.ldy, c, a.cols, w0, w1);
         }
     }
 }
 
 template <int WPR, int NCH>
-static hipError_t launch_norm_held(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+static hipError_t launch_norm_held(const NormArgs &a, bool codes, hipStream_t s)
 {
-    const dim3 g((unsigned)((a.rows + 4 / WPR - 1) / (4 / WPR))), b(256);
+    const bool whole = a.cols % 8 == 0;
+    constexpr int ROWS = WPR > 4 ? 1 : 4 / WPR;
+    const dim3 g((unsigned)((a.rows + ROWS - 1) / ROWS)), b(WPR > 4 ? WPR * 64 : 256);
     if (codes) {
-        if (vec) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, true, true>), g, b, 0, s, a);
+        if (whole) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, true, true>), g, b, 0, s, a);
         else hipLaunchKernelGGL((k_rms_norm<WPR, NCH, true, false>), g, b, 0, s, a);
     } else {
-        if (vec) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, false, true>), g, b, 0, s, a);
+        if (whole) hipLaunchKernelGGL((k_rms_norm<WPR, NCH, false, true>), g, b, 0, s, a);
         else hipLaunchKernelGGL((k_rms_norm<WPR, NCH, false, false>), g, b, 0, s, a);
     }
     return hipGetLastError();
 }
 
-static hipError_t launch_norm_rows(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+static hipError_t launch_norm_rows(const NormArgs &a, bool codes, hipStream_t s)
 {
-    if (a.cols <= 512) return launch_norm_held<1, 1>(a, codes, vec, s);
-    if (a.cols <= 2048) return launch_norm_held<4, 1>(a, codes, vec, s);
-    if (a.cols <= 4096) return launch_norm_held<4, 2>(a, codes, vec, s);
-    if (a.cols <= 8192) return launch_norm_held<4, 4>(a, codes, vec, s);
-    if (a.cols <= 16384) return launch_norm_held<4, 8>(a, codes, vec, s);
+    if (a.cols <= 512) return launch_norm_held<1, 1>(a, codes, s);
+    if (a.cols <= 2048) return launch_norm_held<4, 1>(a, codes, s);
+    if (a.cols <= 4096) return launch_norm_held<4, 2>(a, codes, s);
+    if (a.cols <= 8192) return launch_norm_held<4, 4>(a, codes, s);
+    if (a.cols <= 16384) return launch_norm_held<8, 4>(a, codes, s);
     if (codes) hipLaunchKernelGGL((k_rms_norm_long<true>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_rms_norm_long<false>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 // (a launch holds fewer than 2^32 threads: 2^22 rows at a time)
-hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t s)
+hipError_t launch_rms_norm(const NormArgs &a, bool codes, hipStream_t s)
 {
     constexpr int64_t kRows = (int64_t)1 << 22;
     for (int64_t r = 0; r < a.rows; r += kRows) {
@@ -293,7 +317,7 @@ hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t 
         if (b.scale) b.scale += r;
         if (b.rstd) b.rstd += r;
         b.rows = a.rows - r < kRows ? a.rows - r : kRows;
-        const hipError_t e = launch_norm_rows(b, codes, vec, s);
+        const hipError_t e = launch_norm_rows(b, codes, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -308,51 +332,69 @@ hipError_t launch_rms_norm(const NormArgs &a, bool codes, bool vec, hipStream_t 
 // same columns in every row, so dW's sums over the workgroup's rows stay in
 // its registers (NCH > 0) and go out once, as row b of `part`; a second
 // kernel adds the workgroups' rows in order.
-template <int NCH, bool VEC>
-__global__ void __launch_bounds__(256) k_rms_norm_grad(NormGradArgs a)
+template <int NCH, int NW, bool WHOLE>
+__global__ void __launch_bounds__(NW * 64) k_rms_norm_grad(NormGradArgs a)
 {
-    __shared__ float red[2][4];
+    __shared__ float red[2][NW];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    auto col_of = [&](int j) { return (int64_t)threadIdx.x * 8 + (int64_t)j * 2048; };
+    auto col_of = [&](int j) { return (int64_t)threadIdx.x * 8 + (int64_t)j * (NW * 512); };
+    const NormCols cc{a.cols, !WHOLE && a.cols >= 8};
+    auto at_of = [&](int j) { return WHOLE ? col_of(j) : cc.at(col_of(j)); };
     u32x4 w[NCH];
     float dw[NCH][8];
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
         w[j] = u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};   // ones
-        if (a.W && col_of(j) < a.cols) w[j] = norm_load<VEC>(a.W, col_of(j), a.cols, a.align_w);
+        if (a.W && col_of(j) < a.cols) w[j] = norm_load<WHOLE>(a.W, at_of(j), a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
     }
-    int turn = 0;
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    struct Row {
         u32x4 dy[NCH], h[NCH], dh[NCH];
+        float rstd;
+    };
+    auto load = [&](int64_t r, Row &w) {
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
-            dy[j] = h[j] = dh[j] = u32x4{0u, 0u, 0u, 0u};
+            w.dy[j] = w.h[j] = w.dh[j] = u32x4{0u, 0u, 0u, 0u};
             if (col_of(j) < a.cols) {
-                dy[j] = norm_load<VEC>(a.dY + r * a.lddy, col_of(j), a.cols, a.align_dy);
-                h[j] = norm_load<VEC>(a.H + r * a.ldh, col_of(j), a.cols, a.align_h);
-                if (a.dH) dh[j] = norm_load<VEC>(a.dH + r * a.lddh, col_of(j), a.cols, a.align_dh);
+                w.dy[j] = norm_load<WHOLE>(a.dY + r * a.lddy, at_of(j), a.cols);
+                w.h[j] = norm_load<WHOLE>(a.H + r * a.ldh, at_of(j), a.cols);
+                if (a.dH) w.dh[j] = norm_load<WHOLE>(a.dH + r * a.lddh, at_of(j), a.cols);
             }
         }
-        const float rstd = a.rstd[r];
+        w.rstd = a.rstd[r];
+    };
+    // the next row's loads go out before this row is worked on
+    Row cur, nxt;
+    load(blockIdx.x, cur);
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+        load(r + gridDim.x < a.rows ? r + gridDim.x : r, nxt);
+        const u32x4 (&dy)[NCH] = cur.dy, (&h)[NCH] = cur.h, (&dh)[NCH] = cur.dh;
+        const float rstd = cur.rstd;
         float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < NCH; ++j)
+        for (int j = 0; j < NCH; ++j) {
+            const u32x4 dk = WHOLE ? dy[j] : drop_first(dy[j], cc.dup(col_of(j)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float plo = bf16_lo(dy[j][i]) * (bf16_lo(h[j][i]) * rstd);
-                const float phi = bf16_hi(dy[j][i]) * (bf16_hi(h[j][i]) * rstd);
+                const float plo = bf16_lo(dk[i]) * (bf16_lo(h[j][i]) * rstd);
+                const float phi = bf16_hi(dk[i]) * (bf16_hi(h[j][i]) * rstd);
                 dw[j][2 * i] += plo;
                 dw[j][2 * i + 1] += phi;
                 dot = __builtin_fmaf(plo, bf16_lo(w[j][i]), dot);
                 dot = __builtin_fmaf(phi, bf16_hi(w[j][i]), dot);
             }
+        }
         dot = wave_sum(dot);
         // (two sets of slots in turn: one barrier per row)
         if (lane == 0) red[turn][wv] = dot;
         __syncthreads();
-        const float c = (((red[turn][0] + red[turn][1]) + red[turn][2]) + red[turn][3]) / (float)a.cols;
+        float c = red[turn][0];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) c += red[turn][k];
+        c /= (float)a.cols;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
             u32x4 dx;
@@ -363,15 +405,26 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad(NormGradArgs a)
                 dx[i] = pack_bf16x2(__builtin_fmaf(rstd, glo - xlo * c, bf16_lo(dh[j][i])),
                                     __builtin_fmaf(rstd, ghi - xhi * c, bf16_hi(dh[j][i])));
             }
-            if (col_of(j) < a.cols) norm_store<VEC>(a.dX + r * a.lddx, col_of(j), a.cols, a.align_dx, dx);
+            if (col_of(j) < a.cols) norm_store<WHOLE>(a.dX + r * a.lddx, at_of(j), a.cols, dx);
         }
+        cur = nxt;
     }
     if (a.part) {
+        float *part = a.part + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
-        for (int j = 0; j < NCH; ++j)
+        for (int j = 0; j < NCH; ++j) {
+            if (col_of(j) >= a.cols) continue;
+            float *at = part + at_of(j);
+            if (WHOLE || col_of(j) + 8 <= a.cols) {
+                store16(at, __builtin_bit_cast(u32x4, f32x4{dw[j][0], dw[j][1], dw[j][2], dw[j][3]}));
+                store16(at + 4, __builtin_bit_cast(u32x4, f32x4{dw[j][4], dw[j][5], dw[j][6], dw[j][7]}));
+            } else {
+                const int dup = cc.dup(col_of(j));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col_of(j) + i < a.cols) a.part[(int64_t)blockIdx.x * a.cols + col_of(j) + i] = dw[j][i];
+                for (int i = 0; i < 8; ++i)
+                    if (i >= dup && at_of(j) + i < a.cols) at[i] = dw[j][i];
+            }
+        }
     }
 }
 
@@ -437,22 +490,24 @@ hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW,
     return hipGetLastError();
 }
 
-template <int NCH>
-static void launch_norm_grad_held(const NormGradArgs &a, int grid, bool vec, hipStream_t s)
+template <int NCH, int NW>
+static void launch_norm_grad_held(const NormGradArgs &a, int grid, hipStream_t s)
 {
-    if (vec) hipLaunchKernelGGL((k_rms_norm_grad<NCH, true>), dim3(grid), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_rms_norm_grad<NCH, false>), dim3(grid), dim3(256), 0, s, a);
+    if (a.cols % 8 == 0) hipLaunchKernelGGL((k_rms_norm_grad<NCH, NW, true>), dim3(grid), dim3(NW * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_rms_norm_grad<NCH, NW, false>), dim3(grid), dim3(NW * 64), 0, s, a);
 }
 
 int norm_grad_parts(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
 
-hipError_t launch_rms_norm_grad(const NormGradArgs &a, bool vec, hipStream_t s)
+hipError_t launch_rms_norm_grad(const NormGradArgs &a, hipStream_t s)
 {
     const int grid = norm_grad_parts(a.rows);
-    if (a.cols <= 2048) launch_norm_grad_held<1>(a, grid, vec, s);
-    else if (a.cols <= 4096) launch_norm_grad_held<2>(a, grid, vec, s);
-    else if (a.cols <= 8192) launch_norm_grad_held<4>(a, grid, vec, s);
-    else if (a.cols <= 16384) launch_norm_grad_held<8>(a, grid, vec, s);
+    // (up to 226 registers per lane: rows past 6144 elements take eight waves)
+    if (a.cols <= 2048) launch_norm_grad_held<1, 4>(a, grid, s);
+    else if (a.cols <= 4096) launch_norm_grad_held<2, 4>(a, grid, s);
+    else if (a.cols <= 6144) launch_norm_grad_held<3, 4>(a, grid, s);
+    else if (a.cols <= 8192) launch_norm_grad_held<2, 8>(a, grid, s);
+    else if (a.cols <= 16384) launch_norm_grad_held<4, 8>(a, grid, s);
     else hipLaunchKernelGGL(k_rms_norm_grad_long, dim3(grid), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !a.dW ? e : launch_norm_dw(a.part, grid, a.cols, a.dW, s);

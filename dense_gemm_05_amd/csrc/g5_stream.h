@@ -9,6 +9,37 @@ namespace g5 {
 
 namespace {
 
+// 16 bytes at any address: one load or store instruction (global memory takes
+// any alignment; one that crosses a line is slower).
+__device__ __forceinline__ u32x4 load16(const void *p)
+{
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ void store16(void *p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+// 8 bf16 (16 codes) of which the first `n` lie in the row, zeros behind them.
+__device__ __forceinline__ u32x4 load_part8(const uint16_t *p, int n)
+{
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < n ? (uint32_t)p[i] : 0u;
+    return u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+}
+__device__ __forceinline__ u32x4 load_part16(const uint8_t *p, int n)
+{
+    u32x4 v;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = 4 * w + i < n ? (uint32_t)p[4 * w + i] : 0u;
+        v[w] = e[0] | e[1] << 8 | e[2] << 16 | e[3] << 24;
+    }
+    return v;
+}
+
 // 16 E4M3FN codes as 16 bf16 values (each exact), in order.
 __device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
 {
@@ -58,8 +89,8 @@ struct RowStream {
     static constexpr int XP = kPieces<CODES>, KS = kStep<CODES>;
     u32x4 w[D][RB][2], x[D][NC][XP];
 
-    // Whole step s of 16-byte aligned rows: wave-uniform bases and the lane's
-    // byte offsets (its row and 16 g).  A lane without a token leaves its x
+    // Whole step s: wave-uniform bases and the lane's byte offsets (its row
+    // and 16 g).  A lane without a token leaves its x
     // as it is (its column of the product is never read).
     __device__ __forceinline__ void load_w(int j, const char *const (&wbase)[RB], const uint32_t (&woff)[RB], int s)
     {
@@ -67,7 +98,7 @@ struct RowStream {
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[j][r][h] = *(const u32x4 *)((wbase[r] + (int64_t)s * 128 + 64 * h) + woff[r]);
+                w[j][r][h] = load16((wbase[r] + (int64_t)s * 128 + 64 * h) + woff[r]);
     }
     __device__ __forceinline__ void load_x(int j, const char *xbase, const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s)
     {
@@ -76,12 +107,11 @@ struct RowStream {
             if (xok[c]) {
 #pragma unroll
                 for (int q = 0; q < XP; ++q)
-                    x[j][c][q] = *(const u32x4 *)((xbase + ((int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
+                    x[j][c][q] = load16((xbase + ((int64_t)s * KS + x_piece<CODES>(q, 0)) * 2) + xoff[c]);
             }
     }
 
-    // The last, partial step (K a whole number of 16-byte pieces): pieces
-    // past K are zeros.
+    // The last, partial step: zeros past K.
     __device__ __forceinline__ void load_tail(const char *const (&wbase)[RB], const uint32_t (&woff)[RB], const char *xbase,
                                               const uint32_t (&xoff)[NC], const bool (&xok)[NC], int s, int K, int g)
     {
@@ -89,37 +119,25 @@ struct RowStream {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t at = s * 128 + 64 * h;                     // + 16 g, in woff
-            const bool in = (int)(at + 16 * g) < (CODES ? K : 2 * K);
+            const int left = K - (int)(at + 16 * g) / (CODES ? 1 : 2);
 #pragma unroll
-            for (int r = 0; r < RB; ++r) w[0][r][h] = in ? *(const u32x4 *)(wbase[r] + (woff[r] + at)) : zero;
+            for (int r = 0; r < RB; ++r) {
+                const char *p = wbase[r] + (woff[r] + at);
+                w[0][r][h] = zero;
+                if (left >= (CODES ? 16 : 8)) w[0][r][h] = load16(p);
+                else if (left > 0) w[0][r][h] = CODES ? load_part16((const uint8_t *)p, left) : load_part8((const uint16_t *)p, left);
+            }
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int q = 0; q < XP; ++q)
-                x[0][c][q] = xok[c] && s * KS + x_piece<CODES>(q, g) < K
-                                 ? *(const u32x4 *)(xbase + (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0))))
-                                 : zero;
-    }
-
-    // Step s of rows of any alignment, zero-filled past K.
-    __device__ __forceinline__ void load_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                             const bool (&xok)[NC], int align_x, int s, int K, int g)
-    {
-#pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (CODES)
-                    w[0][r][h] = load_chunk16_u8((const uint8_t *)wrow[r], s * 128 + 64 * h + 16 * g, K, true, align_w);
-                else
-                    w[0][r][h] = load_chunk8_bf16((const uint16_t *)wrow[r], s * 64 + 32 * h + 8 * g, K, true, align_w);
+            for (int q = 0; q < XP; ++q) {
+                const int left = xok[c] ? K - s * KS - x_piece<CODES>(q, g) : 0;
+                const char *p = xbase + (xoff[c] + 2 * (uint32_t)(s * KS + x_piece<CODES>(q, 0)));
+                x[0][c][q] = zero;
+                if (left >= 8) x[0][c][q] = load16(p);
+                else if (left > 0) x[0][c][q] = load_part8((const uint16_t *)p, left);
             }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int q = 0; q < XP; ++q)
-                x[0][c][q] = load_chunk8_bf16(xrow[c], s * KS + x_piece<CODES>(q, g), K, xok[c], align_x);
     }
 
     __device__ __forceinline__ void mma(int j, f32x4 (&acc)[RB][NC]) const
@@ -140,7 +158,7 @@ struct RowStream {
             }
     }
 
-    // Steps s0 .. s1 - 1 of K (the last may be partial), 16-byte aligned.
+    // Steps s0 .. s1 - 1 of K (the last may be partial).
     // tokens(xoff, xok) gives the lane's token rows, asked for when the first
     // weights are on their way.
     template <class F>
@@ -189,15 +207,6 @@ struct RowStream {
             if (s + j < sw) mma(j, acc);
         if (s0 < s1 && s1 > whole) {
             load_tail(wbase, woff, xbase, xoff, xok, whole, K, g);
-            mma(0, acc);
-        }
-    }
-    __device__ __forceinline__ void run_any(const char *const (&wrow)[RB], int align_w, const uint16_t *const (&xrow)[NC],
-                                            const bool (&xok)[NC], int align_x, int s0, int s1, int K, int g,
-                                            f32x4 (&acc)[RB][NC])
-    {
-        for (int s = s0; s < s1; ++s) {
-            load_any(wrow, align_w, xrow, xok, align_x, s, K, g);
             mma(0, acc);
         }
     }
