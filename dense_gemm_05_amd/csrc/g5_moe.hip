@@ -29,24 +29,34 @@ namespace {
 constexpr int kMoeWaves = 4;
 constexpr int kMoeThreads = kMoeWaves * 64;
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float max_dpp(float v)
+// A logit as a key that orders like it: 0 for -inf and NaN (never chosen),
+// the same for both zeros.
+__device__ __forceinline__ uint32_t logit_key(float x)
 {
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xf,
-                                                               false)));
+    if (!(x > -__builtin_inff())) return 0u;
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return (b >> 31) ? ~b : b | 0x80000000u;
 }
-// The largest of the wave's values, in every lane.
-__device__ __forceinline__ float wave_max_dpp(float v)
+__device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k); }
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v)
 {
-    // lane i takes the maximum with lanes i - 1, i - 2, i - 4, i - 8 of its
-    // row of 16, then with the rows before: lane 63 has all
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+    return o > v ? o : v;
+}
+// The largest of the wave's keys, in every lane: lane i takes the maximum
+// with lanes i - 1, i - 2, i - 4, i - 8 of its row of 16, then with the rows
+// before, so that lane 63 has all.
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v)
+{
     v = max_dpp<0x111, 0xf>(v);
     v = max_dpp<0x112, 0xf>(v);
     v = max_dpp<0x114, 0xf>(v);
     v = max_dpp<0x118, 0xf>(v);
     v = max_dpp<0x142, 0xa>(v);
     v = max_dpp<0x143, 0xc>(v);
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -57,36 +67,24 @@ __device__ __forceinline__ float wave_sum(float v)
 }
 
 // One token's routing, by one wave: lane l holds logits l, l + 64, ...
-// (NV of them).  Each of the topk turns takes the largest remaining one, the
+// (NV of them).  Each of the topk turns takes the largest remaining key, the
 // lowest index among equals; lane s ends up with slot s: its expert (-1:
 // none) and gate.
 template <int NV>
-__device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lane, int &id, float &gate)
+__device__ __forceinline__ void route_token(const MoeArgs &a, const float (&x)[NV], int lane, int &id, float &gate)
 {
-    const float *lg = a.logits + t * a.ldl;
-    const float ninf = -__builtin_inff();
-    float v[NV];
+    uint32_t v[NV], my = 0u;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int e = lane + 64 * j;
-        const float x = e < a.E ? lg[e] : ninf;
-        v[j] = x == x ? x : ninf;
-    }
-    float m = 0.f, all = 0.f, my = ninf;
+    for (int j = 0; j < NV; ++j) v[j] = logit_key(x[j]);
+    float m = 0.f;
     id = -1;
     for (int s = 0; s < a.topk; ++s) {
-        float best = v[0];
+        uint32_t best = v[0];
 #pragma unroll
-        for (int j = 1; j < NV; ++j) best = fmaxf(best, v[j]);
-        best = wave_max_dpp(best);
-        if (!(best > ninf)) break;          // nothing left to choose
-        if (s == 0) {
-            m = best;
-            if (!a.renormalize) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) all += v[j] > ninf ? expf(v[j] - m) : 0.f;
-            }
-        }
+        for (int j = 1; j < NV; ++j) best = v[j] > best ? v[j] : best;
+        best = wave_max_key(best);
+        if (best == 0u) break;              // nothing left to choose
+        if (s == 0) m = key_logit(best);
         int at = -1;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -99,10 +97,16 @@ __device__ __forceinline__ void route_token(const MoeArgs &a, int64_t t, int lan
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (at == lane + 64 * j) v[j] = ninf;
+            if (at == lane + 64 * j) v[j] = 0u;
     }
-    const float p = id >= 0 ? expf(my - m) : 0.f;
-    const float sum = wave_sum(a.renormalize ? p : all);
+    const float p = id >= 0 ? expf(key_logit(my) - m) : 0.f;
+    float all = p;
+    if (!a.renormalize) {
+        all = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) all += x[j] > -__builtin_inff() ? expf(x[j] - m) : 0.f;
+    }
+    const float sum = wave_sum(all);
     gate = id >= 0 ? p / sum : 0.f;
 }
 
@@ -119,12 +123,26 @@ __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
     __shared__ int sums[2][16];
     static_assert(kMoeMaxTokens == 64 && NV * 64 <= 1024, "a word of bits per expert, a thread per expert");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, threads = blockDim.x;
+    // the logits of all the wave's tokens first
+    constexpr int PER = kMoeMaxTokens / 16;
+    const int waves = threads / 64;          // T, or 16 for more tokens
+    float v[PER][NV];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int t = wave + i * waves, e = lane + 64 * j;
+            v[i][j] = t < (int)a.T && e < (int)a.E ? a.logits[t * a.ldl + e] : -__builtin_inff();
+        }
     for (int i = tid; i < NV * 64; i += threads) mask[i] = 0ull;
     __syncthreads();
-    for (int t = wave; t < (int)a.T; t += threads / 64) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int t = wave + i * waves;
+        if (t >= (int)a.T) break;
         int id;
         float gate;
-        route_token<NV>(a, t, lane, id, gate);
+        route_token<NV>(a, v[i], lane, id, gate);
         if (lane < a.topk) {
             const int p = t * a.topk + lane;
             ids[p] = id;
