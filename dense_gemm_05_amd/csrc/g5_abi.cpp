@@ -264,6 +264,10 @@ int find_config_by_name(const char *name)
 // Configurations compiled with the fused epilogues (and with fp8 operands).
 bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256x256 || id == CFG_BF16_128x128; }
 
+// The small-M kernel of the projection with adapters: rows of any alignment;
+// it adds 32-bit byte offsets of 16 rows.
+bool lora_streams(const Problem &p) { return p.M <= 16 && p.lda < (1 << 27) && p.ldb < (1 << 27); }
+
 bool config_fits(const Problem &p, int id)
 {
     const ConfigInfo &c = kConfigs[id];
@@ -272,7 +276,7 @@ bool config_fits(const Problem &p, int id)
         if (b_trans(p)) return id == CFG_DECODE_NT && p.M <= 16 && p.batch <= 65535;   // (affine only)
         return (id == CFG_DECODE_64 || id == CFG_DECODE_SPLIT) && p.M <= 16 && p.batch <= 65535;
     }
-    if (p.lora) return has_epilogues(id) || (id == CFG_DECODE_NT && p.M <= 16);   // g5_lora.hip's kernels
+    if (p.lora) return has_epilogues(id) || (id == CFG_DECODE_NT && lora_streams(p));   // g5_lora.hip's kernels
     if (epi_of(p) != EPI_NONE) return has_epilogues(id);
     if (p.op == GEMM_OP_FP8_NT && id == CFG_DECODE_NT) return p.M <= 16 && p.batch <= 65535;   // k_decode_nt_f8
     if (p.op == GEMM_OP_FP8_NT) return has_epilogues(id);         // fp8 ring kernels: 256x192, 256x256, 128x128
@@ -354,7 +358,7 @@ int pick_variant(const Problem &p, const Plan &pl, bool *even)
         return *even ? 1 : 0;
     }
     if (pl.config == CFG_DECODE_NT) {      // 16-byte loads of Bt rows; 3 row blocks per workgroup for M > 1
-        *even = pl.align_b >= 16;
+        *even = p.lora || pl.align_b >= 16;
         return *even ? (p.M > 1 ? 2 : 1) : -1;
     }
     if (c.family == GEMM_FAMILY_DECODE) {
@@ -448,7 +452,7 @@ int select_plan(const Problem &p, Plan &pl, bool ws)
         // 256^3 measured 9.4 us with the double-buffered 64x64 kernel).
         pl.config = CFG_F32_32x32_WK;
     } else if ((p.op == GEMM_OP_BF16_NT || p.op == GEMM_OP_BF16_NT_AFFINE || is_fp8(p)) && p.M <= 16 &&
-               p.batch <= 65535 && pl.align_b >= 16) {
+               p.batch <= 65535 && (p.lora ? lora_streams(p) : pl.align_b >= 16)) {
         // Small M with B transposed: a GEMV over the contiguous rows of Bt.
         pl.config = CFG_DECODE_NT;
     } else if ((p.op == GEMM_OP_BF16 || p.op == GEMM_OP_BF16_AFFINE || p.op == GEMM_OP_BF16_SILU ||
@@ -1503,7 +1507,7 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
     if (st != GEMM_OK) return st;
     const bool some = M > 0 && N > 0 && K > 0;
     g5::LoraArgs q{};
-    Range in[7] = {};
+    Range in[6] = {};
     if (some) {
         in[0] = g5::extent((uint64_t)X, 1, M, K, ldx, 0, 2);
         in[1] = g5::extent((uint64_t)Wt, 1, N, K, ldw, 0, 2);

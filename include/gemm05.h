@@ -612,7 +612,8 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
  * intermediate is rounded to bf16.  Only the chosen experts' weights are
  * read.  Deterministic, and a token's result does not depend on the others
  * in the call.  1 <= topk <= min(E, 16), E <= 1024, H and I <= 65536.
- * 16-byte aligned rows run fastest; any other alignment is taken.
+ * 16-byte aligned rows run fastest; any other alignment is taken.  An
+ * infinite weight may give NaN where the formula gives an infinity.
  * workspace: gemm_moe_workspace_size bytes, 256-byte aligned, its first
  * GEMM_WORKSPACE_COUNTER_BYTES left untouched (gemm_run's workspace serves);
  * calls that may overlap in time need workspaces of their
@@ -621,7 +622,8 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
  * w_type or c_type, factors with bf16 weights, strides below the row
  * lengths, negative expert strides, missing or misaligned pointers, an
  * output or the workspace overlapping an input or another output;
- * GEMM_ERR_WORKSPACE for a missing or small workspace. */
+ * GEMM_ERR_WORKSPACE for a missing or small workspace; GEMM_ERR_UNSUPPORTED
+ * for weight rows 2^27 bytes or more apart or token rows 2^25. */
 int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, int renormalize,
                     const uint16_t *X, int64_t ldx,
                     const float *logits, int64_t ldl,
@@ -656,14 +658,17 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
  * depend on the others.
  *
  * L == 0 or R == 0: the plain product.  K == 0: C := 0.  R <= 4096.  Any
- * alignment is taken; rows of X or Wt that are not 16-byte aligned are
- * copied first as gemm_run does.  workspace: at least
+ * alignment is taken; for M > 16 rows of X or Wt that are not 16-byte
+ * aligned are copied first as gemm_run does, and an infinite element of B_a may
+ * give NaN where the formula gives an infinity (the two parts of a value
+ * meet it apart).  workspace: at least
  * gemm_lora_workspace_size bytes, 256-byte aligned, as gemm_run's (its
  * counter region zero before and after the call).  Errors as gemm_bf16_nt,
  * and GEMM_ERR_INVALID_ARG for L or R out of range, short or negative
  * strides, missing or misaligned pointers of the adapters, C or the
  * workspace overlapping any of them; GEMM_ERR_WORKSPACE for a missing or
- * small workspace. */
+ * small workspace; GEMM_ERR_UNSUPPORTED where X or Wt spans 2 GiB or more
+ * (for M <= 16 only if its rows also lie 2^27 elements or more apart). */
 int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K,
                       const uint16_t *X, int64_t ldx,
                       const uint16_t *Wt, int64_t ldw,

@@ -156,6 +156,24 @@ def test_lora_values_stay_in_their_rows(M):
             assert torch.equal(got[m], clean[m]), m
 
 
+@pytest.mark.parametrize("kind", ["contig", "odd"])
+@pytest.mark.parametrize("order", ["one", "halves"])
+def test_lora_rows_of_sixteen_stand_alone(kind, order):
+    """Sixteen rows, all of one adapter or eight of two, each as if called
+    alone, at any alignment."""
+    M, N, K, L, R = 16, 70, 1100, 2, 20
+    x, w, a, b, scale, idx = _inputs(_gen(8), M, N, K, L, R)
+    idx = torch.zeros_like(idx) if order == "one" else torch.arange(M, dtype=torch.int32) // 8
+    dev = [_strided(t, kind) for t in (x, w, a, b)]
+    y, tol = _formula(x, w, a, b, scale, idx)
+    got = g5.gemm_bf16_nt_lora(*dev, idx.cuda(), scale=scale.cuda(), out_dtype=torch.float32)
+    _check(got.cpu().double(), y, tol + 2.0 ** -24 * y.abs(), order)
+    for m in (0, 7, 8, 15):
+        one = g5.gemm_bf16_nt_lora(dev[0][m:m + 1], *dev[1:], idx[m:m + 1].cuda(), scale=scale.cuda(),
+                                   out_dtype=torch.float32)
+        assert torch.equal(one[0], got[m]), m
+
+
 def test_lora_without_adapters_is_the_product():
     x, w, a, b, scale, idx = _inputs(_gen(5), 40, 96, 264, 2, 8)
     want = g5.gemm_bf16_nt(x.cuda(), w.cuda(), workspace=g5.Workspace())

@@ -149,6 +149,15 @@ def test_moe_refuses(bad, status):
     assert moe(**bad) == status
 
 
+@pytest.mark.parametrize("far", [dict(ldx=1 << 24), dict(ldgu=1 << 26, sgu=1 << 33), dict(ldd=1 << 26, sd=1 << 33),
+                                 dict(wt=2, ldgu=1 << 27, sgu=1 << 33), dict(wt=2, ldd=1 << 27, sd=1 << 33)])
+def test_moe_far_rows_are_refused(far):
+    """Rows farther apart than the kernels' 32-bit byte offsets reach."""
+    apart = dict(X=P + (16 << 44), L=P + (17 << 44), Wgu=P + (18 << 44), Wd=P + (19 << 44), Y=P + (20 << 44),
+                 ids=P + (21 << 44), gates=P + (22 << 44), ws=P + (23 << 44))
+    assert moe(**apart, **far) == g5.GEMM_ERR_UNSUPPORTED
+
+
 def test_moe_workspace_size():
     n = ctypes.c_uint64(1)
     f = g5.lib().gemm_moe_workspace_size
@@ -219,6 +228,20 @@ def test_lora_workspace_size():
     assert lora_size(4, 64, 32, -1, 8)[0] == INV and lora_size(-4, 64, 32, 1, 8)[0] == INV
     # rows that only 4-byte copies could read are realigned: their copy is counted
     assert lora_size(200, 640, 1024, 2, 8, ldx=1026)[1] >= CR + 200 * 1024 * 2
+
+
+def test_lora_far_rows():
+    """Rows of 2^27 elements or more do not reach the small-M kernel's 32-bit
+    offsets: a few of them go to the tiled kernels (a workspace of two bf16
+    parts instead of four slices), an operand past 2 GiB is refused."""
+    def size(M, ldx):
+        n = ctypes.c_uint64(1)
+        st = g5.lib().gemm_lora_workspace_size(M, 64, 2048, 2, 16, P + (16 << 44), ldx, P + (17 << 44), 2048,
+                                               P + (18 << 44), 64, 0, ctypes.byref(n))
+        return st, n.value
+    assert size(16, (1 << 27) - 8) == (OK, CR + 4 * 16 * 16 * 4)
+    assert size(3, 1 << 27)[0] == OK and size(3, 1 << 27)[1] != CR + 4 * 3 * 16 * 4
+    assert size(16, 1 << 27)[0] == g5.GEMM_ERR_UNSUPPORTED
 
 
 def test_lora_empty_calls_do_nothing():
