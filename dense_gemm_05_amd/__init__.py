@@ -1,6 +1,8 @@
 """Dense GEMM for AMD Instinct MI355X (gfx950): FP32 and BF16 (FP32
 accumulation), single and batched, with fused SiLU, SwiGLU and affine
-(alpha, beta, bias) epilogues (SwiGLU also with E4M3FN output),
+(alpha, beta, bias) epilogues (SwiGLU also with E4M3FN output), and the
+operators on token rows around them (RMS norm and its gradient, low-rank
+adapters, mixture-of-experts layers),
 behind the C ABI of include/gemm05.h."""
 from ._lib import (  # noqa: F401
     GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_LAUNCH, GEMM_ERR_NO_DEVICE, GEMM_ERR_WORKSPACE,
