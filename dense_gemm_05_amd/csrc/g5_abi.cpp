@@ -264,9 +264,18 @@ int find_config_by_name(const char *name)
 // Configurations compiled with the fused epilogues (and with fp8 operands).
 bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256x256 || id == CFG_BF16_128x128; }
 
-// The small-M kernel of the projection with adapters: rows of any alignment;
-// it adds 32-bit byte offsets of 16 rows.
-bool lora_streams(const Problem &p) { return p.M <= 16 && p.lda < (1 << 27) && p.ldb < (1 << 27); }
+// The small-M kernels of the projection with adapters: rows of any alignment;
+// up to 16 rows they add 32-bit byte offsets of 16 rows.  Past 16 rows every
+// 64 weight rows read all of X again, M N K / 32 bytes, which the ring kernels
+// do not: measured with 16 adapters of rank 16, K = 4096, streaming against
+// ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 43 / 45 for 128;
+// N = 12288: 44 / 53 for 48 rows, 55 / 55 for 64, 75 / 62 for 128.  So up to
+// M N = 64 x 12288.
+bool lora_streams(const Problem &p)
+{
+    if (p.M <= 16) return p.lda < (1 << 27) && p.ldb < (1 << 27);
+    return p.M <= kLoraStreamRows && p.N <= 64 * 12288 / p.M;
+}
 
 bool config_fits(const Problem &p, int id)
 {
@@ -308,6 +317,8 @@ void fill_grid(const Problem &p, Plan &pl, bool ws)
         pl.tiles_m = 1;
         // (decode_nt: three 16-row blocks per workgroup when M > 1)
         pl.tiles_n = cdiv(p.N, c.tile_n * (pl.config == CFG_DECODE_NT && p.M > 1 ? 3 : 1));
+        // (adapters, more than 16 rows: 64 weight rows per workgroup and slice of K)
+        if (p.lora && p.M > 16) pl.tiles_n = cdiv(p.N, 64);
         pl.grid = pl.tiles_n;  // x; batch goes to grid y
         if (pl.config == CFG_DECODE_SPLIT) {
             // (SwiGLU: a strip's gate and up columns are read by separate workgroups)
@@ -451,8 +462,8 @@ int select_plan(const Problem &p, Plan &pl, bool ws)
         // staged at once (one load latency per tile instead of one per slab;
         // 256^3 measured 9.4 us with the double-buffered 64x64 kernel).
         pl.config = CFG_F32_32x32_WK;
-    } else if ((p.op == GEMM_OP_BF16_NT || p.op == GEMM_OP_BF16_NT_AFFINE || is_fp8(p)) && p.M <= 16 &&
-               p.batch <= 65535 && (p.lora ? lora_streams(p) : pl.align_b >= 16)) {
+    } else if ((p.op == GEMM_OP_BF16_NT || p.op == GEMM_OP_BF16_NT_AFFINE || is_fp8(p)) &&
+               (p.lora ? lora_streams(p) : p.M <= 16 && p.batch <= 65535 && pl.align_b >= 16)) {
         // Small M with B transposed: a GEMV over the contiguous rows of Bt.
         pl.config = CFG_DECODE_NT;
     } else if ((p.op == GEMM_OP_BF16 || p.op == GEMM_OP_BF16_AFFINE || p.op == GEMM_OP_BF16_SILU ||
@@ -765,22 +776,34 @@ int plan_for_call(const Problem &p, const void *ws, size_t ws_bytes, Plan &pl, W
 }
 
 // The adapters' values v follow the product's own scratch.  For the small-M
-// kernel K is cut into up to 4 slices of at least 512 (by K alone, so a row's
-// result does not depend on the other rows); the adapters of a row block are
-// shared out while the grid stays within one workgroup per CU.
+// kernels K is cut into up to 4 slices of at least 512 (by K alone, so a row's
+// result does not depend on the other rows up to 16); the adapters of a row
+// block are shared out while the grid stays within one workgroup per CU of the
+// ring kernels' calls, four where the slices make the work short.
+// Past 16 rows the streaming kernel's own slices of K follow: as many as give
+// every CU two workgroups, at most 8 and at least one phase each.
 size_t lora_layout(const Problem &p, const Plan &pl, const WsLayout &L, LoraArgs &q, size_t *total)
 {
-    const bool small = pl.config == CFG_DECODE_NT;
-    const int64_t room = kNumCU / (cdiv(p.M, 16) * cdiv(q.R, 16));
+    const bool small = pl.config == CFG_DECODE_NT, rows = small && p.M > 16;
     const int64_t splits = p.K / 512 < 4 ? p.K / 512 : 4;
     q.splits = small && splits > 1 ? (int)splits : 1;
+    const int64_t room = (rows ? 4 * kNumCU / q.splits : kNumCU) / (cdiv(p.M, 16) * cdiv(q.R, 16));
     int64_t turns = p.M < 16 ? p.M : 16;
     if (turns > q.L) turns = q.L;
-    if (!small && turns > room) turns = room;
+    if ((!small || rows) && turns > room) turns = room;
     q.turns = turns < 1 ? 1 : (int)turns;
     q.ranks = (int)((q.R + 7) / 8 * 8);
     const size_t at = L.total > kCounterBytes ? L.total : kCounterBytes;
     *total = at + round256((size_t)q.splits * p.M * q.ranks * 4);
+    q.slices = q.per = 1;
+    if (rows) {
+        const int64_t phases = cdiv(p.K, 128 * lora_steps(p.M));
+        int64_t s = 2 * kNumCU / pl.tiles_n;
+        s = s > 8 ? 8 : s < 1 ? 1 : s;
+        q.per = (int)cdiv(phases, s);
+        q.slices = (int)cdiv(phases, q.per);
+        if (q.slices > 1) *total += (size_t)pl.tiles_n * q.slices * 4 * lora_row_blocks(p.M) * 1024;
+    }
     return at;
 }
 
@@ -803,6 +826,8 @@ int run(const Problem &p, void *stream, void *ws = nullptr, size_t ws_bytes = 0)
         if (!ws || need > ws_bytes) return GEMM_ERR_WORKSPACE;
         if (pl.config == CFG_DECODE_NT) lora.V = (float *)((char *)ws + at);
         else lora.V2 = (uint16_t *)((char *)ws + at);
+        lora.part = (float *)((char *)ws + at + round256((size_t)lora.splits * p.M * lora.ranks * 4));
+        lora.count = (unsigned *)ws;
     }
     st = check_device();
     if (st != GEMM_OK) return st;
@@ -1521,7 +1546,7 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
         in[4] = vec_range(scale, L, 4);
         in[5] = vec_range(idx, M, 4);
         if (in[2].hi > ((__int128)1 << 63) || in[3].hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
-        q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB, 0, 0, 0, nullptr, nullptr};
+        q = g5::LoraArgs{A, B, scale, idx, L, R, lda, strideA, ldb, strideB, 0, 0, 0, nullptr, nullptr, 0, 0, nullptr, nullptr};
         p.lora = &q;
     }
     if (some) {

@@ -201,7 +201,17 @@ struct LoraArgs {
     // bf16 parts per row, [M, 2, ranks]
     float *V;
     uint16_t *V2;
+    // 16 < M <= kLoraStreamRows on the small-M config: slices of `per` phases
+    // of K, their partial sums and one counter per 64 weight rows
+    int slices, per;
+    float *part;
+    unsigned *count;
 };
+// Steps (64 elements of K) of each of a phase's two halves, by the rows of X:
+// a phase of X fits twice in a CU's LDS (48 rows: 50 KB, 80: 63, 128: 68).
+constexpr int kLoraStreamRows = 128, kLoraSteps48 = 4, kLoraSteps80 = 3, kLoraSteps128 = 2;
+constexpr int lora_steps(int64_t M) { return M <= 48 ? kLoraSteps48 : M <= 80 ? kLoraSteps80 : kLoraSteps128; }
+constexpr int lora_row_blocks(int64_t M) { return M <= 48 ? 3 : M <= 80 ? 5 : 8; }
 hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s);
 // The product with v B^T joined: configs 256x192, 256x256, 128x128 (also
 // with K split; variants 1 and 2) and the small-M CFG_DECODE_NT.

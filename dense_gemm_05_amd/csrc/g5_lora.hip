@@ -30,6 +30,15 @@ __device__ __forceinline__ int lora_adapter(const LoraArgs &q, int64_t m, int64_
     return a >= 0 && a < q.L ? a : -1;
 }
 
+// Two values as packed pairs of bf16, v = hi + lo to 2^-16 of it (an infinite
+// value has no rest).
+__device__ __forceinline__ void two_parts(float v0, float v1, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(v0, v1);
+    lo = pack_bf16x2((hi & 0x7f80u) == 0x7f80u ? 0.f : v0 - bf16_lo(hi),
+                     (hi & 0x7f800000u) == 0x7f800000u ? 0.f : v1 - bf16_hi(hi));
+}
+
 // Calls f(a, mine) for every adapter among 16 rows, in the order of their
 // first rows; the lane's row is lane % 16 and its adapter `a_row`.
 template <class F>
@@ -121,14 +130,9 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) k_lora_shrink(GemmArgs p, L
             if (q.V) {
                 *(f32x4 *)(q.V + ((int64_t)slice * p.M + m) * q.ranks + r0 + 4 * g) = v;
             } else {
-                // two bf16 parts (an infinite value has no rest)
                 uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-                    lo[i] = pack_bf16x2((hi[i] & 0x7f80u) == 0x7f80u ? 0.f : v[2 * i] - bf16_lo(hi[i]),
-                                        (hi[i] & 0x7f800000u) == 0x7f800000u ? 0.f : v[2 * i + 1] - bf16_hi(hi[i]));
-                }
+                for (int i = 0; i < 2; ++i) two_parts(v[2 * i], v[2 * i + 1], hi[i], lo[i]);
                 uint16_t *dst = q.V2 + m * 2 * q.ranks + r0 + 4 * g;
                 *(u32x2 *)dst = u32x2{hi[0], hi[1]};
                 *(u32x2 *)(dst + q.ranks) = u32x2{lo[0], lo[1]};
@@ -358,6 +362,185 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
     }
 }
 
+// 16 < M <= 16 NC rows: the weight rows still go from HBM straight into the
+// matrix core, once for all rows of X, whose part of a phase (2 ST steps of K)
+// the workgroup stages in LDS.  A workgroup has 64 weight rows and one of
+// q.slices slices of K: wave (kh, rw) multiplies its 16 rows rw with half kh of
+// every phase.  The small work beside it, v B^T, is shared out over the slices
+// and halves 8 ranks of one slice of v at a time, an output per lane and row
+// (rows of any adapters).  The halves meet in LDS, the slices in the workspace
+// as in RingTile::join_slices, each half-wave joining every other 16 rows.
+template <int NC, int ST>
+__global__ void __launch_bounds__(512, 4) k_lora_rows(GemmArgs p, LoraArgs q)
+{
+    constexpr int KC = 2 * ST * 64, LD = KC * 2 + 16;     // (16: rows start four banks apart)
+    // a wave stages RP rows at a time, 16 bytes per lane
+    constexpr int CPR = KC / 8, RP = CPR <= 32 ? 2 : 1, XT = 2 * NC / RP;
+    static_assert(CPR * RP <= 64 && 2 * NC % RP == 0, "whole rows per wave");
+    __shared__ __attribute__((aligned(16))) char xs[16 * NC * LD];
+    __shared__ unsigned arrived;
+    static_assert(16 * NC * LD >= 8 * NC * 64 * 16, "the halves' sums fit");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = lane >> 4, li = lane & 15, rw = wave & 3, kh = wave >> 2;
+    const int wv = __builtin_amdgcn_readfirstlane(wave);
+    const int xr = RP == 2 ? lane >> 5 : 0, xl = RP == 2 ? lane & 31 : lane, xc = xl < CPR ? xl : CPR - 1;
+    const int block = (int)(blockIdx.x % (unsigned)p.tiles_n), slice = (int)(blockIdx.x / (unsigned)p.tiles_n);
+    const int M = (int)p.M, K = (int)p.K;
+    const int64_t nb = (int64_t)block * 64, nw = nb + 16 * rw;
+    const int k0 = slice * q.per * KC, k1 = slice + 1 < q.slices ? k0 + q.per * KC : K;
+    // (rows past N read the block's first, rows past M the first: not stored)
+    const uint16_t *wrow = (const uint16_t *)p.B + (nw + li < p.N ? nw + li : nb) * p.ldb;
+    f32x4 acc[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = k0; k < k1; k += KC) {
+        u32x4 w[ST][2];
+        const int kw = k + kh * ST * 64 + 8 * g;
+        const uint16_t *xcol = (const uint16_t *)p.A + (k + 8 * xc);
+        char *const to = xs + (wv * RP + xr) * LD + xc * 16;
+        if (k + KC <= K) {
+            u32x4 x[XT];
+#pragma unroll
+            for (int i = 0; i < XT; ++i) {
+                const int row = (8 * i + wv) * RP + xr;
+                x[i] = load16(xcol + (row < M ? row : 0) * p.lda);
+            }
+#pragma unroll
+            for (int j = 0; j < ST; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w[j][h] = load16(wrow + (kw + 64 * j + 32 * h));
+            __syncthreads();             // (the phase before has been read)
+#pragma unroll
+            for (int i = 0; i < XT; ++i)
+                if (CPR * RP == 64 || xl < CPR) *(u32x4 *)(to + 8 * i * RP * LD) = x[i];
+        } else {
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int j = 0; j < ST; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int at = kw + 64 * j + 32 * h, left = K - at;
+                    w[j][h] = left >= 8 ? load16(wrow + at) : left > 0 ? load_part8(wrow + at, left) : zero;
+                }
+            __syncthreads();
+            const int left = K - k - 8 * xc;
+#pragma unroll 2
+            for (int i = 0; i < XT; ++i) {
+                const int row = (8 * i + wv) * RP + xr;
+                const uint16_t *src = xcol + (row < M ? row : 0) * p.lda;
+                const u32x4 x = left >= 8 ? load16(src) : left > 0 ? load_part8(src, left) : zero;
+                if (CPR * RP == 64 || xl < CPR) *(u32x4 *)(to + 8 * i * RP * LD) = x;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const u32x4 xf = *(const u32x4 *)(xs + (16 * c + li) * LD + ((kh * ST + j) * 64 + 32 * h + 8 * g) * 2);
+                    acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[j][h]),
+                                                                     __builtin_bit_cast(bf16x8, xf), acc[c], 0, 0, 0);
+                }
+    }
+    // the halves, each keeping every other 16 rows of X, and v B^T (kept in
+    // LDS and not unrolled: the sums of all rows and the adapters' addresses
+    // do not fit the registers together)
+    f32x4 *const red = (f32x4 *)xs;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < NC; ++c) red[(wave * NC + c) * 64 + lane] = acc[c];
+    __syncthreads();
+    const int n_left = (int)(p.N - nw < 16 ? p.N - nw : 16);
+#pragma unroll 1
+    for (int c = kh; c < NC; c += 2) {
+        f32x4 *const mine = red + (rw * NC + c) * 64 + lane;
+        f32x4 sum = mine[0] + mine[4 * NC * 64];
+        const int m = 16 * c + li, a = lora_adapter(q, m, M), one = __builtin_amdgcn_readfirstlane(a);
+        // (a lane without an adapter reads one that is there and keeps nothing)
+        const uint16_t *Ba = q.B + (int64_t)(a >= 0 ? a : 0) * q.strideB + (n_left > 0 ? nw : nb) * q.ldb;
+        if (one >= 0 && !__ballot(m < M && a != one)) {
+            // rows of one adapter: the matrix core, 32 ranks at a time, each
+            // value as two bf16 parts
+            const uint16_t *Bo = q.B + (int64_t)one * q.strideB + (n_left > 0 ? nw + (li < n_left ? li : 0) : nb) * q.ldb;
+            for (int c8 = 4 * slice + g; c8 - g < q.ranks / 8; c8 += 4 * q.slices) {
+                u32x4 b = {0u, 0u, 0u, 0u};
+                uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+                if (c8 < q.ranks / 8) {
+                    f32x4 v[2];
+                    b = lora_b8<false>(q, Bo, c8);
+                    lora_v8(q, M, m < M ? m : 0, c8, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) two_parts(v[i >> 1][2 * (i & 1)], v[i >> 1][2 * (i & 1) + 1], hi[i], lo[i]);
+                }
+                const u32x4 vh = {hi[0], hi[1], hi[2], hi[3]}, vl = {lo[0], lo[1], lo[2], lo[3]};
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, vh),
+                                                              sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, vl),
+                                                              sum, 0, 0, 0);
+            }
+        } else for (int c8 = slice; c8 < q.ranks / 8; c8 += q.slices) {
+            u32x4 b[4];
+            f32x4 v[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = lora_b8<false>(q, Ba + (4 * g + i < n_left ? 4 * g + i : 0) * q.ldb, c8);
+            lora_v8(q, M, a >= 0 ? m : 0, c8, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float d = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d = __builtin_fmaf(v[j >> 1][2 * (j & 1)], bf16_lo(b[i][j]), d);
+                    d = __builtin_fmaf(v[j >> 1][2 * (j & 1) + 1], bf16_hi(b[i][j]), d);
+                }
+                if (a >= 0) sum[i] += d;
+            }
+        }
+        *mine = sum;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        if ((c & 1) == kh) acc[c] = red[(rw * NC + c) * 64 + lane];
+    if (q.slices > 1) {
+        constexpr int TILE = 4 * NC * 64 * 16;
+        char *const tile = (char *)q.part + (int64_t)block * q.slices * TILE;
+        const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(tile + (int64_t)slice * TILE, 0, TILE, 0x00020000);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if ((c & 1) == kh)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[c]), wr,
+                                                       ((rw * NC + c) * 64 + lane) * 16, 0, 16);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (tid == 0) arrived = __hip_atomic_fetch_add(q.count + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (arrived != (unsigned)(q.slices - 1)) return;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int s = 0; s < q.slices; ++s) {
+            const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(tile + (int64_t)s * TILE, 0, TILE, 0x00020000);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if ((c & 1) == kh)
+                    acc[c] += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                        rr, ((rw * NC + c) * 64 + lane) * 16, 0, 16));
+        }
+        if (tid == 0) __hip_atomic_store(q.count + block, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int m = 16 * c + li;
+        if ((c & 1) != kh || m >= M) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = nw + 4 * g + i;
+            if (n < p.N) store_out(p, 0, m, n, acc[c][i]);
+        }
+    }
+}
+
 hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t s)
 {
     const dim3 g((unsigned)((a.M + 15) / 16), (unsigned)((q.ranks + 15) / 16), (unsigned)(q.turns * q.splits));
@@ -393,6 +576,13 @@ static hipError_t launch_lora_ring(const GemmArgs &a, const LoraArgs &q, int var
 
 hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s)
 {
+    if (config_id == CFG_DECODE_NT && a.M > 16) {
+        const dim3 gr((unsigned)(grid * q.slices)), bl(512);
+        if (a.M <= 48) hipLaunchKernelGGL((k_lora_rows<3, kLoraSteps48>), gr, bl, 0, s, a, q);
+        else if (a.M <= 80) hipLaunchKernelGGL((k_lora_rows<5, kLoraSteps80>), gr, bl, 0, s, a, q);
+        else hipLaunchKernelGGL((k_lora_rows<8, kLoraSteps128>), gr, bl, 0, s, a, q);
+        return hipGetLastError();
+    }
     if (config_id == CFG_DECODE_NT) {
         // (fill_grid: three 16-row blocks of Wt per workgroup when M > 1)
         if (a.M > 1) hipLaunchKernelGGL((k_lora_decode<8, 4, 3, 2>), dim3((unsigned)grid), dim3(12 * 64), 0, s, a, q);

@@ -138,7 +138,33 @@ def test_lora_with_k_split(monkeypatch, split):
         assert not ws.buf[:g5.GEMM_WORKSPACE_COUNTER_BYTES].any()
 
 
-@pytest.mark.parametrize("M", [9, 70])
+@pytest.mark.parametrize("M,N,K,L,R,order", [
+    (17, 64, 4096, 3, 16, "mixed"), (32, 70, 1030, 2, 40, "one"), (48, 130, 515, 5, 7, "runs"),
+    (49, 65, 2048, 4, 24, "one"), (80, 1, 900, 3, 33, "runs"), (81, 200, 1288, 20, 8, "mixed"),
+    (128, 96, 3000, 2, 64, "one"), (128, 4200, 130, 9, 4, "mixed"), (65, 33000, 64, 2, 8, "runs")])
+def test_lora_streamed_rows(M, N, K, L, R, order):
+    """17 .. 128 rows: every row-block count, phases and slices of K with odd
+    ends, blocks of one adapter whose last is not full, aligned and not."""
+    _say(f"M={M} N={N} K={K} adapters={L} rank={R} {order}")
+    x, w, a, b, scale, idx = _inputs(_gen(9, M, N, K), M, N, K, L, R)
+    idx = {"mixed": idx, "one": torch.full_like(idx, L - 1), "runs": idx.sort().values}[order]
+    y, tol = _formula(x, w, a, b, scale, idx)
+    ws, outs = g5.Workspace(), []
+    for kind in ("contig", "odd"):
+        dev = [_strided(t, kind) for t in (x, w, a, b)]
+        out = torch.full((M + 2, N + 3), 3.0, device="cuda")
+        got = g5.gemm_bf16_nt_lora(*dev, idx.cuda(), scale=scale.cuda(), C=out[:M, :N], workspace=ws)
+        _check(got.cpu().double(), y, tol + 2.0 ** -24 * y.abs(), kind)
+        assert (out[M:] == 3.0).all() and (out[:, N:] == 3.0).all()
+        assert not ws.buf[:g5.GEMM_WORKSPACE_COUNTER_BYTES].any()
+        ws.buf[g5.GEMM_WORKSPACE_COUNTER_BYTES:] = 255
+        outs.append(got)
+        b16 = g5.gemm_bf16_nt_lora(*dev, idx.cuda(), scale=scale.cuda(), workspace=ws)
+        assert torch.equal(b16, got.bfloat16())
+    assert torch.equal(outs[0], outs[1])      # the alignment does not change the sums
+
+
+@pytest.mark.parametrize("M", [9, 70, 150])
 def test_lora_values_stay_in_their_rows(M):
     """NaN and infinities of other rows and other adapters reach no row."""
     N, K, L, R = 96, 264, 4, 16
