@@ -1335,7 +1335,7 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes)
     if (bytes) *bytes = 0;
     if (rows < 0 || cols < 0 || rows > 0x7fffffff || cols > ((int64_t)1 << 40)) return GEMM_ERR_INVALID_ARG;
     if (bytes && rows > 0 && cols > 0)
-        *bytes = g5::kCounterBytes + g5::round256((size_t)g5::norm_grad_parts(rows) * (size_t)cols * 4);
+        *bytes = g5::kCounterBytes + g5::round256((size_t)g5::norm_grad_parts(rows, cols) * (size_t)cols * 4);
     return GEMM_OK;
 }
 

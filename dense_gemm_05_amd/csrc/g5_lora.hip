@@ -3,13 +3,13 @@
 //   C[m] = X[m] Wt^T + s_a (X[m] A_a^T) B_a^T,   a = idx[m]
 //
 // in two launches: the low-rank values v[m] = s_a X[m] A_a^T (R per row, in
-// FP32 or as two bf16 parts) into the workspace, then the product, whose kernels add v B_a^T to the
-// FP32 sums before they are rounded once.  An adapter adds 2 R (K + N) flops
-// and R (K + N) elements to a row's 2 N K: both are small beside the
-// projection, so the product's kernels stay as they are (the weight stream of
-// the small-M kernel, the ring kernel's tiles) and the adapters join at their
-// ends, where rows of different adapters may stand next to each other in any
-// order.
+// FP32 or as two bf16 parts) into the workspace, then the product, whose
+// kernels add v B_a^T to the FP32 sums before they are rounded once.  An
+// adapter adds 2 R (K + N) flops and R (K + N) elements to a row's 2 N K: both
+// are small beside the projection, so the product is organized as without
+// adapters (up to 16 rows and up to 128 the weights' stream, beyond the ring
+// kernel's tiles) and the adapters join at its end, where rows of different
+// adapters may stand next to each other in any order.
 #include <hip/hip_runtime.h>
 
 #include "g5_device.h"
@@ -61,8 +61,8 @@ __device__ __forceinline__ void each_adapter(int a_row, F f)
 // 16-row operand, X's rows the other: a row's sums are its own whatever
 // stands in the other rows, and only rows of this adapter keep them.  Bound by
 // what one CU reads (about 35 GB/s beside the latency): with K = 4096 in four
-// slices 3.8 us for one row and 5.8 us for 16 rows of 16 adapters, in one
-// slice 11 us for 1024 rows.  The ring kernels take one slice all the same:
+// slices 3.8 us for one row, 5.2 for 16 rows of 16 adapters and 6.0 for 77, in
+// one slice 11 us for 1024 rows.  The ring kernels take one slice all the same:
 // adding four at their ends cost them 10 us and saved 3 here.  Sixteen waves,
 // or eight steps in flight, measured no faster.  WHOLE: K is a
 // multiple of 8.
@@ -264,7 +264,8 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 }  // namespace
 
 // The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
-// sums.
+// sums: 1024 x 12288 x 4096 with two adapters of rank 16 in runs of rows
+// 101 us (1.02 PFLOP/s), the product alone 102.
 template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool WHOLE>
 __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(GemmArgs p, LoraArgs q)
 {
@@ -286,9 +287,13 @@ __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(Ge
     R::store(p, smem, tc, acc);
 }
 
-// M <= 16: k_decode_nt's weight stream on NW waves, and NX more waves that
-// form v B^T of the workgroup's 16 RB columns meanwhile, an output at a time
-// per thread (R products in rank order); the last pass adds both.
+// M <= 16: the weights' stream on NW waves, and NX more waves that form v B^T
+// of the workgroup's 16 RB columns meanwhile, an output at a time per thread
+// (R products in rank order); the last pass adds both.  Bound by the stream:
+// 12288 x 4096 for one row 22 to 24 us (4.2 to 4.5 TB/s), for 16 rows of 16
+// adapters of rank 16 26 to 28 us (the product alone 22.0 and 24.2).  One row takes a
+// block of 16 weight rows per workgroup and four steps in flight, more rows
+// three blocks, which share X (the product alone: 23.8 us, 29.2 with one).
 template <int NW, int NX, int RB, int D>
 __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, LoraArgs q)
 {
@@ -366,10 +371,14 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
 // matrix core, once for all rows of X, whose part of a phase (2 ST steps of K)
 // the workgroup stages in LDS.  A workgroup has 64 weight rows and one of
 // q.slices slices of K: wave (kh, rw) multiplies its 16 rows rw with half kh of
-// every phase.  The small work beside it, v B^T, is shared out over the slices
-// and halves 8 ranks of one slice of v at a time, an output per lane and row
-// (rows of any adapters).  The halves meet in LDS, the slices in the workspace
-// as in RingTile::join_slices, each half-wave joining every other 16 rows.
+// every phase.  The halves meet in LDS.  There v B^T is added, 8 ranks (32 for
+// sixteen rows of X with one adapter, on the matrix core) to a slice in turn.
+// The slices meet in the workspace as in RingTile::join_slices.  Two
+// workgroups per CU cover each other's waits.  Bound by what a CU takes in,
+// the weights and about as much of X again from L2, and by the latencies of
+// the two or three phases that each workgroup has: 77 x 4104 x 4100 with 16
+// adapters of rank 24 27 to 28 us (the weights alone 6.6 us at 5.1 TB/s),
+// where the ring kernel took 33 and the copies of its unaligned rows 17 more.
 template <int NC, int ST>
 __global__ void __launch_bounds__(512, 4) k_lora_rows(GemmArgs p, LoraArgs q)
 {

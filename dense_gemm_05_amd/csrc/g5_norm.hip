@@ -136,6 +136,10 @@ __device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps)
 // 512 elements), in workgroups of four waves, or eight for the longest.  Each
 // wave sums in a fixed order (chunk, element, butterfly), the parts are
 // added in order, so a row's result does not depend on the others.
+// Bound by HBM (2 bytes per element each for x, r, h and y, one for codes):
+// 16384 x 8192 with a residual 194 us, 5.5 TB/s; 1024 x 4096 to codes 9.5 us,
+// 3.1 TB/s, of which about 3 us are the launch and one load's latency, all
+// that 1 x 4096 takes (3.1 us).
 template <int WPR, int NCH, bool CODES, bool WHOLE>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256, 4) k_rms_norm(NormArgs a)
 {
@@ -294,6 +298,9 @@ static hipError_t launch_norm_held(const NormArgs &a, bool codes, hipStream_t s)
 
 static hipError_t launch_norm_rows(const NormArgs &a, bool codes, hipStream_t s)
 {
+    // The fewest waves that hold a row: 131072 x 512 takes 48 us with a wave
+    // per row and 104 with four (three of them idle), 16384 x 4096 44 us with
+    // four and 46 with eight.
     if (a.cols <= 512) return launch_norm_held<1, 1>(a, codes, s);
     if (a.cols <= 2048) return launch_norm_held<4, 1>(a, codes, s);
     if (a.cols <= 4096) return launch_norm_held<4, 2>(a, codes, s);
@@ -331,7 +338,11 @@ hipError_t launch_rms_norm(const NormArgs &a, bool codes, hipStream_t s)
 // One pass: workgroup b takes rows b, b + gridDim.x, ...; a thread owns the
 // same columns in every row, so dW's sums over the workgroup's rows stay in
 // its registers (NCH > 0) and go out once, as row b of `part`; a second
-// kernel adds the workgroups' rows in order.
+// kernel adds the workgroups' rows in order.  The next row is loaded while
+// this one is summed.  Bound by HBM (8 bytes per element with dH): 8192 x 4096
+// 46 us, 5.8 TB/s, and 4.9 us for dW; 1000 x 4100, whose rows start at any
+// 8 bytes, 13.3 and 5.2 us, where a workgroup has two rows and the latency of
+// its first load shows.
 template <int NCH, int NW, bool WHOLE>
 __global__ void __launch_bounds__(NW * 64) k_rms_norm_grad(NormGradArgs a)
 {
@@ -497,11 +508,19 @@ static void launch_norm_grad_held(const NormGradArgs &a, int grid, hipStream_t s
     else hipLaunchKernelGGL((k_rms_norm_grad<NCH, NW, false>), dim3(grid), dim3(NW * 64), 0, s, a);
 }
 
-int norm_grad_parts(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+// Two workgroups per CU, four for rows of up to 1024 elements, which leave
+// more of a workgroup's time to the loads' latency: 16384 x 1024 27.2 us with
+// 1024 workgroups, 34.8 with 512 and 56.7 with 256, while 8192 x 4096 takes
+// 42.7 with 512, 44.0 with 256 and 46.1 with 1024 (no dH).
+int norm_grad_parts(int64_t rows, int64_t cols)
+{
+    const int64_t most = cols <= 1024 ? 1024 : 512;
+    return (int)(rows < most ? rows : most);
+}
 
 hipError_t launch_rms_norm_grad(const NormGradArgs &a, hipStream_t s)
 {
-    const int grid = norm_grad_parts(a.rows);
+    const int grid = norm_grad_parts(a.rows, a.cols);
     // (up to 226 registers per lane: rows past 6144 elements take eight waves)
     if (a.cols <= 2048) launch_norm_grad_held<1, 4>(a, grid, s);
     else if (a.cols <= 4096) launch_norm_grad_held<2, 4>(a, grid, s);
