@@ -270,11 +270,11 @@ bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256
 // do not: measured with 16 adapters of rank 16, K = 4096, streaming against
 // ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 43 / 45 for 128;
 // N = 12288: 44 / 53 for 48 rows, 55 / 55 for 64, 75 / 62 for 128.  So up to
-// M N = 64 x 12288.
+// M N = 64 x 12288 (and columns that 32 bits count).
 bool lora_streams(const Problem &p)
 {
     if (p.M <= 16) return p.lda < (1 << 27) && p.ldb < (1 << 27);
-    return p.M <= kLoraStreamRows && p.N <= 64 * 12288 / p.M;
+    return p.M <= kLoraStreamRows && p.N <= 64 * 12288 / p.M && p.K <= 1 << 30;
 }
 
 bool config_fits(const Problem &p, int id)

@@ -264,8 +264,8 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 }  // namespace
 
 // The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
-// sums: 1024 x 12288 x 4096 with two adapters of rank 16 in runs of rows
-// 101 us (1.02 PFLOP/s), the product alone 102.
+// sums: 1024 x 12288 x 4096 with eight adapters of rank 16 in runs of rows
+// 101 to 104 us (1.0 PFLOP/s), the product alone 102.
 template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool WHOLE>
 __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(GemmArgs p, LoraArgs q)
 {

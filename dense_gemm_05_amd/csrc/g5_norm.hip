@@ -340,9 +340,9 @@ hipError_t launch_rms_norm(const NormArgs &a, bool codes, hipStream_t s)
 // its registers (NCH > 0) and go out once, as row b of `part`; a second
 // kernel adds the workgroups' rows in order.  The next row is loaded while
 // this one is summed.  Bound by HBM (8 bytes per element with dH): 8192 x 4096
-// 46 us, 5.8 TB/s, and 4.9 us for dW; 1000 x 4100, whose rows start at any
-// 8 bytes, 13.3 and 5.2 us, where a workgroup has two rows and the latency of
-// its first load shows.
+// 46 us, 5.8 TB/s, and 4.9 us for dW; 1000 x 4100 without dH, whose rows start
+// at any 8 bytes, 13.3 and 5.2 us, where a workgroup has two rows and the
+// latency of its first load shows.
 template <int NCH, int NW, bool WHOLE>
 __global__ void __launch_bounds__(NW * 64) k_rms_norm_grad(NormGradArgs a)
 {

@@ -658,17 +658,18 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
  * depend on the others.
  *
  * L == 0 or R == 0: the plain product.  K == 0: C := 0.  R <= 4096.  Any
- * alignment is taken; for M > 16 rows of X or Wt that are not 16-byte
- * aligned are copied first as gemm_run does, and an infinite element of B_a may
- * give NaN where the formula gives an infinity (the two parts of a value
- * meet it apart).  workspace: at least
+ * alignment is taken; past 128 rows, and past 16 with M N > 786432, rows of
+ * X or Wt that are not 16-byte aligned are copied first as gemm_run does.
+ * For M > 16 an infinite element of B_a may give NaN where the formula gives
+ * an infinity (the two parts of a value meet it apart).  workspace: at least
  * gemm_lora_workspace_size bytes, 256-byte aligned, as gemm_run's (its
  * counter region zero before and after the call).  Errors as gemm_bf16_nt,
  * and GEMM_ERR_INVALID_ARG for L or R out of range, short or negative
  * strides, missing or misaligned pointers of the adapters, C or the
  * workspace overlapping any of them; GEMM_ERR_WORKSPACE for a missing or
  * small workspace; GEMM_ERR_UNSUPPORTED where X or Wt spans 2 GiB or more
- * (for M <= 16 only if its rows also lie 2^27 elements or more apart). */
+ * and the call is one for the tiled kernels (M > 128; M > 16 and M N > 786432
+ * or K > 2^30; M <= 16 and rows 2^27 elements or more apart). */
 int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K,
                       const uint16_t *X, int64_t ldx,
                       const uint16_t *Wt, int64_t ldw,

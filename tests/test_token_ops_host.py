@@ -244,6 +244,17 @@ def test_lora_far_rows():
     assert size(16, 1 << 27)[0] == g5.GEMM_ERR_UNSUPPORTED
 
 
+def test_lora_long_rows():
+    """Past 2^30 columns, or 128 rows, an operand of 2 GiB is refused."""
+    def status(M, K):
+        n = ctypes.c_uint64(1)
+        return g5.lib().gemm_lora_workspace_size(M, 64, K, 2, 16, P + (16 << 44), K, P + (17 << 44), K, P + (18 << 44), 64,
+                                                 0, ctypes.byref(n))
+    assert status(17, 1 << 30) == OK and status(128, 1 << 26) == OK
+    assert status(17, (1 << 30) + 8) == g5.GEMM_ERR_UNSUPPORTED
+    assert status(129, 1 << 26) == g5.GEMM_ERR_UNSUPPORTED
+
+
 def test_lora_empty_calls_do_nothing():
     assert lora(M=0, X=None, ws=None) == OK and lora(N=0, ldc=0, ws=None) == OK
 
