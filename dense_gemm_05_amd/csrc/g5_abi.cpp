@@ -1384,10 +1384,10 @@ int gemm_rms_norm_backward(int64_t rows, int64_t cols, const uint16_t *dY, int64
 // ---- mixture-of-experts layer for a few tokens
 // Scratch after the counter region, each part 256-byte aligned.
 struct MoeLayout {
-    size_t ids, gates, n_items, items, pairs, z, total;
+    size_t ids, gates, n_items, items, pairs, z, halves, arrived, total;
     int64_t ldz, zplane;
 };
-static MoeLayout moe_layout(int64_t T, int64_t I, int64_t E, int64_t topk)
+static MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk)
 {
     MoeLayout L;
     const size_t pairs = (size_t)T * topk;
@@ -1399,7 +1399,10 @@ static MoeLayout moe_layout(int64_t T, int64_t I, int64_t E, int64_t topk)
     L.items = L.n_items + 256;
     L.pairs = L.items + g5::round256((size_t)g5::moe_items(T, E, topk) * sizeof(g5::MoeItem));
     L.z = L.pairs + g5::round256(pairs * 4);
-    L.total = L.z + g5::round256((size_t)L.zplane * 4);
+    L.halves = L.z + g5::round256((size_t)L.zplane * 4);
+    const size_t blocks = g5::moe_halves(T, H) ? (size_t)(H + 31) / 32 : 0;
+    L.arrived = L.halves + blocks * 2 * g5::kMoeMaxTokens * 32 * 4;
+    L.total = L.arrived + g5::round256(blocks * 4);
     return L;
 }
 static bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk)
@@ -1412,7 +1415,7 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
 {
     if (bytes) *bytes = 0;
     if (!moe_sizes_ok(T, H, I, E, topk)) return GEMM_ERR_INVALID_ARG;
-    if (bytes && T > 0) *bytes = moe_layout(T, I, E, topk).total;
+    if (bytes && T > 0) *bytes = moe_layout(T, H, I, E, topk).total;
     return GEMM_OK;
 }
 
@@ -1444,7 +1447,7 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
                         weights ? g5::extent((uint64_t)Wgu, E, 2 * I, H, ldgu, strideGu, ew) : none,
                         weights ? g5::extent((uint64_t)Wd, E, H, I, ldd, strideD, ew) : none,
                         vec_range(scale_gu, E * 2 * I, 4), vec_range(scale_d, E * H, 4)};
-    const MoeLayout L = moe_layout(T, I, E, topk);
+    const MoeLayout L = moe_layout(T, H, I, E, topk);
     const Range out[] = {H > 0 ? g5::extent((uint64_t)Y, 1, T, H, ldy, 0, ec) : none, vec_range(ids, T * topk, 4),
                          vec_range(gates, T * topk, 4),
                          workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)L.total}
@@ -1491,6 +1494,8 @@ int gemm_moe_swiglu(int64_t T, int64_t H, int64_t I, int64_t E, int64_t topk, in
     a.z = (uint16_t *)(ws + L.z);
     a.ldz = L.ldz;
     a.zplane = L.zplane;
+    a.halves = (float *)(ws + L.halves);
+    a.arrived = (unsigned *)(ws + L.arrived);
     const hipError_t e = g5::launch_moe(a, codes, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }

@@ -162,6 +162,8 @@ inline int64_t moe_items(int64_t T, int64_t E, int64_t topk)
     const int64_t pairs = T * topk, most = E + pairs / moe_chunk(T);
     return most < pairs ? most : pairs;
 }
+// Whether the down kernel's workgroups take half of K each.
+inline bool moe_halves(int64_t T, int64_t H) { return T > 16 && H > 2048; }
 struct MoeArgs {
     const uint16_t *X;
     const float *logits;
@@ -184,6 +186,10 @@ struct MoeArgs {
     float *w_gates;
     uint16_t *z;
     int64_t ldz, zplane;
+    // moe_halves: each half's outputs (64 x 32 floats per workgroup) and a count
+    // per 32 columns
+    float *halves;
+    unsigned *arrived;
 };
 // Rows of any alignment; 16 rows of Wgu or Wd and the T rows of X span less
 // than 2 GiB.

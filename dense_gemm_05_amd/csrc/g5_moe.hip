@@ -195,6 +195,8 @@ __global__ void __launch_bounds__(1024) k_moe_route(MoeArgs a)
         __syncthreads();
     }
     if (tid == 0) *a.n_items = ch0;
+    if (a.cols == 32)
+        for (int i = tid; i < (int)(a.H + 31) / 32; i += threads) a.arrived[i] = 0u;
     for (int p = tid; p < (int)a.T * a.topk; p += threads) {
         const int e = ids[p];
         if (e >= 0) a.pairs[first[e] + __builtin_popcountll(mask[e] & ((1ull << (p / a.topk)) - 1))] = p;
@@ -326,27 +328,35 @@ constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
 // A piece's products for its tokens, 8 to a block of the matrix core's 16
 // columns: columns 0 .. 7 take z's hi parts, 8 .. 15 the lo parts, and the two
 // sums are added at the end.
-template <bool CODES, int NB, int D>
+template <bool CODES, int RB, int NB, int D>
 __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, int from, int slice, int n0,
-                                         const int *pairs, float (&part)[kDownSlices][kMoeMaxPairs][16])
+                                         const int *pairs, float (*part)[16 * RB])
 {
     constexpr int EB = CODES ? 1 : 2, KS = kStep<CODES>;
     const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
     const int K = (int)a.I, steps = (K + KS - 1) / KS;
     const int s0 = steps * slice / kDownSlices, s1 = steps * (slice + 1) / kDownSlices;
-    const char *const wbase[1] = {(const char *)a.Wd + ((int64_t)it.expert * a.strideD + (int64_t)n0 * a.ldd) * EB};
-    const int wrow = li < a.cols && n0 + li < (int)a.H ? li : 0;
+    // (columns past the workgroup's or H repeat its first: not stored)
+    const char *wbase[RB];
+    uint32_t woff[RB];
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+        const int n = n0 + 16 * r < (int)a.H ? n0 + 16 * r : n0;
+        wbase[r] = (const char *)a.Wd + ((int64_t)it.expert * a.strideD + (int64_t)n * a.ldd) * EB;
+        woff[r] = (uint32_t)(16 * r + li < a.cols && n + li < (int)a.H ? li : 0) * (uint32_t)(a.ldd * EB) + 16 * g;
+    }
     bool zok[NB];
     int pair[NB];
-    f32x4 acc[1][NB];
+    f32x4 acc[RB][NB];
 #pragma unroll
     for (int c = 0; c < NB; ++c) {
         const int i = from + 8 * c + (li & 7);
         zok[c] = i < it.count;
         pair[c] = zok[c] ? pairs[it.first + i] : 0;
-        acc[0][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    RowStream<CODES, 1, NB, D> b;
+    RowStream<CODES, RB, NB, D> b;
     auto tokens = [&](uint32_t (&off)[NB], bool (&ok)[NB]) {
 #pragma unroll
         for (int c = 0; c < NB; ++c) {
@@ -354,15 +364,16 @@ __device__ __forceinline__ void moe_down(const MoeArgs &a, const MoeItem &it, in
             off[c] = 2 * ((uint32_t)pair[c] * (uint32_t)a.ldz + (li < 8 ? 0u : (uint32_t)a.zplane)) + x_lane<CODES>(g);
         }
     };
-    const uint32_t woff[1] = {(uint32_t)wrow * (uint32_t)(a.ldd * EB) + 16 * g};
     b.run(wbase, woff, (const char *)a.z, tokens, s0, s1, K, g, acc);
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        f32x4 v = acc[0][c];
+    for (int r = 0; r < RB; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8, 64);
-        if (zok[c] && li < 8) *(f32x4 *)&part[slice][pair[c]][4 * g] = v;
-    }
+        for (int c = 0; c < NB; ++c) {
+            f32x4 v = acc[r][c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8, 64);
+            if (zok[c] && li < 8) *(f32x4 *)&part[pair[c]][16 * r + 4 * g] = v;
+        }
 }
 
 // A piece has 16 tokens at most: a work item's SUB chunks are pieces of their
@@ -382,8 +393,8 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
     for (int piece = wave; piece < n_items * (kDownSlices * SUB);) {
         const MoeItem it = uniform_item(items[piece / (kDownSlices * SUB)]);
         const int slice = piece % kDownSlices, from = piece / kDownSlices % SUB * 16;
-        if (it.count - from > 8) moe_down<CODES, 2, CODES ? 2 : 3>(a, it, from, slice, n0, pairs, part);
-        else if (it.count > from) moe_down<CODES, 1, CODES ? 3 : 5>(a, it, from, slice, n0, pairs, part);
+        if (it.count - from > 8) moe_down<CODES, 1, 2, CODES ? 2 : 3>(a, it, from, slice, n0, pairs, part[slice]);
+        else if (it.count > from) moe_down<CODES, 1, 1, CODES ? 3 : 5>(a, it, from, slice, n0, pairs, part[slice]);
         int p = 0;
         if (lane == 0) p = atomicAdd(&next, 1);
         piece = __builtin_amdgcn_readfirstlane(p);
@@ -405,6 +416,77 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
     else ((uint16_t *)a.Y)[t * a.ldy + n] = (uint16_t)bf16_rne(y);
 }
 
+// The same for many tokens, where z, read by every workgroup, is as much as
+// the weights: a workgroup owns 32 columns and one half of K, so z is read half
+// as often, and the two halves' outputs (FP32, the workgroup's own part of
+// a.halves) are added by whichever comes second, the first half first.  Stores
+// and loads of the halves go to the device's coherence point, and the wait and
+// barrier retire the stores before the arrival is counted, as in
+// RingTile::join_slices; the routing kernel sets the counts to zero.
+template <bool CODES>
+__global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down_halves(MoeArgs a)
+{
+    __shared__ __attribute__((aligned(16))) float part[kMoeMaxPairs][32];
+    __shared__ MoeItem items[kMoeMaxItems];
+    __shared__ int pairs[kMoeMaxPairs], next;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int block = blockIdx.x >> 1, half = blockIdx.x & 1, n0 = block * 32;
+    const int n_items = *a.n_items;
+    for (int i = threadIdx.x; i < n_items; i += kDownWaves * 64) items[i] = a.items[i];
+    for (int i = threadIdx.x; i < (int)a.T * a.topk; i += kDownWaves * 64) pairs[i] = a.pairs[i];
+    if (threadIdx.x == 0) next = kDownWaves;
+    __syncthreads();
+    for (int piece = wave; piece < n_items * 2;) {
+        const MoeItem it = uniform_item(items[piece >> 1]);
+        const int from = (piece & 1) * 16;
+        if (it.count - from > 8) moe_down<CODES, 2, 2, CODES ? 1 : 2>(a, it, from, half, n0, pairs, part);
+        else if (it.count > from) moe_down<CODES, 2, 1, 2>(a, it, from, half, n0, pairs, part);
+        int p = 0;
+        if (lane == 0) p = atomicAdd(&next, 1);
+        piece = __builtin_amdgcn_readfirstlane(p);
+    }
+    __syncthreads();
+    // a thread per column and two tokens
+    constexpr int TILE = kMoeMaxTokens * 32;
+    const int c = threadIdx.x & 31, n = n0 + c;
+    float y[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = (threadIdx.x >> 5) + 32 * j;
+        if (t >= (int)a.T || n >= (int)a.H) continue;
+#pragma unroll 4
+        for (int s = 0; s < a.topk; ++s) {
+            const int p = t * a.topk + s, e = a.w_ids[p];
+            if (e < 0) continue;
+            float v = part[p][c];
+            if (a.scale_d) v *= a.scale_d[(int64_t)e * a.H + n];
+            y[j] = __builtin_fmaf(a.w_gates[p], v, y[j]);
+        }
+    }
+    float *const mine = a.halves + (int64_t)blockIdx.x * TILE;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(mine, 0, TILE * 4, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[j]), wr, (int)(threadIdx.x + 1024 * j) * 4, 0, 16);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        next = (int)__hip_atomic_fetch_add(a.arrived + block, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (next != 1) return;
+    const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(a.halves + (int64_t)(blockIdx.x ^ 1) * TILE, 0,
+                                                                        TILE * 4, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int t = (threadIdx.x >> 5) + 32 * j;
+        const float other = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rr, (int)(threadIdx.x + 1024 * j) * 4, 0, 16));
+        const float v = half ? other + y[j] : y[j] + other;
+        if (t >= (int)a.T || n >= (int)a.H) continue;
+        if (a.out_f32) ((float *)a.Y)[t * a.ldy + n] = v;
+        else ((uint16_t *)a.Y)[t * a.ldy + n] = (uint16_t)bf16_rne(v);
+    }
+}
+
 }  // namespace
 
 template <bool CODES, bool MANY>
@@ -417,7 +499,8 @@ static hipError_t launch_moe_weights(const MoeArgs &a, hipStream_t s)
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_moe_down<CODES, MANY ? 2 : 1>), gd, bd, 0, s, a);
+    if (MANY && a.cols == 32) hipLaunchKernelGGL((k_moe_down_halves<CODES>), dim3(2 * gd.x), bd, 0, s, a);
+    else hipLaunchKernelGGL((k_moe_down<CODES, MANY ? 2 : 1>), gd, bd, 0, s, a);
     return hipGetLastError();
 }
 
@@ -427,7 +510,7 @@ hipError_t launch_moe(const MoeArgs &args, bool codes, hipStream_t s)
     a.chunk = moe_chunk(a.T);
     // hidden columns per workgroup of the down kernel: as many workgroups as
     // the 256 CUs, 16 columns at most and 4 at least
-    a.cols = a.H > 2048 ? 16 : a.H > 1024 ? 8 : 4;
+    a.cols = moe_halves(a.T, a.H) ? 32 : a.H > 2048 ? 16 : a.H > 1024 ? 8 : 4;
     const dim3 rg(1), rb((unsigned)(a.T < 16 ? a.T * 64 : 1024));
     if (a.E <= 64) hipLaunchKernelGGL((k_moe_route<1>), rg, rb, 0, s, a);
     else if (a.E <= 128) hipLaunchKernelGGL((k_moe_route<2>), rg, rb, 0, s, a);

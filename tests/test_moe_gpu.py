@@ -147,6 +147,32 @@ def test_experts(T, H, I, E, k, codes, renorm, kind):
         assert torch.equal(one[0][0], got[t]) and torch.equal(one[1][0], gi[t]) and torch.equal(one[2][0], gg[t])
 
 
+@pytest.mark.parametrize("T,H,I,E,k,codes,kind", [
+    (17, 2056, 72, 40, 2, False, "contig"), (40, 2100, 33, 2, 2, False, "odd"), (64, 4096, 64, 6, 3, True, "contig"),
+    (33, 2049, 200, 3, 1, True, "odd"), (64, 2080, 130, 30, 16, False, "padded"), (64, 2304, 1, 16, 4, True, "padded")])
+def test_experts_for_many_tokens_and_wide_rows(T, H, I, E, k, codes, kind):
+    """More than 16 tokens and 2048 hidden columns: the down kernel's halves,
+    with any number of tokens per expert and odd ends; again on scratch that
+    another call left."""
+    _say(f"T={T} H={H} I={I} E={E} topk={k} codes={codes} {kind}")
+    x, logits, wgu, wd, sgu, sd = _inputs(_gen(5, T, H, I, E, k), T, H, I, E, codes)
+    logits[T // 2], logits[1, 1:] = -torch.inf, torch.nan      # a token without experts, one with one
+    y, tol, ids, gates = _formula(x, logits, wgu, wd, sgu, sd, k, True)
+    dev = (_strided(x, kind), logits.cuda(), k, _strided(wgu, kind), _strided(wd, kind))
+    more = dict(scale_gu=None if sgu is None else sgu.cuda(), scale_d=None if sd is None else sd.cuda())
+    ws, out = g5.Workspace(), torch.full((T + 1, H + 3), 7.0, device="cuda")
+    for turn in range(2):
+        got, gi, gg = g5.moe_swiglu(*dev, **more, Y=out[:T, :H], workspace=ws)
+        assert torch.equal(gi.cpu().long(), ids)
+        _check(gg.cpu().double(), gates, 2.0 ** -20 * gates, "gates")
+        _check(got.cpu().double(), y, tol + 2.0 ** -24 * y.abs(), "y float")
+        assert (out[T:] == 7.0).all() and (out[:, H:] == 7.0).all() and not got[T // 2].any()
+        assert not ws.buf[:g5.GEMM_WORKSPACE_COUNTER_BYTES].any()
+        ws.buf[g5.GEMM_WORKSPACE_COUNTER_BYTES:] = 255
+    b16 = g5.moe_swiglu(*dev, **more, workspace=ws)[0]
+    assert torch.equal(b16, got.bfloat16())
+
+
 def test_expert_choice():
     """Ties, masked experts, rows whose mask leaves fewer than topk or none,
     NaN logits, the type's lowest value."""
