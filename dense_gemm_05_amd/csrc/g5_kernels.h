@@ -162,7 +162,11 @@ inline int64_t moe_items(int64_t T, int64_t E, int64_t topk)
     const int64_t pairs = T * topk, most = E + pairs / moe_chunk(T);
     return most < pairs ? most : pairs;
 }
-// Whether the down kernel's workgroups take half of K each.
+// Whether the down kernel's workgroups take half of K each (whole calls,
+// 4096 x 1536, halves against whole): 64 tokens on 64 experts, topk 8, bf16
+// 451 / 486 us, codes 288 / 324; 64 on 8, topk 2, bf16 89 / 96; 17 on 64,
+// topk 8, bf16 372 / 365, codes 205 / 225.  Up to 2048 columns the whole form
+// has the more workgroups.
 inline bool moe_halves(int64_t T, int64_t H) { return T > 16 && H > 2048; }
 struct MoeArgs {
     const uint16_t *X;

@@ -235,8 +235,8 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
 // rows i0 .. i0 + 15 and the up rows of the same columns.  Bound by the
 // weights' stream from HBM: 8 experts of 2 x 1536 x 4096 for one token 36 us
 // (5.6 TB/s), 56 experts for 16 tokens 242 us (5.8 TB/s; a copy reaches 5.1),
-// 64 in codes for 64 tokens 173 us (4.7 TB/s: half the bytes per matrix-core
-// step, and 32 tokens' x beside them).
+// 64 in codes for 64 tokens 172 to 182 us (4.4 to 4.7 TB/s: half the bytes per
+// matrix-core step, and 32 tokens' x beside them).
 template <bool CODES, int NC, int D>
 __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it, int i0,
                                             f32x4 (&red)[kMoeWaves][2][64])
@@ -321,9 +321,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
 // the next free one each, and leave each pair's sums in the piece's own
 // places.  The order in which pieces are taken does not matter; the halves and
 // the slots are added in order.  8 experts of 4096 x 1536 for one token 22 us
-// (4.6 TB/s), 56 for 16 tokens 128 us (5.5 TB/s), 64 in codes for 64 tokens
-// 145 us (2.8 TB/s): there every workgroup also reads all of z, 3 MB, from
-// L2, twice its own weights; without those loads it would take 103 us.
+// (4.6 TB/s), 56 for 16 tokens 128 us (5.5 TB/s).
 constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
 // A piece's products for its tokens, 8 to a block of the matrix core's 16
 // columns: columns 0 .. 7 take z's hi parts, 8 .. 15 the lo parts, and the two
@@ -416,13 +414,15 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down(MoeArgs a)
     else ((uint16_t *)a.Y)[t * a.ldy + n] = (uint16_t)bf16_rne(y);
 }
 
-// The same for many tokens, where z, read by every workgroup, is as much as
-// the weights: a workgroup owns 32 columns and one half of K, so z is read half
+// The same for many tokens, where every workgroup's z (64 tokens, topk 8: 3 MB
+// from L2) is as much as its weights, or twice with codes: a workgroup owns 32 columns and one half of K, so z is read half
 // as often, and the two halves' outputs (FP32, the workgroup's own part of
 // a.halves) are added by whichever comes second, the first half first.  Stores
 // and loads of the halves go to the device's coherence point, and the wait and
 // barrier retire the stores before the arrival is counted, as in
-// RingTile::join_slices; the routing kernel sets the counts to zero.
+// RingTile::join_slices; the routing kernel sets the counts to zero.  64
+// experts of 4096 x 1536 in codes for 64 tokens: 113 to 116 us (3.5 TB/s; 145
+// with all of K in a workgroup, 103 with none of z's loads).
 template <bool CODES>
 __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down_halves(MoeArgs a)
 {
