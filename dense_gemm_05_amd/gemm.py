@@ -85,7 +85,9 @@ class Workspace:
     replaces the buffer with a larger one when a call needs more; the old
     one is released to torch's stream-ordered allocator.  One Workspace
     serves calls on one stream (calls that may overlap in time need separate
-    workspaces)."""
+    workspaces).  A captured graph goes on using the memory it was captured
+    with: reserve the largest size that is needed before capturing, so that no
+    later call replaces it; graphs that share it must not overlap in time."""
 
     def __init__(self, device=None, nbytes=0):
         if device is None:

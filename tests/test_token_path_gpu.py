@@ -177,3 +177,57 @@ def test_norm_and_product_with_gradients(M, K, N):
     mag = rs * (aw * ay + xh * (aw * ay * xh).mean(1, keepdim=True))
     _check(dx, hd.grad, gtol + 1.01 * through + 2.0 ** -15 * mag, "dX")
     _check(dw, wd.grad, wtol + 1.01 * ((tol + 2.0 ** -17 * ay) * xh).sum(0), "dW")
+
+
+def test_two_graphs_on_one_workspace():
+    """A projection with adapters and an expert layer, both joining slices
+    through the workspace, captured apart on one workspace and replayed in
+    turn, with eager calls on it between."""
+    g = norm._gen(13)
+    M, N, K = 77, 264, 1100
+    x, w, a, b, scale, idx = (t.cuda() for t in lora._inputs(g, M, N, K, 4, 24))
+    T, H, I, E, k = 40, 2100, 72, 6, 3
+    y, logits, gu, wd, _, _ = (None if t is None else t.cuda() for t in moe._inputs(g, T, H, I, E, False))
+    ws = g5.Workspace(nbytes=64 << 20)
+    one = lambda: g5.gemm_bf16_nt_lora(x, w, a, b, idx, scale=scale, workspace=ws)     # noqa: E731
+    two = lambda: g5.moe_swiglu(y, logits, k, gu, wd, workspace=ws)[0]                 # noqa: E731
+    want, graphs, outs = [one(), two()], [], []
+    held = ws.buf.data_ptr()
+    for call in (one, two):
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(call())
+    for turn in range(4):
+        x.copy_(norm._bf((M, K), g))
+        y.copy_(norm._bf((T, H), g))
+        for graph in graphs[::1 if turn % 2 else -1]:
+            graph.replay()
+        got = [o.clone() for o in outs]
+        want = [one(), two()]
+        for n in (0, 1):
+            assert torch.equal(got[n], want[n]), f"turn {turn}, graph {n}"
+    assert ws.buf.data_ptr() == held and not ws.buf[:g5.GEMM_WORKSPACE_COUNTER_BYTES].any()
+
+
+def test_calls_on_two_streams_at_once():
+    """The same two operators on two streams, each with its own workspace."""
+    g = norm._gen(14)
+    M, N, K = 100, 512, 2048
+    x, w, a, b, scale, idx = (t.cuda() for t in lora._inputs(g, M, N, K, 4, 16))
+    T, H, I, E, k = 33, 2304, 64, 8, 2
+    y, logits, gu, wd, _, _ = (None if t is None else t.cuda() for t in moe._inputs(g, T, H, I, E, False))
+    spaces = [g5.Workspace(), g5.Workspace()]
+    calls = [lambda ws: g5.gemm_bf16_nt_lora(x, w, a, b, idx, scale=scale, workspace=ws),
+             lambda ws: g5.moe_swiglu(y, logits, k, gu, wd, workspace=ws)[0]]
+    want = [c(s) for c, s in zip(calls, spaces)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(8):
+        for n in (0, 1):
+            with torch.cuda.stream(streams[n]):
+                got[n].append(calls[n](spaces[n]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[n]) for n in (0, 1) for o in got[n])
