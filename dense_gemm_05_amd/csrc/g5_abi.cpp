@@ -268,7 +268,7 @@ bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256
 // up to 16 rows they add 32-bit byte offsets of 16 rows.  Past 16 rows every
 // 64 weight rows read all of X again, M N K / 32 bytes, which the ring kernels
 // do not: measured with 16 adapters of rank 16, K = 4096, streaming against
-// ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 43 / 45 for 128;
+// ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 40 / 45 for 128;
 // N = 12288: 44 / 53 for 48 rows, 55 / 55 for 64, 75 / 62 for 128.  So up to
 // M N = 64 x 12288 (and columns that 32 bits count).
 bool lora_streams(const Problem &p)
@@ -781,7 +781,9 @@ int plan_for_call(const Problem &p, const void *ws, size_t ws_bytes, Plan &pl, W
 // block are shared out while the grid stays within one workgroup per CU of the
 // ring kernels' calls, four where the slices make the work short.
 // Past 16 rows the streaming kernel's own slices of K follow: as many as give
-// every CU two workgroups, at most 8 and at least one phase each.
+// every CU a workgroup, at most 8 and at least one phase each.  (Whole
+// calls, 80 x 4104 x 4100: 33.9 us, 36.2 with two workgroups per CU and 43.9
+// with three; 128 x 4096 x 4096 39.7, 43.8 and 43.4: the join takes longer.)
 size_t lora_layout(const Problem &p, const Plan &pl, const WsLayout &L, LoraArgs &q, size_t *total)
 {
     const bool small = pl.config == CFG_DECODE_NT, rows = small && p.M > 16;
@@ -798,7 +800,7 @@ size_t lora_layout(const Problem &p, const Plan &pl, const WsLayout &L, LoraArgs
     q.slices = q.per = 1;
     if (rows) {
         const int64_t phases = cdiv(p.K, 128 * lora_steps(p.M));
-        int64_t s = 2 * kNumCU / pl.tiles_n;
+        int64_t s = kNumCU / pl.tiles_n;
         s = s > 8 ? 8 : s < 1 ? 1 : s;
         q.per = (int)cdiv(phases, s);
         q.slices = (int)cdiv(phases, q.per);

@@ -373,11 +373,10 @@ __global__ void __launch_bounds__((NW + NX) * 64) k_lora_decode(GemmArgs p, Lora
 // q.slices slices of K: wave (kh, rw) multiplies its 16 rows rw with half kh of
 // every phase.  The halves meet in LDS.  There v B^T is added, 8 ranks (32 for
 // sixteen rows of X with one adapter, on the matrix core) to a slice in turn.
-// The slices meet in the workspace as in RingTile::join_slices.  Two
-// workgroups per CU cover each other's waits.  Bound by what a CU takes in,
-// the weights and about as much of X again from L2, and by the latencies of
-// the two or three phases that each workgroup has: 77 x 4104 x 4100 with 16
-// adapters of rank 24 27 to 28 us (the weights alone 6.6 us at 5.1 TB/s),
+// The slices meet in the workspace as in RingTile::join_slices.  Bound by
+// what a CU takes in, the weights and about as much of X again from L2, and by
+// the latencies of the few phases that each workgroup has: 77 x 4104 x 4100 with 16
+// adapters of rank 24 28 to 30 us (the weights alone 6.6 us at 5.1 TB/s),
 // where the ring kernel took 33 and the copies of its unaligned rows 17 more.
 template <int NC, int ST>
 __global__ void __launch_bounds__(512, 4) k_lora_rows(GemmArgs p, LoraArgs q)
