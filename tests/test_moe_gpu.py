@@ -261,3 +261,19 @@ def test_experts_on_a_stream_and_in_a_graph():
         got = [t.clone() for t in out]
         want = g5.moe_swiglu(x, logits, k, wgu, wd, workspace=eager)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {r}"
+
+
+@pytest.mark.parametrize("T,H,I,E,k,codes", [
+    (17, 4096, 200, 6, 3, False), (64, 2304, 320, 5, 2, True), (33, 2100, 130, 4, 4, False)])
+def test_a_token_among_many_is_the_token_alone(T, H, I, E, k, codes):
+    """The bits of a token's result are the same alone, among 16 and among
+    more, also at the widths where larger calls divide the work otherwise."""
+    _say(f"alone T={T} H={H} I={I} E={E} topk={k} codes={codes}")
+    x, logits, wgu, wd, sgu, sd = (None if t is None else t.cuda() for t in _inputs(_gen(6, T, H, I), T, H, I, E, codes))
+    ws = g5.Workspace()
+    call = lambda n0, n1: g5.moe_swiglu(x[n0:n1], logits[n0:n1], k, wgu, wd, scale_gu=sgu, scale_d=sd,    # noqa: E731
+                                        out_dtype=torch.float32, workspace=ws)[0]
+    all_of_them = call(0, T)
+    assert torch.equal(call(T - 16, T), all_of_them[T - 16:])
+    for t in range(0, T, 5):
+        assert torch.equal(call(t, t + 1)[0], all_of_them[t]), f"token {t}"
