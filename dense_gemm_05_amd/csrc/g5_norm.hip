@@ -96,10 +96,10 @@ __device__ __forceinline__ u32x4 scale8(u32x4 h, float rstd, u32x4 w, bool has_w
     u32x4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (h w is exact in FP32)
-        const float lo = has_w ? bf16_lo(h[i]) * bf16_lo(w[i]) : bf16_lo(h[i]);
-        const float hi = has_w ? bf16_hi(h[i]) * bf16_hi(w[i]) : bf16_hi(h[i]);
-        y[i] = pack_bf16x2(lo * rstd, hi * rstd);
+        // (h rstd first: at most sqrt(cols), whatever the row's scale, where
+        // h w, although exact, may leave FP32's range while y does not)
+        const float lo = bf16_lo(h[i]) * rstd, hi = bf16_hi(h[i]) * rstd;
+        y[i] = pack_bf16x2(has_w ? lo * bf16_lo(w[i]) : lo, has_w ? hi * bf16_hi(w[i]) : hi);
     }
     return y;
 }

@@ -254,3 +254,21 @@ def test_norm_on_a_stream_and_in_a_graph():
         torch.cuda.synchronize()
         got = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(got, step())), f"replay {k}"
+
+
+@pytest.mark.parametrize("cols", [64, 100, 4100, 16400])
+def test_norm_weights_far_from_the_rows_scale(cols):
+    """Rows and weights whose product leaves FP32's range, or falls among its
+    subnormal numbers, while y does not: bf16(h rstd w) all the same."""
+    g = _gen(7, cols)
+    for hs, ws, eps in ((1e15, 1e25, 1e-6), (1e-16, 1e-28, 0.0)):
+        h, w = (_bf((3, cols), g).double() * hs).bfloat16(), (_bf((cols,), g).double() * ws).bfloat16()
+        hd = h.double()
+        ref = hd / torch.sqrt((hd * hd).mean(1, keepdim=True) + eps) * w.double()
+        assert torch.isfinite(ref.bfloat16()).all()
+        y = g5.rms_norm(h.cuda(), w.cuda(), eps=eps).cpu()
+        # (half a step, the sums and products in FP32; 2^-100: far below any y but the smallest)
+        _check(y.double(), ref, (2.0 ** -8 + 2.0 ** -16) * ref.abs() + 2.0 ** -100 * ws, "y")
+        q, s = g5.rms_norm_e4m3(h.cuda(), w.cuda(), eps=eps)
+        wq, wscale = g5.gemm_fp8_quantize_rows(y.cuda())
+        assert torch.equal(q, wq) and torch.equal(s, wscale)
