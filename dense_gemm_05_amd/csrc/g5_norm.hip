@@ -387,15 +387,17 @@ __global__ void __launch_bounds__(NW * 64) k_rms_norm_grad(NormGradArgs a)
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < NCH; ++j) {
+            // (w too: zero times an infinite weight would be NaN)
             const u32x4 dk = WHOLE ? dy[j] : drop_first(dy[j], cc.dup(col_of(j)));
+            const u32x4 wk = WHOLE ? w[j] : drop_first(w[j], cc.dup(col_of(j)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float plo = bf16_lo(dk[i]) * (bf16_lo(h[j][i]) * rstd);
                 const float phi = bf16_hi(dk[i]) * (bf16_hi(h[j][i]) * rstd);
                 dw[j][2 * i] += plo;
                 dw[j][2 * i + 1] += phi;
-                dot = __builtin_fmaf(plo, bf16_lo(w[j][i]), dot);
-                dot = __builtin_fmaf(phi, bf16_hi(w[j][i]), dot);
+                dot = __builtin_fmaf(plo, bf16_lo(wk[i]), dot);
+                dot = __builtin_fmaf(phi, bf16_hi(wk[i]), dot);
             }
         }
         dot = wave_sum(dot);

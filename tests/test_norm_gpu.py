@@ -272,3 +272,20 @@ def test_norm_weights_far_from_the_rows_scale(cols):
         q, s = g5.rms_norm_e4m3(h.cuda(), w.cuda(), eps=eps)
         wq, wscale = g5.gemm_fp8_quantize_rows(y.cuda())
         assert torch.equal(q, wq) and torch.equal(s, wscale)
+
+
+@pytest.mark.parametrize("cols", [20, 24, 4100])
+def test_norm_gradient_with_an_infinite_weight(cols):
+    """dX is infinite or NaN where the formula's is, also when the weight
+    stands among the last columns of a row that is no multiple of 8 long."""
+    g = _gen(8, cols)
+    for at in (3, cols - 7, cols - 1):
+        dy, h, w = (_bf(s, g) for s in ((4, cols), (4, cols), (cols,)))
+        w[at], dy[1, at], dy[2] = torch.inf, 0.0, dy[2].abs()
+        rstd = torch.ones((4,))
+        xh, gg = h.double(), dy.double() * w.double()
+        ref = gg - xh * (gg * xh).sum(1, keepdim=True) / cols
+        dx, _ = g5.rms_norm_backward(dy.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+        dx = dx.cpu().double()
+        assert torch.equal(dx.isnan(), ref.isnan()) and torch.equal(dx.isposinf(), ref.isposinf())
+        assert torch.equal(dx.isneginf(), ref.isneginf())
