@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256, 4) k_rms_norm(NormAr
     if (WPR == 1 && !r_ok) return;        // a whole wave; nothing below joins waves
     const int64_t rr = r_ok ? r : 0;
     auto col_of = [&](int j) { return (int64_t)lane * 8 + (int64_t)(j * WPR + part) * 512; };
-    const NormCols cc{a.cols, !WHOLE && a.cols >= 8 && a.H != a.X && a.H != a.R};
+    const NormCols cc{a.cols, !WHOLE && a.cols >= 8 && (!a.H || (a.H != a.X && a.H != a.R))};
     auto at_of = [&](int j) { return WHOLE ? col_of(j) : cc.at(col_of(j)); };
     u32x4 h[NCH], w[NCH];
 #pragma unroll

@@ -289,3 +289,23 @@ def test_norm_gradient_with_an_infinite_weight(cols):
         dx = dx.cpu().double()
         assert torch.equal(dx.isnan(), ref.isnan()) and torch.equal(dx.isposinf(), ref.isposinf())
         assert torch.equal(dx.isneginf(), ref.isneginf())
+
+
+@pytest.mark.parametrize("cols", [9, 513, 1001, 4100, 8199, 12283])
+def test_norm_ragged_rows_without_a_residual(cols):
+    """The same bits as with a residual of zeros, whose sum is X, and nothing
+    stored beside the rows."""
+    g = _gen(9, cols)
+    x, w = _bf((5, cols), g).cuda(), _bf((cols,), g).cuda()
+    want, h = g5.rms_norm(x, w, residual=torch.zeros_like(x))
+    assert torch.equal(h, x)
+    buf = torch.full((7, cols + 3), 5.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(g5.rms_norm(x, w, Y=buf[1:6, 1:cols + 1]), want)
+    buf[1:6, 1:cols + 1] = 5.0
+    assert (buf == 5.0).all()
+    codes = torch.full((7, cols + 3), 9, dtype=torch.uint8, device="cuda")
+    q, s = g5.rms_norm_e4m3(x, w, Q=codes[1:6, 1:cols + 1])
+    wq, wscale = g5.gemm_fp8_quantize_rows(want)
+    assert torch.equal(q, wq) and torch.equal(s, wscale)
+    codes[1:6, 1:cols + 1] = 9
+    assert (codes == 9).all()
