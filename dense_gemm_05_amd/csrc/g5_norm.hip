@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(256) k_rms_norm_grad_long(NormGradArgs a)
     }
 }
 
-// dW[n] = sum of rows 0 .. parts - 1 of `part`: a workgroup owns 16 columns
+// dW[n] = sum of rows 0 .. parts - 1 (`stride` floats apart) of `part`: a workgroup owns 16 columns
 // (64 bytes of a row), 64 rows in flight at once; thread (row r, column c)
 // adds rows r, r + 64, ..., and the 64 sums are joined in order of a tree.
-__global__ void __launch_bounds__(1024) k_norm_dw(const float *part, int parts, int64_t cols, float *dW)
+__global__ void __launch_bounds__(1024) k_norm_dw(const float *part, int parts, int64_t stride, int64_t cols, float *dW)
 {
     __shared__ float red[64][17];
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *part, int parts, 
     float s = 0.f;
     if (n < cols) {
 #pragma unroll 8
-        for (int p = r; p < parts; p += 64) s += part[(int64_t)p * cols + n];
+        for (int p = r; p < parts; p += 64) s += part[(int64_t)p * stride + n];
     }
     red[r][c] = s;
     __syncthreads();
@@ -497,10 +497,18 @@ __global__ void __launch_bounds__(1024) k_norm_dw(const float *part, int parts, 
     if (r == 0 && n < cols) dW[n] = red[0][c];
 }
 
+// (a launch holds fewer than 2^32 threads, 64 per column: 2^25 columns at a time)
 hipError_t launch_norm_dw(const float *part, int parts, int64_t cols, float *dW, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((cols + 15) / 16)), dim3(1024), 0, s, part, parts, cols, dW);
-    return hipGetLastError();
+    constexpr int64_t kCols = (int64_t)1 << 25;
+    for (int64_t n = 0; n < cols; n += kCols) {
+        const int64_t c = cols - n < kCols ? cols - n : kCols;
+        hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)((c + 15) / 16)), dim3(1024), 0, s, part ? part + n : nullptr, parts,
+                           cols, c, dW + n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int NCH, int NW>

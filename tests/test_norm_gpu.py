@@ -309,3 +309,26 @@ def test_norm_ragged_rows_without_a_residual(cols):
     assert torch.equal(q, wq) and torch.equal(s, wscale)
     codes[1:6, 1:cols + 1] = 9
     assert (codes == 9).all()
+
+
+def test_norm_gradient_of_very_long_rows():
+    """More columns than one launch of dW's join can have threads for: dW of
+    one row, and the empty sum of none.  Every product is exact (dy one of
+    +-1, h a power of two, w and rstd 1), so dW is exact and dX is 2^-8 off at
+    most but for the row's mean: cols / 256 additions in a thread and 10 in the
+    join, of terms of at most 2."""
+    cols = (1 << 26) + 40
+    _say(f"gradient 1x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(10)
+    dy = torch.randint(0, 2, (1, cols), generator=g, device="cuda").mul_(2).sub_(1).bfloat16()
+    h = torch.randint(0, 2, (1, cols), generator=g, device="cuda").add_(1).bfloat16()
+    rstd, ws = torch.ones((1,), device="cuda"), g5.Workspace()
+    dx, dw = g5.rms_norm_backward(dy, h, None, rstd, workspace=ws)
+    p = dy.double() * h.double()
+    assert torch.equal(dw.double(), p[0])
+    c, off = float(p.mean()), (cols / 256 + 10) * 2.0 ** -24 * float(p.abs().mean())
+    ref = dy.double() - h.double() * c
+    assert ((dx.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1.01 * h.double() * off).all()
+    dw.fill_(3.0)
+    g5.rms_norm_backward(dy[:0], h[:0], None, rstd[:0], dW=dw, workspace=ws)
+    assert not dw.any()
