@@ -1393,7 +1393,7 @@ static MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
 {
     MoeLayout L;
     const size_t pairs = (size_t)T * topk;
-    L.ldz = (I + 127) / 128 * 128;      // whole steps of the down kernel, the rest zeros
+    L.ldz = (I + 127) / 128 * 128;      // rows start on 256 bytes; columns from I on are neither written nor read
     L.zplane = (int64_t)pairs * L.ldz;
     L.ids = g5::kCounterBytes;
     L.gates = L.ids + g5::round256(pairs * 4);

@@ -258,22 +258,18 @@ __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it,
     const int K = (int)a.H, steps = (K + KS - 1) / KS;
     const int s0 = steps * wave / kMoeWaves, s1 = steps * (wave + 1) / kMoeWaves;
     RowStream<CODES, 2, NC, D> b;
-    // (a row past I repeats the block's first and is not stored; whole blocks
-    // past I only fill z's rows with zeros)
-    if (i0 >= a.I) {
-    } else {
-        // (a block's rows, and all token rows, lie within 2 GiB of their first)
-        const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
-        const uint32_t off = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g, woff[2] = {off, off};
-        auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
+    // (a row past I repeats the block's first and is not stored; a block's
+    // rows, and all token rows, lie within 2 GiB of their first)
+    const char *const wbase[2] = {W + (int64_t)i0 * a.ldgu * EB, W + (a.I + i0) * a.ldgu * EB};
+    const uint32_t off = (uint32_t)(wok ? li : 0) * (uint32_t)(a.ldgu * EB) + 16 * g, woff[2] = {off, off};
+    auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                ok[c] = xok[c];
-                xoff[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
-            }
-        };
-        b.run(wbase, woff, (const char *)a.X, tokens, s0, s1, K, g, acc);
-    }
+        for (int c = 0; c < NC; ++c) {
+            ok[c] = xok[c];
+            xoff[c] = (uint32_t)(pair[c] / a.topk) * (uint32_t)(a.ldx * 2) + x_lane<CODES>(g);
+        }
+    };
+    b.run(wbase, woff, (const char *)a.X, tokens, s0, s1, K, g, acc);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         if (16 * c >= it.count) break;       // uniform
@@ -283,9 +279,9 @@ __device__ __forceinline__ void moe_gate_up(const MoeArgs &a, const MoeItem &it,
             const int64_t p = pair[c], i = i0 + 4 * g;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+                if (i + q >= a.I) break;
                 float gt = s[0][q], up = s[1][q];
-                if (i + q >= a.I) gt = up = 0.f;        // z's rows end in zeros
-                else if (a.scale_gu) {
+                if (a.scale_gu) {
                     const float *sc = a.scale_gu + (int64_t)it.expert * 2 * a.I;
                     gt *= sc[i + q];
                     up *= sc[a.I + i + q];
@@ -307,7 +303,7 @@ template <bool CODES, bool MANY>
 __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
 {
     __shared__ f32x4 red[kMoeWaves][2][64];
-    const int strips = (int)(a.ldz / 16), ordinal = blockIdx.x / strips;
+    const int strips = (int)(a.I + 15) / 16, ordinal = blockIdx.x / strips;
     if (ordinal >= *a.n_items) return;
     const MoeItem it = uniform_item(a.items[ordinal]);
     const int i0 = (blockIdx.x - ordinal * strips) * 16;
@@ -494,7 +490,7 @@ __global__ void __launch_bounds__(kDownWaves * 64, 4) k_moe_down_halves(MoeArgs 
 template <bool CODES, bool MANY>
 static hipError_t launch_moe_weights(const MoeArgs &a, hipStream_t s)
 {
-    const dim3 gg((unsigned)(moe_items(a.T, a.E, a.topk) * (a.ldz / 16)));
+    const dim3 gg((unsigned)(moe_items(a.T, a.E, a.topk) * ((a.I + 15) / 16)));
     const dim3 gd((unsigned)((a.H + a.cols - 1) / a.cols)), bg(kMoeThreads), bd(kDownWaves * 64);
     if (a.I > 0) {      // (no inner columns: the down kernel's sums are empty)
         hipLaunchKernelGGL((k_moe_gate_up<CODES, MANY>), gg, bg, 0, s, a);

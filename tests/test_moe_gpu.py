@@ -277,3 +277,17 @@ def test_a_token_among_many_is_the_token_alone(T, H, I, E, k, codes):
     assert torch.equal(call(T - 16, T), all_of_them[T - 16:])
     for t in range(0, T, 5):
         assert torch.equal(call(t, t + 1)[0], all_of_them[t]), f"token {t}"
+
+
+@pytest.mark.parametrize("I", [32, 33, 120])
+def test_experts_store_no_columns_past_the_inner_ones(I):
+    """z's rows (128 bf16 apart, behind the routing's five parts of 256 bytes)
+    hold I columns: what stands behind them is neither written nor read."""
+    x, logits, wgu, wd, _, _ = _inputs(_gen(9, I), 4, 64, I, 8, False)
+    dev = x.cuda(), logits.cuda(), 2, wgu.cuda(), wd.cuda()
+    ws, at = g5.Workspace(), g5.GEMM_WORKSPACE_COUNTER_BYTES + 5 * 256
+    want = g5.moe_swiglu(*dev, workspace=ws)[0]
+    ws.buf[g5.GEMM_WORKSPACE_COUNTER_BYTES:] = 255         # (NaN as z)
+    assert torch.equal(g5.moe_swiglu(*dev, workspace=ws)[0], want)
+    z = ws.buf[at:at + 2 * 8 * 128 * 2].view(torch.int16).view(16, 128)
+    assert (z[:, I:] == -1).all() and (z[:, :I] != -1).all()
