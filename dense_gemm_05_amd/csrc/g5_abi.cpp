@@ -270,10 +270,11 @@ bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256
 // do not: measured with 16 adapters of rank 16, K = 4096, streaming against
 // ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 40 / 45 for 128;
 // N = 12288: 44 / 53 for 48 rows, 55 / 55 for 64, 75 / 62 for 128.  So up to
-// M N = 64 x 12288 (and columns that 32 bits count).
+// M N = 64 x 12288 (and columns that 32 bits count).  (Up to 16 rows a launch
+// has up to 36 threads per weight row, and fewer than 2^32.)
 bool lora_streams(const Problem &p)
 {
-    if (p.M <= 16) return p.lda < (1 << 27) && p.ldb < (1 << 27);
+    if (p.M <= 16) return p.lda < (1 << 27) && p.ldb < (1 << 27) && p.N <= 1 << 26;
     return p.M <= kLoraStreamRows && p.N <= 64 * 12288 / p.M && p.K <= 1 << 30;
 }
 
@@ -615,6 +616,8 @@ int select_plan(const Problem &p, Plan &pl, bool ws)
     // fused epilogues and a transposed B exist in the ring kernels only (variants 1-3)
     if (ring_only(p) && tiled(pl.config) && pl.variant == 0) return GEMM_ERR_UNSUPPORTED;
     if (p.lora && tiled(pl.config) && pl.variant == 3) return GEMM_ERR_UNSUPPORTED;   // (16-byte copies only)
+    // (k_lora_shrink: 512 threads for 16 rows, fewer than 2^32 in a launch)
+    if (p.lora && p.M > ((int64_t)1 << 27) - 16) return GEMM_ERR_UNSUPPORTED;
     if (const char *fs = std::getenv("GEMM_FORCE_STREAMK")) {
         // diagnostic: the persistent stream-K schedule for the chosen tile
         if (*fs == '1') {

@@ -654,8 +654,8 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
  * in the products of M > 16) and joined to the FP32 sums of the projection,
  * which are rounded once to C's type.  A row depends on its own adapter
  * only: values of other rows and adapters, NaN and infinities among them,
- * do not reach it.  Deterministic; for M <= 16 a row's result does not
- * depend on the others.
+ * do not reach it.  Deterministic; for M <= 16 (rows less than 2^27 elements
+ * apart, N <= 2^26) a row's result does not depend on the others.
  *
  * L == 0 or R == 0: the plain product.  K == 0: C := 0.  R <= 4096.  Any
  * alignment is taken; past 128 rows, and past 16 with M N > 786432, rows of
@@ -669,7 +669,8 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
  * workspace overlapping any of them; GEMM_ERR_WORKSPACE for a missing or
  * small workspace; GEMM_ERR_UNSUPPORTED where X or Wt spans 2 GiB or more
  * and the call is one for the tiled kernels (M > 128; M > 16 and M N > 786432
- * or K > 2^30; M <= 16 and rows 2^27 elements or more apart). */
+ * or K > 2^30; M <= 16 and rows 2^27 elements or more apart or N > 2^26), and
+ * for M > 2^27 - 16. */
 int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K,
                       const uint16_t *X, int64_t ldx,
                       const uint16_t *Wt, int64_t ldw,

@@ -270,3 +270,19 @@ def test_lora_binding_refuses(no_lib):
                 dict(idx=torch.zeros(4, dtype=torch.int32)), dict(C=torch.empty((4, 64), dtype=torch.bfloat16))):
         with pytest.raises(ValueError):
             g5.gemm_bf16_nt_lora(**{**good, **bad})
+
+
+def test_lora_launches_stay_below_their_threads():
+    """What one launch has threads for: up to 16 rows of X, 2^26 weight rows
+    on the small-M kernel (beyond, the tiled kernels, as long as Wt spans less
+    than 2 GiB); 2^27 - 16 rows of X."""
+    def status(M, N, K):
+        n = ctypes.c_uint64(1)
+        return g5.lib().gemm_lora_workspace_size(M, N, K, 2, 16, P + (16 << 44), K, P + (17 << 44), K, P + (18 << 44), N,
+                                                 0, ctypes.byref(n))
+    for M in (1, 16):
+        assert status(M, 1 << 26, 1024) == OK
+        assert status(M, (1 << 26) + 1, 1024) == g5.GEMM_ERR_UNSUPPORTED
+        assert status(M, (1 << 26) + 1, 8) == OK
+    assert status((1 << 27) - 16, 8, 8) == OK
+    assert status((1 << 27) - 15, 8, 8) == g5.GEMM_ERR_UNSUPPORTED
