@@ -248,3 +248,26 @@ def test_lora_on_a_stream_and_in_a_graph(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.clone(), call(eager)), f"replay {r}"
+
+
+@pytest.mark.parametrize("M,N,K,L,R,order", [
+    (64, 12288, 1100, 3, 12, "mixed"), (80, 9000, 900, 2, 20, "one"), (128, 6144, 1300, 5, 8, "runs"),
+    (17, 16400, 1100, 2, 30, "mixed")])
+def test_lora_streamed_wide(M, N, K, L, R, order):
+    """17 .. 128 rows and so many columns that one or two slices of K have
+    several phases each; the next call on the same workspace, unaligned, too."""
+    _say(f"wide M={M} N={N} K={K} adapters={L} rank={R} {order}")
+    x, w, a, b, scale, idx = _inputs(_gen(10, M, N, K), M, N, K, L, R)
+    idx = {"mixed": idx, "one": torch.full_like(idx, L - 1), "runs": idx.sort().values}[order]
+    y, tol = _formula(x, w, a, b, scale, idx)
+    ws, outs = g5.Workspace(), []
+    for kind in ("contig", "odd"):
+        dev = [_strided(t, kind) for t in (x, w, a, b)]
+        out = torch.full((M + 2, N + 3), 3.0, device="cuda")
+        got = g5.gemm_bf16_nt_lora(*dev, idx.cuda(), scale=scale.cuda(), C=out[:M, :N], workspace=ws)
+        _check(got.cpu().double(), y, tol + 2.0 ** -24 * y.abs(), kind)
+        assert (out[M:] == 3.0).all() and (out[:, N:] == 3.0).all()
+        assert not ws.buf[:g5.GEMM_WORKSPACE_COUNTER_BYTES].any()
+        ws.buf[g5.GEMM_WORKSPACE_COUNTER_BYTES:] = 255
+        outs.append(got)
+    assert torch.equal(outs[0], outs[1])

@@ -286,3 +286,27 @@ def test_lora_launches_stay_below_their_threads():
         assert status(M, (1 << 26) + 1, 8) == OK
     assert status((1 << 27) - 16, 8, 8) == OK
     assert status((1 << 27) - 15, 8, 8) == g5.GEMM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("M,N,K,R,slices", [
+    (17, 64, 4096, 16, 8), (80, 1, 900, 33, 3), (128, 4200, 130, 4, 1), (64, 12288, 1100, 12, 1), (80, 9000, 900, 20, 1),
+    (128, 6144, 1300, 8, 2), (17, 16400, 1100, 30, 1)])
+def test_lora_sizes_of_the_streaming_kernel(M, N, K, R, slices):
+    """17 .. 128 rows up to M N = 786432: K's slices of the low-rank values in
+    FP32, and 16-row blocks of 64 columns for each slice of the product (a
+    tiled kernel's call has one slice of values and none of these)."""
+    blocks = 3 if M <= 48 else 5 if M <= 80 else 8
+    values = max(1, min(4, K // 512)) * M * ((R + 7) // 8 * 8) * 4
+    parts = (N + 63) // 64 * slices * 4 * blocks * 1024 if slices > 1 else 0
+    assert lora_size(M, N, K, 3, R) == (OK, CR + (values + 255) // 256 * 256 + parts)
+
+
+def test_lora_rows_and_columns_choose_the_kernel():
+    """Both sides of M N = 786432: four slices of FP32 values, or the tiled
+    kernels' one."""
+    for M in (32, 64, 128):
+        N = 786432 // M
+        assert lora_size(M, N, 2048, 3, 16) == (OK, CR + 4 * M * 16 * 4 + (2 * 96 * 4 * 8 * 1024 if M == 128 else 0))
+        st, n = lora_size(M, N + 8, 2048, 3, 16)
+        product = g5.plan_query(g5.GEMM_OP_BF16_NT, M, N + 8, 2048)[1].workspace_bytes
+        assert st == OK and n == max(product, CR) + M * 16 * 4
