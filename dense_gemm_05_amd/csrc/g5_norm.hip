@@ -91,15 +91,21 @@ __device__ __forceinline__ float sumsq8(float s, u32x4 h)
     return s;
 }
 
+// h w rstd.  h takes rstd's power of two first, which is exact: then neither
+// h 2^e, whatever the row's scale, nor its product with w (exact too, two bf16)
+// leaves FP32's range unless y does, and y is rounded once in FP32 by rstd's
+// mantissa.  (rstd 0, infinite or NaN: the mantissa is 1 or NaN.)
 __device__ __forceinline__ u32x4 scale8(u32x4 h, float rstd, u32x4 w, bool has_w)
 {
+    const uint32_t bits = __float_as_uint(rstd);
+    const float two_e = __uint_as_float(bits & 0x7f800000u);
+    const float man = rstd != rstd ? rstd : __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
     u32x4 y;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        // (h rstd first: at most sqrt(cols), whatever the row's scale, where
-        // h w, although exact, may leave FP32's range while y does not)
-        const float lo = bf16_lo(h[i]) * rstd, hi = bf16_hi(h[i]) * rstd;
-        y[i] = pack_bf16x2(has_w ? lo * bf16_lo(w[i]) : lo, has_w ? hi * bf16_hi(w[i]) : hi);
+        const float lo = has_w ? bf16_lo(h[i]) * two_e * bf16_lo(w[i]) * man : bf16_lo(h[i]) * rstd;
+        const float hi = has_w ? bf16_hi(h[i]) * two_e * bf16_hi(w[i]) * man : bf16_hi(h[i]) * rstd;
+        y[i] = pack_bf16x2(lo, hi);
     }
     return y;
 }
