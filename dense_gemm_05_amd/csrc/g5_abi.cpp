@@ -267,10 +267,14 @@ bool has_epilogues(int id) { return id == CFG_BF16_256x192 || id == CFG_BF16_256
 // The small-M kernels of the projection with adapters: rows of any alignment;
 // up to 16 rows they add 32-bit byte offsets of 16 rows.  Past 16 rows every
 // 64 weight rows read all of X again, M N K / 32 bytes, which the ring kernels
-// do not: measured with 16 adapters of rank 16, K = 4096, streaming against
-// ring, N = 4096: 24 / 37 us for 32 rows, 32 / 41 for 80, 40 / 45 for 128;
-// N = 12288: 44 / 53 for 48 rows, 55 / 55 for 64, 75 / 62 for 128.  So up to
-// M N = 64 x 12288 (and columns that 32 bits count).  (Up to 16 rows a launch
+// do not: measured with 16 adapters of rank 16, mixed, K = 4096, streaming
+// against ring, N = 4096: 22 / 36 us for 32 rows, 31 / 40 for 80, 40 / 45 for
+// 128; N = 12288: 43 / 53 for 48 rows, 56 / 54 for 64, 77 / 62 for 128.  So up
+// to M N = 64 x 12288 (and columns that 32 bits count).  At that bound the
+// other K and ranks are, 64 x 12288 and 128 x 4096: K = 1024 27 / 29 and 27 /
+// 31, K = 8192 91 / 82 and 57 / 59, rank 64 at K = 4096 97 / 78 and 62 / 98
+// (in runs of rows 88 / 67 and 50 / 59): the rule takes the slower side by up
+// to a quarter where the columns are many and the rank is high.  (Up to 16 rows a launch
 // has up to 36 threads per weight row, and fewer than 2^32.)
 bool lora_streams(const Problem &p)
 {

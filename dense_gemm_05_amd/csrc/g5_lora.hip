@@ -61,8 +61,10 @@ __device__ __forceinline__ void each_adapter(int a_row, F f)
 // 16-row operand, X's rows the other: a row's sums are its own whatever
 // stands in the other rows, and only rows of this adapter keep them.  Bound by
 // what one CU reads (about 35 GB/s beside the latency): with K = 4096 in four
-// slices 3.8 us for one row, 5.2 for 16 rows of 16 adapters and 6.0 for 77, in
-// one slice 11 us for 1024 rows.  The ring kernels take one slice all the same:
+// slices 4.4 us for one row, 5.4 for 16 rows of 16 adapters and 6.7 for 77, in
+// one slice 11 us for 1024 rows in runs; where rows of 64 adapters are mixed,
+// so that a block's adapters follow each other, 34 us, and 118 at rank 64 (30
+// in runs).  The ring kernels take one slice all the same:
 // adding four at their ends cost them 10 us and saved 3 here.  Sixteen waves,
 // or eight steps in flight, measured no faster.  WHOLE: K is a
 // multiple of 8.
@@ -171,10 +173,11 @@ __device__ __forceinline__ u32x4 lora_b8(const LoraArgs &q, const uint16_t *row,
 //    each other (v = hi + lo to 2^-16 of it): 2 R deep, both parts against
 //    the same rows of B.  Rows of B stay in registers while the adapter stays.
 //  - Any other sixteen rows: each lane forms its own outputs from its row's
-//    values and its adapter's rows of B, R products each.  Every load is
-//    independent, so rows of sixteen adapters cost little more than the
-//    latency of one (a loop over the adapters measured 85 us at
-//    77 x 4104 x 4100 with 16 of them).
+//    values and its adapter's rows of B, R products each, with nothing shared
+//    between the rows.  That grows with M N R: this kernel at N = 12288, K =
+//    4096 with 64 adapters, mixed rows against runs of rows, 512 rows of rank
+//    16 139 / 115 us, 1024 of rank 16 149 / 124, 512 of rank 64 590 / 202,
+//    1024 of rank 64 1162 / 201.
 template <class RT, int WGN, bool WHOLE>
 __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q, typename RT::Acc &acc, int wave,
                                             int64_t m0, int64_t n0)
@@ -265,7 +268,8 @@ __device__ __forceinline__ void lora_expand(const GemmArgs &p, const LoraArgs &q
 
 // The ring kernel on Bt (k_bf16_ms) with the adapters joined to its finished
 // sums: 1024 x 12288 x 4096 with eight adapters of rank 16 in runs of rows
-// 101 to 104 us (1.0 PFLOP/s), the product alone 102.
+// 101 to 104 us (1.0 PFLOP/s), the product alone 102; 64 adapters of rank 16
+// 124, of rank 64 201 (mixed rows: above).
 template <int BM, int BN, int WGM, int WGN, bool MASKED, bool SK, bool WHOLE>
 __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(GemmArgs p, LoraArgs q)
 {
@@ -291,7 +295,9 @@ __global__ void __launch_bounds__(WGM *WGN * 64, BM == 128 ? 4 : 2) k_lora_ms(Ge
 // of the workgroup's 16 RB columns meanwhile, an output at a time per thread
 // (R products in rank order); the last pass adds both.  Bound by the stream:
 // 12288 x 4096 for one row 22 to 24 us (4.2 to 4.5 TB/s), for 16 rows of 16
-// adapters of rank 16 26 to 28 us (the product alone 22.0 and 24.2).  One row takes a
+// adapters of rank 16 26 to 28 us (the product alone 22.0 and 24.2).  At rank
+// 64 the values of v, which every output reads and adds up from K's slices
+// anew, weigh more: 31 and 40 us.  One row takes a
 // block of 16 weight rows per workgroup and four steps in flight, more rows
 // three blocks, which share X (the product alone: 23.8 us, 29.2 with one).
 template <int NW, int NX, int RB, int D>

@@ -143,9 +143,9 @@ __device__ __forceinline__ float rstd_of(float ss, int64_t cols, float eps)
 // wave sums in a fixed order (chunk, element, butterfly), the parts are
 // added in order, so a row's result does not depend on the others.
 // Bound by HBM (2 bytes per element each for x, r, h and y, one for codes):
-// 16384 x 8192 with a residual 194 us, 5.5 TB/s; 1024 x 4096 to codes 9.5 us,
-// 3.1 TB/s, of which about 3 us are the launch and one load's latency, all
-// that 1 x 4096 takes (3.1 us).
+// 16384 x 8192 with a residual 194 us, 5.5 TB/s, to codes 173 us, 5.4 TB/s;
+// 1024 x 4096 to codes 9.5 us, 3.1 TB/s, of which about 3 us are the launch and
+// one load's latency, all that 1 x 4096 takes (3.1 us).
 template <int WPR, int NCH, bool CODES, bool WHOLE>
 __global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256, 4) k_rms_norm(NormArgs a)
 {
@@ -304,9 +304,10 @@ static hipError_t launch_norm_held(const NormArgs &a, bool codes, hipStream_t s)
 
 static hipError_t launch_norm_rows(const NormArgs &a, bool codes, hipStream_t s)
 {
-    // The fewest waves that hold a row: 131072 x 512 takes 48 us with a wave
-    // per row and 104 with four (three of them idle), 16384 x 4096 44 us with
-    // four and 46 with eight.
+    // A wave for rows of up to 512 elements, four up to 8192 (past 1536 all
+    // of them at work), then eight: 131072 x 512 takes 48 us with a wave per
+    // row and 104 with four (three of them idle), 16384 x 4096 44 us with four
+    // and 46 with eight.
     if (a.cols <= 512) return launch_norm_held<1, 1>(a, codes, s);
     if (a.cols <= 2048) return launch_norm_held<4, 1>(a, codes, s);
     if (a.cols <= 4096) return launch_norm_held<4, 2>(a, codes, s);
@@ -347,8 +348,9 @@ hipError_t launch_rms_norm(const NormArgs &a, bool codes, hipStream_t s)
 // kernel adds the workgroups' rows in order.  The next row is loaded while
 // this one is summed.  Bound by HBM (8 bytes per element with dH): 8192 x 4096
 // 46 us, 5.8 TB/s, and 4.9 us for dW; 1000 x 4100 without dH, whose rows start
-// at any 8 bytes, 13.3 and 5.2 us, where a workgroup has two rows and the
-// latency of its first load shows.
+// at any 8 bytes, 13.5 and 5.4 us, where a workgroup has two rows, the latency
+// of its first load shows, and the 512 rows of `part` are 8.4 MB written and
+// read again beside 24.6 MB of rows.
 template <int NCH, int NW, bool WHOLE>
 __global__ void __launch_bounds__(NW * 64) k_rms_norm_grad(NormGradArgs a)
 {

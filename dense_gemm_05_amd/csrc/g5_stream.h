@@ -56,11 +56,12 @@ __device__ __forceinline__ void codes16_to_bf16(u32x4 c, u32x4 &lo, u32x4 &hi)
 // A step is a 128-byte line of every weight row, read in two pieces: lane
 // group g (of four) takes bytes 16 g .. 16 g + 15 of each half.  The halves
 // are loaded one right after the other and with ordinary loads: the bytes in
-// flight exceed an XCD's L2, so a line whose second half is asked for later
-// is fetched again (measured: 1.6 times the bytes with the halves a batch
-// apart), and loads marked non-temporal give it up sooner (16 tokens, down
-// rows: 170 us against 132).  Piece h meets the same elements
-// of the token's row (8 of bf16, or 16 codes in two products).
+// flight exceed an XCD's L2, so of the lines whose second half is asked for
+// later some are fetched again (the halves of D steps behind each other: 1.01
+// to 1.09 times the bytes and 1.04 to 1.21 times the time in the expert
+// layer's kernels), and loads marked non-temporal give them up sooner (16
+// tokens, down rows: 170 us against 132).  Piece h meets the same elements of
+// the token's row (8 of bf16, or 16 codes in two products).
 template <bool CODES>
 constexpr int kStep = CODES ? 128 : 64;       // elements
 template <bool CODES>

@@ -533,9 +533,10 @@ int gemm_workspace_size(int op, int64_t batch, int64_t M, int64_t N, int64_t K,
  * gives for the bf16 y (the A operand of gemm_fp8_nt); scale is not touched
  * otherwise.  rstd[rows] (float) or NULL receives each row's rstd, which the
  * gradient reads.  The sums, rstd and the products are FP32 (a row's sum of
- * squares must stay below 3.4e38); a row's result does not depend on the
- * other rows.  A row of zeros with eps == 0 gives NaN, as the formula does;
- * an infinite or NaN element spreads over its row only.
+ * squares must stay below 3.4e38 and, with eps == 0, their mean above
+ * 1.2e-38); a row's result does not depend on the other rows.  A row of zeros
+ * with eps == 0 gives NaN, as the formula does; an infinite or NaN element
+ * spreads over its row only.
  *
  * H may be X or R itself (same pointer and stride: the sum is formed in
  * place); no other output may overlap an input or another output.  Rows of
@@ -649,7 +650,8 @@ int gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
  * [R, K] at A + a*strideA (row stride lda) and B_a [N, R] at B + a*strideB
  * (row stride ldb), bf16; scale[L] (float) or NULL for 1.  idx[M] (int32,
  * device memory): rows whose index lies outside [0, L) -- by convention -1 --
- * have no adapter.  Rows of different adapters may stand in any order.  The
+ * have no adapter.  Rows of different adapters may stand in any order (past 128
+ * rows, sorted by adapter they run faster, at high ranks several times).  The
  * adapter's R values per row are kept in FP32 (as two bf16 parts, to 2^-16,
  * in the products of M > 16) and joined to the FP32 sums of the projection,
  * which are rounded once to C's type.  A row depends on its own adapter
