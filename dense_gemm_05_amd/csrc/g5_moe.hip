@@ -234,7 +234,8 @@ __device__ __forceinline__ void moe_join(f32x4 (&red)[kMoeWaves][2][64], const f
 // z of 16 inner columns for the tokens of one work item (at most 16 NC): gate
 // rows i0 .. i0 + 15 and the up rows of the same columns.  Bound by the
 // weights' stream from HBM: 8 experts of 2 x 1536 x 4096 for one token 36 us
-// (5.6 TB/s), 56 experts for 16 tokens 242 us (5.8 TB/s; a copy reaches 5.1),
+// (5.6 TB/s), 56 experts for 16 tokens 242 to 250 us (5.6 to 5.8 TB/s; a copy
+// reaches 5.1),
 // 64 in codes for 64 tokens 172 to 182 us (4.4 to 4.7 TB/s: half the bytes per
 // matrix-core step, and 32 tokens' x beside them).
 template <bool CODES, int NC, int D>
@@ -317,8 +318,9 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_gate_up(MoeArgs a)
 // the next free one each, and leave each pair's sums in the piece's own
 // places.  The order in which pieces are taken does not matter: the slots of
 // each half are added in order, then the halves, here and in the kernel for
-// many tokens below, so a token's bits do not depend on the number of tokens.  8 experts of 4096 x 1536 for one token 22 us
-// (4.6 TB/s), 56 for 16 tokens 128 us (5.5 TB/s).
+// many tokens below, so a token's bits do not depend on the number of tokens.
+// 8 experts of 4096 x 1536 for one token 22 to 24 us (4.2 to 4.6 TB/s), 56 for
+// 16 tokens 128 to 131 us (5.4 to 5.5 TB/s).
 constexpr int kDownWaves = 16, kDownSlices = 2, kMoeMaxItems = kMoeMaxPairs;
 // A piece's products for its tokens, 8 to a block of the matrix core's 16
 // columns: columns 0 .. 7 take z's hi parts, 8 .. 15 the lo parts, and the two
