@@ -51,7 +51,8 @@ EXPORTS = ("gemm_sgemm", "gemm_bf16", "gemm_bf16_batched", "gemm_bf16_nt", "gemm
            "gemm_tile_map",
            "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size",
            "gemm_moe_swiglu", "gemm_moe_workspace_size",
-           "gemm_bf16_nt_lora", "gemm_lora_workspace_size")
+           "gemm_bf16_nt_lora", "gemm_lora_workspace_size",
+           "gemm_bf16_grouped_nt", "gemm_bf16_grouped", "gemm_bf16_grouped_tn", "gemm_grouped_workspace_size")
 
 
 class GemmPlan(ctypes.Structure):
@@ -174,6 +175,15 @@ def lib():
     L.gemm_lora_workspace_size.argtypes = [i64, i64, i64, i64, i64, u64, i64, u64, i64, u64, i64, i32,
                                            ctypes.POINTER(u64)]
     L.gemm_lora_workspace_size.restype = i32
+    L.gemm_bf16_grouped_nt.argtypes = [i64, i64, i64, i64, p, p, i64, p, i64, i64, p, i64, i32, p, u64, p]
+    L.gemm_bf16_grouped_nt.restype = i32
+    L.gemm_bf16_grouped.argtypes = L.gemm_bf16_grouped_nt.argtypes
+    L.gemm_bf16_grouped.restype = i32
+    L.gemm_bf16_grouped_tn.argtypes = [i64, i64, i64, i64, p, p, i64, p, i64, p, i64, i64, i32, p, u64, p]
+    L.gemm_bf16_grouped_tn.restype = i32
+    L.gemm_grouped_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64, u64, i64, u64, i64, i64,
+                                              ctypes.POINTER(u64)]
+    L.gemm_grouped_workspace_size.restype = i32
     _lib = L
     return L
 

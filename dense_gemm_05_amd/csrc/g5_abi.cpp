@@ -1577,6 +1577,184 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
     return g5::run(p, stream, workspace, (size_t)workspace_bytes);
 }
 
+// ---- products grouped by expert
+namespace {
+struct GroupedPlan {
+    int tile = g5::GROUPED_128;
+    bool copy_a = false, copy_b = false;
+    int64_t lda2 = 0, ldb2 = 0, batch_b = 1, rows_b = 0, cols_a = 0;
+    size_t at_a = 0, at_b = 0, total = 0;
+};
+}  // namespace
+
+static bool grouped_sizes_ok(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int64_t K)
+{
+    const int64_t top = (int64_t)1 << 30;
+    return kind >= g5::GROUPED_NT && kind <= g5::GROUPED_TN && E >= 0 && E <= g5::kGroupedMaxGroups && rows >= 0 &&
+           rows <= 0x7fffffff && M >= 0 && N >= 0 && K >= 0 && M <= top && N <= top && K <= top;
+}
+
+// Tile and row copies of a call with work in it.
+static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int64_t K, uint64_t a, int64_t lda,
+                        uint64_t b, int64_t ldb, int64_t sB, GroupedPlan &pl)
+{
+    const bool tn = kind == g5::GROUPED_TN, nt = kind == g5::GROUPED_NT;
+    pl = GroupedPlan();
+    pl.cols_a = tn ? M : K;
+    pl.rows_b = nt ? N : tn ? rows : K;
+    const int64_t cols_b = nt ? K : N;
+    pl.batch_b = tn || sB == 0 ? 1 : E;
+    const bool stream = nt && lda < (1 << 24) && ldb < (1 << 26);
+    const char *force = std::getenv("GEMM_FORCE_CONFIG");
+    if (force && *force) {
+        const int id = g5::find_config_by_name(force);
+        if (id == g5::CFG_BF16_256x256) pl.tile = g5::GROUPED_256;
+        else if (id == g5::CFG_DECODE_NT && stream) pl.tile = g5::GROUPED_STREAM;
+        else if (id != g5::CFG_BF16_128x128) return GEMM_ERR_UNSUPPORTED;
+    } else if (stream && rows <= 32 * E) {
+        pl.tile = g5::GROUPED_STREAM;
+    } else if (tn ? E * g5::cdiv(M, 256) * g5::cdiv(N, 256) >= g5::kNumCU
+                  : rows >= 256 * E && g5::cdiv(rows, 256) * g5::cdiv(N, 256) >= g5::kNumCU) {
+        pl.tile = g5::GROUPED_256;
+    }
+    if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
+    if (pl.tile == g5::GROUPED_STREAM) return GEMM_OK;
+    // The ring tiles copy whole 16-byte chunks: rows that start elsewhere, or
+    // that end inside a chunk where the chunk runs across the summed axis,
+    // are copied to padded ones first.
+    pl.copy_a = g5::row_alignment(a, lda, 0, 1, 2) < 16 || (tn && M % 8 != 0);
+    pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 16 || (!nt && N % 8 != 0);
+    pl.lda2 = pl.copy_a ? (pl.cols_a + 7) / 8 * 8 : lda;
+    pl.ldb2 = pl.copy_b ? (cols_b + 7) / 8 * 8 : ldb;
+    // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 32
+    // along the summed axis)
+    if (pl.lda2 > (1 << 21) || pl.ldb2 > (1 << 21)) return GEMM_ERR_UNSUPPORTED;
+    if (pl.copy_a || pl.copy_b) {
+        pl.at_a = g5::kCounterBytes;
+        pl.at_b = pl.at_a + (pl.copy_a ? g5::round256((size_t)rows * pl.lda2 * 2) : 0);
+        pl.total = pl.at_b + (pl.copy_b ? g5::round256((size_t)pl.batch_b * pl.rows_b * pl.ldb2 * 2) : 0);
+    }
+    return GEMM_OK;
+}
+
+int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int64_t K, uint64_t a_addr,
+                                int64_t lda, uint64_t b_addr, int64_t ldb, int64_t strideB, uint64_t *bytes)
+{
+    if (bytes) *bytes = 0;
+    if (!grouped_sizes_ok(kind, E, rows, M, N, K)) return GEMM_ERR_INVALID_ARG;
+    if (E == 0 || N == 0 || rows == 0 || (kind == g5::GROUPED_TN ? M : K) == 0) return GEMM_OK;
+    GroupedPlan pl;
+    const int st = grouped_plan(kind, E, rows, M, N, K, a_addr, lda, b_addr, ldb, strideB, pl);
+    if (st == GEMM_OK && bytes) *bytes = pl.total;
+    return st;
+}
+
+// M: output rows of TN (else unused); K: the summed axis of NT and NN.
+static int grouped_run(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int64_t K, const int32_t *offsets,
+                       const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t sB, void *C,
+                       int64_t ldc, int64_t sC, int c_type, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    using g5::Range;
+    const bool tn = kind == g5::GROUPED_TN, nt = kind == g5::GROUPED_NT;
+    if (!grouped_sizes_ok(kind, E, rows, M, N, K)) return GEMM_ERR_INVALID_ARG;
+    if (c_type != GEMM_OUT_BF16 && c_type != GEMM_OUT_F32) return GEMM_ERR_INVALID_ARG;
+    if (E == 0 || N == 0 || (tn ? M == 0 : rows == 0)) return GEMM_OK;
+    const int ec = c_type == GEMM_OUT_F32 ? 4 : 2;
+    if (!offsets || !C || ((uint64_t)offsets % 4) || ((uint64_t)C % ec) || ldc < N || sB < 0 || sC < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (tn && E > 1 && (__int128)sC < (__int128)(M - 1) * ldc + N) return GEMM_ERR_INVALID_ARG;
+    const bool some = tn ? rows > 0 : K > 0;        // (else: empty sums)
+    const int64_t cols_a = tn ? M : K, rows_b = nt ? N : tn ? rows : K, cols_b = nt ? K : N;
+    if (some && (!A || !B || lda < cols_a || ldb < cols_b || ((uint64_t)A % 2) || ((uint64_t)B % 2)))
+        return GEMM_ERR_INVALID_ARG;
+    const Range none{0, 0};
+    const Range in[] = {some ? g5::extent((uint64_t)A, 1, rows, cols_a, lda, 0, 2) : none,
+                        some ? g5::extent((uint64_t)B, tn ? 1 : E, rows_b, cols_b, ldb, sB, 2) : none,
+                        vec_range(offsets, E + 1, 4)};
+    GroupedPlan pl;
+    if (some) {
+        const int st = grouped_plan(kind, E, rows, M, N, K, (uint64_t)A, lda, (uint64_t)B, ldb, sB, pl);
+        if (st != GEMM_OK) return st;
+    } else if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) {
+        return GEMM_ERR_UNSUPPORTED;
+    }
+    const Range out[] = {g5::extent((uint64_t)C, tn ? E : 1, tn ? M : rows, N, ldc, sC, ec),
+                         pl.total && workspace
+                             ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                             : none};
+    for (const Range &r : in)
+        if (r.hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
+    if (out[0].hi > ((__int128)1 << 63) || outputs_overlap(out, 2, in, 3)) return GEMM_ERR_INVALID_ARG;
+    if (pl.total && (!workspace || workspace_bytes < pl.total)) return GEMM_ERR_WORKSPACE;
+    if (pl.total && ((uint64_t)workspace % 256)) return GEMM_ERR_INVALID_ARG;
+    const int st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    g5::GroupedArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.offsets = offsets;
+    a.E = E;
+    a.rows = rows;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.lda = some ? lda : 0;
+    a.ldb = some ? ldb : 0;
+    a.sB = some ? sB : 0;
+    a.ldc = ldc;
+    a.sC = sC;
+    a.align_c = g5::row_alignment((uint64_t)C, ldc, sC, tn ? E : 1, ec);
+    a.out_f32 = ec == 4;
+    char *ws = (char *)workspace;
+    if (pl.copy_a) {
+        uint16_t *A2 = (uint16_t *)(ws + pl.at_a);
+        if (g5::launch_realign_rows(A, lda, 0, 1, rows, pl.cols_a, g5::row_alignment((uint64_t)A, lda, 0, 1, 2), A2, pl.lda2,
+                                    (hipStream_t)stream) != hipSuccess)
+            return GEMM_ERR_LAUNCH;
+        a.A = A2;
+        a.lda = pl.lda2;
+    }
+    if (pl.copy_b) {
+        uint16_t *B2 = (uint16_t *)(ws + pl.at_b);
+        if (g5::launch_realign_rows(B, ldb, sB, pl.batch_b, pl.rows_b, cols_b,
+                                    g5::row_alignment((uint64_t)B, ldb, sB, pl.batch_b, 2), B2, pl.ldb2,
+                                    (hipStream_t)stream) != hipSuccess)
+            return GEMM_ERR_LAUNCH;
+        a.B = B2;
+        a.ldb = pl.ldb2;
+        a.sB = pl.batch_b > 1 ? pl.rows_b * pl.ldb2 : 0;
+    }
+    const int64_t widest = tn && a.lda > a.ldb ? a.lda : a.ldb;
+    a.piece = widest > 0 ? (((int64_t)1 << 29) / widest) / 32 * 32 : 32;
+    const hipError_t e = g5::launch_grouped(kind, a, pl.tile, (hipStream_t)stream);
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+int gemm_bf16_grouped_nt(int64_t E, int64_t M, int64_t N, int64_t K, const int32_t *offsets, const uint16_t *A,
+                         int64_t lda, const uint16_t *Bt, int64_t ldbt, int64_t strideBt, void *C, int64_t ldc,
+                         int c_type, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    return grouped_run(g5::GROUPED_NT, E, M, 0, N, K, offsets, A, lda, Bt, ldbt, strideBt, C, ldc, 0, c_type, workspace,
+                       workspace_bytes, stream);
+}
+
+int gemm_bf16_grouped(int64_t E, int64_t M, int64_t N, int64_t K, const int32_t *offsets, const uint16_t *A,
+                      int64_t lda, const uint16_t *B, int64_t ldb, int64_t strideB, void *C, int64_t ldc, int c_type,
+                      void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    return grouped_run(g5::GROUPED_NN, E, M, 0, N, K, offsets, A, lda, B, ldb, strideB, C, ldc, 0, c_type, workspace,
+                       workspace_bytes, stream);
+}
+
+int gemm_bf16_grouped_tn(int64_t E, int64_t rows, int64_t M, int64_t N, const int32_t *offsets, const uint16_t *At,
+                         int64_t ldat, const uint16_t *B, int64_t ldb, void *C, int64_t ldc, int64_t strideC,
+                         int c_type, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    return grouped_run(g5::GROUPED_TN, E, rows, M, N, 0, offsets, At, ldat, B, ldb, 0, C, ldc, strideC, c_type, workspace,
+                       workspace_bytes, stream);
+}
+
 const char *gemm_status_string(int status)
 {
     switch (status) {

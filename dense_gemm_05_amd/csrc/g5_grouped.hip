@@ -1,0 +1,270 @@
+// g5_grouped.hip -- products grouped by expert with ragged numbers of rows.
+//
+// The rows of the token operand stand group behind group; offsets[e] ..
+// offsets[e + 1] - 1 are group e's:
+//
+//   NT  C[r] = A[r] . Bt_e^T      the experts' projection, Bt [E, N, K]
+//   NN  C[r] = A[r] . B_e         its input gradient, B [E, K, N]
+//   TN  C_e = At_e^T . B_e        its weight gradient, C [E, M, N], the sum
+//                                 over the group's rows
+//
+// The group sizes are known on the device only (a router's counts), so every
+// workgroup finds its tile from the offsets itself: a wave takes a lane per
+// group and adds up the tiles before it.  The grid is the most tiles that any
+// offsets can give; workgroups past the last tile end at once.
+#include <hip/hip_runtime.h>
+
+#include "g5_device.h"
+#include "g5_kernels.h"
+#include "g5_stream.h"
+
+namespace g5 {
+
+namespace {
+
+// 64 groups, a lane each: first row, rows, and tiles of BM rows up to and with
+// the group.  Offsets are held to [0, M] and to ascending order (one lower
+// than an earlier one counts as that), so that whatever they hold no row lies
+// in two groups or outside the operands.  `floor`: the end of the group
+// before; becomes the end of the last of these.
+struct GroupLanes {
+    int first, rows, tiles;
+};
+__device__ __forceinline__ GroupLanes scan_groups(const GroupedArgs &p, int base, int bm, int &floor)
+{
+    const int lane = threadIdx.x & 63, e = base + lane, M = (int)p.rows;
+    auto held = [&](int v) { return v < 0 ? 0 : v > M ? M : v; };
+    const int s = e < p.E ? held(p.offsets[e]) : 0, t = e < p.E ? held(p.offsets[e + 1]) : 0;
+    int first = s > floor ? s : floor;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(first, o, 64);
+        if (lane >= o && v > first) first = v;
+    }
+    const int end = t > first ? t : first;
+    GroupLanes g{first, end - first, (end - first + bm - 1) / bm};
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(g.tiles, o, 64);
+        if (lane >= o) g.tiles += v;
+    }
+    floor = __builtin_amdgcn_readlane(end, 63);
+    return g;
+}
+
+// The tile of workgroup `wg`: tiles run group by group, and within a group in
+// column bands of up to 8 tiles (the rows of a band meet each column panel of
+// the group's weight one after the other), the whole sequence shared out over
+// the XCDs in contiguous runs.
+struct GroupTile {
+    int group, row, rows, tn;      // its first row in A and C, and its rows
+};
+__device__ __forceinline__ bool find_tile(const GroupedArgs &p, int bm, GroupTile &t)
+{
+    int total = 0, floor = 0;
+    for (int base = 0; base < p.E; base += 64) {
+        const GroupLanes g = scan_groups(p, base, bm, floor);
+        total += __builtin_amdgcn_readlane(g.tiles, 63);
+    }
+    const int64_t all = (int64_t)total * p.tiles_n;
+    if ((int64_t)blockIdx.x >= all) return false;
+    const int L = (int)tile_map(blockIdx.x, 1, all, 1, 1).tm;
+    const int tiles_n = (int)p.tiles_n;
+    const int at = L / tiles_n;                // in tiles of BM rows
+    int before = 0;
+    floor = 0;
+    for (int base = 0; base < p.E; base += 64) {
+        const GroupLanes g = scan_groups(p, base, bm, floor);
+        const uint64_t past = __ballot(before + g.tiles > at);
+        if (past) {
+            const int lane = __builtin_ctzll(past);
+            const int first = __builtin_amdgcn_readlane(g.first, lane), rows = __builtin_amdgcn_readlane(g.rows, lane);
+            const int tiles = (rows + bm - 1) / bm;
+            const int r = L - (before + __builtin_amdgcn_readlane(g.tiles, lane) - tiles) * tiles_n;
+            const int band = r / (8 * tiles_n), left = tiles - 8 * band, h = left < 8 ? left : 8;
+            const int rr = r - band * 8 * tiles_n, tm = 8 * band + rr % h;
+            t.group = base + lane;
+            t.row = first + tm * bm;
+            t.rows = rows - tm * bm;
+            if (t.rows > bm) t.rows = bm;
+            t.tn = rr / h;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(g.tiles, 63);
+    }
+    return false;
+}
+
+// Group e's rows alone.
+__device__ __forceinline__ void find_group(const GroupedArgs &p, int e, int &first, int &rows)
+{
+    int floor = 0;
+    for (int base = 0; base <= e; base += 64) {
+        const GroupLanes g = scan_groups(p, base, 1, floor);
+        if (e - base < 64) {
+            first = __builtin_amdgcn_readlane(g.first, e - base);
+            rows = __builtin_amdgcn_readlane(g.rows, e - base);
+        }
+    }
+}
+
+// An output tile on the LDS ring (RingTile): operand bases moved to the
+// tile's own first row and column, so that 32-bit offsets span no more than
+// the tile's rows.  Where the summed axis walks rows (B of NN, both of TN),
+// it goes in pieces of p.piece that keep them so.
+template <int BM, int BN, int WGM, int WGN, int KIND>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, KIND == GROUPED_NT, false, KIND == GROUPED_TN>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    GemmArgs q{};
+    int64_t K;
+    const char *A = (const char *)p.A, *B = (const char *)p.B;
+    int n0;
+    if constexpr (KIND == GROUPED_TN) {
+        const TileCoord tc = tile_map(blockIdx.x, p.E, p.tiles_m, p.tiles_n, p.group_m);
+        int first, rows;
+        find_group(p, (int)tc.b, first, rows);
+        const int m0 = (int)tc.tm * BM;
+        n0 = (int)tc.tn * BN;
+        K = rows;
+        A += (first * p.lda + m0) * 2;
+        B += (first * p.ldb + n0) * 2;
+        q.C = (char *)p.C + (tc.b * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        q.M = p.M - m0 < BM ? p.M - m0 : BM;
+    } else {
+        GroupTile t;
+        if (!find_tile(p, BM, t)) return;
+        n0 = t.tn * BN;
+        K = p.K;
+        A += t.row * p.lda * 2;
+        B += (t.group * p.sB + (KIND == GROUPED_NT ? n0 * p.ldb : n0)) * 2;
+        q.C = (char *)p.C + (t.row * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        q.M = t.rows;
+    }
+    q.A = A;
+    q.B = B;
+    q.lda = p.lda;
+    q.ldb = p.ldb;
+    q.ldc = p.ldc;
+    q.align_a = q.align_b = 16;
+    q.align_c = p.align_c;
+    q.out_f32 = p.out_f32;
+    // (rows of B are read in whole 16-byte chunks: the host pads them)
+    const int64_t left = p.N - n0;
+    q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 7) & ~(int64_t)7) : BN;
+    const TileCoord here{0, 0, 0};
+    f32x4 acc[R::FN][R::FM];
+    R::zero(acc);
+    for (int64_t done = 0; done < K;) {
+        q.K = KIND != GROUPED_NT && K - done > p.piece ? p.piece : K - done;
+        if (done > 0) __syncthreads();            // every wave is through with the ring
+        R::accumulate(q, smem, here, 0, q.K, acc);
+        done += q.K;
+        q.A = (const char *)q.A + q.K * (KIND == GROUPED_TN ? p.lda : 1) * 2;
+        q.B = (const char *)q.B + q.K * (KIND == GROUPED_NT ? 1 : p.ldb) * 2;
+    }
+    q.N = left < BN ? left : BN;
+    R::store(q, smem, here, acc);
+}
+
+// NT with a few rows per group (a decoding step): bound by reading the
+// groups' weights once, so a workgroup owns 32 weight rows of one group,
+// streamed from HBM into the matrix core by four waves on contiguous pieces of
+// K, and up to 32 of the group's rows.
+constexpr int kStreamWaves = 4, kStreamCols = 32;
+
+template <int NC, int D>
+__device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTile &t, f32x4 (&red)[kStreamWaves][2][64])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int n0 = t.tn * kStreamCols, N = (int)p.N;
+    const char *const W = (const char *)p.B + t.group * p.sB * 2;
+    f32x4 acc[2][NC];
+    bool xok[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        xok[c] = 16 * c + li < t.rows;
+        acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    const int K = (int)p.K, steps = (K + 63) / 64;
+    const int s0 = steps * wave / kStreamWaves, s1 = steps * (wave + 1) / kStreamWaves;
+    // (rows past N repeat the block's first and are not stored)
+    const char *wbase[2];
+    uint32_t woff[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int n = n0 + 16 * r < N ? n0 + 16 * r : n0;
+        wbase[r] = W + n * p.ldb * 2;
+        woff[r] = (uint32_t)(n + li < N ? li : 0) * (uint32_t)(p.ldb * 2) + 16 * g;
+    }
+    RowStream<false, 2, NC, D> b;
+    auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            ok[c] = xok[c];
+            xoff[c] = (uint32_t)(xok[c] ? 16 * c + li : 0) * (uint32_t)(p.lda * 2) + x_lane<false>(g);
+        }
+    };
+    b.run(wbase, woff, (const char *)p.A + t.row * p.lda * 2, tokens, s0, s1, K, g, acc);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        __syncthreads();             // (the chunk before has been read)
+        red[wave][0][lane] = acc[0][c];
+        red[wave][1][lane] = acc[1][c];
+        __syncthreads();
+        // a wave per block of 16 columns adds the waves' parts in order
+        if (wave < 2 && xok[c]) {
+            f32x4 s = red[0][wave][lane];
+#pragma unroll
+            for (int w = 1; w < kStreamWaves; ++w) s += red[w][wave][lane];
+            const int64_t n = n0 + 16 * wave + 4 * g;
+            if (n < N) store4(p.C, p.out_f32 != 0, p.ldc, t.row + 16 * c + li, n, s, n + 4 <= N, t.row + t.rows, N, p.align_c);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kStreamWaves * 64, 4) k_grouped_stream(GroupedArgs p)
+{
+    __shared__ f32x4 red[kStreamWaves][2][64];
+    GroupTile t;
+    if (!find_tile(p, kGroupedStreamRows, t)) return;
+    if (t.rows > 16) stream_tile<2, 2>(p, t, red);
+    else stream_tile<1, 3>(p, t, red);
+}
+
+template <int BM, int BN, int WGM, int WGN>
+hipError_t launch_kind(int kind, const GroupedArgs &a, int64_t grid, hipStream_t s)
+{
+    const dim3 g((unsigned)grid), b(WGM * WGN * 64);
+    switch (kind) {
+    case GROUPED_NT: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NT>), g, b, 0, s, a); break;
+    case GROUPED_NN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NN>), g, b, 0, s, a); break;
+    case GROUPED_TN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_TN>), g, b, 0, s, a); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream_t s)
+{
+    GroupedArgs a = args;
+    const int64_t grid = grouped_grid(kind, a.E, a.rows, a.M, a.N, tile);
+    const int64_t bn = grouped_tile_n(tile);
+    a.tiles_n = (a.N + bn - 1) / bn;
+    a.tiles_m = (a.M + grouped_tile_m(tile) - 1) / grouped_tile_m(tile);
+    a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
+    switch (tile) {
+    case GROUPED_STREAM:
+        if (kind != GROUPED_NT) return hipErrorInvalidValue;
+        hipLaunchKernelGGL(k_grouped_stream, dim3((unsigned)grid), dim3(kStreamWaves * 64), 0, s, a);
+        return hipGetLastError();
+    case GROUPED_128: return launch_kind<128, 128, 4, 2>(kind, a, grid, s);
+    case GROUPED_256: return launch_kind<256, 256, 2, 4>(kind, a, grid, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace g5

@@ -231,4 +231,36 @@ hipError_t launch_lora_shrink(const GemmArgs &a, const LoraArgs &q, hipStream_t 
 // with K split; variants 1 and 2) and the small-M CFG_DECODE_NT.
 hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int variant, int64_t grid, hipStream_t s);
 
+// Products grouped by expert with ragged numbers of rows (g5_grouped.hip):
+// group e's rows are offsets[e] .. offsets[e + 1] - 1 of A and C (NT, NN) or
+// of A and B (TN).  Rows of A and B 16-byte aligned for the ring tiles (B's of
+// NN and TN, and A's of TN, whole 16-byte chunks long), of any alignment for
+// the stream; C's of any.
+enum GroupedKind { GROUPED_NT = 0, GROUPED_NN = 1, GROUPED_TN = 2 };
+enum GroupedTile { GROUPED_STREAM = 0, GROUPED_128 = 1, GROUPED_256 = 2 };
+constexpr int kGroupedMaxGroups = 4096;
+constexpr int kGroupedStreamRows = 32;          // rows of a group per workgroup of the stream
+struct GroupedArgs {
+    const uint16_t *A, *B;
+    void *C;
+    const int32_t *offsets;          // [E + 1]
+    int64_t E, rows;                 // rows of A (TN: of A and B)
+    int64_t M, N, K;                 // M: TN's output rows; K: the summed axis of NT and NN
+    int64_t lda, ldb, sB, ldc, sC;   // sB: B's group stride (NT, NN); sC: C's (TN)
+    int64_t piece;                   // NN, TN: elements of the summed axis at a time, a multiple of 32
+    int align_c, out_f32;
+    int64_t tiles_m, tiles_n, group_m;   // (set by the launch)
+};
+inline int64_t grouped_tile_m(int tile) { return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : kGroupedStreamRows; }
+inline int64_t grouped_tile_n(int tile) { return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : 32; }
+// Workgroups: the most tiles that E groups of `rows` rows can have.
+inline int64_t grouped_grid(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int tile)
+{
+    const int64_t bm = grouped_tile_m(tile), bn = grouped_tile_n(tile), tn = (N + bn - 1) / bn;
+    if (kind == GROUPED_TN) return E * ((M + bm - 1) / bm) * tn;
+    const int64_t most = (rows + E * (bm - 1)) / bm;
+    return (most < rows ? most : rows) * tn;
+}
+hipError_t launch_grouped(int kind, const GroupedArgs &a, int tile, hipStream_t s);
+
 }  // namespace g5

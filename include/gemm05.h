@@ -690,6 +690,75 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t
                              uint64_t x_addr, int64_t ldx, uint64_t w_addr, int64_t ldw,
                              uint64_t c_addr, int64_t ldc, int c_type, uint64_t *bytes);
 
+/* ---- products grouped by expert -------------------------------------------------
+ *
+ * The experts' products of a mixture-of-experts layer for prompts and
+ * training, where every expert has another number of rows.  The rows stand
+ * group behind group: group e's are offsets[e] .. offsets[e + 1] - 1
+ * (offsets: E + 1 int32 in device memory, 0 <= offsets[0] <= offsets[1] <=
+ * ...).  bf16 operands, FP32 sums rounded once to C's type:
+ *
+ *   gemm_bf16_grouped_nt  C[r] = A[r] . Bt_e^T   A [M, K], Bt_e [N, K] at
+ *                         Bt + e*strideBt: a projection, weights [out, in]
+ *   gemm_bf16_grouped     C[r] = A[r] . B_e      A [M, K], B_e [K, N] at
+ *                         B + e*strideB: the projection's input gradient (A =
+ *                         dY, B = the weights [out, in])
+ *   gemm_bf16_grouped_tn  C_e = At_e^T . B_e     At [rows, M], B [rows, N];
+ *                         C_e [M, N] at C + e*strideC: the projection's weight
+ *                         gradient (At = dY, B = the layer's input)
+ *
+ * Rows of no group (before offsets[0], from offsets[E] on) are neither read
+ * nor written: C's are left as they were, and values in one group's rows, NaN
+ * and infinities among them, do not reach another's outputs.  A group without
+ * rows gives nothing, its C_e of the weight gradient zeros.  The offsets are
+ * read on the device and cannot be refused: they are held to the rows there
+ * are, and one lower than an earlier one counts as that one.  strideBt or
+ * strideB 0: one weight for every group.  K == 0: C := 0 in the groups' rows.
+ * Deterministic, no atomics.
+ *
+ * E <= 4096, M (rows) < 2^31, other sizes <= 2^30.  With at most 32 rows per
+ * group in the mean (M <= 32 E) the projection streams the weights past the
+ * rows (any alignment); else rows of A or B that are not 16-byte aligned (and
+ * those whose length is not a multiple of 8 elements, in the gradients: rows
+ * of B and of At) are first copied to padded ones in the workspace
+ * (gemm_grouped_workspace_size bytes, 0 where no copy is needed; its first
+ * GEMM_WORKSPACE_COUNTER_BYTES are left untouched, so gemm_run's serves).
+ * Errors, nothing enqueued: GEMM_ERR_INVALID_ARG for sizes outside these
+ * ranges, a c_type other than bf16 and float, strides below the row lengths,
+ * negative strides, strideC below C_e's extent, missing or misaligned
+ * pointers, C or the workspace overlapping an input or each other;
+ * GEMM_ERR_WORKSPACE for a missing or small workspace; GEMM_ERR_UNSUPPORTED
+ * for rows more than 2^21 elements apart in the tiled kernels, and more than
+ * 2^22 workgroups. */
+int gemm_bf16_grouped_nt(int64_t E, int64_t M, int64_t N, int64_t K,
+                         const int32_t *offsets,
+                         const uint16_t *A, int64_t lda,
+                         const uint16_t *Bt, int64_t ldbt, int64_t strideBt,
+                         void *C, int64_t ldc, int c_type,
+                         void *workspace, uint64_t workspace_bytes,
+                         void *stream);
+int gemm_bf16_grouped(int64_t E, int64_t M, int64_t N, int64_t K,
+                      const int32_t *offsets,
+                      const uint16_t *A, int64_t lda,
+                      const uint16_t *B, int64_t ldb, int64_t strideB,
+                      void *C, int64_t ldc, int c_type,
+                      void *workspace, uint64_t workspace_bytes,
+                      void *stream);
+int gemm_bf16_grouped_tn(int64_t E, int64_t rows, int64_t M, int64_t N,
+                         const int32_t *offsets,
+                         const uint16_t *At, int64_t ldat,
+                         const uint16_t *B, int64_t ldb,
+                         void *C, int64_t ldc, int64_t strideC, int c_type,
+                         void *workspace, uint64_t workspace_bytes,
+                         void *stream);
+
+/* Workspace bytes of the three (host only; pointers as integers, their
+ * alignment decides).  kind: 0 gemm_bf16_grouped_nt and 1 gemm_bf16_grouped
+ * (rows: M; M unused), 2 gemm_bf16_grouped_tn (K and strideB unused). */
+int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int64_t K,
+                                uint64_t a_addr, int64_t lda, uint64_t b_addr, int64_t ldb, int64_t strideB,
+                                uint64_t *bytes);
+
 /* Static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 
