@@ -23,4 +23,7 @@ from .gemm import (  # noqa: F401
     gemm_bf16_nt_affine, gemm_bf16_tn_affine, plan_query, workspace_size, Workspace,
 )
 from .token_ops import rms_norm, rms_norm_e4m3, rms_norm_backward, moe_swiglu, gemm_bf16_nt_lora  # noqa: F401
-from .train_ops import gemm_bf16_grouped_nt, gemm_bf16_grouped, gemm_bf16_grouped_tn  # noqa: F401
+from .train_ops import (  # noqa: F401
+    gemm_bf16_grouped_nt, gemm_bf16_grouped, gemm_bf16_grouped_tn, linear_cross_entropy, linear_cross_entropy_backward,
+    linear_distill, linear_distill_backward,
+)

@@ -52,7 +52,9 @@ EXPORTS = ("gemm_sgemm", "gemm_bf16", "gemm_bf16_batched", "gemm_bf16_nt", "gemm
            "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_workspace_size",
            "gemm_moe_swiglu", "gemm_moe_workspace_size",
            "gemm_bf16_nt_lora", "gemm_lora_workspace_size",
-           "gemm_bf16_grouped_nt", "gemm_bf16_grouped", "gemm_bf16_grouped_tn", "gemm_grouped_workspace_size")
+           "gemm_bf16_grouped_nt", "gemm_bf16_grouped", "gemm_bf16_grouped_tn", "gemm_grouped_workspace_size",
+           "gemm_linear_cross_entropy", "gemm_linear_cross_entropy_backward", "gemm_linear_distill",
+           "gemm_linear_distill_backward", "gemm_linear_loss_workspace_size")
 
 
 class GemmPlan(ctypes.Structure):
@@ -184,6 +186,18 @@ def lib():
     L.gemm_grouped_workspace_size.argtypes = [i32, i64, i64, i64, i64, i64, u64, i64, u64, i64, i64,
                                               ctypes.POINTER(u64)]
     L.gemm_grouped_workspace_size.restype = i32
+    L.gemm_linear_cross_entropy.argtypes = [i64, i64, i64, p, i64, p, i64, f32, p, i32, p, p, p, u64, p]
+    L.gemm_linear_cross_entropy.restype = i32
+    L.gemm_linear_cross_entropy_backward.argtypes = [i64, i64, i64, p, i64, p, i64, f32, p, i32, p, p, p, i64, p, i64,
+                                                     i32, p, u64, p]
+    L.gemm_linear_cross_entropy_backward.restype = i32
+    L.gemm_linear_distill.argtypes = [i64, i64, i64, p, i64, p, i64, f32, i64, p, i32, p, p, p, p, u64, p]
+    L.gemm_linear_distill.restype = i32
+    L.gemm_linear_distill_backward.argtypes = [i64, i64, i64, p, i64, p, i64, f32, i64, p, i32, p, p, p, p, i64, p, i64,
+                                               i32, p, u64, p]
+    L.gemm_linear_distill_backward.restype = i32
+    L.gemm_linear_loss_workspace_size.argtypes = [i32, i64, i64, i64, i64, u64, i64, u64, i64, ctypes.POINTER(u64)]
+    L.gemm_linear_loss_workspace_size.restype = i32
     _lib = L
     return L
 

@@ -1755,6 +1755,350 @@ int gemm_bf16_grouped_tn(int64_t E, int64_t rows, int64_t M, int64_t N, const in
                        workspace_bytes, stream);
 }
 
+// ---- the loss over a vocabulary behind the last projection
+namespace {
+// Scratch of a call, behind the counter region, each part 256-byte aligned.
+struct VocabPlan {
+    int tile = 128;                      // 256, 128, or 0: the stream (forward)
+    int64_t piece = 0, parts = 0;        // vocabulary rows at a time; column tiles (forward)
+    bool copy_x = false, copy_w = false;
+    int64_t ld2 = 0;                     // row length of the copies
+    size_t run = 0;                      // what the products' own paths take (with the counter region)
+    size_t x2 = 0, w2 = 0, part = 0, zt = 0, d = 0, sums = 0, ids = 0, q = 0, has = 0, weight = 0, alpha = 0, total = 0;
+};
+struct VocabCall {
+    bool grad;
+    int64_t M, V, K, topk;
+    uint64_t x;
+    int64_t ldx;
+    uint64_t w;
+    int64_t ldw;
+};
+}  // namespace
+
+static bool vocab_sizes_ok(const VocabCall &c)
+{
+    return c.M >= 0 && c.M <= 1 << 24 && c.V >= 1 && c.V <= 0x7fffffff - 256 && c.K >= 1 && c.K <= 1 << 21 && c.topk >= 1 &&
+           c.topk <= g5::kVocabMaxTopk;
+}
+
+// dX's share of a piece: sums := D . W (+ sums), an ordinary product.
+static Problem vocab_dx_problem(const VocabCall &c, int64_t rows, uint64_t d, int64_t ldd, uint64_t w, int64_t ldw,
+                                uint64_t sums, int64_t ld2, bool more)
+{
+    Problem p{GEMM_OP_BF16_AFFINE, 1, c.M, ld2, rows, d, w, sums, ldd, ldw, ld2, 0, 0, 0, GEMM_OUT_F32};
+    p.beta = more ? 1.0f : 0.0f;
+    return p;
+}
+
+static int vocab_plan(const VocabCall &c, VocabPlan &pl)
+{
+    pl = VocabPlan();
+    pl.ld2 = (c.K + 7) / 8 * 8;
+    const int align_x = g5::row_alignment(c.x, c.ldx, 0, 1, 2), align_w = g5::row_alignment(c.w, c.ldw, 0, 1, 2);
+    const size_t CR = g5::kCounterBytes;
+    size_t at = CR;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += g5::round256(bytes);
+        return here;
+    };
+    if (!c.grad && c.M <= g5::kVocabStreamRows && c.ldx < (1 << 24) && c.ldw < (1 << 26)) {
+        pl.tile = 0;
+        pl.piece = c.V;
+        pl.parts = g5::cdiv(c.V, 32);
+        if (pl.parts > (int64_t)1 << 23) return GEMM_ERR_UNSUPPORTED;
+    } else {
+        if (g5::cdiv(c.M, 256) * g5::cdiv(c.V, 256) >= g5::kNumCU && c.M > 128) pl.tile = 256;
+        pl.copy_x = c.grad || align_x < 16;
+        // (dX's product reads W's rows in whole 16-byte chunks)
+        pl.copy_w = align_w < 16 || (c.grad && c.K % 8 != 0);
+        const int64_t ldw = pl.copy_w ? pl.ld2 : c.ldw;
+        if (c.ldx > 1 << 21 || ldw > 1 << 21) return GEMM_ERR_UNSUPPORTED;
+        // A piece: D of 2^27 elements (256 MiB, the Infinity Cache's size), the
+        // copy of W as many, and W's rows within 32-bit offsets.
+        int64_t rows = c.V;
+        const int64_t cache = (int64_t)1 << 27;
+        if (c.grad && c.M > 0 && rows > cache / c.M) rows = cache / c.M;
+        if (pl.copy_w && rows > cache / pl.ld2) rows = cache / pl.ld2;
+        if (c.grad && rows > ((int64_t)1 << 29) / ldw) rows = ((int64_t)1 << 29) / ldw;
+        if (rows < c.V) rows = rows < 256 ? 256 : rows / 256 * 256;
+        pl.piece = rows < c.V ? rows : c.V;
+        pl.parts = g5::cdiv(c.V, pl.tile);
+        if (g5::cdiv(c.M, pl.tile) * g5::cdiv(pl.piece, pl.tile) > (int64_t)1 << 22 ||
+            g5::cdiv(pl.piece, 128) * g5::cdiv(c.K, 128) > (int64_t)1 << 22)
+            return GEMM_ERR_UNSUPPORTED;
+    }
+    if (c.grad) {
+        const int64_t ldd = (pl.piece + 7) / 8 * 8, ldw = pl.copy_w ? pl.ld2 : c.ldw;
+        // (placeholder addresses: their alignment is what counts)
+        const uint64_t base = (uint64_t)1 << 40;
+        for (int64_t rows : {pl.piece, c.V % pl.piece ? c.V % pl.piece : pl.piece}) {
+            const Problem p = vocab_dx_problem(c, rows, base, ldd, pl.copy_w ? 2 * base : c.w, ldw, 3 * base, pl.ld2, true);
+            g5::Plan sub;
+            const int st = g5::select_plan(p, sub, true);
+            if (st != GEMM_OK) return st;
+            const size_t n = g5::ws_layout(p, sub).total;
+            pl.run = n > pl.run ? n : pl.run;
+        }
+        at = pl.run > CR ? g5::round256(pl.run) : CR;
+    }
+    if (pl.copy_x) pl.x2 = take((size_t)c.M * pl.ld2 * 2);
+    if (pl.copy_w) pl.w2 = take((size_t)pl.piece * pl.ld2 * 2);
+    if (!c.grad) {
+        pl.part = take((size_t)pl.parts * c.M * 8);
+        pl.zt = take((size_t)c.M * c.topk * 4);
+    } else {
+        pl.d = take((size_t)c.M * ((pl.piece + 7) / 8 * 8) * 2);
+        pl.sums = take((size_t)c.M * pl.ld2 * 4);
+        pl.ids = take((size_t)c.M * c.topk * 4);
+        pl.q = take((size_t)c.M * c.topk * 4);
+        pl.has = take((size_t)c.M * 4);
+        pl.weight = take((size_t)c.M * 4);
+        pl.alpha = take(4);
+    }
+    pl.total = at;
+    return GEMM_OK;
+}
+
+int gemm_linear_loss_workspace_size(int backward, int64_t M, int64_t V, int64_t K, int64_t topk, uint64_t x_addr,
+                                    int64_t ldx, uint64_t w_addr, int64_t ldw, uint64_t *bytes)
+{
+    if (bytes) *bytes = 0;
+    const VocabCall c{backward != 0, M, V, K, topk, x_addr, ldx, w_addr, ldw};
+    if (!vocab_sizes_ok(c)) return GEMM_ERR_INVALID_ARG;
+    if (M == 0) return GEMM_OK;
+    VocabPlan pl;
+    const int st = vocab_plan(c, pl);
+    if (st == GEMM_OK && bytes) *bytes = pl.total;
+    return st;
+}
+
+// teacher NULL: ids are labels (topk 1).
+static int vocab_check(const VocabCall &c, const uint16_t *X, const uint16_t *W, float scale, const void *ids,
+                       int id_bytes, g5::Range (&in)[6], const float *teacher)
+{
+    if (!vocab_sizes_ok(c) || !std::isfinite(scale) || !(scale > 0.0f) || (id_bytes != 4 && id_bytes != 8))
+        return GEMM_ERR_INVALID_ARG;
+    if (c.M > 0 && (!X || !W || !ids || c.ldx < c.K || c.ldw < c.K || (c.x % 2) || (c.w % 2) ||
+                    ((uint64_t)ids % id_bytes) || ((uint64_t)teacher % 4)))
+        return GEMM_ERR_INVALID_ARG;
+    if (c.M == 0) return GEMM_OK;
+    in[0] = g5::extent(c.x, 1, c.M, c.K, c.ldx, 0, 2);
+    in[1] = g5::extent(c.w, 1, c.V, c.K, c.ldw, 0, 2);
+    in[2] = vec_range(ids, c.M * c.topk, id_bytes);
+    in[3] = vec_range(teacher, c.M * c.topk, 4);
+    return in[0].hi > ((__int128)1 << 63) || in[1].hi > ((__int128)1 << 63) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+}
+
+static g5::VocabArgs vocab_args(const VocabCall &c, const uint16_t *X, const uint16_t *W, float scale, const void *ids,
+                                int id_bytes, const float *teacher)
+{
+    g5::VocabArgs a{};
+    a.X = X;
+    a.W = W;
+    a.M = c.M;
+    a.V = a.vocab = c.V;
+    a.K = c.K;
+    a.ldx = c.ldx;
+    a.ldw = c.ldw;
+    a.scale = scale;
+    a.ids = ids;
+    a.ids64 = id_bytes == 8;
+    a.topk = (int)c.topk;
+    a.teacher = teacher;
+    return a;
+}
+
+// The rows of W of the piece that starts at v0, as they are or copied.
+static hipError_t vocab_piece(const VocabCall &c, const VocabPlan &pl, char *ws, const uint16_t *W, int64_t v0,
+                              g5::VocabArgs &a, hipStream_t s)
+{
+    a.v0 = v0;
+    a.V = c.V - v0 < pl.piece ? c.V - v0 : pl.piece;
+    a.W = W + v0 * c.ldw;
+    a.ldw = c.ldw;
+    if (!pl.copy_w) return hipSuccess;
+    uint16_t *W2 = (uint16_t *)(ws + pl.w2);
+    const hipError_t e = g5::launch_realign_rows(a.W, c.ldw, 0, 1, a.V, c.K, g5::row_alignment(c.w, c.ldw, 0, 1, 2), W2,
+                                                 pl.ld2, s);
+    a.W = W2;
+    a.ldw = pl.ld2;
+    return e;
+}
+
+static int vocab_forward(const VocabCall &c, const uint16_t *X, const uint16_t *W, float scale, const void *ids,
+                         int id_bytes, const float *teacher, float *loss, float *lse, void *workspace,
+                         uint64_t workspace_bytes, void *stream)
+{
+    using g5::Range;
+    Range in[6] = {};
+    int st = vocab_check(c, X, W, scale, ids, id_bytes, in, teacher);
+    if (st != GEMM_OK || c.M == 0) return st;
+    if (!loss || ((uint64_t)loss % 4) || ((uint64_t)lse % 4)) return GEMM_ERR_INVALID_ARG;
+    VocabPlan pl;
+    st = vocab_plan(c, pl);
+    if (st != GEMM_OK) return st;
+    const Range out[] = {vec_range(loss, c.M, 4), vec_range(lse, c.M, 4),
+                         workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                                   : Range{0, 0}};
+    if (outputs_overlap(out, 3, in, 4)) return GEMM_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < pl.total) return GEMM_ERR_WORKSPACE;
+    if ((uint64_t)workspace % 256) return GEMM_ERR_INVALID_ARG;
+    st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    char *ws = (char *)workspace;
+    const hipStream_t s = (hipStream_t)stream;
+    g5::VocabArgs a = vocab_args(c, X, W, scale, ids, id_bytes, teacher);
+    a.part = (float2 *)(ws + pl.part);
+    a.zt = (float *)(ws + pl.zt);
+    a.parts = pl.parts;
+    a.loss = loss;
+    a.lse_out = lse;
+    if (pl.copy_x) {
+        uint16_t *X2 = (uint16_t *)(ws + pl.x2);
+        if (g5::launch_realign_rows(X, c.ldx, 0, 1, c.M, c.K, g5::row_alignment(c.x, c.ldx, 0, 1, 2), X2, pl.ld2, s) !=
+            hipSuccess)
+            return GEMM_ERR_LAUNCH;
+        a.X = X2;
+        a.ldx = pl.ld2;
+    }
+    for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
+        if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+        a.tile0 = pl.tile ? v0 / pl.tile : 0;
+        if (g5::launch_vocab_stats(a, pl.tile, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+    }
+    return g5::launch_vocab_join(a, s) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t *W, float scale, const void *ids,
+                          int id_bytes, const float *teacher, const float *dloss, const float *lse, uint16_t *dX,
+                          int64_t lddx, void *dW, int64_t lddw, int dw_type, void *workspace,
+                          uint64_t workspace_bytes, void *stream)
+{
+    using g5::Range;
+    Range in[6] = {};
+    int st = vocab_check(c, X, W, scale, ids, id_bytes, in, teacher);
+    if (st != GEMM_OK) return st;
+    if (dw_type != GEMM_OUT_BF16 && dw_type != GEMM_OUT_F32) return GEMM_ERR_INVALID_ARG;
+    const int ew = dw_type == GEMM_OUT_F32 ? 4 : 2;
+    if (c.M == 0) dX = nullptr;
+    if (!dX && !dW) return GEMM_OK;
+    if ((c.M > 0 && (!dloss || !lse || ((uint64_t)dloss % 4) || ((uint64_t)lse % 4))) || (dX && (lddx < c.K || ((uint64_t)dX % 2))) ||
+        (dW && (lddw < c.K || ((uint64_t)dW % ew))))
+        return GEMM_ERR_INVALID_ARG;
+    const Range none{0, 0};
+    in[4] = c.M > 0 ? vec_range(dloss, c.M, 4) : none;
+    in[5] = c.M > 0 ? vec_range(lse, c.M, 4) : none;
+    VocabPlan pl;
+    if (c.M > 0) {
+        st = vocab_plan(c, pl);
+        if (st != GEMM_OK) return st;
+    } else if (g5::cdiv(c.V, 128) * g5::cdiv(c.K, 128) > (int64_t)1 << 22) {
+        return GEMM_ERR_UNSUPPORTED;
+    }
+    const Range out[] = {dX ? g5::extent((uint64_t)dX, 1, c.M, c.K, lddx, 0, 2) : none,
+                         dW ? g5::extent((uint64_t)dW, 1, c.V, c.K, lddw, 0, ew) : none,
+                         c.M > 0 && workspace
+                             ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                             : none};
+    for (const Range &r : out)
+        if (r.hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
+    if (outputs_overlap(out, 3, in, 6)) return GEMM_ERR_INVALID_ARG;
+    if (c.M > 0 && (!workspace || workspace_bytes < pl.total)) return GEMM_ERR_WORKSPACE;
+    if (c.M > 0 && ((uint64_t)workspace % 256)) return GEMM_ERR_INVALID_ARG;
+    st = g5::check_device();
+    if (st != GEMM_OK) return st;
+    char *ws = (char *)workspace;
+    const hipStream_t s = (hipStream_t)stream;
+    g5::VocabArgs a = vocab_args(c, X, W, scale, ids, id_bytes, teacher);
+    g5::VocabGrad b{};
+    b.dX = dX;
+    b.lddx = lddx;
+    b.dW = dW;
+    b.lddw = lddw;
+    b.dw_f32 = ew == 4;
+    b.align_dw = g5::row_alignment((uint64_t)dW, lddw, 0, 1, ew);
+    b.ldx2 = (c.K + 7) / 8 * 8;
+    b.rows_at_once = 32;
+    if (c.M == 0) {                  // the empty sum
+        a.V = c.V;
+        return g5::launch_vocab_dw(a, b, 128, s) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+    }
+    b.dloss = dloss;
+    b.lse = lse;
+    b.ids = (int32_t *)(ws + pl.ids);
+    b.has = (int32_t *)(ws + pl.has);
+    b.q = (float *)(ws + pl.q);
+    b.weight = (float *)(ws + pl.weight);
+    b.alpha = (float *)(ws + pl.alpha);
+    b.X2 = (uint16_t *)(ws + pl.x2);
+    b.align_x = g5::row_alignment(c.x, c.ldx, 0, 1, 2);
+    b.D = (uint16_t *)(ws + pl.d);
+    b.ldd = (pl.piece + 7) / 8 * 8;
+    b.sums = (float *)(ws + pl.sums);
+    const int64_t widest = b.ldd > b.ldx2 ? b.ldd : b.ldx2;
+    b.rows_at_once = (((int64_t)1 << 29) / widest) / 32 * 32;
+    if (g5::launch_vocab_prep(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+    a.X = b.X2;
+    a.ldx = b.ldx2;
+    const int tile_w = g5::cdiv(pl.piece, 256) * g5::cdiv(c.K, 256) >= g5::kNumCU ? 256 : 128;
+    for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
+        if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+        if (g5::launch_vocab_dlogits(a, b, pl.tile, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+        if (dW && g5::launch_vocab_dw(a, b, tile_w, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+        if (dX) {
+            const Problem p = vocab_dx_problem(c, a.V, (uint64_t)b.D, b.ldd, (uint64_t)a.W, a.ldw, (uint64_t)b.sums, b.ldx2,
+                                               v0 > 0);
+            st = g5::run(p, stream, workspace, pl.run);
+            if (st != GEMM_OK) return st;
+        }
+    }
+    if (dX && g5::launch_vocab_dx(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+    return GEMM_OK;
+}
+
+int gemm_linear_cross_entropy(int64_t M, int64_t V, int64_t K, const uint16_t *X, int64_t ldx, const uint16_t *Wt,
+                              int64_t ldw, float scale, const void *targets, int index_bytes, float *loss, float *lse,
+                              void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    const VocabCall c{false, M, V, K, 1, (uint64_t)X, ldx, (uint64_t)Wt, ldw};
+    return vocab_forward(c, X, Wt, scale, targets, index_bytes, nullptr, loss, lse, workspace, workspace_bytes, stream);
+}
+
+int gemm_linear_cross_entropy_backward(int64_t M, int64_t V, int64_t K, const uint16_t *X, int64_t ldx,
+                                       const uint16_t *Wt, int64_t ldw, float scale, const void *targets,
+                                       int index_bytes, const float *dloss, const float *lse, uint16_t *dX,
+                                       int64_t lddx, void *dW, int64_t lddw, int dw_type, void *workspace,
+                                       uint64_t workspace_bytes, void *stream)
+{
+    const VocabCall c{true, M, V, K, 1, (uint64_t)X, ldx, (uint64_t)Wt, ldw};
+    return vocab_backward(c, X, Wt, scale, targets, index_bytes, nullptr, dloss, lse, dX, lddx, dW, lddw, dw_type, workspace,
+                          workspace_bytes, stream);
+}
+
+int gemm_linear_distill(int64_t M, int64_t V, int64_t K, const uint16_t *X, int64_t ldx, const uint16_t *Wt,
+                        int64_t ldw, float scale, int64_t topk, const void *ids, int index_bytes,
+                        const float *teacher, float *loss, float *lse, void *workspace, uint64_t workspace_bytes,
+                        void *stream)
+{
+    const VocabCall c{false, M, V, K, topk, (uint64_t)X, ldx, (uint64_t)Wt, ldw};
+    if (M > 0 && !teacher) return GEMM_ERR_INVALID_ARG;
+    return vocab_forward(c, X, Wt, scale, ids, index_bytes, teacher, loss, lse, workspace, workspace_bytes, stream);
+}
+
+int gemm_linear_distill_backward(int64_t M, int64_t V, int64_t K, const uint16_t *X, int64_t ldx, const uint16_t *Wt,
+                                 int64_t ldw, float scale, int64_t topk, const void *ids, int index_bytes,
+                                 const float *teacher, const float *dloss, const float *lse, uint16_t *dX,
+                                 int64_t lddx, void *dW, int64_t lddw, int dw_type, void *workspace,
+                                 uint64_t workspace_bytes, void *stream)
+{
+    const VocabCall c{true, M, V, K, topk, (uint64_t)X, ldx, (uint64_t)Wt, ldw};
+    if (M > 0 && !teacher) return GEMM_ERR_INVALID_ARG;
+    return vocab_backward(c, X, Wt, scale, ids, index_bytes, teacher, dloss, lse, dX, lddx, dW, lddw, dw_type, workspace,
+                          workspace_bytes, stream);
+}
+
 const char *gemm_status_string(int status)
 {
     switch (status) {

@@ -263,4 +263,47 @@ inline int64_t grouped_grid(int kind, int64_t E, int64_t rows, int64_t M, int64_
 }
 hipError_t launch_grouped(int kind, const GroupedArgs &a, int tile, hipStream_t s);
 
+// The loss over a vocabulary behind the last projection, and its gradient
+// (g5_vocab.hip).  A piece of the vocabulary: V rows of W from v0 on.
+constexpr int kVocabMaxTopk = 256;
+constexpr int kVocabStreamRows = 32;    // rows of X up to which the weight is streamed past them
+struct VocabArgs {
+    const uint16_t *X, *W;              // 16-byte aligned rows for the ring tiles, any for the stream
+    int64_t M, V, K, ldx, ldw;
+    int64_t v0, vocab;                  // the piece's first token; all tokens
+    float scale;
+    const void *ids;                    // [M, topk], int32 or (ids64) int64
+    int ids64, topk;
+    const float *teacher;               // [M, topk], or NULL: ids are labels (topk 1)
+    float2 *part;                       // [parts, M]: maximum and sum of a row in a column tile
+    float *zt;                          // [M, topk]: the targets' logits
+    int64_t parts, tile0;               // column tiles in all; the piece's first
+    float *loss, *lse_out;              // [M]; lse_out or NULL
+    int64_t tiles_m, tiles_n, group_m;  // (set by the launches)
+};
+struct VocabGrad {
+    const float *dloss, *lse;           // [M]
+    int32_t *ids, *has;                 // scratch: targets, each once ([M, topk]); whether a row has any
+    float *q, *weight, *alpha;          // [M, topk], [M], one
+    uint16_t *X2;                       // X with zeros as padding and in rows without targets
+    int64_t ldx2;                       // K rounded up to 8
+    int align_x;                        // byte alignment of X's rows
+    uint16_t *D;                        // a piece's gradient of the logits
+    int64_t ldd;                        // a multiple of 8
+    float *sums;                        // [M, ldx2]: dX before its factor
+    uint16_t *dX;
+    int64_t lddx;
+    void *dW;
+    int64_t lddw;
+    int dw_f32, align_dw;
+    int64_t rows_at_once;               // a multiple of 32
+};
+// tile: 256, 128, or 0 for the stream (its parts are 32 columns wide)
+hipError_t launch_vocab_stats(const VocabArgs &a, int tile, hipStream_t s);
+hipError_t launch_vocab_join(const VocabArgs &a, hipStream_t s);
+hipError_t launch_vocab_prep(const VocabArgs &a, const VocabGrad &b, hipStream_t s);
+hipError_t launch_vocab_dlogits(const VocabArgs &a, const VocabGrad &b, int tile, hipStream_t s);
+hipError_t launch_vocab_dw(const VocabArgs &a, const VocabGrad &b, int tile, hipStream_t s);
+hipError_t launch_vocab_dx(const VocabArgs &a, const VocabGrad &b, hipStream_t s);
+
 }  // namespace g5

@@ -1,0 +1,621 @@
+// g5_vocab.hip -- the loss over a large vocabulary behind the last projection,
+// and its gradient, without the logits in memory.
+//
+//   z = X . Wt^T, l = scale z, lse_m = log sum_v exp(l_mv)
+//   loss_m = sum_j q_mj (log q_mj - l_m,id(m,j) + lse_m)
+//
+// with the targets q: one token of weight 1 (cross entropy), or a teacher's
+// best tokens, q_m = softmax of its logits there (distillation).
+//
+// Forward: an output tile of the product keeps its logits in registers and
+// leaves, for each of its rows, their maximum and the sum of exp(l - maximum)
+// (one pass: a later tile's maximum rescales the sum) and the logits of the
+// row's targets that lie in it; a second kernel joins the tiles.
+//
+// Backward, vocabulary piece by piece: the logits again, from them
+// D = g (exp(l - lse) - q) in bf16, then dW = D^T X of the piece and dX += D W.
+#include <hip/hip_runtime.h>
+
+#include "g5_device.h"
+#include "g5_kernels.h"
+#include "g5_stream.h"
+
+namespace g5 {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ int64_t target_id(const VocabArgs &p, int64_t i)
+{
+    return p.ids64 ? ((const int64_t *)p.ids)[i] : (int64_t)((const int32_t *)p.ids)[i];
+}
+
+// (maximum, sum of exp2(c (z - maximum))) of two parts.  A part without finite
+// logits has maximum -inf and sum 0 (or NaN, which stays).
+struct Stat {
+    float top, sum;
+};
+__device__ __forceinline__ Stat join_stat(Stat a, Stat b, float c)
+{
+    const float top = fmaxf(a.top, b.top), base = top == -__builtin_inff() ? 0.f : top;
+    return Stat{top, a.sum * __builtin_amdgcn_exp2f(c * (a.top - base)) + b.sum * __builtin_amdgcn_exp2f(c * (b.top - base))};
+}
+
+// The tile's operands, bases moved to its first row and column.
+template <int BM, int BN>
+__device__ __forceinline__ GemmArgs tile_args(const VocabArgs &p, int64_t m0, int64_t n0)
+{
+    GemmArgs q{};
+    q.A = p.X + m0 * p.ldx;
+    q.B = p.W + n0 * p.ldw;
+    q.M = p.M - m0 < BM ? p.M - m0 : BM;
+    q.N = p.V - n0 < BN ? p.V - n0 : BN;
+    q.K = p.K;
+    q.lda = p.ldx;
+    q.ldb = p.ldw;
+    q.align_a = q.align_b = 16;
+    return q;
+}
+
+// Rows of the accumulators go through LDS as FP32, RP at a time.
+template <class R, int BM, int BN>
+struct Staged {
+    static constexpr int PITCH = BN + 4;                                  // floats; (4: bank conflicts)
+    static constexpr int FITS = R::LDS_BYTES / (PITCH * 4);
+    static constexpr int RP = FITS >= BM ? BM : FITS >= BM / 2 ? BM / 2 : BM / 4;
+    static_assert(RP * PITCH * 4 <= R::LDS_BYTES && RP % 16 == 0, "staging passes");
+
+    __device__ static __forceinline__ void put(const typename R::Acc &acc, float *L, int pass, int wm, int wn, int g, int li)
+    {
+#pragma unroll
+        for (int fm = 0; fm < R::FM; ++fm) {
+            const int row = wm * R::TM + fm * 16;
+            if (row / RP != pass) continue;
+#pragma unroll
+            for (int fn = 0; fn < R::FN; ++fn)
+                *(f32x4 *)(L + (row - pass * RP + li) * PITCH + wn * R::TN + fn * 16 + g * 4) = acc[fn][fm];
+        }
+    }
+};
+
+// Forward on the LDS ring.  The tile's epilogue is registers but for the join of
+// the four waves side by side, and tiles that hold a target.
+template <int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, true>;
+    using S = Staged<R, BM, BN>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    const TileCoord tc = tile_map(blockIdx.x, 1, p.tiles_m, p.tiles_n, p.group_m);
+    const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN;
+    const GemmArgs q = tile_args<BM, BN>(p, m0, n0);
+    f32x4 acc[R::FN][R::FM];
+    R::zero(acc);
+    R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, wave = tid >> 6, wm = wave / WGN, wn = wave % WGN, g = lane >> 4, li = lane & 15;
+    const float c = p.scale * kLog2e;
+    if (q.N < BN) {
+#pragma unroll
+        for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (wn * R::TN + fn * 16 + g * 4 + i >= q.N) {
+#pragma unroll
+                    for (int fm = 0; fm < R::FM; ++fm) acc[fn][fm][i] = -__builtin_inff();
+                }
+    }
+    __syncthreads();
+    Stat *st = (Stat *)smem;                       // [WGN][BM]
+#pragma unroll
+    for (int fm = 0; fm < R::FM; ++fm) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, acc[fn][fm][i]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        // (the difference first: it is exact near the maximum, where it counts)
+        float sum = 0.f;
+#pragma unroll
+        for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (acc[fn][fm][i] - base));
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        if (g == 0) st[wn * BM + wm * R::TM + fm * 16 + li] = Stat{top, sum};
+    }
+    // targets in this tile
+    const int64_t first = p.v0 + n0, pairs = q.M * p.topk;
+    int some = 0;
+    for (int64_t i = tid; i < pairs; i += WGM * WGN * 64) {
+        const int64_t col = target_id(p, m0 * p.topk + i) - first;
+        some |= col >= 0 && col < q.N;
+    }
+    some = __syncthreads_or(some);
+    if (tid < q.M) {
+        Stat s = st[tid];
+#pragma unroll
+        for (int w = 1; w < WGN; ++w) s = join_stat(s, st[w * BM + tid], c);
+        p.part[(p.tile0 + tc.tn) * p.M + m0 + tid] = float2{s.top, s.sum};
+    }
+    if (!some) return;
+    float *L = (float *)smem;
+    for (int pass = 0; pass < BM / S::RP; ++pass) {
+        __syncthreads();
+        // (the accumulators' places are compile-time constants)
+#pragma unroll
+        for (int k = 0; k < BM / S::RP; ++k)
+            if (k == pass) S::put(acc, L, k, wm, wn, g, li);
+        __syncthreads();
+        const int64_t lo = pass * S::RP * p.topk, end = (pass + 1) * S::RP * p.topk, hi = end < pairs ? end : pairs;
+        for (int64_t i = lo + tid; i < hi; i += WGM * WGN * 64) {
+            const int64_t col = target_id(p, m0 * p.topk + i) - first;
+            if (col >= 0 && col < q.N) p.zt[m0 * p.topk + i] = L[(int)(i / p.topk - pass * S::RP) * S::PITCH + (int)col];
+        }
+    }
+}
+
+// Forward for up to 32 rows: bound by reading the weight once, so a workgroup
+// owns 32 rows of it, streamed from HBM into the matrix core by four waves on
+// contiguous pieces of K.
+constexpr int kVocabWaves = 4, kVocabCols = 32;
+
+template <int NC, int D>
+__global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs p)
+{
+    __shared__ f32x4 red[kVocabWaves][2][64];
+    __shared__ float tile[kVocabCols][17];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * kVocabCols;
+    f32x4 acc[2][NC];
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) acc[0][cc] = acc[1][cc] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int K = (int)p.K, steps = (K + 63) / 64, M = (int)p.M;
+    const int s0 = steps * wave / kVocabWaves, s1 = steps * (wave + 1) / kVocabWaves;
+    // (rows past V repeat the block's first and are masked below)
+    const char *wbase[2];
+    uint32_t woff[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int64_t n = n0 + 16 * r < p.V ? n0 + 16 * r : n0;
+        wbase[r] = (const char *)(p.W + n * p.ldw);
+        woff[r] = (uint32_t)(n + li < p.V ? li : 0) * (uint32_t)(p.ldw * 2) + 16 * g;
+    }
+    RowStream<false, 2, NC, D> b;
+    auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            ok[cc] = 16 * cc + li < M;
+            xoff[cc] = (uint32_t)(ok[cc] ? 16 * cc + li : 0) * (uint32_t)(p.ldx * 2) + x_lane<false>(g);
+        }
+    };
+    b.run(wbase, woff, (const char *)p.X, tokens, s0, s1, K, g, acc);
+    const float c = p.scale * kLog2e;
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) {
+        if (16 * cc >= M) break;         // uniform
+        __syncthreads();                 // (the chunk before has been read)
+        red[wave][0][lane] = acc[0][cc];
+        red[wave][1][lane] = acc[1][cc];
+        __syncthreads();
+        if (wave != 0) continue;
+        f32x4 s[2];
+        float top = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            s[r] = red[0][r][lane];
+#pragma unroll
+            for (int w = 1; w < kVocabWaves; ++w) s[r] += red[w][r][lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (n0 + 16 * r + 4 * g + i >= p.V) s[r][i] = -__builtin_inff();
+                top = fmaxf(top, s[r][i]);
+                tile[16 * r + 4 * g + i][li] = s[r][i];
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float base = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (s[r][i] - base));
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        if (g == 0 && 16 * cc + li < M) p.part[(int64_t)blockIdx.x * M + 16 * cc + li] = float2{top, sum};
+        // (one wave writes and reads the tile: in order)
+        __builtin_amdgcn_wave_barrier();
+        const int rows = M - 16 * cc < 16 ? M - 16 * cc : 16;
+        for (int i = lane; i < rows * p.topk; i += 64) {
+            const int64_t at = (int64_t)16 * cc * p.topk + i, col = target_id(p, at) - n0;
+            if (col >= 0 && col < kVocabCols && n0 + col < p.V) p.zt[at] = tile[col][i / p.topk];
+        }
+    }
+}
+
+// A teacher's entry: a token of the vocabulary whose logit is not -inf.
+__device__ __forceinline__ bool has_entry(int64_t id, int64_t vocab, float t)
+{
+    return id >= 0 && id < vocab && !(t == -__builtin_inff());
+}
+__device__ __forceinline__ float max64(float v)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+__device__ __forceinline__ float sum64(float v)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+constexpr int kTopkPer = kVocabMaxTopk / 64;
+
+// A row's targets, by one wave: lane j holds entries j, j + 64, ...: their
+// weights (0: none) and, for the loss, log q.  False where the row has none.
+struct RowTargets {
+    int64_t id[kTopkPer];
+    float q[kTopkPer], logq[kTopkPer];
+};
+__device__ __forceinline__ bool row_targets(const VocabArgs &p, int64_t m, int lane, RowTargets &t)
+{
+    bool has[kTopkPer];
+    float v[kTopkPer], top = -__builtin_inff();
+    bool some = false;
+#pragma unroll
+    for (int j = 0; j < kTopkPer; ++j) {
+        const int at = lane + 64 * j;
+        t.id[j] = at < p.topk ? target_id(p, m * p.topk + at) : -1;
+        v[j] = at < p.topk && p.teacher ? p.teacher[m * p.topk + at] : 0.f;
+        has[j] = has_entry(t.id[j], p.vocab, v[j]);
+        some |= has[j];
+        if (has[j]) top = fmaxf(top, v[j]);
+    }
+    const bool any = __any(some);
+    top = max64(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kTopkPer; ++j) {
+        t.logq[j] = has[j] ? p.scale * (v[j] - top) : 0.f;
+        t.q[j] = has[j] ? expf(t.logq[j]) : 0.f;
+        sum += t.q[j];
+    }
+    sum = sum64(sum);
+    const float log_sum = logf(sum);
+#pragma unroll
+    for (int j = 0; j < kTopkPer; ++j) {
+        if (!has[j]) t.id[j] = -1;
+        else t.q[j] /= sum;
+        t.logq[j] -= log_sum;
+    }
+    return any;
+}
+
+// The tiles' parts of R rows joined by a workgroup, then each row's loss by a
+// wave.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) k_vocab_join(VocabArgs p, int rows)
+{
+    __shared__ Stat st[kJoinThreads];
+    const int tid = threadIdx.x, r = tid % rows, turn = tid / rows, turns = kJoinThreads / rows;
+    const int64_t m0 = (int64_t)blockIdx.x * rows, m = m0 + r;
+    const float c = p.scale * kLog2e;
+    Stat s{-__builtin_inff(), 0.f};
+    if (m < p.M) {
+#pragma unroll 8
+        for (int64_t i = turn; i < p.parts; i += turns) {
+            const float2 v = p.part[i * p.M + m];
+            s = join_stat(s, Stat{v.x, v.y}, c);
+        }
+    }
+    st[tid] = s;
+    // (always the same pairs: the same call gives the same bits)
+    for (int o = turns / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (turn < o) st[tid] = s = join_stat(s, st[tid + o * rows], c);
+    }
+    __syncthreads();
+    const int lane = tid & 63, wave = tid >> 6;
+    for (int i = wave; i < rows; i += kJoinThreads / 64) {
+        const int64_t row = m0 + i;
+        if (row >= p.M) break;
+        const Stat t = st[i];
+        const float log_sum = logf(t.sum);
+        if (lane == 0 && p.lse_out) p.lse_out[row] = p.scale * t.top + log_sum;
+        float loss = 0.f;
+        if (!p.teacher) {
+            const int64_t id = target_id(p, row);
+            // (the difference of the logits first: exact where the loss is small)
+            if (id >= 0 && id < p.vocab) loss = p.scale * (t.top - p.zt[row]) + log_sum;
+        } else {
+            RowTargets q;
+            if (row_targets(p, row, lane, q)) {
+#pragma unroll
+                for (int j = 0; j < kTopkPer; ++j)
+                    if (q.id[j] >= 0)
+                        loss += q.q[j] * (q.logq[j] + (p.scale * (t.top - p.zt[row * p.topk + lane + 64 * j]) + log_sum));
+                loss = sum64(loss);
+            }
+        }
+        if (lane == 0) p.loss[row] = loss;
+    }
+}
+
+// Before the gradient, a wave per row: its targets as int32 ids, each once
+// (one listed twice has both weights at its first place), their weights,
+// whether there are any, and its row of X with zero padding, all zeros for a
+// row without targets, whose contents must not reach dW.
+constexpr int kPrepWaves = 4;
+__global__ void __launch_bounds__(kPrepWaves * 64) k_vocab_prep(VocabArgs p, VocabGrad b)
+{
+    __shared__ int ids[kPrepWaves][kVocabMaxTopk];
+    __shared__ float qs[kPrepWaves][kVocabMaxTopk];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = (int64_t)blockIdx.x * kPrepWaves + wave;
+    if (m >= p.M) return;                 // (a wave works alone)
+    bool some;
+    if (!p.teacher) {
+        const int64_t id = target_id(p, m);
+        some = id >= 0 && id < p.vocab;
+        if (lane == 0) {
+            b.ids[m] = some ? (int32_t)id : -1;
+            b.q[m] = 1.f;
+        }
+    } else {
+        RowTargets t;
+        some = row_targets(p, m, lane, t);
+#pragma unroll
+        for (int j = 0; j < kTopkPer; ++j) {
+            ids[wave][lane + 64 * j] = (int)t.id[j];
+            qs[wave][lane + 64 * j] = t.q[j];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < kTopkPer; ++j) {
+            const int at = lane + 64 * j, id = ids[wave][at];
+            if (at >= p.topk) break;
+            bool again = id < 0;
+            float q = 0.f;
+            for (int i = 0; i < p.topk; ++i) {
+                const bool same = ids[wave][i] == id;
+                again |= same && i < at;
+                if (same && i >= at) q += qs[wave][i];
+            }
+            b.ids[m * p.topk + at] = again ? -1 : id;
+            b.q[m * p.topk + at] = q;
+        }
+    }
+    if (lane == 0) {
+        b.has[m] = some;
+        b.weight[m] = some ? b.dloss[m] : 0.f;
+    }
+    const uint16_t *x = p.X + m * p.ldx;
+    for (int64_t col = lane * 8; col < b.ldx2; col += 512)
+        *(u32x4 *)(b.X2 + m * b.ldx2 + col) = load_chunk8_bf16(x, col, p.K, some, b.align_x);
+}
+
+// The largest |dloss| of the rows with targets into alpha, every row's weight
+// divided by it.  D holds weight (p - q) and the products multiply their sums
+// by alpha: where all weights are alike (a mean over the rows) they are then
+// exactly 1 and D's rounding to bf16 does not round that common factor, which
+// would move whole gradients by up to 2^-8 at once.
+__global__ void __launch_bounds__(1024) k_vocab_weights(float *weight, int64_t M, float *alpha)
+{
+    __shared__ float tops[16];
+    const int tid = threadIdx.x;
+    float top = 0.f;
+    for (int64_t m = tid; m < M; m += 1024) top = fmaxf(top, fabsf(weight[m]));
+    top = max64(top);
+    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    __syncthreads();
+    top = 0.f;
+    for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[w]);
+    // (no weight at all, or an infinite one: as they are)
+    const float a = top > 0.f && top < __builtin_inff() ? top : 1.f;
+    for (int64_t m = tid; m < M; m += 1024) weight[m] = weight[m] / a;
+    if (tid == 0) *alpha = a;
+}
+
+// D of a piece: exp(l - lse) in registers, staged as FP32, the targets'
+// weights taken off where they lie, then weighted and rounded to bf16.
+template <int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p, VocabGrad b)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, true>;
+    using S = Staged<R, BM, BN>;
+    constexpr int NT = WGM * WGN * 64;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    const TileCoord tc = tile_map(blockIdx.x, 1, p.tiles_m, p.tiles_n, p.group_m);
+    const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN;
+    const GemmArgs q = tile_args<BM, BN>(p, m0, n0);
+    f32x4 acc[R::FN][R::FM];
+    R::zero(acc);
+    R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, wave = tid >> 6, wm = wave / WGN, wn = wave % WGN, g = lane >> 4, li = lane & 15;
+#pragma unroll
+    for (int fm = 0; fm < R::FM; ++fm) {
+        const int r = wm * R::TM + fm * 16 + li;
+        const float lse = r < q.M ? b.lse[m0 + r] : 0.f;
+#pragma unroll
+        for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[fn][fm][i] = __builtin_amdgcn_exp2f(kLog2e * __builtin_fmaf(p.scale, acc[fn][fm][i], -lse));
+    }
+    float *L = (float *)smem;
+    const int64_t pairs = q.M * p.topk;
+    const int first = (int)(p.v0 + n0);
+    for (int pass = 0; pass < BM / S::RP; ++pass) {
+        if (pass * S::RP >= q.M) break;          // uniform
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < BM / S::RP; ++k)
+            if (k == pass) S::put(acc, L, k, wm, wn, g, li);
+        __syncthreads();
+        const int64_t lo = pass * S::RP * p.topk, end = (pass + 1) * S::RP * p.topk, hi = end < pairs ? end : pairs;
+        for (int64_t i = lo + tid; i < hi; i += NT) {
+            const int id = b.ids[m0 * p.topk + i], col = id - first;
+            if (id >= 0 && col >= 0 && col < q.N)
+                L[(int)(i / p.topk - pass * S::RP) * S::PITCH + col] -= b.q[m0 * p.topk + i];
+        }
+        __syncthreads();
+        for (int i = tid; i < S::RP * (BN / 8); i += NT) {
+            const int r = i / (BN / 8), ch = i % (BN / 8) * 8, row = pass * S::RP + r;
+            if (row >= q.M || ch >= q.N) continue;
+            const f32x4 a0 = *(const f32x4 *)(L + r * S::PITCH + ch), a1 = *(const f32x4 *)(L + r * S::PITCH + ch + 4);
+            const float w = b.weight[m0 + row];
+            u32x4 d = {pack_bf16x2(w * a0[0], w * a0[1]), pack_bf16x2(w * a0[2], w * a0[3]),
+                       pack_bf16x2(w * a1[0], w * a1[1]), pack_bf16x2(w * a1[2], w * a1[3])};
+            if (!b.has[m0 + row]) d = u32x4{0u, 0u, 0u, 0u};
+            *(u32x4 *)(b.D + (m0 + row) * b.ldd + n0 + ch) = d;
+        }
+    }
+}
+
+// dW rows of a piece: scale alpha D^T X2, summed over the rows in pieces whose
+// 32-bit offsets fit.
+template <int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, VocabGrad b)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, false, false, true>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    const TileCoord tc = tile_map(blockIdx.x, 1, p.tiles_m, p.tiles_n, p.group_m);
+    const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN;          // vocabulary, hidden
+    GemmArgs q{};
+    q.A = b.D + m0;
+    q.B = b.X2 + n0;
+    q.C = (char *)b.dW + ((p.v0 + m0) * b.lddw + n0) * (b.dw_f32 ? 4 : 2);
+    q.lda = b.ldd;
+    q.ldb = b.ldx2;
+    q.ldc = b.lddw;
+    q.align_a = q.align_b = 16;
+    q.align_c = b.align_dw;
+    q.out_f32 = b.dw_f32;
+    q.M = p.V - m0 < BM ? p.V - m0 : BM;
+    q.N = b.ldx2 - n0 < BN ? b.ldx2 - n0 : BN;               // (whole padded chunks)
+    f32x4 acc[R::FN][R::FM];
+    R::zero(acc);
+    for (int64_t done = 0; done < p.M;) {
+        q.K = p.M - done < b.rows_at_once ? p.M - done : b.rows_at_once;
+        if (done > 0) __syncthreads();
+        R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+        done += q.K;
+        q.A = b.D + m0 + done * b.ldd;
+        q.B = b.X2 + n0 + done * b.ldx2;
+    }
+    const float a = p.M > 0 ? p.scale * *b.alpha : 0.f;
+#pragma unroll
+    for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+        for (int fm = 0; fm < R::FM; ++fm)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[fn][fm][i] *= a;
+    q.N = p.K - n0 < BN ? p.K - n0 : BN;
+    R::store(q, smem, TileCoord{0, 0, 0}, acc);
+}
+
+// dX from the sums over all pieces: bf16(scale alpha sum), zeros for rows
+// without targets.  A thread per 8 columns at a time.
+__global__ void __launch_bounds__(256) k_vocab_dx(VocabArgs p, VocabGrad b)
+{
+    const int64_t chunks = (p.K + 7) / 8, total = p.M * chunks;
+    const float a = p.scale * *b.alpha;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+        const int64_t m = at / chunks, col = at % chunks * 8;
+        const float *s = b.sums + m * b.ldx2 + col;
+        const f32x4 v0 = *(const f32x4 *)s, v1 = *(const f32x4 *)(s + 4);
+        u32x4 d = {pack_bf16x2(a * v0[0], a * v0[1]), pack_bf16x2(a * v0[2], a * v0[3]),
+                   pack_bf16x2(a * v1[0], a * v1[1]), pack_bf16x2(a * v1[2], a * v1[3])};
+        if (!b.has[m]) d = u32x4{0u, 0u, 0u, 0u};
+        uint16_t *out = b.dX + m * b.lddx + col;
+        if (col + 8 <= p.K) {
+            store16(out, d);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.K) out[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+}  // namespace
+
+static void tiles_of(VocabArgs &p, int64_t M, int64_t N, int tile)
+{
+    p.tiles_m = (M + tile - 1) / tile;
+    p.tiles_n = (N + tile - 1) / tile;
+    p.group_m = p.tiles_m < 8 ? p.tiles_m : 8;
+}
+
+hipError_t launch_vocab_stats(const VocabArgs &args, int tile, hipStream_t s)
+{
+    VocabArgs p = args;
+    if (tile == 0) {
+        const dim3 g((unsigned)((p.V + kVocabCols - 1) / kVocabCols)), b(kVocabWaves * 64);
+        if (p.M > 16) hipLaunchKernelGGL((k_vocab_stream<2, 2>), g, b, 0, s, p);
+        else hipLaunchKernelGGL((k_vocab_stream<1, 3>), g, b, 0, s, p);
+        return hipGetLastError();
+    }
+    tiles_of(p, p.M, p.V, tile);
+    const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), b(512);
+    if (tile == 256) hipLaunchKernelGGL((k_vocab_stats<256, 256, 2, 4>), g, b, 0, s, p);
+    else hipLaunchKernelGGL((k_vocab_stats<128, 128, 4, 2>), g, b, 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_join(const VocabArgs &p, hipStream_t s)
+{
+    int rows = 1;
+    while (rows < 16 && rows < p.M) rows *= 2;
+    hipLaunchKernelGGL(k_vocab_join, dim3((unsigned)((p.M + rows - 1) / rows)), dim3(kJoinThreads), 0, s, p, rows);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_prep(const VocabArgs &p, const VocabGrad &b, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_vocab_prep, dim3((unsigned)((p.M + kPrepWaves - 1) / kPrepWaves)), dim3(kPrepWaves * 64), 0, s, p, b);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_vocab_weights, dim3(1), dim3(1024), 0, s, b.weight, p.M, b.alpha);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_dlogits(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
+{
+    VocabArgs p = args;
+    tiles_of(p, p.M, p.V, tile);
+    const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), t(512);
+    if (tile == 256) hipLaunchKernelGGL((k_vocab_dlogits<256, 256, 2, 4>), g, t, 0, s, p, b);
+    else hipLaunchKernelGGL((k_vocab_dlogits<128, 128, 4, 2>), g, t, 0, s, p, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_dw(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
+{
+    VocabArgs p = args;
+    tiles_of(p, p.V, p.K, tile);
+    const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), t(512);
+    if (tile == 256) hipLaunchKernelGGL((k_vocab_dw<256, 256, 2, 4>), g, t, 0, s, p, b);
+    else hipLaunchKernelGGL((k_vocab_dw<128, 128, 4, 2>), g, t, 0, s, p, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_dx(const VocabArgs &p, const VocabGrad &b, hipStream_t s)
+{
+    const int64_t groups = (p.M * ((p.K + 7) / 8) + 255) / 256;
+    hipLaunchKernelGGL(k_vocab_dx, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0, s, p, b);
+    return hipGetLastError();
+}
+
+}  // namespace g5

@@ -1,6 +1,8 @@
 """Binding of the operators at both ends of a training step's products: the
-experts' products with ragged numbers of rows.  As gemm.py: argument
-marshalling only; the arithmetic runs in the gfx950 kernels of libgemm05.so.
+experts' products with ragged numbers of rows, and the loss over a vocabulary
+behind the last projection with its gradient, from labels or from a teacher's
+best logits.  As gemm.py: argument marshalling only; the arithmetic runs in the
+gfx950 kernels of libgemm05.so.
 """
 import ctypes
 
@@ -8,9 +10,10 @@ import torch
 
 from ._lib import GEMM_ERR_WORKSPACE, GemmError, lib
 from .gemm import Workspace, _bstride, _check_dev, _launch, _out_code
-from .token_ops import _ptr, _scratch, _stride, _vector
+from .token_ops import _ptr, _rows, _scratch, _stride, _vector
 
-__all__ = ["gemm_bf16_grouped_nt", "gemm_bf16_grouped", "gemm_bf16_grouped_tn"]
+__all__ = ["gemm_bf16_grouped_nt", "gemm_bf16_grouped", "gemm_bf16_grouped_tn",
+           "linear_cross_entropy", "linear_cross_entropy_backward", "linear_distill", "linear_distill_backward"]
 
 _NT, _NN, _TN = range(3)
 
@@ -113,3 +116,131 @@ def gemm_bf16_grouped_tn(At, B, offsets, C=None, out_dtype=torch.float32, worksp
     if B.shape[0] != rows:
         raise ValueError("expected At [rows, M], B [rows, N] and offsets [E + 1]")
     return _grouped("gemm_bf16_grouped_tn", _TN, At, B, offsets, C, (E, M, N), out_dtype, workspace, E, rows, M, N, 0)
+
+
+def _loss_operands(what, X, Wt, ids, teacher):
+    """(M, V, K, topk, bytes of an index)"""
+    if X.dtype != torch.bfloat16 or Wt.dtype != torch.bfloat16:
+        raise TypeError(f"{what} takes a bfloat16 X and Wt")
+    if X.dim() != 2 or Wt.dim() != 2 or X.shape[1] != Wt.shape[1]:
+        raise ValueError(f"{what} takes X [M, K] and Wt [V, K]")
+    M, K = X.shape
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what} takes int32 or int64 indices")
+    if teacher is None:
+        if ids.dim() != 1 or ids.shape[0] != M or (M > 1 and ids.stride(0) != 1):
+            raise ValueError("targets must be a contiguous vector of M elements")
+        topk = 1
+    else:
+        if ids.dim() != 2 or ids.shape[0] != M or not ids.is_contiguous():
+            raise ValueError("ids must be contiguous [M, topk]")
+        topk = ids.shape[1]
+        if not 1 <= topk <= 256:
+            raise ValueError("topk must be 1 to 256")
+        _rows(teacher, ids.shape, torch.float32, "teacher")
+        if not teacher.is_contiguous():
+            raise ValueError("teacher must be contiguous [M, topk]")
+    return M, Wt.shape[0], K, topk, 4 if ids.dtype == torch.int32 else 8
+
+
+def _loss(what, X, Wt, ids, teacher, scale, loss, lse, workspace):
+    M, V, K, topk, nb = _loss_operands(what, X, Wt, ids, teacher)
+    _vector(loss, M, torch.float32, "loss")
+    _vector(lse, M, torch.float32, "lse")
+    dev = _check_dev(X, Wt, ids, teacher, loss, lse)
+    if loss is None:
+        loss = torch.empty((M,), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((M,), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = Workspace(dev)
+    px, pw, ldx, ldw = X.data_ptr(), Wt.data_ptr(), _stride(X, K), _stride(Wt, K)
+    picks = (ids.data_ptr(), nb) if teacher is None else (topk, ids.data_ptr(), nb, teacher.data_ptr())
+    fn = getattr(lib(), what)
+
+    def run(buf):
+        return _launch(fn, dev, M, V, K, px, ldx, pw, ldw, scale, *picks, loss.data_ptr(), lse.data_ptr(), _ptr(buf),
+                       0 if buf is None else buf.numel())
+
+    # (the size depends on the pointers only through their alignment)
+    _with_scratch(what, workspace, dev, (what, M, V, K, topk, px % 256, ldx, pw % 256, ldw),
+                  lambda n: lib().gemm_linear_loss_workspace_size(0, M, V, K, topk, px, ldx, pw, ldw, n), run)
+    return loss, lse
+
+
+def _loss_backward(what, dloss, X, Wt, ids, teacher, lse, scale, dX, dW, need_dx, need_dw, dw_dtype, workspace):
+    M, V, K, topk, nb = _loss_operands(what, X, Wt, ids, teacher)
+    if dloss is None or lse is None:
+        raise ValueError("dloss and the forward call's lse are needed")
+    _vector(dloss, M, torch.float32, "dloss")
+    _vector(lse, M, torch.float32, "lse")
+    _rows(dX, (M, K), torch.bfloat16, "dX")
+    if dW is not None and tuple(dW.shape) != (V, K):
+        raise ValueError("dW must be [V, K]")
+    code = _out_code(dw_dtype if dW is None else dW.dtype)
+    dev = _check_dev(X, Wt, ids, teacher, dloss, lse, dX, dW)
+    if not need_dx:
+        dX = None
+    elif dX is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    if not need_dw:
+        dW = None
+    elif dW is None:
+        dW = torch.empty((V, K), dtype=dw_dtype, device=dev)
+    if workspace is None:
+        workspace = Workspace(dev)
+    px, pw, ldx, ldw = X.data_ptr(), Wt.data_ptr(), _stride(X, K), _stride(Wt, K)
+    picks = (ids.data_ptr(), nb) if teacher is None else (topk, ids.data_ptr(), nb, teacher.data_ptr())
+    fn = getattr(lib(), what)
+
+    def run(buf):
+        return _launch(fn, dev, M, V, K, px, ldx, pw, ldw, scale, *picks, dloss.data_ptr(), lse.data_ptr(), _ptr(dX),
+                       K if dX is None else _stride(dX, K), _ptr(dW), K if dW is None else _stride(dW, K), code,
+                       _ptr(buf), 0 if buf is None else buf.numel())
+
+    _with_scratch(what, workspace, dev, (what, M, V, K, topk, px % 256, ldx, pw % 256, ldw),
+                  lambda n: lib().gemm_linear_loss_workspace_size(1, M, V, K, topk, px, ldx, pw, ldw, n), run)
+    return dX, dW
+
+
+def linear_cross_entropy(X, Wt, targets, scale=1.0, loss=None, lse=None, workspace=None):
+    """The cross entropy of softmax(scale X . Wt^T) with targets, without the
+    logits in memory (gemm_linear_cross_entropy): X [M, K] and the vocabulary's
+    weight Wt [V, K] in bfloat16, targets [M] int32 or int64; a target outside
+    [0, V) (-100, -1) leaves its row out.  Returns (loss, lse), float32 [M]:
+    loss 0 in rows left out, lse what the gradient needs."""
+    return _loss("gemm_linear_cross_entropy", X, Wt, targets, None, scale, loss, lse, workspace)
+
+
+def linear_cross_entropy_backward(dloss, X, Wt, targets, lse, scale=1.0, dX=None, dW=None, need_dx=True, need_dw=True,
+                                  dw_dtype=torch.bfloat16, workspace=None):
+    """The gradient of linear_cross_entropy (gemm_linear_cross_entropy_backward):
+    from dloss float32 [M] (1 / rows for a mean) and the forward call's lse,
+    returns (dX bfloat16 [M, K], dW [V, K] in dw_dtype, bfloat16 or float32);
+    None for one that is not needed."""
+    return _loss_backward("gemm_linear_cross_entropy_backward", dloss, X, Wt, targets, None, lse, scale, dX, dW, need_dx,
+                          need_dw, dw_dtype, workspace)
+
+
+def _teacher(teacher):
+    if teacher is None:
+        raise ValueError("teacher: the logits of ids")
+    return teacher
+
+
+def linear_distill(X, Wt, ids, teacher, scale=1.0, loss=None, lse=None, workspace=None):
+    """The distance (Kullback-Leibler) of softmax(scale X . Wt^T) to a teacher of
+    which each row's topk best tokens are kept (gemm_linear_distill): ids [M,
+    topk] (int32 or int64, outside [0, V): no entry) and their logits teacher
+    [M, topk] (float32; -inf: no entry), weighted by softmax(scale teacher).
+    scale: 1 over the temperature.  Returns (loss, lse), float32 [M]; a row
+    without entries has loss 0."""
+    return _loss("gemm_linear_distill", X, Wt, ids, _teacher(teacher), scale, loss, lse, workspace)
+
+
+def linear_distill_backward(dloss, X, Wt, ids, teacher, lse, scale=1.0, dX=None, dW=None, need_dx=True, need_dw=True,
+                            dw_dtype=torch.bfloat16, workspace=None):
+    """The gradient of linear_distill in X and Wt (gemm_linear_distill_backward);
+    otherwise as linear_cross_entropy_backward."""
+    return _loss_backward("gemm_linear_distill_backward", dloss, X, Wt, ids, _teacher(teacher), lse, scale, dX, dW, need_dx,
+                          need_dw, dw_dtype, workspace)

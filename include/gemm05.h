@@ -759,6 +759,98 @@ int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, in
                                 uint64_t a_addr, int64_t lda, uint64_t b_addr, int64_t ldb, int64_t strideB,
                                 uint64_t *bytes);
 
+/* ---- the loss over a vocabulary behind the last projection ---------------------
+ *
+ * The last projection of a language model and its loss in one, without the
+ * logits in memory: X [M, K] the last hidden rows, Wt [V, K] the vocabulary's
+ * weight ([out, in], both bf16, row strides ldx and ldw), l = scale * X.Wt^T
+ * (scale > 0: 1 over a temperature), kept in FP32 registers, and per row
+ *
+ *     lse    = log sum_v exp(l_v)                       (float [M], or NULL)
+ *     loss   = lse - l_target                           (float [M])
+ *
+ * for the cross entropy with targets [M], and for the distance to a teacher of
+ * which the topk best logits are kept (ids and teacher [M, topk], contiguous;
+ * teacher float, before the temperature)
+ *
+ *     q_j    = exp(scale t_j) / sum_i exp(scale t_i)
+ *     loss   = sum_j q_j (log q_j - l_ids[j] + lse)
+ *
+ * Indices are int32 or int64 (index_bytes 4 or 8).  A target outside [0, V) --
+ * by convention -100 or -1 -- leaves its row out: loss 0, gradients 0, whatever
+ * the row holds.  So does a teacher's entry whose id lies outside or whose logit
+ * is -inf, and a row that has no entry is left out; an id listed twice counts
+ * twice.  lse is written for every row.  NaN in a row of X makes that row's loss
+ * NaN and no other's; an infinite logit may give NaN where the formula gives an
+ * infinity.
+ *
+ * The gradients, from dloss [M] (float: 1/rows for a mean, temperature^2 and
+ * weights of rows with it) and the forward call's lse:
+ *
+ *     D  = dloss * scale * (exp(l - lse) - q)   per row and token
+ *     dX = D . Wt    (bf16 [M, K], or NULL)
+ *     dW = D^T . X   (bf16 or float [V, K] by dw_type, or NULL), overwritten
+ *
+ * are formed piece by piece of the vocabulary, the logits anew from X and Wt.
+ * D meets the matrix cores in bf16, relative to the largest |dloss| (so a weight
+ * common to all rows is not rounded): gradients are off by up to 2^-8 of the sum
+ * of their terms' sizes beside their own rounding; sums are FP32.  Rows whose
+ * |dloss| is less than 2^-100 of the largest may lose their smallest terms
+ * (what is below 2^-126 beside it counts as 0).
+ *
+ * Deterministic, no atomics; a row's loss does not depend on the other rows'
+ * values.  0 <= M <= 2^24, 1 <= V < 2^31 - 256, 1 <= K <= 2^21, topk <= 256.  Up
+ * to 32 rows the forward call streams the weight past them.  Rows of any
+ * alignment; those that are not 16-byte aligned (gradients: or whose length is
+ * not a multiple of 8) are copied, a piece of the vocabulary at a time.  M == 0:
+ * dW := 0.  workspace: gemm_linear_loss_workspace_size bytes, 256-byte aligned,
+ * as gemm_run's (its counter region zero before and after the call); calls that
+ * may overlap in time need workspaces of their own.  Errors, nothing enqueued:
+ * GEMM_ERR_INVALID_ARG for sizes outside these ranges, a scale that is not
+ * finite and positive, other index_bytes or dw_type, strides below K, missing
+ * or misaligned pointers, an output or the workspace overlapping an input or
+ * another output; GEMM_ERR_WORKSPACE for a missing or small workspace;
+ * GEMM_ERR_UNSUPPORTED for rows more than 2^21 elements apart in the tiled
+ * kernels, and more than 2^22 workgroups. */
+int gemm_linear_cross_entropy(int64_t M, int64_t V, int64_t K,
+                              const uint16_t *X, int64_t ldx,
+                              const uint16_t *Wt, int64_t ldw, float scale,
+                              const void *targets, int index_bytes,
+                              float *loss, float *lse,
+                              void *workspace, uint64_t workspace_bytes,
+                              void *stream);
+int gemm_linear_cross_entropy_backward(int64_t M, int64_t V, int64_t K,
+                                       const uint16_t *X, int64_t ldx,
+                                       const uint16_t *Wt, int64_t ldw, float scale,
+                                       const void *targets, int index_bytes,
+                                       const float *dloss, const float *lse,
+                                       uint16_t *dX, int64_t lddx,
+                                       void *dW, int64_t lddw, int dw_type,
+                                       void *workspace, uint64_t workspace_bytes,
+                                       void *stream);
+int gemm_linear_distill(int64_t M, int64_t V, int64_t K,
+                        const uint16_t *X, int64_t ldx,
+                        const uint16_t *Wt, int64_t ldw, float scale,
+                        int64_t topk, const void *ids, int index_bytes, const float *teacher,
+                        float *loss, float *lse,
+                        void *workspace, uint64_t workspace_bytes,
+                        void *stream);
+int gemm_linear_distill_backward(int64_t M, int64_t V, int64_t K,
+                                 const uint16_t *X, int64_t ldx,
+                                 const uint16_t *Wt, int64_t ldw, float scale,
+                                 int64_t topk, const void *ids, int index_bytes, const float *teacher,
+                                 const float *dloss, const float *lse,
+                                 uint16_t *dX, int64_t lddx,
+                                 void *dW, int64_t lddw, int dw_type,
+                                 void *workspace, uint64_t workspace_bytes,
+                                 void *stream);
+
+/* Workspace bytes of the four (host only; topk 1 for the cross entropy;
+ * pointers as integers, their alignment decides). */
+int gemm_linear_loss_workspace_size(int backward, int64_t M, int64_t V, int64_t K, int64_t topk,
+                                    uint64_t x_addr, int64_t ldx, uint64_t w_addr, int64_t ldw,
+                                    uint64_t *bytes);
+
 /* Static, NUL-terminated description of a status code. */
 const char *gemm_status_string(int status);
 

@@ -7,7 +7,13 @@ import torch
 
 import dense_gemm_05_amd as g5
 from dense_gemm_05_amd import train_ops as ops
-from test_binding_host import FakeGpuTensor
+from test_binding_host import FakeGpuTensor as _Fake
+
+
+class FakeGpuTensor(_Fake):
+    def is_contiguous(self):
+        return True
+
 
 P = 0x7F0000000000     # fake, aligned addresses 16 GiB apart, never dereferenced
 A, B, C, O, T, W = (P + (i << 34) for i in range(6))
@@ -123,3 +129,117 @@ def test_grouped_binding_counts_groups(no_lib):
         g5.gemm_bf16_grouped_nt(_bf(300, 64), _bf(4, 48, 64), _i32(4))
     with pytest.raises(ValueError):
         g5.gemm_bf16_grouped(_bf(300, 64), _bf(4, 64, 48), _i32(6))
+
+
+X, D = P + (6 << 34), P + (7 << 34)
+
+
+def loss(kind, **kw):
+    """kind: 'ce', 'ce_grad', 'kd', 'kd_grad'; 300 rows of 64, 1000 tokens, 4 entries."""
+    a = dict(M=300, V=1000, K=64, X=A, ldx=64, W=B, ldw=64, scale=1.0, topk=4, ids=O, nb=8, t=T, dl=X, lse=X + 4096,
+             loss=C, out=C + 4096, dX=C, lddx=64, dW=D, lddw=64, dt=0, ws=W, n=1 << 30)
+    a.update(kw)
+    L = g5.lib()
+    head = (a["M"], a["V"], a["K"], a["X"], a["ldx"], a["W"], a["ldw"], a["scale"])
+    head += (a["topk"], a["ids"], a["nb"], a["t"]) if kind.startswith("kd") else (a["ids"], a["nb"])
+    tail = (a["ws"], a["n"], None)
+    grad = (a["dl"], a["lse"], a["dX"], a["lddx"], a["dW"], a["lddw"], a["dt"])
+    fn = {"ce": L.gemm_linear_cross_entropy, "ce_grad": L.gemm_linear_cross_entropy_backward,
+          "kd": L.gemm_linear_distill, "kd_grad": L.gemm_linear_distill_backward}[kind]
+    return fn(*head, *(grad if kind.endswith("grad") else (a["loss"], a["out"])), *tail)
+
+
+KINDS = ["ce", "ce_grad", "kd", "kd_grad"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad,status", [
+    (dict(M=-1), INV), (dict(M=(1 << 24) + 1), INV), (dict(V=0), INV), (dict(V=1 << 31), INV), (dict(K=0), INV),
+    (dict(K=(1 << 21) + 1), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV),
+    (dict(scale=float("inf")), INV), (dict(nb=2), INV), (dict(X=None), INV), (dict(W=None), INV), (dict(ids=None), INV),
+    (dict(ldx=63), INV), (dict(ldw=63), INV), (dict(X=A + 1), INV), (dict(W=B + 1), INV), (dict(ids=O + 4), INV),
+    (dict(nb=4, ids=O + 2), INV), (dict(ws=None), WS), (dict(n=CR), WS), (dict(ws=W + 128), INV), (dict(ws=A), INV),
+    (dict(ws=B), INV), (dict(ldx=(1 << 21) + 8), UNS), (dict(ldw=(1 << 21) + 8), UNS)])
+def test_loss_refuses(kind, bad, status):
+    assert loss(kind, **bad) == status
+
+
+@pytest.mark.parametrize("kind", ["ce", "kd"])
+@pytest.mark.parametrize("bad", [dict(loss=None), dict(loss=C + 2), dict(out=C + 4098), dict(loss=A), dict(out=B), dict(out=C),
+                                 dict(loss=O), dict(ws=C)])
+def test_loss_forward_refuses(kind, bad):
+    assert loss(kind, **bad) == INV
+
+
+@pytest.mark.parametrize("kind", ["ce_grad", "kd_grad"])
+@pytest.mark.parametrize("bad", [dict(dl=None), dict(lse=None), dict(dl=X + 2), dict(lse=X + 2), dict(lddx=63),
+                                 dict(lddw=63), dict(dX=C + 1), dict(dW=D + 1), dict(dt=1, dW=D + 2), dict(dt=2),
+                                 dict(dX=A), dict(dX=B), dict(dW=B), dict(dW=C), dict(dX=X), dict(dW=O), dict(ws=D)])
+def test_loss_gradient_refuses(kind, bad):
+    assert loss(kind, **bad) == INV
+
+
+@pytest.mark.parametrize("kind", ["kd", "kd_grad"])
+@pytest.mark.parametrize("bad", [dict(topk=0), dict(topk=257), dict(t=None), dict(t=T + 2)])
+def test_distill_refuses(kind, bad):
+    assert loss(kind, **bad) == INV
+
+
+def test_loss_empty_calls_do_nothing():
+    assert loss("ce", M=0, X=None, ids=None, loss=None) == OK and loss("kd", M=0, t=None, loss=None) == OK
+    assert loss("ce_grad", dX=None, dW=None, dl=X) == OK and loss("kd_grad", M=0, dW=None, t=None) == OK
+
+
+def test_loss_workspace_size():
+    n = ctypes.c_uint64(1)
+
+    def size(back, M=300, V=1000, K=64, topk=1, x=A, ldx=64, w=B, ldw=64):
+        st = g5.lib().gemm_linear_loss_workspace_size(back, M, V, K, topk, x, ldx, w, ldw, ctypes.byref(n))
+        return st, n.value
+
+    up = lambda b: -(-b // 256) * 256                                      # noqa: E731
+    assert size(0) == (OK, CR + up(8 * 300 * 8) + up(300 * 4))             # 8 column tiles, the targets' logits
+    assert size(0, x=A + 2) == (OK, CR + up(300 * 64 * 2) + up(8 * 300 * 8) + up(300 * 4))
+    assert size(0, M=32, x=A + 2, w=B + 2) == (OK, CR + up(32 * 32 * 8) + up(32 * 4))     # the stream
+    assert size(0, M=0) == size(1, M=0) == (OK, 0)
+    st, whole = size(1)
+    assert st == OK and whole >= CR + 300 * 64 * 2 + 300 * 1000 * 2 + 300 * 64 * 4
+    # a large vocabulary goes in pieces: far less than the logits
+    st, b = size(1, M=1 << 15, V=1 << 17, K=1024, ldx=1024, ldw=1024)
+    assert st == OK and b < 1 << 29
+    assert size(0, V=0)[0] == INV and size(0, K=0)[0] == INV and size(1, topk=0)[0] == INV
+    assert g5.lib().gemm_linear_loss_workspace_size(1, 300, 1000, 64, 1, A, 64, B, 64, None) == OK
+
+
+def test_loss_binding_refuses(no_lib):
+    x, w, t, f = _bf(30, 64), _bf(100, 64), FakeGpuTensor((30,), torch.int64), _f32(30)
+    ids, lg = _i32(30, 4), _f32(30, 4)
+    for bad in ((_f32(30, 64), w, t), (x, _f32(100, 64), t), (x, w, _f32(30))):
+        with pytest.raises(TypeError):
+            g5.linear_cross_entropy(*bad)
+        with pytest.raises(TypeError):
+            g5.linear_cross_entropy_backward(f, *bad, f)
+    for bad in ((_bf(30, 65), w, t), (_bf(2, 30, 64), w, t), (x, w, _i32(31)), (x, w, _i32(30, 1)),
+                (torch.zeros((30, 64), dtype=torch.bfloat16), w, t), (x, w, torch.zeros(30, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            g5.linear_cross_entropy(*bad)
+        with pytest.raises(ValueError):
+            g5.linear_cross_entropy_backward(f, *bad, f)
+    for kw in (dict(loss=_f32(31)), dict(lse=_bf(30)), dict(loss=torch.zeros(30))):
+        with pytest.raises(ValueError):
+            g5.linear_cross_entropy(x, w, t, **kw)
+    with pytest.raises(ValueError):
+        g5.linear_cross_entropy_backward(_f32(29), x, w, t, f)
+    with pytest.raises(ValueError):
+        g5.linear_cross_entropy_backward(f, x, w, t, None)
+    for kw in (dict(dX=_bf(30, 65)), dict(dX=_f32(30, 64)), dict(dW=_bf(99, 64)), dict(dW=torch.zeros((100, 64)))):
+        with pytest.raises(ValueError):
+            g5.linear_cross_entropy_backward(f, x, w, t, f, **kw)
+    with pytest.raises(TypeError):
+        g5.linear_cross_entropy_backward(f, x, w, t, f, dw_dtype=torch.float16)
+    for bad in ((t, lg), (_i32(31, 4), lg), (_i32(30, 257), _f32(30, 257)), (_i32(30, 0), _f32(30, 0)), (ids, _f32(30, 5)),
+                (ids, _bf(30, 4)), (ids, None)):
+        with pytest.raises(ValueError):
+            g5.linear_distill(x, w, *bad)
+        with pytest.raises(ValueError):
+            g5.linear_distill_backward(f, x, w, *bad, f)
