@@ -1626,7 +1626,7 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
     pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 16 || (!nt && N % 8 != 0);
     pl.lda2 = pl.copy_a ? (pl.cols_a + 7) / 8 * 8 : lda;
     pl.ldb2 = pl.copy_b ? (cols_b + 7) / 8 * 8 : ldb;
-    // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 32
+    // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 64
     // along the summed axis)
     if (pl.lda2 > (1 << 21) || pl.ldb2 > (1 << 21)) return GEMM_ERR_UNSUPPORTED;
     if (pl.copy_a || pl.copy_b) {
@@ -1726,7 +1726,7 @@ static int grouped_run(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, 
         a.sB = pl.batch_b > 1 ? pl.rows_b * pl.ldb2 : 0;
     }
     const int64_t widest = tn && a.lda > a.ldb ? a.lda : a.ldb;
-    a.piece = widest > 0 ? (((int64_t)1 << 29) / widest) / 32 * 32 : 32;
+    a.piece = widest > 0 ? (((int64_t)1 << 29) / widest) / 64 * 64 : 32;
     const hipError_t e = g5::launch_grouped(kind, a, pl.tile, (hipStream_t)stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
@@ -1763,7 +1763,10 @@ struct VocabPlan {
     int64_t piece = 0, parts = 0;        // vocabulary rows at a time; column tiles (forward)
     bool copy_x = false, copy_w = false;
     int64_t ld2 = 0;                     // row length of the copies
-    size_t run = 0;                      // what the products' own paths take (with the counter region)
+    int parts_d = 1;                     // of D (gradient)
+    int tile_x = 128, tile_w = 128;      // of dX's and dW's products
+    int slices = 1;                      // of a piece's tokens in dX's product
+    int64_t per = 0;                     // tokens in each
     size_t x2 = 0, w2 = 0, part = 0, zt = 0, d = 0, sums = 0, ids = 0, q = 0, has = 0, weight = 0, alpha = 0, total = 0;
 };
 struct VocabCall {
@@ -1780,15 +1783,6 @@ static bool vocab_sizes_ok(const VocabCall &c)
 {
     return c.M >= 0 && c.M <= 1 << 24 && c.V >= 1 && c.V <= 0x7fffffff - 256 && c.K >= 1 && c.K <= 1 << 21 && c.topk >= 1 &&
            c.topk <= g5::kVocabMaxTopk;
-}
-
-// dX's share of a piece: sums := D . W (+ sums), an ordinary product.
-static Problem vocab_dx_problem(const VocabCall &c, int64_t rows, uint64_t d, int64_t ldd, uint64_t w, int64_t ldw,
-                                uint64_t sums, int64_t ld2, bool more)
-{
-    Problem p{GEMM_OP_BF16_AFFINE, 1, c.M, ld2, rows, d, w, sums, ldd, ldw, ld2, 0, 0, 0, GEMM_OUT_F32};
-    p.beta = more ? 1.0f : 0.0f;
-    return p;
 }
 
 static int vocab_plan(const VocabCall &c, VocabPlan &pl)
@@ -1830,27 +1824,28 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
             return GEMM_ERR_UNSUPPORTED;
     }
     if (c.grad) {
-        const int64_t ldd = (pl.piece + 7) / 8 * 8, ldw = pl.copy_w ? pl.ld2 : c.ldw;
-        // (placeholder addresses: their alignment is what counts)
-        const uint64_t base = (uint64_t)1 << 40;
-        for (int64_t rows : {pl.piece, c.V % pl.piece ? c.V % pl.piece : pl.piece}) {
-            const Problem p = vocab_dx_problem(c, rows, base, ldd, pl.copy_w ? 2 * base : c.w, ldw, 3 * base, pl.ld2, true);
-            g5::Plan sub;
-            const int st = g5::select_plan(p, sub, true);
-            if (st != GEMM_OK) return st;
-            const size_t n = g5::ws_layout(p, sub).total;
-            pl.run = n > pl.run ? n : pl.run;
-        }
-        at = pl.run > CR ? g5::round256(pl.run) : CR;
+        pl.parts_d = c.M <= g5::kVocabSplitRows ? 2 : 1;
+        if (g5::cdiv(pl.piece, 256) * g5::cdiv(c.K, 256) >= g5::kNumCU) pl.tile_w = 256;
+        // dX's output tiles shared out over slices of the tokens until every
+        // CU has one (two of 128), each slice at least 16 stages long
+        const int64_t rows = c.M * pl.parts_d;
+        if (rows > 128) pl.tile_x = 256;
+        const int64_t tiles = g5::cdiv(rows, pl.tile_x) * g5::cdiv(pl.ld2, pl.tile_x);
+        int64_t s = (pl.tile_x == 256 ? 1 : 2) * g5::kNumCU / tiles;
+        if (s > pl.piece / 512) s = pl.piece / 512;
+        s = s > 16 ? 16 : s < 1 ? 1 : s;
+        pl.per = g5::cdiv(g5::cdiv(pl.piece, s), 32) * 32;
+        pl.slices = (int)g5::cdiv(pl.piece, pl.per);
+        if (tiles * pl.slices > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
     }
-    if (pl.copy_x) pl.x2 = take((size_t)c.M * pl.ld2 * 2);
+    if (pl.copy_x) pl.x2 = take((size_t)c.M * pl.parts_d * pl.ld2 * 2);
     if (pl.copy_w) pl.w2 = take((size_t)pl.piece * pl.ld2 * 2);
     if (!c.grad) {
         pl.part = take((size_t)pl.parts * c.M * 8);
         pl.zt = take((size_t)c.M * c.topk * 4);
     } else {
-        pl.d = take((size_t)c.M * ((pl.piece + 7) / 8 * 8) * 2);
-        pl.sums = take((size_t)c.M * pl.ld2 * 4);
+        pl.d = take((size_t)c.M * pl.parts_d * ((pl.piece + 7) / 8 * 8) * 2);
+        pl.sums = take((size_t)pl.slices * c.M * pl.parts_d * pl.ld2 * 4);
         pl.ids = take((size_t)c.M * c.topk * 4);
         pl.q = take((size_t)c.M * c.topk * 4);
         pl.has = take((size_t)c.M * 4);
@@ -2021,6 +2016,7 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.align_dw = g5::row_alignment((uint64_t)dW, lddw, 0, 1, ew);
     b.ldx2 = (c.K + 7) / 8 * 8;
     b.rows_at_once = 32;
+    b.parts = 1;
     if (c.M == 0) {                  // the empty sum
         a.V = c.V;
         return g5::launch_vocab_dw(a, b, 128, s) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
@@ -2036,23 +2032,21 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.align_x = g5::row_alignment(c.x, c.ldx, 0, 1, 2);
     b.D = (uint16_t *)(ws + pl.d);
     b.ldd = (pl.piece + 7) / 8 * 8;
+    b.parts = pl.parts_d;
     b.sums = (float *)(ws + pl.sums);
+    b.slices = pl.slices;
+    b.per = pl.per;
     const int64_t widest = b.ldd > b.ldx2 ? b.ldd : b.ldx2;
-    b.rows_at_once = (((int64_t)1 << 29) / widest) / 32 * 32;
+    b.rows_at_once = (((int64_t)1 << 29) / widest) / 64 * 64;
     if (g5::launch_vocab_prep(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
     a.X = b.X2;
     a.ldx = b.ldx2;
-    const int tile_w = g5::cdiv(pl.piece, 256) * g5::cdiv(c.K, 256) >= g5::kNumCU ? 256 : 128;
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;
         if (g5::launch_vocab_dlogits(a, b, pl.tile, s) != hipSuccess) return GEMM_ERR_LAUNCH;
-        if (dW && g5::launch_vocab_dw(a, b, tile_w, s) != hipSuccess) return GEMM_ERR_LAUNCH;
-        if (dX) {
-            const Problem p = vocab_dx_problem(c, a.V, (uint64_t)b.D, b.ldd, (uint64_t)a.W, a.ldw, (uint64_t)b.sums, b.ldx2,
-                                               v0 > 0);
-            st = g5::run(p, stream, workspace, pl.run);
-            if (st != GEMM_OK) return st;
-        }
+        if (dW && g5::launch_vocab_dw(a, b, pl.tile_w, s) != hipSuccess) return GEMM_ERR_LAUNCH;
+        b.more = v0 > 0;
+        if (dX && g5::launch_vocab_sums(a, b, pl.tile_x, s) != hipSuccess) return GEMM_ERR_LAUNCH;
     }
     if (dX && g5::launch_vocab_dx(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
     return GEMM_OK;

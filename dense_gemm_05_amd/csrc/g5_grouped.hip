@@ -16,6 +16,7 @@
 
 #include "g5_device.h"
 #include "g5_kernels.h"
+#include "g5_ping.h"
 #include "g5_stream.h"
 
 namespace g5 {
@@ -108,42 +109,13 @@ __device__ __forceinline__ void find_group(const GroupedArgs &p, int e, int &fir
     }
 }
 
-// An output tile on the LDS ring (RingTile): operand bases moved to the
-// tile's own first row and column, so that 32-bit offsets span no more than
-// the tile's rows.  Where the summed axis walks rows (B of NN, both of TN),
-// it goes in pieces of p.piece that keep them so.
-template <int BM, int BN, int WGM, int WGN, int KIND>
-__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
+// An output tile on the LDS ring (RingTile): q's operand bases are at the
+// tile's own first row and column, so that 32-bit offsets span no more than the
+// tile's rows.  Where the summed axis walks rows (B of NN, both of TN), it
+// goes in pieces of p.piece that keep them so.
+template <class R, int KIND, int BM, int BN>
+__device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uint16_t *smem, int64_t K, int n0)
 {
-    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, KIND == GROUPED_NT, false, KIND == GROUPED_TN>;
-    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
-    GemmArgs q{};
-    int64_t K;
-    const char *A = (const char *)p.A, *B = (const char *)p.B;
-    int n0;
-    if constexpr (KIND == GROUPED_TN) {
-        const TileCoord tc = tile_map(blockIdx.x, p.E, p.tiles_m, p.tiles_n, p.group_m);
-        int first, rows;
-        find_group(p, (int)tc.b, first, rows);
-        const int m0 = (int)tc.tm * BM;
-        n0 = (int)tc.tn * BN;
-        K = rows;
-        A += (first * p.lda + m0) * 2;
-        B += (first * p.ldb + n0) * 2;
-        q.C = (char *)p.C + (tc.b * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
-        q.M = p.M - m0 < BM ? p.M - m0 : BM;
-    } else {
-        GroupTile t;
-        if (!find_tile(p, BM, t)) return;
-        n0 = t.tn * BN;
-        K = p.K;
-        A += t.row * p.lda * 2;
-        B += (t.group * p.sB + (KIND == GROUPED_NT ? n0 * p.ldb : n0)) * 2;
-        q.C = (char *)p.C + (t.row * p.ldc + n0) * (p.out_f32 ? 4 : 2);
-        q.M = t.rows;
-    }
-    q.A = A;
-    q.B = B;
     q.lda = p.lda;
     q.ldb = p.ldb;
     q.ldc = p.ldc;
@@ -154,18 +126,58 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
     const int64_t left = p.N - n0;
     q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 7) & ~(int64_t)7) : BN;
     const TileCoord here{0, 0, 0};
-    f32x4 acc[R::FN][R::FM];
+    typename R::Acc acc;
     R::zero(acc);
     for (int64_t done = 0; done < K;) {
         q.K = KIND != GROUPED_NT && K - done > p.piece ? p.piece : K - done;
         if (done > 0) __syncthreads();            // every wave is through with the ring
-        R::accumulate(q, smem, here, 0, q.K, acc);
+        multiply_tile<R, BM, BN, KIND == GROUPED_NT, KIND == GROUPED_TN>(q, smem, q.K, acc);
         done += q.K;
         q.A = (const char *)q.A + q.K * (KIND == GROUPED_TN ? p.lda : 1) * 2;
         q.B = (const char *)q.B + q.K * (KIND == GROUPED_NT ? 1 : p.ldb) * 2;
     }
     q.N = left < BN ? left : BN;
     R::store(q, smem, here, acc);
+}
+
+template <int BM, int BN, int WGM, int WGN, int KIND>
+using GroupedRing = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, KIND == GROUPED_NT, false, KIND == GROUPED_TN>;
+
+// HALF: a group's last tile that has no more than BM / 2 rows runs as one of
+// that height (a mean of 512 rows in tiles of 256 otherwise multiplies a fifth
+// of the rows for nothing).
+template <int BM, int BN, int WGM, int WGN, int KIND, bool HALF>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
+{
+    using R = GroupedRing<BM, BN, WGM, WGN, KIND>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    GemmArgs q{};
+    if constexpr (KIND == GROUPED_TN) {
+        const TileCoord tc = tile_map(blockIdx.x, p.E, p.tiles_m, p.tiles_n, p.group_m);
+        int first, rows;
+        find_group(p, (int)tc.b, first, rows);
+        const int m0 = (int)tc.tm * BM, n0 = (int)tc.tn * BN;
+        q.A = p.A + (first * p.lda + m0);
+        q.B = p.B + (first * p.ldb + n0);
+        q.C = (char *)p.C + (tc.b * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        q.M = p.M - m0 < BM ? p.M - m0 : BM;
+        ring_tile<R, KIND, BM, BN>(p, q, smem, rows, n0);
+    } else {
+        GroupTile t;
+        if (!find_tile(p, BM, t)) return;
+        const int n0 = t.tn * BN;
+        q.A = p.A + t.row * p.lda;
+        q.B = p.B + (t.group * p.sB + (KIND == GROUPED_NT ? n0 * p.ldb : n0));
+        q.C = (char *)p.C + (t.row * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        q.M = t.rows;
+        if constexpr (HALF) {
+            if (t.rows <= BM / 2) {
+                ring_tile<GroupedRing<BM / 2, BN, WGM, WGN, KIND>, KIND, BM / 2, BN>(p, q, smem, p.K, n0);
+                return;
+            }
+        }
+        ring_tile<R, KIND, BM, BN>(p, q, smem, p.K, n0);
+    }
 }
 
 // NT with a few rows per group (a decoding step): bound by reading the
@@ -237,10 +249,11 @@ template <int BM, int BN, int WGM, int WGN>
 hipError_t launch_kind(int kind, const GroupedArgs &a, int64_t grid, hipStream_t s)
 {
     const dim3 g((unsigned)grid), b(WGM * WGN * 64);
+    constexpr bool HALF = BM == 256;
     switch (kind) {
-    case GROUPED_NT: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NT>), g, b, 0, s, a); break;
-    case GROUPED_NN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NN>), g, b, 0, s, a); break;
-    case GROUPED_TN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_TN>), g, b, 0, s, a); break;
+    case GROUPED_NT: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NT, HALF>), g, b, 0, s, a); break;
+    case GROUPED_NN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_NN, HALF>), g, b, 0, s, a); break;
+    case GROUPED_TN: hipLaunchKernelGGL((k_grouped<BM, BN, WGM, WGN, GROUPED_TN, false>), g, b, 0, s, a); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();

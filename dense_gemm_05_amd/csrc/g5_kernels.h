@@ -267,6 +267,12 @@ hipError_t launch_grouped(int kind, const GroupedArgs &a, int tile, hipStream_t 
 // (g5_vocab.hip).  A piece of the vocabulary: V rows of W from v0 on.
 constexpr int kVocabMaxTopk = 256;
 constexpr int kVocabStreamRows = 32;    // rows of X up to which the weight is streamed past them
+// Up to so many rows D is kept as two bf16 parts (2^-16 of it): with few rows
+// the roundings of a few large elements decide about whole gradients (one row:
+// 3.0e-3 of dW's size off, of which its own rounding is 1.7e-3), and the
+// products are bound by reading the weight and writing its gradient, not by
+// twice the rows.
+constexpr int kVocabSplitRows = 64;
 struct VocabArgs {
     const uint16_t *X, *W;              // 16-byte aligned rows for the ring tiles, any for the stream
     int64_t M, V, K, ldx, ldw;
@@ -275,7 +281,7 @@ struct VocabArgs {
     const void *ids;                    // [M, topk], int32 or (ids64) int64
     int ids64, topk;
     const float *teacher;               // [M, topk], or NULL: ids are labels (topk 1)
-    float2 *part;                       // [parts, M]: maximum and sum of a row in a column tile
+    float2 *part;                       // [M, parts]: maximum and sum of a row in a column tile
     float *zt;                          // [M, topk]: the targets' logits
     int64_t parts, tile0;               // column tiles in all; the piece's first
     float *loss, *lse_out;              // [M]; lse_out or NULL
@@ -290,7 +296,11 @@ struct VocabGrad {
     int align_x;                        // byte alignment of X's rows
     uint16_t *D;                        // a piece's gradient of the logits
     int64_t ldd;                        // a multiple of 8
-    float *sums;                        // [M, ldx2]: dX before its factor
+    int parts;                          // of D: 1, or 2 behind each other ([2 M, ldd], X2 [2 M, ldx2])
+    float *sums;                        // [slices, parts M, ldx2]: dX before its factor
+    int slices;                         // of a piece's tokens in dX's product
+    int64_t per;                        // tokens in each, a multiple of 32
+    int more;                           // sums of pieces before
     uint16_t *dX;
     int64_t lddx;
     void *dW;
@@ -304,6 +314,7 @@ hipError_t launch_vocab_join(const VocabArgs &a, hipStream_t s);
 hipError_t launch_vocab_prep(const VocabArgs &a, const VocabGrad &b, hipStream_t s);
 hipError_t launch_vocab_dlogits(const VocabArgs &a, const VocabGrad &b, int tile, hipStream_t s);
 hipError_t launch_vocab_dw(const VocabArgs &a, const VocabGrad &b, int tile, hipStream_t s);
+hipError_t launch_vocab_sums(const VocabArgs &a, const VocabGrad &b, int tile, hipStream_t s);
 hipError_t launch_vocab_dx(const VocabArgs &a, const VocabGrad &b, hipStream_t s);
 
 }  // namespace g5

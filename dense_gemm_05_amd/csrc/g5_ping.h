@@ -1,0 +1,245 @@
+// g5_ping.h -- the main loop of large bf16 tiles: two groups of waves that
+// take turns at the matrix cores and at memory.
+#pragma once
+
+#include "g5_device.h"
+
+namespace g5 {
+
+// A 256 x 256 output tile by eight waves as 2 x 4 (wave tile 128 x 64), with
+// RingTile's operand layouts (BT: B given as Bt [N, K]; AT: A given as At [K,
+// M]), masks, accumulators and epilogues.
+//
+// K goes in stages of 64 through two LDS buffers.  A wave multiplies a stage
+// in four phases of 16 MFMAs, a quarter of its tile each: (A0, B0), (A0, B1),
+// (A1, B1), (A1, B0), with A0, A1 its upper and lower 64 rows and B0, B1 its
+// left and right 32 columns.  Before each phase it reads the fragments that
+// this phase or the next one lacks (four or eight) and copies a sixteenth of
+// half an operand's stage.  The waves with the upper rows and those with the
+// lower rows, one of each on every SIMD, are kept half a phase apart by one
+// more barrier at the start: while one feeds the matrix core, the other reads
+// and copies.
+//
+// What a phase read is free behind the next barrier that both groups passed,
+// so the copies of stage t + 2 follow the reads of stage t region by region
+// (A0, B0, B1, A1, in the order of reading) and have six phases to land:
+// vmcnt(12) holds at each point with two copies per phase and wave.
+//
+// LDS.  A K-contiguous operand's stage has rows of 128 bytes (a copy
+// instruction moves eight whole lines), 16-byte chunks at chunk ^ (row & 7).
+// One given across K is kept as its two regions, each 64 rows (k) of the 128
+// columns that the waves' halves hold, chunks at chunk ^ swz_bn(k), and read by
+// the transposing read.
+//
+// Against the ring's 32-deep stages, in which all waves read at once and then
+// multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3108 us
+// (1415 TFLOP/s) for 3550.
+template <bool BT, bool AT>
+struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, AT> {
+    using R = RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, AT>;
+    using typename R::Acc;
+    static constexpr int KSTAGE = 64, BUF = 256 * 64, REGION = BUF / 2;      // elements
+    static_assert(R::LDS_BYTES == 4 * BUF * 2, "two buffers of A and of B");
+
+    // Rows of q.A (q.M of them) and columns of q.B (q.N) from the tile's first
+    // on, K summed elements.  The LDS must be free on entry; it is free again
+    // behind the caller's next barrier.
+    __device__ static __forceinline__ void accumulate(const GemmArgs &p, uint16_t *smem, const int64_t K, Acc &acc)
+    {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
+        const int g = lane >> 4, li = lane & 15;
+        const char *A = (const char *)p.A, *B = (const char *)p.B;
+        const uint32_t a_bytes = (uint32_t)((AT ? (p.K - 1) * p.lda + ((p.M + 7) & ~(int64_t)7) : (p.M - 1) * p.lda + p.K) * 2);
+        const uint32_t b_bytes = (uint32_t)((BT ? (p.N - 1) * p.ldb + p.K : (p.K - 1) * p.ldb + p.N) * 2);
+
+        // Copies: region r of a stage (0: A0, 1: B0, 2: B1, 3: A1) is 16 blocks
+        // of 1 KiB, two for each wave: eight rows, or four of the region's k.
+        constexpr auto of_a = [](int r) { return r == 0 || r == 3; };
+        constexpr auto across = [](bool a) { return a ? AT : !BT; };
+        auto place = [&](int r, int i) {       // of the block, in KiB of the stage's buffer
+            const int b = 2 * wave + i, h = r >= 2;
+            if (across(of_a(r))) return h * 16 + b;
+            return of_a(r) ? (b >> 3) * 16 + h * 8 + (b & 7) : (b >> 2) * 8 + h * 4 + (b & 3);
+        };
+        uint32_t voff[4][2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool a = of_a(r);
+                const int64_t ld = a ? p.lda : p.ldb, limit = a ? p.M : p.N;
+                if (across(a)) {
+                    const int k = 4 * (2 * wave + i) + (lane >> 4), col = ((lane & 15) ^ swz_bn<128>(k)) * 8, h = r >= 2;
+                    const int at = a ? (col >> 6) * 128 + h * 64 + (col & 63) : (col >> 5) * 64 + h * 32 + (col & 31);
+                    voff[r][i] = (uint32_t)((k * ld + at) * 2);
+                } else {
+                    const int row = 8 * place(r, i) + (lane >> 3), chunk = (lane & 7) ^ (row & 7);
+                    voff[r][i] = row >= limit ? 0x80000000u : (uint32_t)(row * ld * 2 + chunk * 16);
+                }
+            }
+        const int KT = (int)(K / KSTAGE);
+        // (a stage past the last copies the last one again, into a place that
+        // is read no more)
+        auto copy = [&](int r, int t) {
+            const int kt = t < KT ? t : KT - 1;
+            const bool a = of_a(r);
+            const int64_t adv = (int64_t)kt * KSTAGE * 2 * (across(a) ? (a ? p.lda : p.ldb) : 1);
+            const i32x4_t d = make_rsrc((a ? A : B) + adv, (a ? a_bytes : b_bytes) - (uint32_t)adv);
+            uint16_t *to = smem + (a ? 0 : 2 * BUF) + (t & 1) * BUF;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) dma<16>(d, voff[r][i], 0, to + place(r, i) * 512);
+        };
+
+        // Fragments: lane (g, li) holds K elements 8 g .. 8 g + 7 of row li, in
+        // steps s of 32.  K-contiguous: chunk (4 s + g) ^ (row & 7) of the row.
+        bf16x8 a0[4][2], a1[4][2], b0[2][2], b1[2][2];
+        const int at = li * 64 + ((g ^ (li & 7)) * 8), at1 = at ^ 32;
+        // Across K: two transposing reads of four k each.
+        const int k0 = g * 8 + (li >> 2);
+        int at_a[4], at_b[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at_a[i] = k0 * 128 + (((wm * 8 + i * 2 + ((li & 3) >> 1)) ^ swz_bn<128>(k0)) * 8) + (li & 1) * 4;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) at_b[j] = k0 * 128 + (((wn * 4 + j * 2 + ((li & 3) >> 1)) ^ swz_bn<128>(k0)) * 8) + (li & 1) * 4;
+        auto transposed = [&](const uint16_t *s) {
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(G5_LDS(i16x4, s));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(G5_LDS(i16x4, s + 4 * 128));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        auto read_a = [&](bf16x8 (&f)[4][2], int t, int h) {
+            const uint16_t *s = smem + (t & 1) * BUF;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if constexpr (AT) f[i][q] = transposed(s + h * REGION + at_a[i] + q * 32 * 128);
+                    else f[i][q] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(s + (wm * 128 + h * 64) * 64 + (q ? at1 : at) + i * 1024));
+                }
+        };
+        auto read_b = [&](bf16x8 (&f)[2][2], int t, int h) {
+            const uint16_t *s = smem + (2 + (t & 1)) * BUF;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if constexpr (!BT) f[j][q] = transposed(s + h * REGION + at_b[j] + q * 32 * 128);
+                    else f[j][q] = __builtin_bit_cast(bf16x8, *(const u32x4 *)(s + (wn * 64 + h * 32) * 64 + (q ? at1 : at) + j * 1024));
+                }
+        };
+        auto mma = [&](const bf16x8 (&a)[4][2], const bf16x8 (&b)[2][2], int ha, int hb) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[hb * 2 + j][ha * 4 + i] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][q], a[i][q], acc[hb * 2 + j][ha * 4 + i], 0, 0, 0);
+            __builtin_amdgcn_s_setprio(0);
+        };
+        auto barrier = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // the end of a phase's reads and copies: the reads are done, and the
+        // copies of what the next phase (of either group) reads have landed
+        auto landed = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(12, 0));
+            barrier();
+        };
+
+        if (KT > 0) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) copy(r, t);
+            landed();
+            read_a(a0, 0, 0);
+            landed();
+            if (wm == 1) barrier();
+            auto stage = [&](int t) {
+                read_b(b0, t, 0);
+                copy(0, t + 2);
+                landed();
+                mma(a0, b0, 0, 0);
+                barrier();
+                read_b(b1, t, 1);
+                copy(1, t + 2);
+                landed();
+                mma(a0, b1, 0, 1);
+                barrier();
+                read_a(a1, t, 1);
+                copy(2, t + 2);
+                landed();
+                mma(a1, b1, 1, 1);
+                barrier();
+                read_a(a0, t + 1, 0);
+                copy(3, t + 2);
+                landed();
+                mma(a1, b0, 1, 0);
+                barrier();
+            };
+            int t = 0;
+            for (; t + 1 < KT; t += 2) {
+                stage(t);
+                stage(t + 1);
+            }
+            if (t < KT) stage(t);
+            if (wm == 0) barrier();
+        }
+        if (K % KSTAGE != 0) {
+            // what is left of K: chunk by chunk with zeros behind it, once
+            // every copy in flight has landed
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            const int64_t from = (int64_t)KT * KSTAGE;
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const bool a = o == 0;
+                const uint16_t *src = (const uint16_t *)(a ? A : B);
+                const int64_t ld = a ? p.lda : p.ldb, limit = a ? p.M : p.N;
+                uint16_t *to = smem + o * 2 * BUF;
+                for (int q = tid; q < 256 * 8; q += 512) {
+                    if (across(a)) {
+                        const int k = q >> 5, cc = q & 31;       // chunk of the tile's 32
+                        const int h = a ? (cc >> 3) & 1 : (cc >> 2) & 1;
+                        const int c = a ? (cc >> 4) * 8 + (cc & 7) : (cc >> 3) * 4 + (cc & 3);
+                        const u32x4 v = load_chunk8_bf16(src + (from + k) * ld, 8 * cc, limit, from + k < K, 16);
+                        *(u32x4 *)(to + h * REGION + k * 128 + ((c ^ swz_bn<128>(k)) * 8)) = v;
+                    } else {
+                        const int row = q >> 3, c = q & 7;
+                        const u32x4 v = load_chunk8_bf16(src + row * ld, from + 8 * c, K, row < limit, 16);
+                        *(u32x4 *)(to + row * 64 + ((c ^ (row & 7)) * 8)) = v;
+                    }
+                }
+            }
+            __syncthreads();
+            read_a(a0, 0, 0);
+            read_a(a1, 0, 1);
+            read_b(b0, 0, 0);
+            read_b(b1, 0, 1);
+            mma(a0, b0, 0, 0);
+            mma(a0, b1, 0, 1);
+            mma(a1, b1, 1, 1);
+            mma(a1, b0, 1, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(0);
+    }
+};
+
+// The product of a tile whose operands' bases are at its own first row and
+// column: 256 x 256 tiles by two groups of waves in turn, others on the ring.
+template <class R, int BM, int BN, bool BT, bool AT>
+__device__ __forceinline__ void multiply_tile(const GemmArgs &q, uint16_t *smem, int64_t K, typename R::Acc &acc)
+{
+    if constexpr (BM == 256 && BN == 256) PingTile<BT, AT>::accumulate(q, smem, K, acc);
+    else R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, K, acc);
+}
+
+}  // namespace g5

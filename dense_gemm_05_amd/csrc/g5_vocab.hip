@@ -18,6 +18,7 @@
 
 #include "g5_device.h"
 #include "g5_kernels.h"
+#include "g5_ping.h"
 #include "g5_stream.h"
 
 namespace g5 {
@@ -86,13 +87,14 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
 {
     using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, true>;
     using S = Staged<R, BM, BN>;
+    constexpr int NT = WGM * WGN * 64;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
     const TileCoord tc = tile_map(blockIdx.x, 1, p.tiles_m, p.tiles_n, p.group_m);
     const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN;
     const GemmArgs q = tile_args<BM, BN>(p, m0, n0);
     f32x4 acc[R::FN][R::FM];
     R::zero(acc);
-    R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+    multiply_tile<R, BM, BN, true, false>(q, smem, q.K, acc);
 
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
@@ -131,9 +133,11 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         if (g == 0) st[wn * BM + wm * R::TM + fm * 16 + li] = Stat{top, sum};
     }
     // targets in this tile
-    const int64_t first = p.v0 + n0, pairs = q.M * p.topk;
+    const int64_t first = p.v0 + n0;
+    const int pairs = (int)q.M * p.topk;
     int some = 0;
-    for (int64_t i = tid; i < pairs; i += WGM * WGN * 64) {
+#pragma unroll 8
+    for (int i = tid; i < pairs; i += NT) {
         const int64_t col = target_id(p, m0 * p.topk + i) - first;
         some |= col >= 0 && col < q.N;
     }
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         Stat s = st[tid];
 #pragma unroll
         for (int w = 1; w < WGN; ++w) s = join_stat(s, st[w * BM + tid], c);
-        p.part[(p.tile0 + tc.tn) * p.M + m0 + tid] = float2{s.top, s.sum};
+        p.part[(m0 + tid) * p.parts + p.tile0 + tc.tn] = float2{s.top, s.sum};
     }
     if (!some) return;
     float *L = (float *)smem;
@@ -153,10 +157,11 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         for (int k = 0; k < BM / S::RP; ++k)
             if (k == pass) S::put(acc, L, k, wm, wn, g, li);
         __syncthreads();
-        const int64_t lo = pass * S::RP * p.topk, end = (pass + 1) * S::RP * p.topk, hi = end < pairs ? end : pairs;
-        for (int64_t i = lo + tid; i < hi; i += WGM * WGN * 64) {
+        const int lo = pass * S::RP * p.topk, end = lo + S::RP * p.topk, hi = end < pairs ? end : pairs;
+#pragma unroll 8
+        for (int i = lo + tid; i < hi; i += NT) {
             const int64_t col = target_id(p, m0 * p.topk + i) - first;
-            if (col >= 0 && col < q.N) p.zt[m0 * p.topk + i] = L[(int)(i / p.topk - pass * S::RP) * S::PITCH + (int)col];
+            if (col >= 0 && col < q.N) p.zt[m0 * p.topk + i] = L[(i / p.topk - pass * S::RP) * S::PITCH + (int)col];
         }
     }
 }
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
             for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (s[r][i] - base));
         sum += __shfl_xor(sum, 16, 64);
         sum += __shfl_xor(sum, 32, 64);
-        if (g == 0 && 16 * cc + li < M) p.part[(int64_t)blockIdx.x * M + 16 * cc + li] = float2{top, sum};
+        if (g == 0 && 16 * cc + li < M) p.part[(16 * cc + li) * p.parts + blockIdx.x] = float2{top, sum};
         // (one wave writes and reads the tile: in order)
         __builtin_amdgcn_wave_barrier();
         const int rows = M - 16 * cc < 16 ? M - 16 * cc : 16;
@@ -299,60 +304,61 @@ __device__ __forceinline__ bool row_targets(const VocabArgs &p, int64_t m, int l
     return any;
 }
 
-// The tiles' parts of R rows joined by a workgroup, then each row's loss by a
-// wave.
-constexpr int kJoinThreads = 512;
-__global__ void __launch_bounds__(kJoinThreads) k_vocab_join(VocabArgs p, int rows)
+// The tiles' parts of a row joined by a workgroup, then its loss.  Always the
+// same parts in the same order: the same call gives the same bits.
+constexpr int kJoinWaves = 4;
+__global__ void __launch_bounds__(kJoinWaves * 64) k_vocab_join(VocabArgs p)
 {
-    __shared__ Stat st[kJoinThreads];
-    const int tid = threadIdx.x, r = tid % rows, turn = tid / rows, turns = kJoinThreads / rows;
-    const int64_t m0 = (int64_t)blockIdx.x * rows, m = m0 + r;
+    __shared__ Stat st[kJoinWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float c = p.scale * kLog2e;
-    Stat s{-__builtin_inff(), 0.f};
-    if (m < p.M) {
+    auto base = [](float top) { return top == -__builtin_inff() ? 0.f : top; };
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        Stat s{-__builtin_inff(), 0.f};
 #pragma unroll 8
-        for (int64_t i = turn; i < p.parts; i += turns) {
-            const float2 v = p.part[i * p.M + m];
+        for (int64_t i = threadIdx.x; i < p.parts; i += kJoinWaves * 64) {
+            const float2 v = p.part[m * p.parts + i];
             s = join_stat(s, Stat{v.x, v.y}, c);
         }
-    }
-    st[tid] = s;
-    // (always the same pairs: the same call gives the same bits)
-    for (int o = turns / 2; o > 0; o >>= 1) {
+        float top = max64(s.top);
+        float sum = sum64(s.sum * __builtin_amdgcn_exp2f(c * (s.top - base(top))));
+        __syncthreads();                 // (the row before has been read)
+        if (lane == 0) st[wave] = Stat{top, sum};
         __syncthreads();
-        if (turn < o) st[tid] = s = join_stat(s, st[tid + o * rows], c);
-    }
-    __syncthreads();
-    const int lane = tid & 63, wave = tid >> 6;
-    for (int i = wave; i < rows; i += kJoinThreads / 64) {
-        const int64_t row = m0 + i;
-        if (row >= p.M) break;
-        const Stat t = st[i];
-        const float log_sum = logf(t.sum);
-        if (lane == 0 && p.lse_out) p.lse_out[row] = p.scale * t.top + log_sum;
+        if (wave != 0) continue;
+        s = st[lane % kJoinWaves];
+        top = s.top;
+#pragma unroll
+        for (int o = kJoinWaves / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        sum = s.sum * __builtin_amdgcn_exp2f(c * (s.top - base(top)));
+#pragma unroll
+        for (int o = kJoinWaves / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+        const float log_sum = logf(sum);
+        if (lane == 0 && p.lse_out) p.lse_out[m] = p.scale * top + log_sum;
         float loss = 0.f;
         if (!p.teacher) {
-            const int64_t id = target_id(p, row);
+            const int64_t id = target_id(p, m);
             // (the difference of the logits first: exact where the loss is small)
-            if (id >= 0 && id < p.vocab) loss = p.scale * (t.top - p.zt[row]) + log_sum;
+            if (id >= 0 && id < p.vocab) loss = p.scale * (top - p.zt[m]) + log_sum;
         } else {
             RowTargets q;
-            if (row_targets(p, row, lane, q)) {
+            if (row_targets(p, m, lane, q)) {
 #pragma unroll
                 for (int j = 0; j < kTopkPer; ++j)
                     if (q.id[j] >= 0)
-                        loss += q.q[j] * (q.logq[j] + (p.scale * (t.top - p.zt[row * p.topk + lane + 64 * j]) + log_sum));
+                        loss += q.q[j] * (q.logq[j] + (p.scale * (top - p.zt[m * p.topk + lane + 64 * j]) + log_sum));
                 loss = sum64(loss);
             }
         }
-        if (lane == 0) p.loss[row] = loss;
+        if (lane == 0) p.loss[m] = loss;
     }
 }
 
 // Before the gradient, a wave per row: its targets as int32 ids, each once
 // (one listed twice has both weights at its first place), their weights,
 // whether there are any, and its row of X with zero padding, all zeros for a
-// row without targets, whose contents must not reach dW.
+// row without targets, whose contents must not reach dW (twice with b.parts 2:
+// D's two parts meet it one after the other).
 constexpr int kPrepWaves = 4;
 __global__ void __launch_bounds__(kPrepWaves * 64) k_vocab_prep(VocabArgs p, VocabGrad b)
 {
@@ -398,8 +404,11 @@ __global__ void __launch_bounds__(kPrepWaves * 64) k_vocab_prep(VocabArgs p, Voc
         b.weight[m] = some ? b.dloss[m] : 0.f;
     }
     const uint16_t *x = p.X + m * p.ldx;
-    for (int64_t col = lane * 8; col < b.ldx2; col += 512)
-        *(u32x4 *)(b.X2 + m * b.ldx2 + col) = load_chunk8_bf16(x, col, p.K, some, b.align_x);
+    for (int64_t col = lane * 8; col < b.ldx2; col += 512) {
+        const u32x4 v = load_chunk8_bf16(x, col, p.K, some, b.align_x);
+        *(u32x4 *)(b.X2 + m * b.ldx2 + col) = v;
+        if (b.parts == 2) *(u32x4 *)(b.X2 + (p.M + m) * b.ldx2 + col) = v;
+    }
 }
 
 // The largest |dloss| of the rows with targets into alpha, every row's weight
@@ -425,7 +434,9 @@ __global__ void __launch_bounds__(1024) k_vocab_weights(float *weight, int64_t M
 }
 
 // D of a piece: exp(l - lse) in registers, staged as FP32, the targets'
-// weights taken off where they lie, then weighted and rounded to bf16.
+// weights taken off where they lie, then weighted and rounded to bf16.  With
+// b.parts 2 (few rows) the rounding's rest, as a bf16 of its own, follows in
+// rows M .. 2 M - 1.
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p, VocabGrad b)
 {
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
     const GemmArgs q = tile_args<BM, BN>(p, m0, n0);
     f32x4 acc[R::FN][R::FM];
     R::zero(acc);
-    R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+    multiply_tile<R, BM, BN, true, false>(q, smem, q.K, acc);
 
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
                 acc[fn][fm][i] = __builtin_amdgcn_exp2f(kLog2e * __builtin_fmaf(p.scale, acc[fn][fm][i], -lse));
     }
     float *L = (float *)smem;
-    const int64_t pairs = q.M * p.topk;
+    const int pairs = (int)q.M * p.topk;
     const int first = (int)(p.v0 + n0);
     for (int pass = 0; pass < BM / S::RP; ++pass) {
         if (pass * S::RP >= q.M) break;          // uniform
@@ -463,22 +474,32 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
         for (int k = 0; k < BM / S::RP; ++k)
             if (k == pass) S::put(acc, L, k, wm, wn, g, li);
         __syncthreads();
-        const int64_t lo = pass * S::RP * p.topk, end = (pass + 1) * S::RP * p.topk, hi = end < pairs ? end : pairs;
-        for (int64_t i = lo + tid; i < hi; i += NT) {
+        const int lo = pass * S::RP * p.topk, end = lo + S::RP * p.topk, hi = end < pairs ? end : pairs;
+#pragma unroll 8
+        for (int i = lo + tid; i < hi; i += NT) {
             const int id = b.ids[m0 * p.topk + i], col = id - first;
             if (id >= 0 && col >= 0 && col < q.N)
-                L[(int)(i / p.topk - pass * S::RP) * S::PITCH + col] -= b.q[m0 * p.topk + i];
+                L[(i / p.topk - pass * S::RP) * S::PITCH + col] -= b.q[m0 * p.topk + i];
         }
         __syncthreads();
+#pragma unroll 2
         for (int i = tid; i < S::RP * (BN / 8); i += NT) {
             const int r = i / (BN / 8), ch = i % (BN / 8) * 8, row = pass * S::RP + r;
             if (row >= q.M || ch >= q.N) continue;
-            const f32x4 a0 = *(const f32x4 *)(L + r * S::PITCH + ch), a1 = *(const f32x4 *)(L + r * S::PITCH + ch + 4);
             const float w = b.weight[m0 + row];
-            u32x4 d = {pack_bf16x2(w * a0[0], w * a0[1]), pack_bf16x2(w * a0[2], w * a0[3]),
-                       pack_bf16x2(w * a1[0], w * a1[1]), pack_bf16x2(w * a1[2], w * a1[3])};
-            if (!b.has[m0 + row]) d = u32x4{0u, 0u, 0u, 0u};
-            *(u32x4 *)(b.D + (m0 + row) * b.ldd + n0 + ch) = d;
+            const bool some = b.has[m0 + row] != 0;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = some ? w * L[r * S::PITCH + ch + j] : 0.f;
+            const u32x4 d = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+            uint16_t *out = b.D + (m0 + row) * b.ldd + n0 + ch;
+            *(u32x4 *)out = d;
+            if (b.parts == 2) {
+                u32x4 rest;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) rest[j] = pack_bf16x2(v[2 * j] - bf16_lo(d[j]), v[2 * j + 1] - bf16_hi(d[j]));
+                *(u32x4 *)(out + p.M * b.ldd) = rest;
+            }
         }
     }
 }
@@ -506,15 +527,16 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, Voca
     q.N = b.ldx2 - n0 < BN ? b.ldx2 - n0 : BN;               // (whole padded chunks)
     f32x4 acc[R::FN][R::FM];
     R::zero(acc);
-    for (int64_t done = 0; done < p.M;) {
-        q.K = p.M - done < b.rows_at_once ? p.M - done : b.rows_at_once;
+    const int64_t rows = p.M * b.parts;
+    for (int64_t done = 0; done < rows;) {
+        q.K = rows - done < b.rows_at_once ? rows - done : b.rows_at_once;
         if (done > 0) __syncthreads();
-        R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, q.K, acc);
+        multiply_tile<R, BM, BN, false, true>(q, smem, q.K, acc);
         done += q.K;
         q.A = b.D + m0 + done * b.ldd;
         q.B = b.X2 + n0 + done * b.ldx2;
     }
-    const float a = p.M > 0 ? p.scale * *b.alpha : 0.f;
+    const float a = rows > 0 ? p.scale * *b.alpha : 0.f;
 #pragma unroll
     for (int fn = 0; fn < R::FN; ++fn)
 #pragma unroll
@@ -525,16 +547,63 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, Voca
     R::store(q, smem, TileCoord{0, 0, 0}, acc);
 }
 
-// dX from the sums over all pieces: bf16(scale alpha sum), zeros for rows
-// without targets.  A thread per 8 columns at a time.
+// A piece's share of dX before its factor: sums (+)= D W over one of b.slices
+// parts of the piece's tokens, each with sums of its own.  Few output tiles
+// would leave CUs idle over a long summed axis.
+template <int BM, int BN, int WGM, int WGN>
+__global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, VocabGrad b)
+{
+    using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true>;
+    __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
+    const TileCoord tc = tile_map(blockIdx.x, b.slices, p.tiles_m, p.tiles_n, p.group_m);
+    const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN, rows = p.M * b.parts;
+    const int64_t k0 = tc.b * b.per < p.V ? tc.b * b.per : p.V;
+    GemmArgs q{};
+    q.A = b.D + m0 * b.ldd + k0;
+    q.B = p.W + k0 * p.ldw + n0;
+    q.C = b.sums + (tc.b * rows + m0) * b.ldx2 + n0;
+    q.M = rows - m0 < BM ? rows - m0 : BM;
+    q.N = b.ldx2 - n0 < BN ? b.ldx2 - n0 : BN;
+    q.K = p.V - k0 < b.per ? p.V - k0 : b.per;
+    q.lda = b.ldd;
+    q.ldb = p.ldw;
+    q.ldc = b.ldx2;
+    q.align_a = q.align_b = q.align_c = 16;
+    q.out_f32 = 1;
+    f32x4 acc[R::FN][R::FM];
+    R::zero(acc);
+    if (b.more) {
+        // the pieces before
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / WGN, wn = wave % WGN;
+#pragma unroll
+        for (int fm = 0; fm < R::FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < R::FN; ++fn) {
+                const int r = wm * R::TM + fm * 16 + (lane & 15), n = wn * R::TN + fn * 16 + (lane >> 4) * 4;
+                if (r < q.M && n < q.N) acc[fn][fm] = *(const f32x4 *)((const float *)q.C + r * b.ldx2 + n);
+            }
+    }
+    multiply_tile<R, BM, BN, false, false>(q, smem, q.K, acc);
+    R::store(q, smem, TileCoord{0, 0, 0}, acc);
+}
+
+// dX from the sums of all pieces, their slices and D's parts added in order:
+// bf16(scale alpha sum), zeros for rows without targets.  A thread per 8
+// columns at a time.
 __global__ void __launch_bounds__(256) k_vocab_dx(VocabArgs p, VocabGrad b)
 {
-    const int64_t chunks = (p.K + 7) / 8, total = p.M * chunks;
+    const int64_t chunks = (p.K + 7) / 8, total = p.M * chunks, plane = p.M * b.ldx2;
     const float a = p.scale * *b.alpha;
     for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
         const int64_t m = at / chunks, col = at % chunks * 8;
         const float *s = b.sums + m * b.ldx2 + col;
-        const f32x4 v0 = *(const f32x4 *)s, v1 = *(const f32x4 *)(s + 4);
+        f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+        const int n = b.slices * b.parts;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            v0 += *(const f32x4 *)(s + i * plane);
+            v1 += *(const f32x4 *)(s + i * plane + 4);
+        }
         u32x4 d = {pack_bf16x2(a * v0[0], a * v0[1]), pack_bf16x2(a * v0[2], a * v0[3]),
                    pack_bf16x2(a * v1[0], a * v1[1]), pack_bf16x2(a * v1[2], a * v1[3])};
         if (!b.has[m]) d = u32x4{0u, 0u, 0u, 0u};
@@ -576,9 +645,7 @@ hipError_t launch_vocab_stats(const VocabArgs &args, int tile, hipStream_t s)
 
 hipError_t launch_vocab_join(const VocabArgs &p, hipStream_t s)
 {
-    int rows = 1;
-    while (rows < 16 && rows < p.M) rows *= 2;
-    hipLaunchKernelGGL(k_vocab_join, dim3((unsigned)((p.M + rows - 1) / rows)), dim3(kJoinThreads), 0, s, p, rows);
+    hipLaunchKernelGGL(k_vocab_join, dim3((unsigned)(p.M < 65536 ? p.M : 65536)), dim3(kJoinWaves * 64), 0, s, p);
     return hipGetLastError();
 }
 
@@ -608,6 +675,16 @@ hipError_t launch_vocab_dw(const VocabArgs &args, const VocabGrad &b, int tile, 
     const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), t(512);
     if (tile == 256) hipLaunchKernelGGL((k_vocab_dw<256, 256, 2, 4>), g, t, 0, s, p, b);
     else hipLaunchKernelGGL((k_vocab_dw<128, 128, 4, 2>), g, t, 0, s, p, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_vocab_sums(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
+{
+    VocabArgs p = args;
+    tiles_of(p, p.M * b.parts, b.ldx2, tile);
+    const dim3 g((unsigned)(b.slices * p.tiles_m * p.tiles_n)), t(512);
+    if (tile == 256) hipLaunchKernelGGL((k_vocab_sums<256, 256, 2, 4>), g, t, 0, s, p, b);
+    else hipLaunchKernelGGL((k_vocab_sums<128, 128, 4, 2>), g, t, 0, s, p, b);
     return hipGetLastError();
 }
 

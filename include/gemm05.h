@@ -794,7 +794,8 @@ int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, in
  * are formed piece by piece of the vocabulary, the logits anew from X and Wt.
  * D meets the matrix cores in bf16, relative to the largest |dloss| (so a weight
  * common to all rows is not rounded): gradients are off by up to 2^-8 of the sum
- * of their terms' sizes beside their own rounding; sums are FP32.  Rows whose
+ * of their terms' sizes beside their own rounding (up to 64 rows as two bf16
+ * parts: 2^-16); sums are FP32.  Rows whose
  * |dloss| is less than 2^-100 of the largest may lose their smallest terms
  * (what is below 2^-126 beside it counts as 0).
  *

@@ -100,9 +100,10 @@ class Case:
         p = torch.exp(l - lse) * some[:, None]
         d = g * (p - q)
         # exp's argument: the logit's sums, and roundings of its parts; the
-        # exponential itself; q's rounding; D's one rounding to bf16 (half a step)
+        # exponential itself; q's rounding; D's one rounding to bf16 (half a
+        # step), or up to 64 rows a second one of the first one's rest
         ed = g * (p * torch.expm1(el + 2.0 ** -21 * (l.abs() + lse.abs()) + 2.0 ** -20) + 2.0 ** -19 * q)
-        ed = ed + (2.0 ** -8 + 2.0 ** -20) * (d.abs() + ed)
+        ed = ed + ((2.0 ** -8 if self.M > 64 else 2.0 ** -16) + 2.0 ** -20) * (d.abs() + ed)
         # Below the normal numbers of FP32 and bf16, 2^-126, an exponential, a
         # D, a product or a sum may be a zero: each is formed relative to the
         # largest weight, so that many times it per D and per addition.
@@ -110,7 +111,7 @@ class Case:
         ed = ed + least
         x, w = torch.where(some[:, None], self.x.double(), 0.0), self.w.double()
         out = []
-        for a, e, b, n in ((d, ed, w, self.V), (d.t(), ed.t(), x, self.M)):
+        for a, e, b, n in ((d, ed, w, 2 * self.V), (d.t(), ed.t(), x, 2 * self.M)):
             size = a.abs() @ b.abs()
             sums = 1.01 * (n + 8) * 2.0 ** -23 * size + 2 * (n + 8) * least
             out.append((s * (a @ b), s * (e @ b.abs() * (1 + 2.0 ** -10) + sums) + 2.0 ** -126))
