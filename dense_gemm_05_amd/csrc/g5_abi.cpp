@@ -1604,26 +1604,41 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
     pl.rows_b = nt ? N : tn ? rows : K;
     const int64_t cols_b = nt ? K : N;
     pl.batch_b = tn || sB == 0 ? 1 : E;
+    pl.copy_a = g5::row_alignment(a, lda, 0, 1, 2) < 16 || (tn && M % 8 != 0);
+    pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 16 || (!nt && N % 8 != 0);
     const bool stream = nt && lda < (1 << 24) && ldb < (1 << 26);
+    // The projection of few rows streams the weights past them.  Measured,
+    // stream against 128-row tiles: 64 experts of 1536 x 4096, 8 rows each
+    // 142 / 143 us, 16 rows 186 / 149; 8 of 12288 x 4096, 8 rows 146 / 146, 16
+    // rows 174 / 161.  Where there are too few tiles for the CUs it carries
+    // further (one of 4096 x 4096, 128 rows: 25 / 36), and where the tiles would
+    // need the weights copied to aligned rows (16 of 1540 x 4100, 63 rows each:
+    // 84 / 177, 125 rows: 130 / 254).
+    const bool stream_far = E * g5::cdiv(N, 128) < 2 * g5::kNumCU || pl.copy_b;
+    // Tiles of 256 rows: 64 experts of 1536 x 4096, 64 rows each 206 us against
+    // 208, 128 rows 205 / 245; 8 of 12288 x 4096, 64 rows 206 / 170, 128 rows
+    // 211 / 241; the input gradient to 4096 columns, 64 rows each 167 / 196,
+    // 16 rows 144 / 150 (64 x 512 x 512, 64 rows: 17 / 14, too few tiles).
     const char *force = std::getenv("GEMM_FORCE_CONFIG");
     if (force && *force) {
         const int id = g5::find_config_by_name(force);
         if (id == g5::CFG_BF16_256x256) pl.tile = g5::GROUPED_256;
-        else if (id == g5::CFG_DECODE_NT && stream) pl.tile = g5::GROUPED_STREAM;
+        else if (id == g5::CFG_DECODE_NT && stream) pl.tile = rows <= 16 * E ? g5::GROUPED_STREAM : g5::GROUPED_STREAM_64;
         else if (id != g5::CFG_BF16_128x128) return GEMM_ERR_UNSUPPORTED;
-    } else if (stream && rows <= 32 * E) {
-        pl.tile = g5::GROUPED_STREAM;
+    } else if (stream && rows <= (stream_far ? 128 : 8) * E) {
+        pl.tile = rows <= 16 * E ? g5::GROUPED_STREAM : g5::GROUPED_STREAM_64;
     } else if (tn ? E * g5::cdiv(M, 256) * g5::cdiv(N, 256) >= g5::kNumCU
-                  : rows >= 256 * E && g5::cdiv(rows, 256) * g5::cdiv(N, 256) >= g5::kNumCU) {
+                  : rows >= (nt ? 96 : 32) * E && (E + rows / 256) * g5::cdiv(N, 256) >= g5::kNumCU) {
         pl.tile = g5::GROUPED_256;
     }
     if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
-    if (pl.tile == g5::GROUPED_STREAM) return GEMM_OK;
+    if (pl.tile == g5::GROUPED_STREAM || pl.tile == g5::GROUPED_STREAM_64) {
+        pl.copy_a = pl.copy_b = false;
+        return GEMM_OK;
+    }
     // The ring tiles copy whole 16-byte chunks: rows that start elsewhere, or
     // that end inside a chunk where the chunk runs across the summed axis,
     // are copied to padded ones first.
-    pl.copy_a = g5::row_alignment(a, lda, 0, 1, 2) < 16 || (tn && M % 8 != 0);
-    pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 16 || (!nt && N % 8 != 0);
     pl.lda2 = pl.copy_a ? (pl.cols_a + 7) / 8 * 8 : lda;
     pl.ldb2 = pl.copy_b ? (cols_b + 7) / 8 * 8 : ldb;
     // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 64

@@ -63,8 +63,9 @@ struct GroupTile {
 __device__ __forceinline__ bool find_tile(const GroupedArgs &p, int bm, GroupTile &t)
 {
     int total = 0, floor = 0;
+    GroupLanes g{};
     for (int base = 0; base < p.E; base += 64) {
-        const GroupLanes g = scan_groups(p, base, bm, floor);
+        g = scan_groups(p, base, bm, floor);
         total += __builtin_amdgcn_readlane(g.tiles, 63);
     }
     const int64_t all = (int64_t)total * p.tiles_n;
@@ -75,7 +76,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs &p, int bm, GroupTil
     int before = 0;
     floor = 0;
     for (int base = 0; base < p.E; base += 64) {
-        const GroupLanes g = scan_groups(p, base, bm, floor);
+        if (p.E > 64) g = scan_groups(p, base, bm, floor);
         const uint64_t past = __ballot(before + g.tiles > at);
         if (past) {
             const int lane = __builtin_ctzll(past);
@@ -236,13 +237,25 @@ __device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTil
     }
 }
 
-__global__ void __launch_bounds__(kStreamWaves * 64, 4) k_grouped_stream(GroupedArgs p)
+// MANY: up to 64 rows of a group per workgroup.
+template <bool MANY>
+__global__ void __launch_bounds__(kStreamWaves * 64, MANY ? 2 : 4) k_grouped_stream(GroupedArgs p)
 {
     __shared__ f32x4 red[kStreamWaves][2][64];
     GroupTile t;
-    if (!find_tile(p, kGroupedStreamRows, t)) return;
-    if (t.rows > 16) stream_tile<2, 2>(p, t, red);
-    else stream_tile<1, 3>(p, t, red);
+    if (!find_tile(p, MANY ? 64 : 32, t)) return;
+    if constexpr (MANY) {
+        if (t.rows > 48) {
+            stream_tile<4, 3>(p, t, red);
+            return;
+        }
+        if (t.rows > 32) {
+            stream_tile<3, 3>(p, t, red);
+            return;
+        }
+    }
+    if (t.rows > 16) stream_tile<2, MANY ? 4 : 2>(p, t, red);
+    else stream_tile<1, MANY ? 5 : 3>(p, t, red);
 }
 
 template <int BM, int BN, int WGM, int WGN>
@@ -271,9 +284,13 @@ hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream
     a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
     switch (tile) {
     case GROUPED_STREAM:
+    case GROUPED_STREAM_64: {
         if (kind != GROUPED_NT) return hipErrorInvalidValue;
-        hipLaunchKernelGGL(k_grouped_stream, dim3((unsigned)grid), dim3(kStreamWaves * 64), 0, s, a);
+        const dim3 g((unsigned)grid), b(kStreamWaves * 64);
+        if (tile == GROUPED_STREAM) hipLaunchKernelGGL(k_grouped_stream<false>, g, b, 0, s, a);
+        else hipLaunchKernelGGL(k_grouped_stream<true>, g, b, 0, s, a);
         return hipGetLastError();
+    }
     case GROUPED_128: return launch_kind<128, 128, 4, 2>(kind, a, grid, s);
     case GROUPED_256: return launch_kind<256, 256, 2, 4>(kind, a, grid, s);
     default: return hipErrorInvalidValue;

@@ -79,7 +79,10 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                     voff[r][i] = row >= limit ? 0x80000000u : (uint32_t)(row * ld * 2 + chunk * 16);
                 }
             }
-        const int KT = (int)(K / KSTAGE);
+        // Both operands across K: rows from K on lie past their descriptors and
+        // arrive as zeros, so the last stage may be a partial one.
+        constexpr bool ZEROS = AT && !BT;
+        const int KT = (int)(ZEROS ? (K + KSTAGE - 1) / KSTAGE : K / KSTAGE);
         // (a stage past the last copies the last one again, into a place that
         // is read no more)
         auto copy = [&](int r, int t) {
@@ -193,32 +196,38 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
             if (t < KT) stage(t);
             if (wm == 0) barrier();
         }
-        if (K % KSTAGE != 0) {
-            // what is left of K: chunk by chunk with zeros behind it, once
-            // every copy in flight has landed
+        if (!ZEROS && K % KSTAGE != 0) {
+            // what is left of K: chunk by chunk with zeros behind it, all asked
+            // for first, once every copy in flight has landed
+            const int64_t from = (int64_t)KT * KSTAGE;
+            u32x4 v[2][4];
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int q = tid + 512 * i;
+                    const uint16_t *src = (const uint16_t *)(o ? B : A);
+                    const int64_t ld = o ? p.ldb : p.lda, limit = o ? p.N : p.M;
+                    if (across(!o)) v[o][i] = load_chunk8_bf16(src + (from + (q >> 5)) * ld, 8 * (q & 31), limit, from + (q >> 5) < K, 16);
+                    else v[o][i] = load_chunk8_bf16(src + (q >> 3) * ld, from + 8 * (q & 7), K, (q >> 3) < limit, 16);
+                }
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();
-            const int64_t from = (int64_t)KT * KSTAGE;
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const bool a = o == 0;
-                const uint16_t *src = (const uint16_t *)(a ? A : B);
-                const int64_t ld = a ? p.lda : p.ldb, limit = a ? p.M : p.N;
-                uint16_t *to = smem + o * 2 * BUF;
-                for (int q = tid; q < 256 * 8; q += 512) {
-                    if (across(a)) {
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int q = tid + 512 * i;
+                    uint16_t *to = smem + o * 2 * BUF;
+                    if (across(!o)) {
                         const int k = q >> 5, cc = q & 31;       // chunk of the tile's 32
-                        const int h = a ? (cc >> 3) & 1 : (cc >> 2) & 1;
-                        const int c = a ? (cc >> 4) * 8 + (cc & 7) : (cc >> 3) * 4 + (cc & 3);
-                        const u32x4 v = load_chunk8_bf16(src + (from + k) * ld, 8 * cc, limit, from + k < K, 16);
-                        *(u32x4 *)(to + h * REGION + k * 128 + ((c ^ swz_bn<128>(k)) * 8)) = v;
+                        const int h = o ? (cc >> 2) & 1 : (cc >> 3) & 1;
+                        const int c = o ? (cc >> 3) * 4 + (cc & 3) : (cc >> 4) * 8 + (cc & 7);
+                        *(u32x4 *)(to + h * REGION + k * 128 + ((c ^ swz_bn<128>(k)) * 8)) = v[o][i];
                     } else {
-                        const int row = q >> 3, c = q & 7;
-                        const u32x4 v = load_chunk8_bf16(src + row * ld, from + 8 * c, K, row < limit, 16);
-                        *(u32x4 *)(to + row * 64 + ((c ^ (row & 7)) * 8)) = v;
+                        *(u32x4 *)(to + (q >> 3) * 64 + (((q & 7) ^ ((q >> 3) & 7)) * 8)) = v[o][i];
                     }
                 }
-            }
             __syncthreads();
             read_a(a0, 0, 0);
             read_a(a1, 0, 1);

@@ -268,3 +268,19 @@ def test_gradients_are_the_projection_s():
         got = (grad * step.double()).sum()
         bound = 2 * slack + 1e-5 * (grad.abs() * step.double().abs()).sum()
         assert abs(got - want) <= bound, (float(got), float(want), float(bound))
+
+
+@pytest.mark.parametrize("rows", [1, 31, 63, 65, 100, 128])
+def test_rows_past_a_group_are_zeros(rows):
+    """A weight gradient whose last stage is partial, behind one that leaves
+    NaN and infinities in its place, rows of NaN behind the group."""
+    n = k = 256
+    a, b, o = _case("tn", [rows] * 300, n, k, 15)
+    ref, tol = _formula("tn", a[:3 * rows], b[:3 * rows], o[:4])
+    bad = torch.full((rows * 300, n), NAN, dtype=torch.bfloat16).cuda()
+    ad, bd = a.cuda(), b.cuda()
+    ad[3 * rows:], bd[3 * rows:] = NAN, INF
+    for _ in range(2):
+        _run("tn", bad, bad, o)
+        got = _run("tn", ad, bd, o)
+        _check(got[:3], ref, tol, f"{rows} rows")
