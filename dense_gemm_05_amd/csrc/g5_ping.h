@@ -11,19 +11,19 @@ namespace g5 {
 // M]), masks, accumulators and epilogues.
 //
 // K goes in stages of 64 through two LDS buffers.  A wave multiplies a stage
-// in four phases of 16 MFMAs, a quarter of its tile each: (A0, B0), (A0, B1),
-// (A1, B1), (A1, B0), with A0, A1 its upper and lower 64 rows and B0, B1 its
-// left and right 32 columns.  Before each phase it reads the fragments that
-// this phase or the next one lacks (four or eight) and copies a sixteenth of
-// half an operand's stage.  The waves with the upper rows and those with the
-// lower rows, one of each on every SIMD, are kept half a phase apart by one
-// more barrier at the start: while one feeds the matrix core, the other reads
-// and copies.
+// in two phases of 32 MFMAs: A0, its upper 64 rows, by both halves B0 and B1 of
+// its columns, then A1, its lower 64, by the same.  Before each phase it reads
+// the fragments that the phase lacks (all but A1's, then A1's) and copies its
+// part of the stages ahead.  The waves with the tile's upper rows and those
+// with the lower rows, one of each on every SIMD, are kept half a phase apart
+// by one more barrier at the start: while one feeds the matrix core, the other
+// reads and copies.
 //
-// What a phase read is free behind the next barrier that both groups passed,
-// so the copies of stage t + 2 follow the reads of stage t region by region
-// (A0, B0, B1, A1, in the order of reading) and have six phases to land:
-// vmcnt(12) holds at each point with two copies per phase and wave.
+// What a phase read is free behind the next barrier that both groups passed:
+// the second phase of stage t copies A0, B0 and B1 of stage t + 2 and the first
+// of stage t + 1 A1, each four phases before it is read.  With two copies per
+// region and wave vmcnt(8) says at the end of either phase's copies that the
+// next phase's regions have landed.
 //
 // LDS.  A K-contiguous operand's stage has rows of 128 bytes (a copy
 // instruction moves eight whole lines), 16-byte chunks at chunk ^ (row & 7).
@@ -32,8 +32,11 @@ namespace g5 {
 // the transposing read.
 //
 // Against the ring's 32-deep stages, in which all waves read at once and then
-// multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3108 us
-// (1415 TFLOP/s) for 3550.
+// multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3150 us (1397
+// TFLOP/s; the platform's library without it 3081) for 3550.  Four phases of 16
+// MFMAs 3215, raised wave priority around the MFMAs 1 to 2 % slower, copies
+// ahead of the reads 3 % slower; workgroups that walk over several tiles and
+// copy the next one's first stage under the epilogue 2 to 20 % slower.
 template <bool BT, bool AT>
 struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, AT> {
     using R = RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, AT>;
@@ -132,7 +135,6 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                 }
         };
         auto mma = [&](const bf16x8 (&a)[4][2], const bf16x8 (&b)[2][2], int ha, int hb) {
-            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -141,7 +143,6 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                     for (int i = 0; i < 4; ++i)
                         acc[hb * 2 + j][ha * 4 + i] =
                             __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][q], a[i][q], acc[hb * 2 + j][ha * 4 + i], 0, 0, 0);
-            __builtin_amdgcn_s_setprio(0);
         };
         auto barrier = [&]() {
             __builtin_amdgcn_sched_barrier(0);
@@ -153,38 +154,32 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
         // copies of what the next phase (of either group) reads have landed
         auto landed = [&]() {
             __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(12, 0));
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
             barrier();
         };
 
         if (KT > 0) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int r = 0; r < 4; ++r) copy(r, 0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) copy(r, t);
-            landed();
-            read_a(a0, 0, 0);
+            for (int r = 0; r < 3; ++r) copy(r, 1);
             landed();
             if (wm == 1) barrier();
             auto stage = [&](int t) {
+                read_a(a0, t, 0);
                 read_b(b0, t, 0);
-                copy(0, t + 2);
+                read_b(b1, t, 1);
+                copy(3, t + 1);
                 landed();
                 mma(a0, b0, 0, 0);
-                barrier();
-                read_b(b1, t, 1);
-                copy(1, t + 2);
-                landed();
                 mma(a0, b1, 0, 1);
                 barrier();
                 read_a(a1, t, 1);
+                copy(0, t + 2);
+                copy(1, t + 2);
                 copy(2, t + 2);
                 landed();
                 mma(a1, b1, 1, 1);
-                barrier();
-                read_a(a0, t + 1, 0);
-                copy(3, t + 2);
-                landed();
                 mma(a1, b0, 1, 0);
                 barrier();
             };

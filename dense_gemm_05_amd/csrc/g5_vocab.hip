@@ -80,6 +80,24 @@ struct Staged {
     }
 };
 
+// The targets of a tile's rows that lie in its columns, found by all threads:
+// pair i = tid + NT k (of row i / topk) sets bit k % 64.  Few pairs do, so the
+// scan asks for many at once and what is done with them walks the bits.
+template <int NT, class In>
+__device__ __forceinline__ uint64_t scan_targets(int tid, int pairs, In in)
+{
+    uint64_t bits = 0;
+#pragma unroll 16
+    for (int i = tid, k = 0; i < pairs; i += NT, ++k) bits |= (uint64_t)in(i) << (k & 63);
+    return bits;
+}
+template <int NT, class Do>
+__device__ __forceinline__ void each_target(int tid, int pairs, uint64_t bits, Do act)
+{
+    for (; bits; bits &= bits - 1)
+        for (int i = tid + NT * __builtin_ctzll(bits); i < pairs; i += NT * 64) act(i);
+}
+
 // Forward on the LDS ring.  The tile's epilogue is registers but for the join of
 // the four waves side by side, and tiles that hold a target.
 template <int BM, int BN, int WGM, int WGN>
@@ -135,13 +153,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
     // targets in this tile
     const int64_t first = p.v0 + n0;
     const int pairs = (int)q.M * p.topk;
-    int some = 0;
-#pragma unroll 8
-    for (int i = tid; i < pairs; i += NT) {
-        const int64_t col = target_id(p, m0 * p.topk + i) - first;
-        some |= col >= 0 && col < q.N;
-    }
-    some = __syncthreads_or(some);
+    auto col_of = [&](int i) { return target_id(p, m0 * p.topk + i) - first; };
+    auto in = [&](int64_t col) { return col >= 0 && col < q.N; };
+    const uint64_t bits = scan_targets<NT>(tid, pairs, [&](int i) { return in(col_of(i)); });
+    const int some = __syncthreads_or(bits != 0);
     if (tid < q.M) {
         Stat s = st[tid];
 #pragma unroll
@@ -157,12 +172,11 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         for (int k = 0; k < BM / S::RP; ++k)
             if (k == pass) S::put(acc, L, k, wm, wn, g, li);
         __syncthreads();
-        const int lo = pass * S::RP * p.topk, end = lo + S::RP * p.topk, hi = end < pairs ? end : pairs;
-#pragma unroll 8
-        for (int i = lo + tid; i < hi; i += NT) {
-            const int64_t col = target_id(p, m0 * p.topk + i) - first;
-            if (col >= 0 && col < q.N) p.zt[m0 * p.topk + i] = L[(i / p.topk - pass * S::RP) * S::PITCH + (int)col];
-        }
+        each_target<NT>(tid, pairs, bits, [&](int i) {
+            const int64_t col = col_of(i);
+            const int r = i / p.topk - pass * S::RP;
+            if (in(col) && r >= 0 && r < S::RP) p.zt[m0 * p.topk + i] = L[r * S::PITCH + (int)col];
+        });
     }
 }
 
@@ -467,6 +481,14 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
     float *L = (float *)smem;
     const int pairs = (int)q.M * p.topk;
     const int first = (int)(p.v0 + n0);
+    auto col_of = [&](int i) {
+        const int id = b.ids[m0 * p.topk + i];
+        return id < 0 ? -1 : id - first;
+    };
+    const uint64_t bits = scan_targets<NT>(tid, pairs, [&](int i) {
+        const int col = col_of(i);
+        return col >= 0 && col < q.N;
+    });
     for (int pass = 0; pass < BM / S::RP; ++pass) {
         if (pass * S::RP >= q.M) break;          // uniform
         __syncthreads();
@@ -474,13 +496,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
         for (int k = 0; k < BM / S::RP; ++k)
             if (k == pass) S::put(acc, L, k, wm, wn, g, li);
         __syncthreads();
-        const int lo = pass * S::RP * p.topk, end = lo + S::RP * p.topk, hi = end < pairs ? end : pairs;
-#pragma unroll 8
-        for (int i = lo + tid; i < hi; i += NT) {
-            const int id = b.ids[m0 * p.topk + i], col = id - first;
-            if (id >= 0 && col >= 0 && col < q.N)
-                L[(i / p.topk - pass * S::RP) * S::PITCH + col] -= b.q[m0 * p.topk + i];
-        }
+        each_target<NT>(tid, pairs, bits, [&](int i) {
+            const int col = col_of(i), r = i / p.topk - pass * S::RP;
+            if (col >= 0 && col < q.N && r >= 0 && r < S::RP) L[r * S::PITCH + col] -= b.q[m0 * p.topk + i];
+        });
         __syncthreads();
 #pragma unroll 2
         for (int i = tid; i < S::RP * (BN / 8); i += NT) {
@@ -599,7 +618,7 @@ __global__ void __launch_bounds__(256) k_vocab_dx(VocabArgs p, VocabGrad b)
         const float *s = b.sums + m * b.ldx2 + col;
         f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
         const int n = b.slices * b.parts;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < n; ++i) {
             v0 += *(const f32x4 *)(s + i * plane);
             v1 += *(const f32x4 *)(s + i * plane + 4);
