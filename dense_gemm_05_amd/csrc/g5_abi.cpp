@@ -1800,6 +1800,23 @@ static bool vocab_sizes_ok(const VocabCall &c)
            c.topk <= g5::kVocabMaxTopk;
 }
 
+// The tile with the shorter time: rounds of workgroups (one of 256 rows per CU,
+// two of 128) times what a tile takes beside its stages of 64 and per stage,
+// in us as measured: the logits' 4096 x 131072 x 4096 32 rounds of 98, 3000 x
+// 3000 x 1000 42 in tiles of 128 and 29 in those of 256, 700 x 5000 x 2000 27
+// and 51; dW (`across`) of 131072 x 4096 from 2, 120, 500 and 1000 rows 242,
+// 420, 853 and 1410 in tiles of 128 and 276, 347, 689 and 1101 in those of 256.
+static int vocab_tile(int64_t M, int64_t N, int64_t K, bool across)
+{
+    const double stages = (double)g5::cdiv(K, 64);
+    const int64_t t256 = g5::cdiv(M, 256) * g5::cdiv(N, 256), t128 = g5::cdiv(M, 128) * g5::cdiv(N, 128);
+    const double big = (double)g5::cdiv(t256, g5::kNumCU) * (across ? 8.3 + 1.63 * stages : 6.0 + 1.45 * stages);
+    const double small = t128 <= g5::kNumCU ? 4.0 + 0.75 * stages
+                                            : (double)g5::cdiv(t128, 2 * g5::kNumCU) *
+                                                  (across ? 3.8 + 1.15 * stages : 4.0 + 1.05 * stages);
+    return big < small ? 256 : 128;
+}
+
 static int vocab_plan(const VocabCall &c, VocabPlan &pl)
 {
     pl = VocabPlan();
@@ -1818,7 +1835,7 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         pl.parts = g5::cdiv(c.V, 32);
         if (pl.parts > (int64_t)1 << 23) return GEMM_ERR_UNSUPPORTED;
     } else {
-        if (g5::cdiv(c.M, 256) * g5::cdiv(c.V, 256) >= g5::kNumCU && c.M > 128) pl.tile = 256;
+        pl.tile = vocab_tile(c.M, c.V, c.K, false);
         pl.copy_x = c.grad || align_x < 16;
         // (dX's product reads W's rows in whole 16-byte chunks)
         pl.copy_w = align_w < 16 || (c.grad && c.K % 8 != 0);
@@ -1840,15 +1857,15 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
     }
     if (c.grad) {
         pl.parts_d = c.M <= g5::kVocabSplitRows ? 2 : 1;
-        if (g5::cdiv(pl.piece, 256) * g5::cdiv(c.K, 256) >= g5::kNumCU) pl.tile_w = 256;
-        // dX's output tiles shared out over slices of the tokens until every
-        // CU has one (two of 128), each slice at least 16 stages long
         const int64_t rows = c.M * pl.parts_d;
+        pl.tile_w = vocab_tile(pl.piece, c.K, rows, true);
+        // dX's output tiles shared out over slices of the tokens until every
+        // CU has one (two of 128), each slice at least 256 tokens
         if (rows > 128) pl.tile_x = 256;
         const int64_t tiles = g5::cdiv(rows, pl.tile_x) * g5::cdiv(pl.ld2, pl.tile_x);
         int64_t s = (pl.tile_x == 256 ? 1 : 2) * g5::kNumCU / tiles;
-        if (s > pl.piece / 512) s = pl.piece / 512;
-        s = s > 16 ? 16 : s < 1 ? 1 : s;
+        if (s > pl.piece / 256) s = pl.piece / 256;
+        s = s > 32 ? 32 : s < 1 ? 1 : s;
         pl.per = g5::cdiv(g5::cdiv(pl.piece, s), 32) * 32;
         pl.slices = (int)g5::cdiv(pl.piece, pl.per);
         if (tiles * pl.slices > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;

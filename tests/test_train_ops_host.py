@@ -22,9 +22,10 @@ CR = g5.GEMM_WORKSPACE_COUNTER_BYTES
 
 
 def grouped(kind, **kw):
-    """4 groups, 300 rows: nt and nn [300, 64] by [4, ., .] to 48 columns; tn [300, 48] by [300, 64]."""
+    """4 groups, 600 rows (more than are streamed): nt and nn [600, 64] by [4, ., .] to 48 columns; tn
+    [600, 48] by [600, 64]."""
     tn = kind == 2
-    a = dict(E=4, rows=300, M=48, N=64 if tn else 48, K=64, O=O, A=A, lda=48 if tn else 64, B=B,
+    a = dict(E=4, rows=600, M=48, N=64 if tn else 48, K=64, O=O, A=A, lda=48 if tn else 64, B=B,
              ldb=64 if kind in (0, 2) else 48, sB=64 * 48, C=C, ldc=64 if tn else 48, sC=48 * 64, t=0, ws=None, n=0)
     a.update(kw)
     L = g5.lib()
@@ -66,18 +67,18 @@ def test_grouped_empty_calls_do_nothing():
 def test_grouped_workspace_size():
     n = ctypes.c_uint64(1)
 
-    def size(kind, E=4, rows=300, M=48, N=64, K=64, a=A, lda=64, b=B, ldb=64, sB=4096):
+    def size(kind, E=4, rows=600, M=48, N=64, K=64, a=A, lda=64, b=B, ldb=64, sB=4096):
         st = g5.lib().gemm_grouped_workspace_size(kind, E, rows, M, N, K, a, lda, b, ldb, sB, ctypes.byref(n))
         return st, n.value
 
     assert size(0) == size(1) == size(2) == (OK, 0)
     up = lambda b: -(-b // 256) * 256                                      # noqa: E731
-    assert size(0, a=A + 2) == (OK, CR + up(300 * 64 * 2))
+    assert size(0, a=A + 2) == (OK, CR + up(600 * 64 * 2))
     assert size(0, K=60, ldb=60, sB=64 * 60) == (OK, CR + up(4 * 64 * 64 * 2))
     assert size(1, N=60) == (OK, CR + up(4 * 64 * 64 * 2)) and size(1, N=60, sB=0) == (OK, CR + up(64 * 64 * 2))
-    assert size(2, M=44, N=60) == (OK, CR + up(300 * 48 * 2) + up(300 * 64 * 2))
+    assert size(2, M=44, N=60) == (OK, CR + up(600 * 48 * 2) + up(600 * 64 * 2))
     # the stream takes rows of any alignment
-    assert size(0, rows=128, a=A + 2, b=B + 2) == (OK, 0)
+    assert size(0, rows=512, a=A + 2, b=B + 2) == (OK, 0) and size(0, rows=512, lda=1 << 23, ldb=1 << 25) == (OK, 0)
     assert size(3)[0] == INV and size(0, E=-1)[0] == INV and size(0, rows=0) == (OK, 0)
 
 
