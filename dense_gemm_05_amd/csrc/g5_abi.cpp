@@ -1613,26 +1613,33 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
     // rows 174 / 161.  Where there are too few tiles for the CUs it carries
     // further (one of 4096 x 4096, 128 rows: 25 / 36), and where the tiles would
     // need the weights copied to aligned rows (16 of 1540 x 4100, 63 rows each:
-    // 84 / 177, 125 rows: 130 / 254).
+    // 80 / 177, 125 rows: 97 / 254).
     const bool stream_far = E * g5::cdiv(N, 128) < 2 * g5::kNumCU || pl.copy_b;
     // Tiles of 256 rows: 64 experts of 1536 x 4096, 64 rows each 206 us against
     // 208, 128 rows 205 / 245; 8 of 12288 x 4096, 64 rows 206 / 170, 128 rows
     // 211 / 241; the input gradient to 4096 columns, 64 rows each 167 / 196,
     // 16 rows 144 / 150 (64 x 512 x 512, 64 rows: 17 / 14, too few tiles).
+    // Streams past more than 16 rows in the mean: 64 weight rows a workgroup
+    // read the group's rows half as often as 32 do, where that leaves a
+    // workgroup per CU (16 of 1540 x 4100, 31 rows each 52 us for 64, 125 rows
+    // 97 for 130; one of 4096 x 4096, 128 rows 33 for 26).
+    const int streamed = rows <= 16 * E                               ? g5::GROUPED_STREAM
+                         : E * g5::cdiv(N, 64) >= g5::kNumCU ? g5::GROUPED_STREAM_64x64
+                                                                      : g5::GROUPED_STREAM_64x32;
     const char *force = std::getenv("GEMM_FORCE_CONFIG");
     if (force && *force) {
         const int id = g5::find_config_by_name(force);
         if (id == g5::CFG_BF16_256x256) pl.tile = g5::GROUPED_256;
-        else if (id == g5::CFG_DECODE_NT && stream) pl.tile = rows <= 16 * E ? g5::GROUPED_STREAM : g5::GROUPED_STREAM_64;
+        else if (id == g5::CFG_DECODE_NT && stream) pl.tile = streamed;
         else if (id != g5::CFG_BF16_128x128) return GEMM_ERR_UNSUPPORTED;
     } else if (stream && rows <= (stream_far ? 128 : 8) * E) {
-        pl.tile = rows <= 16 * E ? g5::GROUPED_STREAM : g5::GROUPED_STREAM_64;
+        pl.tile = streamed;
     } else if (tn ? E * g5::cdiv(M, 256) * g5::cdiv(N, 256) >= g5::kNumCU
                   : rows >= (nt ? 96 : 32) * E && (E + rows / 256) * g5::cdiv(N, 256) >= g5::kNumCU) {
         pl.tile = g5::GROUPED_256;
     }
     if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
-    if (pl.tile == g5::GROUPED_STREAM || pl.tile == g5::GROUPED_STREAM_64) {
+    if (pl.tile != g5::GROUPED_128 && pl.tile != g5::GROUPED_256) {
         pl.copy_a = pl.copy_b = false;
         return GEMM_OK;
     }

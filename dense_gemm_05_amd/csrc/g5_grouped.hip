@@ -185,33 +185,36 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
 // groups' weights once, so a workgroup owns 32 weight rows of one group,
 // streamed from HBM into the matrix core by four waves on contiguous pieces of
 // K, and up to 32 of the group's rows.
-constexpr int kStreamWaves = 4, kStreamCols = 32;
+constexpr int kStreamWaves = 4;
 
-template <int NC, int D>
-__device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTile &t, f32x4 (&red)[kStreamWaves][2][64])
+// NC chunks of 16 of the group's rows, RB blocks of 16 weight rows, D steps of
+// 64 of K in flight.
+template <int NC, int RB, int D>
+__device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTile &t, f32x4 (&red)[kStreamWaves][RB][64])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, li = lane & 15;
-    const int n0 = t.tn * kStreamCols, N = (int)p.N;
+    const int n0 = t.tn * (16 * RB), N = (int)p.N;
     const char *const W = (const char *)p.B + t.group * p.sB * 2;
-    f32x4 acc[2][NC];
+    f32x4 acc[RB][NC];
     bool xok[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         xok[c] = 16 * c + li < t.rows;
-        acc[0][c] = acc[1][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < RB; ++r) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const int K = (int)p.K, steps = (K + 63) / 64;
     const int s0 = steps * wave / kStreamWaves, s1 = steps * (wave + 1) / kStreamWaves;
-    // (rows past N repeat the block's first and are not stored)
-    const char *wbase[2];
-    uint32_t woff[2];
+    // (rows past N repeat the tile's first and are not stored)
+    const char *wbase[RB];
+    uint32_t woff[RB];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < RB; ++r) {
         const int n = n0 + 16 * r < N ? n0 + 16 * r : n0;
         wbase[r] = W + n * p.ldb * 2;
         woff[r] = (uint32_t)(n + li < N ? li : 0) * (uint32_t)(p.ldb * 2) + 16 * g;
     }
-    RowStream<false, 2, NC, D> b;
+    RowStream<false, RB, NC, D> b;
     auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -223,11 +226,11 @@ __device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTil
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         __syncthreads();             // (the chunk before has been read)
-        red[wave][0][lane] = acc[0][c];
-        red[wave][1][lane] = acc[1][c];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) red[wave][r][lane] = acc[r][c];
         __syncthreads();
         // a wave per block of 16 columns adds the waves' parts in order
-        if (wave < 2 && xok[c]) {
+        if (wave < RB && xok[c]) {
             f32x4 s = red[0][wave][lane];
 #pragma unroll
             for (int w = 1; w < kStreamWaves; ++w) s += red[w][wave][lane];
@@ -237,25 +240,28 @@ __device__ __forceinline__ void stream_tile(const GroupedArgs &p, const GroupTil
     }
 }
 
-// MANY: up to 64 rows of a group per workgroup.
-template <bool MANY>
-__global__ void __launch_bounds__(kStreamWaves * 64, MANY ? 2 : 4) k_grouped_stream(GroupedArgs p)
+// 32 weight rows past up to 32 rows of a group.
+__global__ void __launch_bounds__(kStreamWaves * 64, 4) k_grouped_stream(GroupedArgs p)
 {
     __shared__ f32x4 red[kStreamWaves][2][64];
     GroupTile t;
-    if (!find_tile(p, MANY ? 64 : 32, t)) return;
-    if constexpr (MANY) {
-        if (t.rows > 48) {
-            stream_tile<4, 3>(p, t, red);
-            return;
-        }
-        if (t.rows > 32) {
-            stream_tile<3, 3>(p, t, red);
-            return;
-        }
-    }
-    if (t.rows > 16) stream_tile<2, MANY ? 4 : 2>(p, t, red);
-    else stream_tile<1, MANY ? 5 : 3>(p, t, red);
+    if (!find_tile(p, 32, t)) return;
+    if (t.rows > 16) stream_tile<2, 2, 2>(p, t, red);
+    else stream_tile<1, 2, 3>(p, t, red);
+}
+
+// 16 RB weight rows past up to 64.
+template <int RB>
+__global__ void __launch_bounds__(kStreamWaves * 64, 2) k_grouped_stream_many(GroupedArgs p)
+{
+    __shared__ f32x4 red[kStreamWaves][RB][64];
+    GroupTile t;
+    if (!find_tile(p, 64, t)) return;
+    constexpr int D = RB == 4 ? 2 : 3;
+    if (t.rows > 48) stream_tile<4, RB, D>(p, t, red);
+    else if (t.rows > 32) stream_tile<3, RB, D>(p, t, red);
+    else if (t.rows > 16) stream_tile<2, RB, D + 1>(p, t, red);
+    else stream_tile<1, RB, D + 1>(p, t, red);
 }
 
 template <int BM, int BN, int WGM, int WGN>
@@ -284,11 +290,13 @@ hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream
     a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
     switch (tile) {
     case GROUPED_STREAM:
-    case GROUPED_STREAM_64: {
+    case GROUPED_STREAM_64x32:
+    case GROUPED_STREAM_64x64: {
         if (kind != GROUPED_NT) return hipErrorInvalidValue;
         const dim3 g((unsigned)grid), b(kStreamWaves * 64);
-        if (tile == GROUPED_STREAM) hipLaunchKernelGGL(k_grouped_stream<false>, g, b, 0, s, a);
-        else hipLaunchKernelGGL(k_grouped_stream<true>, g, b, 0, s, a);
+        if (tile == GROUPED_STREAM) hipLaunchKernelGGL(k_grouped_stream, g, b, 0, s, a);
+        else if (tile == GROUPED_STREAM_64x32) hipLaunchKernelGGL(k_grouped_stream_many<2>, g, b, 0, s, a);
+        else hipLaunchKernelGGL(k_grouped_stream_many<4>, g, b, 0, s, a);
         return hipGetLastError();
     }
     case GROUPED_128: return launch_kind<128, 128, 4, 2>(kind, a, grid, s);

@@ -237,7 +237,7 @@ hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int 
 // NN and TN, and A's of TN, whole 16-byte chunks long), of any alignment for
 // the stream; C's of any.
 enum GroupedKind { GROUPED_NT = 0, GROUPED_NN = 1, GROUPED_TN = 2 };
-enum GroupedTile { GROUPED_STREAM = 0, GROUPED_128 = 1, GROUPED_256 = 2, GROUPED_STREAM_64 = 3 };
+enum GroupedTile { GROUPED_STREAM = 0, GROUPED_128 = 1, GROUPED_256 = 2, GROUPED_STREAM_64x32 = 3, GROUPED_STREAM_64x64 = 4 };
 constexpr int kGroupedMaxGroups = 4096;
 struct GroupedArgs {
     const uint16_t *A, *B;
@@ -253,9 +253,12 @@ struct GroupedArgs {
 // (the streams: rows of a group per workgroup)
 inline int64_t grouped_tile_m(int tile)
 {
-    return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : tile == GROUPED_STREAM_64 ? 64 : 32;
+    return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : tile == GROUPED_STREAM ? 32 : 64;
 }
-inline int64_t grouped_tile_n(int tile) { return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : 32; }
+inline int64_t grouped_tile_n(int tile)
+{
+    return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : tile == GROUPED_STREAM_64x64 ? 64 : 32;
+}
 // Workgroups: the most tiles that E groups of `rows` rows can have.
 inline int64_t grouped_grid(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int tile)
 {

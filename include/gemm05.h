@@ -716,9 +716,10 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t
  * strideB 0: one weight for every group.  K == 0: C := 0 in the groups' rows.
  * Deterministic, no atomics.
  *
- * E <= 4096, M (rows) < 2^31, other sizes <= 2^30.  With at most 32 rows per
- * group in the mean (M <= 32 E) the projection streams the weights past the
- * rows (any alignment); else rows of A or B that are not 16-byte aligned (and
+ * E <= 4096, M (rows) < 2^31, other sizes <= 2^30.  With few rows per group in
+ * the mean (up to 8, up to 128 where there are few weights or they are not
+ * 16-byte aligned) the projection streams the weights past the rows (any
+ * alignment); else rows of A or B that are not 16-byte aligned (and
  * those whose length is not a multiple of 8 elements, in the gradients: rows
  * of B and of At) are first copied to padded ones in the workspace
  * (gemm_grouped_workspace_size bytes, 0 where no copy is needed; its first
