@@ -1787,9 +1787,9 @@ struct VocabPlan {
     int64_t ld2 = 0;                     // row length of the copies
     int parts_d = 1;                     // of D (gradient)
     int tile_x = 128, tile_w = 128;      // of dX's and dW's products
-    int slices = 1;                      // of a piece's tokens in dX's product
-    int64_t per = 0;                     // tokens in each
-    size_t x2 = 0, w2 = 0, part = 0, zt = 0, d = 0, sums = 0, ids = 0, q = 0, has = 0, weight = 0, alpha = 0, total = 0;
+    int slices = 1, w_slices = 1;        // of a piece's tokens in dX's product, of the rows in dW's
+    int64_t per = 0, w_per = 0;          // tokens, rows in each
+    size_t x2 = 0, w2 = 0, part = 0, zt = 0, d = 0, sums = 0, w_sums = 0, ids = 0, q = 0, has = 0, weight = 0, alpha = 0, total = 0;
 };
 struct VocabCall {
     bool grad;
@@ -1836,13 +1836,20 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         at += g5::round256(bytes);
         return here;
     };
-    if (!c.grad && c.M <= g5::kVocabStreamRows && c.ldx < (1 << 24) && c.ldw < (1 << 26)) {
-        pl.tile = 0;
+    const bool stream = c.M <= g5::kVocabStreamRows && c.ldx < (1 << 24) && c.ldw < (1 << 26);
+    const char *force = std::getenv("GEMM_FORCE_CONFIG");
+    int forced = -1;                     // 0: the stream
+    if (force && *force) {
+        const int id = g5::find_config_by_name(force);
+        forced = id == g5::CFG_BF16_256x256 ? 256 : id == g5::CFG_BF16_128x128 ? 128 : id == g5::CFG_DECODE_NT ? 0 : -1;
+        if (forced < 0 || (forced == 0 && !stream)) return GEMM_ERR_UNSUPPORTED;
+    }
+    pl.tile = forced >= 0 ? forced : stream ? 0 : vocab_tile(c.M, c.V, c.K, false);
+    if (!c.grad && pl.tile == 0) {
         pl.piece = c.V;
         pl.parts = g5::cdiv(c.V, 32);
         if (pl.parts > (int64_t)1 << 23) return GEMM_ERR_UNSUPPORTED;
     } else {
-        pl.tile = vocab_tile(c.M, c.V, c.K, false);
         pl.copy_x = c.grad || align_x < 16;
         // (dX's product reads W's rows in whole 16-byte chunks)
         pl.copy_w = align_w < 16 || (c.grad && c.K % 8 != 0);
@@ -1857,25 +1864,36 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         if (c.grad && rows > ((int64_t)1 << 29) / ldw) rows = ((int64_t)1 << 29) / ldw;
         if (rows < c.V) rows = rows < 256 ? 256 : rows / 256 * 256;
         pl.piece = rows < c.V ? rows : c.V;
-        pl.parts = g5::cdiv(c.V, pl.tile);
-        if (g5::cdiv(c.M, pl.tile) * g5::cdiv(pl.piece, pl.tile) > (int64_t)1 << 22 ||
+        pl.parts = pl.tile ? g5::cdiv(c.V, pl.tile) : 0;
+        if (g5::cdiv(c.M, 128) * g5::cdiv(pl.piece, 128) > (int64_t)1 << 22 ||
             g5::cdiv(pl.piece, 128) * g5::cdiv(c.K, 128) > (int64_t)1 << 22)
             return GEMM_ERR_UNSUPPORTED;
     }
     if (c.grad) {
         pl.parts_d = c.M <= g5::kVocabSplitRows ? 2 : 1;
         const int64_t rows = c.M * pl.parts_d;
-        pl.tile_w = vocab_tile(pl.piece, c.K, rows, true);
-        // dX's output tiles shared out over slices of the tokens until every
-        // CU has one (two of 128), each slice at least 256 tokens
-        if (rows > 128) pl.tile_x = 256;
-        const int64_t tiles = g5::cdiv(rows, pl.tile_x) * g5::cdiv(pl.ld2, pl.tile_x);
-        int64_t s = (pl.tile_x == 256 ? 1 : 2) * g5::kNumCU / tiles;
-        if (s > pl.piece / 256) s = pl.piece / 256;
-        s = s > 32 ? 32 : s < 1 ? 1 : s;
-        pl.per = g5::cdiv(g5::cdiv(pl.piece, s), 32) * 32;
+        pl.tile_w = forced > 0 ? forced : vocab_tile(pl.piece, c.K, rows, true);
+        pl.tile_x = forced > 0 ? forced : rows > 128 ? 256 : 128;
+        // Output tiles shared out over slices of the summed axis until every
+        // CU has one (two of 128): dX's, as many as 64 of at least 256 tokens,
+        // and dW's, as many as 16 of at least 512 rows, while the planes of
+        // sums stay within a quarter of the Infinity Cache.
+        const auto slots = [](int tile) { return (tile == 256 ? 1 : 2) * (int64_t)g5::kNumCU; };
+        const auto slices = [](int64_t most, int64_t tiles, int64_t slots, int64_t len, int64_t least, double plane) {
+            int64_t s = slots / tiles;
+            if (s > len / least) s = len / least;
+            if (plane * s > (1 << 26)) s = (int64_t)((1 << 26) / plane);
+            return s > most ? most : s < 1 ? 1 : s;
+        };
+        const int64_t tiles_x = g5::cdiv(rows, pl.tile_x) * g5::cdiv(pl.ld2, pl.tile_x);
+        const int64_t sx = slices(64, tiles_x, slots(pl.tile_x), pl.piece, 256, 4.0 * rows * pl.ld2);
+        pl.per = g5::cdiv(g5::cdiv(pl.piece, sx), 32) * 32;
         pl.slices = (int)g5::cdiv(pl.piece, pl.per);
-        if (tiles * pl.slices > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
+        const int64_t tiles_w = g5::cdiv(pl.piece, pl.tile_w) * g5::cdiv(c.K, pl.tile_w);
+        const int64_t sw = slices(16, tiles_w, slots(pl.tile_w), rows, 512, 4.0 * pl.piece * pl.ld2);
+        pl.w_per = g5::cdiv(g5::cdiv(rows, sw), 64) * 64;
+        pl.w_slices = (int)g5::cdiv(rows, pl.w_per);
+        if (tiles_x * pl.slices > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
     }
     if (pl.copy_x) pl.x2 = take((size_t)c.M * pl.parts_d * pl.ld2 * 2);
     if (pl.copy_w) pl.w2 = take((size_t)pl.piece * pl.ld2 * 2);
@@ -1885,6 +1903,7 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
     } else {
         pl.d = take((size_t)c.M * pl.parts_d * ((pl.piece + 7) / 8 * 8) * 2);
         pl.sums = take((size_t)pl.slices * c.M * pl.parts_d * pl.ld2 * 4);
+        if (pl.w_slices > 1) pl.w_sums = take((size_t)pl.w_slices * pl.piece * pl.ld2 * 4);
         pl.ids = take((size_t)c.M * c.topk * 4);
         pl.q = take((size_t)c.M * c.topk * 4);
         pl.has = take((size_t)c.M * 4);
@@ -2054,8 +2073,8 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.dw_f32 = ew == 4;
     b.align_dw = g5::row_alignment((uint64_t)dW, lddw, 0, 1, ew);
     b.ldx2 = (c.K + 7) / 8 * 8;
-    b.rows_at_once = 32;
-    b.parts = 1;
+    b.rows_at_once = b.w_per = 64;
+    b.parts = b.w_slices = 1;
     if (c.M == 0) {                  // the empty sum
         a.V = c.V;
         return g5::launch_vocab_dw(a, b, 128, s) == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
@@ -2075,10 +2094,13 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.sums = (float *)(ws + pl.sums);
     b.slices = pl.slices;
     b.per = pl.per;
+    b.w_slices = pl.w_slices;
+    b.w_per = pl.w_per;
+    b.w_sums = (float *)(ws + pl.w_sums);
     const int64_t widest = b.ldd > b.ldx2 ? b.ldd : b.ldx2;
     b.rows_at_once = (((int64_t)1 << 29) / widest) / 64 * 64;
     if (g5::launch_vocab_prep(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
-    a.X = b.X2;
+    a.X = b.X2;                       // (the stream's rows of X too: at most kVocabStreamRows of them)
     a.ldx = b.ldx2;
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;

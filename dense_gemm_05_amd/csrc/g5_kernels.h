@@ -246,7 +246,7 @@ struct GroupedArgs {
     int64_t E, rows;                 // rows of A (TN: of A and B)
     int64_t M, N, K;                 // M: TN's output rows; K: the summed axis of NT and NN
     int64_t lda, ldb, sB, ldc, sC;   // sB: B's group stride (NT, NN); sC: C's (TN)
-    int64_t piece;                   // NN, TN: elements of the summed axis at a time, a multiple of 32
+    int64_t piece;                   // NN, TN: elements of the summed axis at a time, a multiple of 64
     int align_c, out_f32;
     int64_t tiles_m, tiles_n, group_m;   // (set by the launch)
 };
@@ -312,9 +312,13 @@ struct VocabGrad {
     void *dW;
     int64_t lddw;
     int dw_f32, align_dw;
-    int64_t rows_at_once;               // a multiple of 32
+    int64_t rows_at_once;               // a multiple of 64
+    int w_slices;                       // of the rows in dW's product
+    int64_t w_per;                      // rows in each, a multiple of 64
+    float *w_sums;                      // w_slices > 1: [w_slices, V of the piece, ldx2]
 };
-// tile: 256, 128, or 0 for the stream (its parts are 32 columns wide)
+// tile: 256, 128, or 0 for the stream of up to kVocabStreamRows rows (its parts
+// are 32 columns wide; D in two parts)
 hipError_t launch_vocab_stats(const VocabArgs &a, int tile, hipStream_t s);
 hipError_t launch_vocab_join(const VocabArgs &a, hipStream_t s);
 hipError_t launch_vocab_prep(const VocabArgs &a, const VocabGrad &b, hipStream_t s);

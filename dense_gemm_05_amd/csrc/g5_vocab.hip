@@ -98,7 +98,7 @@ __device__ __forceinline__ void each_target(int tid, int pairs, uint64_t bits, D
         for (int i = tid + NT * __builtin_ctzll(bits); i < pairs; i += NT * 64) act(i);
 }
 
-// Forward on the LDS ring.  The tile's epilogue is registers but for the join of
+// Forward by tiles.  The tile's epilogue is registers but for the join of
 // the four waves side by side, and tiles that hold a target.
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
@@ -180,13 +180,16 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
     }
 }
 
-// Forward for up to 32 rows: bound by reading the weight once, so a workgroup
-// owns 32 rows of it, streamed from HBM into the matrix core by four waves on
-// contiguous pieces of K.
+// Up to 32 rows: bound by reading the weight once, so a workgroup owns 32 rows
+// of it, streamed from HBM into the matrix core by four waves on contiguous
+// pieces of K, and one wave joins them: forward the statistics and the targets'
+// logits, GRAD the rows' D, in two bf16 parts.  One row of 4096 by 32768 tokens
+// 42.7 us (6.3 TB/s), 16 of 2048 by 128003 100 us (5.2); D of 3 rows of 3712
+// by 1302 tokens 12 us for 34 in tiles of 128.
 constexpr int kVocabWaves = 4, kVocabCols = 32;
 
-template <int NC, int D>
-__global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs p)
+template <int NC, int D, bool GRAD>
+__global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs p, VocabGrad b)
 {
     __shared__ f32x4 red[kVocabWaves][2][64];
     __shared__ float tile[kVocabCols][17];
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
         wbase[r] = (const char *)(p.W + n * p.ldw);
         woff[r] = (uint32_t)(n + li < p.V ? li : 0) * (uint32_t)(p.ldw * 2) + 16 * g;
     }
-    RowStream<false, 2, NC, D> b;
+    RowStream<false, 2, NC, D> rows_of_w;
     auto tokens = [&](uint32_t (&xoff)[NC], bool (&ok)[NC]) {
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
             xoff[cc] = (uint32_t)(ok[cc] ? 16 * cc + li : 0) * (uint32_t)(p.ldx * 2) + x_lane<false>(g);
         }
     };
-    b.run(wbase, woff, (const char *)p.X, tokens, s0, s1, K, g, acc);
+    rows_of_w.run(wbase, woff, (const char *)p.X, tokens, s0, s1, K, g, acc);
     const float c = p.scale * kLog2e;
 #pragma unroll
     for (int cc = 0; cc < NC; ++cc) {
@@ -224,36 +227,73 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
         red[wave][1][lane] = acc[1][cc];
         __syncthreads();
         if (wave != 0) continue;
+        const int m = 16 * cc + li, rows = M - 16 * cc < 16 ? M - 16 * cc : 16;
         f32x4 s[2];
-        float top = -__builtin_inff(), sum = 0.f;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             s[r] = red[0][r][lane];
 #pragma unroll
             for (int w = 1; w < kVocabWaves; ++w) s[r] += red[w][r][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (n0 + 16 * r + 4 * g + i >= p.V) s[r][i] = -__builtin_inff();
-                top = fmaxf(top, s[r][i]);
-                tile[16 * r + 4 * g + i][li] = s[r][i];
-            }
         }
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float base = top == -__builtin_inff() ? 0.f : top;
+        if constexpr (GRAD) {
+            const bool some = m < M && b.has[m] != 0;
+            const float lse = some ? b.lse[m] : 0.f, weight = some ? b.weight[m] : 0.f;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (s[r][i] - base));
-        sum += __shfl_xor(sum, 16, 64);
-        sum += __shfl_xor(sum, 32, 64);
-        if (g == 0 && 16 * cc + li < M) p.part[(16 * cc + li) * p.parts + blockIdx.x] = float2{top, sum};
-        // (one wave writes and reads the tile: in order)
-        __builtin_amdgcn_wave_barrier();
-        const int rows = M - 16 * cc < 16 ? M - 16 * cc : 16;
-        for (int i = lane; i < rows * p.topk; i += 64) {
-            const int64_t at = (int64_t)16 * cc * p.topk + i, col = target_id(p, at) - n0;
-            if (col >= 0 && col < kVocabCols && n0 + col < p.V) p.zt[at] = tile[col][i / p.topk];
+                for (int i = 0; i < 4; ++i)
+                    tile[16 * r + 4 * g + i][li] = __builtin_amdgcn_exp2f(kLog2e * __builtin_fmaf(p.scale, s[r][i], -lse));
+            // (one wave writes and reads the tile: in order)
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 8
+            for (int i = lane; i < rows * p.topk; i += 64) {
+                const int64_t at = (int64_t)16 * cc * p.topk + i;
+                const int id = b.ids[at], col = id - (int)(p.v0 + n0);
+                if (id >= 0 && col >= 0 && col < kVocabCols) tile[col][i / p.topk] -= b.q[at];
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int64_t n = n0 + 16 * r + 4 * g;
+                if (m >= M || n >= b.ldd) continue;      // (columns from V on are padding)
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = some ? weight * tile[16 * r + 4 * g + i][li] : 0.f;
+                const u32x2 d = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                const u32x2 rest = {pack_bf16x2(v[0] - bf16_lo(d[0]), v[1] - bf16_hi(d[0])),
+                                    pack_bf16x2(v[2] - bf16_lo(d[1]), v[3] - bf16_hi(d[1]))};
+                *(u32x2 *)(b.D + m * b.ldd + n) = d;
+                *(u32x2 *)(b.D + (M + m) * b.ldd + n) = rest;
+            }
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            float top = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (n0 + 16 * r + 4 * g + i >= p.V) s[r][i] = -__builtin_inff();
+                    top = fmaxf(top, s[r][i]);
+                    tile[16 * r + 4 * g + i][li] = s[r][i];
+                }
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float base = top == -__builtin_inff() ? 0.f : top;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (s[r][i] - base));
+            sum += __shfl_xor(sum, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            if (g == 0 && m < M) p.part[m * p.parts + blockIdx.x] = float2{top, sum};
+            // (one wave writes and reads the tile: in order)
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 8
+            for (int i = lane; i < rows * p.topk; i += 64) {
+                const int64_t at = (int64_t)16 * cc * p.topk + i, col = target_id(p, at) - n0;
+                if (col >= 0 && col < kVocabCols && n0 + col < p.V) p.zt[at] = tile[col][i / p.topk];
+            }
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }
@@ -524,45 +564,54 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
 }
 
 // dW rows of a piece: scale alpha D^T X2, summed over the rows in pieces whose
-// 32-bit offsets fit.
+// 32-bit offsets fit.  Few output tiles over many rows: b.w_slices parts of the
+// rows, each part's sums as FP32 in a plane of its own (k_vocab_total).
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, VocabGrad b)
 {
     using R = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, false, false, true>;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
-    const TileCoord tc = tile_map(blockIdx.x, 1, p.tiles_m, p.tiles_n, p.group_m);
+    const TileCoord tc = tile_map(blockIdx.x, b.w_slices, p.tiles_m, p.tiles_n, p.group_m);
     const int64_t m0 = tc.tm * BM, n0 = tc.tn * BN;          // vocabulary, hidden
+    const int64_t all = p.M * b.parts;
+    const int64_t from = tc.b * b.w_per < all ? tc.b * b.w_per : all, to = all - from < b.w_per ? all : from + b.w_per;
     GemmArgs q{};
-    q.A = b.D + m0;
-    q.B = b.X2 + n0;
-    q.C = (char *)b.dW + ((p.v0 + m0) * b.lddw + n0) * (b.dw_f32 ? 4 : 2);
+    if (b.w_slices == 1) {
+        q.C = (char *)b.dW + ((p.v0 + m0) * b.lddw + n0) * (b.dw_f32 ? 4 : 2);
+        q.ldc = b.lddw;
+        q.align_c = b.align_dw;
+        q.out_f32 = b.dw_f32;
+    } else {
+        q.C = b.w_sums + (tc.b * p.V + m0) * b.ldx2 + n0;
+        q.ldc = b.ldx2;
+        q.align_c = 16;
+        q.out_f32 = 1;
+    }
     q.lda = b.ldd;
     q.ldb = b.ldx2;
-    q.ldc = b.lddw;
     q.align_a = q.align_b = 16;
-    q.align_c = b.align_dw;
-    q.out_f32 = b.dw_f32;
     q.M = p.V - m0 < BM ? p.V - m0 : BM;
     q.N = b.ldx2 - n0 < BN ? b.ldx2 - n0 : BN;               // (whole padded chunks)
     f32x4 acc[R::FN][R::FM];
     R::zero(acc);
-    const int64_t rows = p.M * b.parts;
-    for (int64_t done = 0; done < rows;) {
-        q.K = rows - done < b.rows_at_once ? rows - done : b.rows_at_once;
-        if (done > 0) __syncthreads();
-        multiply_tile<R, BM, BN, false, true>(q, smem, q.K, acc);
-        done += q.K;
+    for (int64_t done = from; done < to;) {
         q.A = b.D + m0 + done * b.ldd;
         q.B = b.X2 + n0 + done * b.ldx2;
+        q.K = to - done < b.rows_at_once ? to - done : b.rows_at_once;
+        if (done > from) __syncthreads();
+        multiply_tile<R, BM, BN, false, true>(q, smem, q.K, acc);
+        done += q.K;
     }
-    const float a = rows > 0 ? p.scale * *b.alpha : 0.f;
+    if (b.w_slices == 1) {
+        const float a = all > 0 ? p.scale * *b.alpha : 0.f;
 #pragma unroll
-    for (int fn = 0; fn < R::FN; ++fn)
+        for (int fn = 0; fn < R::FN; ++fn)
 #pragma unroll
-        for (int fm = 0; fm < R::FM; ++fm)
+            for (int fm = 0; fm < R::FM; ++fm)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[fn][fm][i] *= a;
-    q.N = p.K - n0 < BN ? p.K - n0 : BN;
+                for (int i = 0; i < 4; ++i) acc[fn][fm][i] *= a;
+        q.N = p.K - n0 < BN ? p.K - n0 : BN;
+    }
     R::store(q, smem, TileCoord{0, 0, 0}, acc);
 }
 
@@ -606,42 +655,63 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, Vo
     R::store(q, smem, TileCoord{0, 0, 0}, acc);
 }
 
-// dX from the sums of all pieces, their slices and D's parts added in a fixed
-// order: bf16(scale alpha sum), zeros for rows without targets.  SHARE threads
-// per 8 columns, each with every SHARE-th slice: four where the columns alone
-// would leave most CUs idle over many slices (20 x 300, 50 slices 6.3 us for
-// 11.0; 4096 x 4096, one slice 42 for 22).
+// dX or a piece's dW from planes of FP32 sums, added in a fixed order: scale
+// alpha sum, rounded to the output's type; zeros for rows that `has` leaves out.
+// SHARE threads per 8 columns, each with every SHARE-th plane: more than one
+// where the columns alone would leave most CUs idle over many planes (20 x 300
+// from 50 planes 6.3 us with four, 11.0 with one; 4096 x 4096 from one 42 and
+// 22).
+struct Total {
+    const float *sums;
+    const int32_t *has;          // or NULL
+    void *out;
+    int64_t rows, cols, ld, ldo, plane;
+    int planes, out_f32;
+    const float *alpha;
+    float scale;
+};
 template <int SHARE>
-__global__ void __launch_bounds__(256) k_vocab_dx(VocabArgs p, VocabGrad b)
+__global__ void __launch_bounds__(256) k_vocab_total(Total t)
 {
-    const int64_t chunks = (p.K + 7) / 8, total = p.M * chunks, plane = p.M * b.ldx2;
-    const float a = p.scale * *b.alpha;
-    const int share = threadIdx.x % SHARE, n = b.slices * b.parts;
+    const int64_t chunks = (t.cols + 7) / 8, total = t.rows * chunks;
+    const float a = t.scale * *t.alpha;
+    const int share = threadIdx.x % SHARE;
     for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / SHARE; at < total; at += (int64_t)gridDim.x * (256 / SHARE)) {
         const int64_t m = at / chunks, col = at % chunks * 8;
-        const float *s = b.sums + m * b.ldx2 + col;
+        const float *s = t.sums + m * t.ld + col;
         f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 8
-        for (int i = share; i < n; i += SHARE) {
-            v[0] += *(const f32x4 *)(s + i * plane);
-            v[1] += *(const f32x4 *)(s + i * plane + 4);
+        for (int i = share; i < t.planes; i += SHARE) {
+            v[0] += *(const f32x4 *)(s + i * t.plane);
+            v[1] += *(const f32x4 *)(s + i * t.plane + 4);
         }
 #pragma unroll
         for (int o = 1; o < SHARE; o <<= 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j >> 2][j & 3] += __shfl_xor(v[j >> 2][j & 3], o, 64);
         if (share != 0) continue;
-        u32x4 d = {pack_bf16x2(a * v[0][0], a * v[0][1]), pack_bf16x2(a * v[0][2], a * v[0][3]),
-                   pack_bf16x2(a * v[1][0], a * v[1][1]), pack_bf16x2(a * v[1][2], a * v[1][3])};
-        if (!b.has[m]) d = u32x4{0u, 0u, 0u, 0u};
-        uint16_t *out = b.dX + m * b.lddx + col;
-        if (col + 8 <= p.K) {
+        const bool some = !t.has || t.has[m] != 0;
+        float r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = some ? a * v[j >> 2][j & 3] : 0.f;
+        const int64_t to = m * t.ldo + col;
+        const int left = t.cols - col < 8 ? (int)(t.cols - col) : 8;
+        if (t.out_f32) {
+            float *out = (float *)t.out + to;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) out[j] = r[j];
+            continue;
+        }
+        const u32x4 d = {pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]), pack_bf16x2(r[6], r[7])};
+        uint16_t *out = (uint16_t *)t.out + to;
+        if (left == 8) {
             store16(out, d);
             continue;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (col + i < p.K) out[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+            if (i < left) out[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
     }
 }
 
@@ -659,8 +729,8 @@ hipError_t launch_vocab_stats(const VocabArgs &args, int tile, hipStream_t s)
     VocabArgs p = args;
     if (tile == 0) {
         const dim3 g((unsigned)((p.V + kVocabCols - 1) / kVocabCols)), b(kVocabWaves * 64);
-        if (p.M > 16) hipLaunchKernelGGL((k_vocab_stream<2, 2>), g, b, 0, s, p);
-        else hipLaunchKernelGGL((k_vocab_stream<1, 3>), g, b, 0, s, p);
+        if (p.M > 16) hipLaunchKernelGGL((k_vocab_stream<2, 2, false>), g, b, 0, s, p, VocabGrad{});
+        else hipLaunchKernelGGL((k_vocab_stream<1, 3, false>), g, b, 0, s, p, VocabGrad{});
         return hipGetLastError();
     }
     tiles_of(p, p.M, p.V, tile);
@@ -688,6 +758,12 @@ hipError_t launch_vocab_prep(const VocabArgs &p, const VocabGrad &b, hipStream_t
 hipError_t launch_vocab_dlogits(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
 {
     VocabArgs p = args;
+    if (tile == 0) {
+        const dim3 g((unsigned)((p.V + kVocabCols - 1) / kVocabCols)), t(kVocabWaves * 64);
+        if (p.M > 16) hipLaunchKernelGGL((k_vocab_stream<2, 2, true>), g, t, 0, s, p, b);
+        else hipLaunchKernelGGL((k_vocab_stream<1, 3, true>), g, t, 0, s, p, b);
+        return hipGetLastError();
+    }
     tiles_of(p, p.M, p.V, tile);
     const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), t(512);
     if (tile == 256) hipLaunchKernelGGL((k_vocab_dlogits<256, 256, 2, 4>), g, t, 0, s, p, b);
@@ -695,14 +771,30 @@ hipError_t launch_vocab_dlogits(const VocabArgs &args, const VocabGrad &b, int t
     return hipGetLastError();
 }
 
+static hipError_t launch_total(const Total &t, hipStream_t s)
+{
+    const int64_t chunks = t.rows * ((t.cols + 7) / 8);
+    const int share = chunks <= 8192 && t.planes >= 32 ? 16 : chunks <= 32768 && t.planes >= 8 ? 4 : 1;
+    const int64_t groups = (chunks * share + 255) / 256;
+    const dim3 g((unsigned)(groups < 65536 ? groups : 65536)), b(256);
+    if (share == 16) hipLaunchKernelGGL(k_vocab_total<16>, g, b, 0, s, t);
+    else if (share == 4) hipLaunchKernelGGL(k_vocab_total<4>, g, b, 0, s, t);
+    else hipLaunchKernelGGL(k_vocab_total<1>, g, b, 0, s, t);
+    return hipGetLastError();
+}
+
 hipError_t launch_vocab_dw(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
 {
     VocabArgs p = args;
     tiles_of(p, p.V, p.K, tile);
-    const dim3 g((unsigned)(p.tiles_m * p.tiles_n)), t(512);
+    const dim3 g((unsigned)(b.w_slices * p.tiles_m * p.tiles_n)), t(512);
     if (tile == 256) hipLaunchKernelGGL((k_vocab_dw<256, 256, 2, 4>), g, t, 0, s, p, b);
     else hipLaunchKernelGGL((k_vocab_dw<128, 128, 4, 2>), g, t, 0, s, p, b);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || b.w_slices == 1) return e;
+    return launch_total(Total{b.w_sums, nullptr, (char *)b.dW + p.v0 * b.lddw * (b.dw_f32 ? 4 : 2), p.V, p.K, b.ldx2, b.lddw,
+                              p.V * b.ldx2, b.w_slices, b.dw_f32, b.alpha, p.scale},
+                        s);
 }
 
 hipError_t launch_vocab_sums(const VocabArgs &args, const VocabGrad &b, int tile, hipStream_t s)
@@ -717,12 +809,8 @@ hipError_t launch_vocab_sums(const VocabArgs &args, const VocabGrad &b, int tile
 
 hipError_t launch_vocab_dx(const VocabArgs &p, const VocabGrad &b, hipStream_t s)
 {
-    const int64_t chunks = p.M * ((p.K + 7) / 8), share = chunks <= 32768 && b.slices * b.parts >= 8 ? 4 : 1;
-    const int64_t groups = (chunks * share + 255) / 256;
-    const dim3 g((unsigned)(groups < 65536 ? groups : 65536)), t(256);
-    if (share == 4) hipLaunchKernelGGL(k_vocab_dx<4>, g, t, 0, s, p, b);
-    else hipLaunchKernelGGL(k_vocab_dx<1>, g, t, 0, s, p, b);
-    return hipGetLastError();
+    return launch_total(Total{b.sums, b.has, b.dX, p.M, p.K, b.ldx2, b.lddx, p.M * b.ldx2, b.slices * b.parts, 0, b.alpha, p.scale},
+                        s);
 }
 
 }  // namespace g5

@@ -132,7 +132,8 @@ def _close(got, ref, tol, what):
 
 
 SIZES = [(1, 1, 1), (1, 5, 8), (2, 17, 3), (3, 40, 64), (5, 2000, 520), (16, 1000, 100), (17, 33, 65), (32, 300, 72),
-         (33, 300, 72), (64, 128, 32), (130, 515, 136), (257, 257, 31), (1000, 130, 33), (300, 33000, 264)]
+         (33, 300, 72), (64, 128, 32), (130, 515, 136), (257, 257, 31), (1000, 130, 33), (2000, 200, 40),
+         (300, 33000, 264)]
 
 
 @pytest.mark.parametrize("topk", [0, 1, 5, 70])
@@ -144,6 +145,28 @@ def test_loss_and_gradients(M, V, K, topk):
     c.check_forward(loss, lse)
     dx, dw = c.backward(lse)
     c.check_backward(lse, dx, dw)
+
+
+@pytest.mark.parametrize("topk", [0, 7, 256])
+@pytest.mark.parametrize("config", ["bf16_256x256", "bf16_128x128", "decode_nt"])
+@pytest.mark.parametrize("M,V,K", [(1, 40, 8), (20, 300, 65), (32, 513, 256), (70, 260, 129), (600, 1000, 200)])
+def test_every_tile_takes_every_size(monkeypatch, M, V, K, topk, config):
+    if config == "decode_nt" and M > 32:
+        pytest.skip("the stream is for up to 32 rows")
+    monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{config} {M} {V} {K} {topk}")
+    c = Case(M, V, K, topk, seed=5)
+    loss, lse = c.forward(workspace=None)
+    c.check_forward(loss, lse, config)
+    c.check_backward(lse, *c.backward(lse, workspace=None), config)
+
+
+def test_a_tile_that_does_not_fit_is_refused(monkeypatch):
+    c = Case(33, 40, 16)
+    for config in ("decode_nt", "bf16_256x192", "f32_64x64", "no such"):
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+        with pytest.raises(g5.GemmError):
+            c.forward(workspace=None)
 
 
 @pytest.mark.parametrize("topk", [0, 9])
