@@ -1809,18 +1809,26 @@ static bool vocab_sizes_ok(const VocabCall &c)
 
 // The tile with the shorter time: rounds of workgroups (one of 256 rows per CU,
 // two of 128) times what a tile takes beside its stages of 64 and per stage,
-// in us as measured: the logits' 4096 x 131072 x 4096 32 rounds of 98, 3000 x
-// 3000 x 1000 42 in tiles of 128 and 29 in those of 256, 700 x 5000 x 2000 27
-// and 51; dW (`across`) of 131072 x 4096 from 2, 120, 500 and 1000 rows 242,
-// 420, 853 and 1410 in tiles of 128 and 276, 347, 689 and 1101 in those of 256.
-static int vocab_tile(int64_t M, int64_t N, int64_t K, bool across)
+// in us, fitted to the measured (tiles of 128 / 256): the loss's logits of 3594
+// x 4740 x 128 20 / 25, 300 x 100000 x 128 29 / 36, 4096 x 32768 x 512 177 / 135,
+// 700 x 9000 x 700 22 / 27, 3000 x 3000 x 1000 42 / 36; D of the first 24 / 36,
+// of the third 198 / 188; dW of 131072 x 4096 from 2, 120, 500 and 1000 rows 242
+// / 276, 420 / 347, 853 / 689 and 1410 / 1101.
+enum VocabProduct { VOCAB_STATS, VOCAB_D, VOCAB_DW };
+static int vocab_tile(VocabProduct what, int64_t M, int64_t N, int64_t K)
 {
-    const double stages = (double)g5::cdiv(K, 64);
+    struct Cost {
+        double start, tile, stage, rest;     // per kernel, tile, stage of 64, and a K that ends inside one
+    };
+    static const Cost kBig[] = {{8, 4, 1.45, 5}, {8, 9, 1.45, 5}, {0, 8.3, 1.63, 0}};
+    static const Cost kSmall[] = {{6, 2.3, 1.05, 5}, {6, 3.6, 1.05, 5}, {0, 3.8, 1.15, 0}};
+    const double stages = (double)g5::cdiv(K, 64), rest = K % 64 != 0;
     const int64_t t256 = g5::cdiv(M, 256) * g5::cdiv(N, 256), t128 = g5::cdiv(M, 128) * g5::cdiv(N, 128);
-    const double big = (double)g5::cdiv(t256, g5::kNumCU) * (across ? 8.3 + 1.63 * stages : 6.0 + 1.45 * stages);
-    const double small = t128 <= g5::kNumCU ? 4.0 + 0.75 * stages
-                                            : (double)g5::cdiv(t128, 2 * g5::kNumCU) *
-                                                  (across ? 3.8 + 1.15 * stages : 4.0 + 1.05 * stages);
+    const Cost &b = kBig[what], &s = kSmall[what];
+    const double big = b.start + (double)g5::cdiv(t256, g5::kNumCU) * (b.tile + b.stage * stages + b.rest * rest);
+    // (a CU with one tile of 128 goes through it faster than one with two)
+    const double small = s.start + (double)g5::cdiv(t128, 2 * g5::kNumCU) *
+                                       (s.tile + (t128 <= g5::kNumCU ? 0.75 : s.stage) * stages + s.rest * rest);
     return big < small ? 256 : 128;
 }
 
@@ -1844,7 +1852,7 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         forced = id == g5::CFG_BF16_256x256 ? 256 : id == g5::CFG_BF16_128x128 ? 128 : id == g5::CFG_DECODE_NT ? 0 : -1;
         if (forced < 0 || (forced == 0 && !stream)) return GEMM_ERR_UNSUPPORTED;
     }
-    pl.tile = forced >= 0 ? forced : stream ? 0 : vocab_tile(c.M, c.V, c.K, false);
+    pl.tile = forced >= 0 ? forced : stream ? 0 : vocab_tile(c.grad ? VOCAB_D : VOCAB_STATS, c.M, c.V, c.K);
     if (!c.grad && pl.tile == 0) {
         pl.piece = c.V;
         pl.parts = g5::cdiv(c.V, 32);
@@ -1872,7 +1880,7 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
     if (c.grad) {
         pl.parts_d = c.M <= g5::kVocabSplitRows ? 2 : 1;
         const int64_t rows = c.M * pl.parts_d;
-        pl.tile_w = forced > 0 ? forced : vocab_tile(pl.piece, c.K, rows, true);
+        pl.tile_w = forced > 0 ? forced : vocab_tile(VOCAB_DW, pl.piece, c.K, rows);
         pl.tile_x = forced > 0 ? forced : rows > 128 ? 256 : 128;
         // Output tiles shared out over slices of the summed axis until every
         // CU has one (two of 128): dX's, as many as 64 of at least 256 tokens,

@@ -80,15 +80,26 @@ struct Staged {
     }
 };
 
-// The targets of a tile's rows that lie in its columns, found by all threads:
-// pair i = tid + NT k (of row i / topk) sets bit k % 64.  Few pairs do, so the
-// scan asks for many at once and what is done with them walks the bits.
-template <int NT, class In>
-__device__ __forceinline__ uint64_t scan_targets(int tid, int pairs, In in)
+// The targets of a tile's rows that lie in its columns [first, first + cols),
+// found by all threads: pair i = tid + NT k (of row i / topk) sets bit k % 64.
+// Few pairs do, so the scan asks for sixteen ids at once, unconditionally, and
+// what is done with them walks the bits.
+template <int NT, class T>
+__device__ __forceinline__ uint64_t scan_ids(const T *ids, int tid, int pairs, T first, int cols)
 {
     uint64_t bits = 0;
-#pragma unroll 16
-    for (int i = tid, k = 0; i < pairs; i += NT, ++k) bits |= (uint64_t)in(i) << (k & 63);
+    for (int i = tid, k = 0; i < pairs; i += NT * 16, k += 16) {
+        T id[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) id[j] = ids[i + NT * j < pairs ? i + NT * j : i];
+        uint32_t found = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const T col = id[j] - first;
+            found |= (uint32_t)(i + NT * j < pairs & id[j] >= 0 & col >= 0 & col < (T)cols) << j;
+        }
+        bits |= (uint64_t)found << (k & 63);
+    }
     return bits;
 }
 template <int NT, class Do>
@@ -97,6 +108,57 @@ __device__ __forceinline__ void each_target(int tid, int pairs, uint64_t bits, D
     for (; bits; bits &= bits - 1)
         for (int i = tid + NT * __builtin_ctzll(bits); i < pairs; i += NT * 64) act(i);
 }
+
+// They are then listed for the wave that holds the logit, each of whose lanes
+// takes its own, one after the other, out of all its registers.  A tile with
+// more for one wave than the list holds is staged through LDS instead.
+template <class R, int WGM, int WGN>
+struct TargetList {
+    static constexpr int PER = 64;
+    int count[WGM * WGN];
+    uint32_t at[WGM * WGN][PER];         // pair << 16 | row << 8 | column
+
+    __device__ __forceinline__ void clear(int tid)
+    {
+        if (tid < WGM * WGN) count[tid] = 0;
+    }
+    __device__ __forceinline__ void add(int i, int row, int col)
+    {
+        const int w = row / R::TM * WGN + col / R::TN, k = atomicAdd(&count[w], 1);
+        if (k < PER) at[w][k] = (uint32_t)i << 16 | (uint32_t)row << 8 | (uint32_t)col;
+    }
+    __device__ __forceinline__ bool over() const
+    {
+        bool o = false;
+#pragma unroll
+        for (int w = 0; w < WGM * WGN; ++w) o |= count[w] > PER;
+        return o;
+    }
+    // act(place, pair), by all lanes of the wave together: the lane's target
+    // lies in element place % 4 of acc[place / 4 / FM][place / 4 % FM] (place -1:
+    // it has none this time).
+    template <class Do>
+    __device__ __forceinline__ void each(int wave, int lane, Do act) const
+    {
+        const int n = __builtin_amdgcn_readfirstlane(count[wave]);
+        uint64_t mine = 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const uint32_t e = at[wave][k], row = e >> 8 & 255, col = e & 255;
+            mine |= (uint64_t)(lane == (int)(col % 16 / 4 * 16 + row % 16)) << k;
+        }
+        while (__any(mine != 0)) {
+            int place = -1, pair = 0;
+            if (mine) {
+                const uint32_t e = at[wave][__builtin_ctzll(mine)], row = e >> 8 & 255, col = e & 255;
+                mine &= mine - 1;
+                place = (int)((col % R::TN / 16 * R::FM + row % R::TM / 16) * 4 + col % 4);
+                pair = (int)(e >> 16);
+            }
+            act(place, pair);
+        }
+    }
+};
 
 // Forward by tiles.  The tile's epilogue is registers but for the join of
 // the four waves side by side, and tiles that hold a target.
@@ -130,6 +192,16 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
     }
     __syncthreads();
     Stat *st = (Stat *)smem;                       // [WGN][BM]
+    TargetList<R, WGM, WGN> &list = *(TargetList<R, WGM, WGN> *)(st + WGN * BM);
+    static_assert(WGN * BM * sizeof(Stat) + sizeof(list) <= R::LDS_BYTES, "behind the ring");
+    list.clear(tid);
+    // targets in this tile
+    const int64_t first = p.v0 + n0;
+    const int pairs = (int)q.M * p.topk;
+    auto col_of = [&](int i) { return target_id(p, m0 * p.topk + i) - first; };
+    auto in = [&](int64_t col) { return col >= 0 && col < q.N; };
+    const uint64_t bits = p.ids64 ? scan_ids<NT>((const int64_t *)p.ids + m0 * p.topk, tid, pairs, first, (int)q.N)
+                                  : scan_ids<NT>((const int32_t *)p.ids + m0 * p.topk, tid, pairs, (int32_t)first, (int)q.N);
 #pragma unroll
     for (int fm = 0; fm < R::FM; ++fm) {
         float top = -__builtin_inff();
@@ -150,20 +222,27 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         sum += __shfl_xor(sum, 32, 64);
         if (g == 0) st[wn * BM + wm * R::TM + fm * 16 + li] = Stat{top, sum};
     }
-    // targets in this tile
-    const int64_t first = p.v0 + n0;
-    const int pairs = (int)q.M * p.topk;
-    auto col_of = [&](int i) { return target_id(p, m0 * p.topk + i) - first; };
-    auto in = [&](int64_t col) { return col >= 0 && col < q.N; };
-    const uint64_t bits = scan_targets<NT>(tid, pairs, [&](int i) { return in(col_of(i)); });
-    const int some = __syncthreads_or(bits != 0);
+    __syncthreads();
+    each_target<NT>(tid, pairs, bits, [&](int i) {
+        const int64_t col = col_of(i);
+        if (in(col)) list.add(i, i / p.topk, (int)col);
+    });
     if (tid < q.M) {
         Stat s = st[tid];
 #pragma unroll
         for (int w = 1; w < WGN; ++w) s = join_stat(s, st[w * BM + tid], c);
         p.part[(m0 + tid) * p.parts + p.tile0 + tc.tn] = float2{s.top, s.sum};
     }
-    if (!some) return;
+    __syncthreads();
+    if (!list.over()) {
+        list.each(wave, lane, [&](int place, int pair) {
+            float v = 0.f;
+#pragma unroll
+            for (int c = 0; c < R::FN * R::FM * 4; ++c) v = c == place ? acc[c / 4 / R::FM][c / 4 % R::FM][c % 4] : v;
+            if (place >= 0) p.zt[m0 * p.topk + pair] = v;
+        });
+        return;
+    }
     float *L = (float *)smem;
     for (int pass = 0; pass < BM / S::RP; ++pass) {
         __syncthreads();
@@ -487,10 +566,10 @@ __global__ void __launch_bounds__(1024) k_vocab_weights(float *weight, int64_t M
     if (tid == 0) *alpha = a;
 }
 
-// D of a piece: exp(l - lse) in registers, staged as FP32, the targets'
-// weights taken off where they lie, then weighted and rounded to bf16.  With
-// b.parts 2 (few rows) the rounding's rest, as a bf16 of its own, follows in
-// rows M .. 2 M - 1.
+// D of a piece: exp(l - lse) in registers, the targets' weights taken off where
+// they lie, then weighted and rounded to bf16.  Many targets in a tile, and
+// b.parts 2 (few rows: the rounding's rest, as a bf16 of its own, follows in
+// rows M .. 2 M - 1), go through LDS as FP32.
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p, VocabGrad b)
 {
@@ -518,17 +597,51 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
             for (int i = 0; i < 4; ++i)
                 acc[fn][fm][i] = __builtin_amdgcn_exp2f(kLog2e * __builtin_fmaf(p.scale, acc[fn][fm][i], -lse));
     }
-    float *L = (float *)smem;
     const int pairs = (int)q.M * p.topk;
     const int first = (int)(p.v0 + n0);
     auto col_of = [&](int i) {
         const int id = b.ids[m0 * p.topk + i];
         return id < 0 ? -1 : id - first;
     };
-    const uint64_t bits = scan_targets<NT>(tid, pairs, [&](int i) {
-        const int col = col_of(i);
-        return col >= 0 && col < q.N;
-    });
+    auto in = [&](int col) { return col >= 0 && col < q.N; };
+    const uint64_t bits = scan_ids<NT>(b.ids + m0 * p.topk, tid, pairs, (int32_t)first, (int)q.N);
+    __syncthreads();
+    if (b.parts == 1) {
+        TargetList<R, WGM, WGN> &list = *(TargetList<R, WGM, WGN> *)smem;
+        list.clear(tid);
+        __syncthreads();
+        each_target<NT>(tid, pairs, bits, [&](int i) {
+            const int col = col_of(i);
+            if (in(col)) list.add(i, i / p.topk, col);
+        });
+        __syncthreads();
+        if (!list.over()) {
+            list.each(wave, lane, [&](int place, int pair) {
+                const float t = place >= 0 ? b.q[m0 * p.topk + pair] : 0.f;
+#pragma unroll
+                for (int c = 0; c < R::FN * R::FM * 4; ++c) acc[c / 4 / R::FM][c / 4 % R::FM][c % 4] -= c == place ? t : 0.f;
+            });
+#pragma unroll
+            for (int fm = 0; fm < R::FM; ++fm) {
+                const int r = wm * R::TM + fm * 16 + li;
+                const bool some = r < q.M && b.has[m0 + r] != 0;
+                const float w = some ? b.weight[m0 + r] : 0.f;
+#pragma unroll
+                for (int fn = 0; fn < R::FN; ++fn)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[fn][fm][i] = some ? w * acc[fn][fm][i] : 0.f;
+            }
+            __syncthreads();
+            GemmArgs out = q;
+            out.C = b.D + m0 * b.ldd + n0;
+            out.ldc = b.ldd;
+            out.N = b.ldd - n0 < BN ? b.ldd - n0 : BN;       // (padding columns too: whole chunks)
+            out.align_c = 16;
+            R::store(out, smem, TileCoord{0, 0, 0}, acc);
+            return;
+        }
+    }
+    float *L = (float *)smem;
     for (int pass = 0; pass < BM / S::RP; ++pass) {
         if (pass * S::RP >= q.M) break;          // uniform
         __syncthreads();
