@@ -1604,38 +1604,42 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
     pl.rows_b = nt ? N : tn ? rows : K;
     const int64_t cols_b = nt ? K : N;
     pl.batch_b = tn || sB == 0 ? 1 : E;
-    pl.copy_a = g5::row_alignment(a, lda, 0, 1, 2) < 16 || (tn && M % 8 != 0);
-    pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 16 || (!nt && N % 8 != 0);
+    pl.copy_a = g5::row_alignment(a, lda, 0, 1, 2) < 4 || (tn && M % 2 != 0);
+    pl.copy_b = g5::row_alignment(b, ldb, sB, pl.batch_b, 2) < 4 || (!nt && N % 2 != 0);
     const bool stream = nt && lda < (1 << 24) && ldb < (1 << 26);
     // The projection of few rows streams the weights past them.  Measured,
     // stream against 128-row tiles: 64 experts of 1536 x 4096, 8 rows each
-    // 142 / 143 us, 16 rows 186 / 149; 8 of 12288 x 4096, 8 rows 146 / 146, 16
-    // rows 174 / 161.  Where there are too few tiles for the CUs it carries
-    // further (one of 4096 x 4096, 128 rows: 25 / 36), and where the tiles would
-    // need the weights copied to aligned rows (16 of 1540 x 4100, 63 rows each:
-    // 80 / 177, 125 rows: 97 / 254).
-    const bool stream_far = E * g5::cdiv(N, 128) < 2 * g5::kNumCU || pl.copy_b;
-    // Tiles of 256 rows: 64 experts of 1536 x 4096, 64 rows each 206 us against
-    // 208, 128 rows 205 / 245; 8 of 12288 x 4096, 64 rows 206 / 170, 128 rows
-    // 211 / 241; the input gradient to 4096 columns, 64 rows each 167 / 196,
-    // 16 rows 144 / 150 (64 x 512 x 512, 64 rows: 17 / 14, too few tiles).
+    // 140 / 142 us, 16 rows 183 / 148; 16 of them 37 / 37 and 55 / 38.  Where
+    // tiles leave most CUs idle it carries further (one of 4096 x 4096, 125
+    // rows 26 / 37, 200 rows 47 / 36; 4 of 4096 x 1030, 48 rows 14 / 16, 63 rows
+    // 20 / 16; 16 of 700 x 1100, 63 rows 14 / 18, 90 rows 23 / 21), and where
+    // they would need the weights copied (32 of 1001 x 2001, 31 rows 75 / 101,
+    // 48 rows 121 / 104).
+    const int64_t tiles = E * g5::cdiv(N, 128);
+    const int far = tiles <= g5::kNumCU / 4 ? 128 : tiles <= g5::kNumCU / 2 ? 48 : pl.copy_b ? 32 : 8;
     // Streams past more than 16 rows in the mean: 64 weight rows a workgroup
     // read the group's rows half as often as 32 do, where that leaves a
-    // workgroup per CU (16 of 1540 x 4100, 31 rows each 52 us for 64, 125 rows
-    // 97 for 130; one of 4096 x 4096, 128 rows 33 for 26).
+    // workgroup per CU (16 of 1540 x 4100, 31 rows each 52 us for 64; one of
+    // 4096 x 4096, 128 rows 33 for 26).
     const int streamed = rows <= 16 * E                               ? g5::GROUPED_STREAM
                          : E * g5::cdiv(N, 64) >= g5::kNumCU ? g5::GROUPED_STREAM_64x64
                                                                       : g5::GROUPED_STREAM_64x32;
+    // Tiles of 256 rows where they keep most CUs busy (128 / 256): 64 experts
+    // of 1536 x 4096, 48 rows each 195 / 183 us, 90 rows 202 / 191, 125 rows 239
+    // / 195; 8 of 12288 x 4096, 63 rows 169 / 186, 125 rows 241 / 195; 16 of 1540
+    // x 4100, 63 rows 56 / 79, 125 rows 105 / 85; 40 of 512 x 1024, 200 rows 22 /
+    // 25; the input gradient to 4096 columns, 64 rows each 196 / 167, 16 rows
+    // 150 / 144.
     const char *force = std::getenv("GEMM_FORCE_CONFIG");
     if (force && *force) {
         const int id = g5::find_config_by_name(force);
         if (id == g5::CFG_BF16_256x256) pl.tile = g5::GROUPED_256;
         else if (id == g5::CFG_DECODE_NT && stream) pl.tile = streamed;
         else if (id != g5::CFG_BF16_128x128) return GEMM_ERR_UNSUPPORTED;
-    } else if (stream && rows <= (stream_far ? 128 : 8) * E) {
+    } else if (stream && rows <= far * E) {
         pl.tile = streamed;
     } else if (tn ? E * g5::cdiv(M, 256) * g5::cdiv(N, 256) >= g5::kNumCU
-                  : rows >= (nt ? 96 : 32) * E && (E + rows / 256) * g5::cdiv(N, 256) >= g5::kNumCU) {
+                  : rows >= (nt ? 96 : 32) * E && (E + rows / 256) * g5::cdiv(N, 256) >= g5::kNumCU * 5 / 8) {
         pl.tile = g5::GROUPED_256;
     }
     if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
@@ -1643,9 +1647,8 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
         pl.copy_a = pl.copy_b = false;
         return GEMM_OK;
     }
-    // The ring tiles copy whole 16-byte chunks: rows that start elsewhere, or
-    // that end inside a chunk where the chunk runs across the summed axis,
-    // are copied to padded ones first.
+    // The tiles copy dwords: rows that start elsewhere, or that end inside one
+    // where they lie across the summed axis, are copied to padded ones first.
     pl.lda2 = pl.copy_a ? (pl.cols_a + 7) / 8 * 8 : lda;
     pl.ldb2 = pl.copy_b ? (cols_b + 7) / 8 * 8 : ldb;
     // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 64
@@ -1726,6 +1729,8 @@ static int grouped_run(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, 
     a.sB = some ? sB : 0;
     a.ldc = ldc;
     a.sC = sC;
+    a.align_a = pl.copy_a || !some ? 16 : g5::row_alignment((uint64_t)A, lda, 0, 1, 2);
+    a.align_b = pl.copy_b || !some ? 16 : g5::row_alignment((uint64_t)B, ldb, sB, tn ? 1 : E, 2);
     a.align_c = g5::row_alignment((uint64_t)C, ldc, sC, tn ? E : 1, ec);
     a.out_f32 = ec == 4;
     char *ws = (char *)workspace;
@@ -1858,9 +1863,9 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         pl.parts = g5::cdiv(c.V, 32);
         if (pl.parts > (int64_t)1 << 23) return GEMM_ERR_UNSUPPORTED;
     } else {
-        pl.copy_x = c.grad || align_x < 16;
-        // (dX's product reads W's rows in whole 16-byte chunks)
-        pl.copy_w = align_w < 16 || (c.grad && c.K % 8 != 0);
+        pl.copy_x = c.grad || align_x < 4;
+        // (dX's product reads W's rows in whole dwords)
+        pl.copy_w = align_w < 4 || (c.grad && c.K % 2 != 0);
         const int64_t ldw = pl.copy_w ? pl.ld2 : c.ldw;
         if (c.ldx > 1 << 21 || ldw > 1 << 21) return GEMM_ERR_UNSUPPORTED;
         // A piece: D of 2^27 elements (256 MiB, the Infinity Cache's size), the
@@ -1963,6 +1968,7 @@ static g5::VocabArgs vocab_args(const VocabCall &c, const uint16_t *X, const uin
     a.K = c.K;
     a.ldx = c.ldx;
     a.ldw = c.ldw;
+    a.align_x = g5::row_alignment(c.x, c.ldx, 0, 1, 2);
     a.scale = scale;
     a.ids = ids;
     a.ids64 = id_bytes == 8;
@@ -1976,6 +1982,7 @@ static hipError_t vocab_piece(const VocabCall &c, const VocabPlan &pl, char *ws,
                               g5::VocabArgs &a, hipStream_t s)
 {
     a.v0 = v0;
+    a.align_w = pl.copy_w ? 16 : g5::row_alignment(c.w, c.ldw, 0, 1, 2);
     a.V = c.V - v0 < pl.piece ? c.V - v0 : pl.piece;
     a.W = W + v0 * c.ldw;
     a.ldw = c.ldw;
@@ -2023,6 +2030,7 @@ static int vocab_forward(const VocabCall &c, const uint16_t *X, const uint16_t *
             return GEMM_ERR_LAUNCH;
         a.X = X2;
         a.ldx = pl.ld2;
+        a.align_x = 16;
     }
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;
@@ -2095,7 +2103,6 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.weight = (float *)(ws + pl.weight);
     b.alpha = (float *)(ws + pl.alpha);
     b.X2 = (uint16_t *)(ws + pl.x2);
-    b.align_x = g5::row_alignment(c.x, c.ldx, 0, 1, 2);
     b.D = (uint16_t *)(ws + pl.d);
     b.ldd = (pl.piece + 7) / 8 * 8;
     b.parts = pl.parts_d;
@@ -2110,6 +2117,7 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     if (g5::launch_vocab_prep(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
     a.X = b.X2;                       // (the stream's rows of X too: at most kVocabStreamRows of them)
     a.ldx = b.ldx2;
+    a.align_x = 16;
     for (int64_t v0 = 0; v0 < c.V; v0 += pl.piece) {
         if (vocab_piece(c, pl, ws, W, v0, a, s) != hipSuccess) return GEMM_ERR_LAUNCH;
         if (g5::launch_vocab_dlogits(a, b, pl.tile, s) != hipSuccess) return GEMM_ERR_LAUNCH;

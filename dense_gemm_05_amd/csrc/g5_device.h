@@ -731,10 +731,10 @@ struct RingTile {
     const char *Bbat = (const char *)p.B + (tc.b * p.sB + (BT ? kbase : kbase * ldb)) * EB;
     // Byte extents of this batch entry's operands from those bases (reads
     // past them return 0).
-    // (At: the last row is read up to M rounded up to 8, which the host
-    // guarantees is inside the allocation: M % 8 == 0 or padded rows.)
+    // (The range check is per dword.  At: the last row's is M rounded up to
+    // whole dwords; the host guarantees an even M or padded rows.)
     const uint32_t a_bytes = !MASKED ? 0x7fffffffu
-                             : AT    ? (uint32_t)(((p.K - kbase - 1) * lda + ((M + 7) & ~(int64_t)7)) * 2)
+                             : AT    ? (uint32_t)(((p.K - kbase - 1) * lda + ((M + 1) & ~(int64_t)1)) * 2)
                                      : (uint32_t)(((M - 1) * lda + (p.K - kbase)) * (QA ? 2 : EB));
     const uint32_t b_bytes =
         !MASKED ? 0x7fffffffu

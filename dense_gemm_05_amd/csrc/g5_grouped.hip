@@ -120,12 +120,13 @@ __device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uin
     q.lda = p.lda;
     q.ldb = p.ldb;
     q.ldc = p.ldc;
-    q.align_a = q.align_b = 16;
+    q.align_a = p.align_a;
+    q.align_b = p.align_b;
     q.align_c = p.align_c;
     q.out_f32 = p.out_f32;
-    // (rows of B are read in whole 16-byte chunks: the host pads them)
+    // (columns of B in whole dwords: even, or padded by the host)
     const int64_t left = p.N - n0;
-    q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 7) & ~(int64_t)7) : BN;
+    q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 1) & ~(int64_t)1) : BN;
     const TileCoord here{0, 0, 0};
     typename R::Acc acc;
     R::zero(acc);

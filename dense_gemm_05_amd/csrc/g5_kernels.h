@@ -233,9 +233,9 @@ hipError_t launch_lora(int config_id, const GemmArgs &a, const LoraArgs &q, int 
 
 // Products grouped by expert with ragged numbers of rows (g5_grouped.hip):
 // group e's rows are offsets[e] .. offsets[e + 1] - 1 of A and C (NT, NN) or
-// of A and B (TN).  Rows of A and B 16-byte aligned for the ring tiles (B's of
-// NN and TN, and A's of TN, whole 16-byte chunks long), of any alignment for
-// the stream; C's of any.
+// of A and B (TN).  Rows of A and B 4-byte aligned for the tiles (B's of NN and TN,
+// and A's of TN, an even number of elements long), of any alignment for the
+// stream; C's of any.
 enum GroupedKind { GROUPED_NT = 0, GROUPED_NN = 1, GROUPED_TN = 2 };
 enum GroupedTile { GROUPED_STREAM = 0, GROUPED_128 = 1, GROUPED_256 = 2, GROUPED_STREAM_64x32 = 3, GROUPED_STREAM_64x64 = 4 };
 constexpr int kGroupedMaxGroups = 4096;
@@ -247,7 +247,7 @@ struct GroupedArgs {
     int64_t M, N, K;                 // M: TN's output rows; K: the summed axis of NT and NN
     int64_t lda, ldb, sB, ldc, sC;   // sB: B's group stride (NT, NN); sC: C's (TN)
     int64_t piece;                   // NN, TN: elements of the summed axis at a time, a multiple of 64
-    int align_c, out_f32;
+    int align_a, align_b, align_c, out_f32;
     int64_t tiles_m, tiles_n, group_m;   // (set by the launch)
 };
 // (the streams: rows of a group per workgroup)
@@ -280,7 +280,8 @@ constexpr int kVocabStreamRows = 32;    // rows of X up to which the weight is s
 // twice the rows.
 constexpr int kVocabSplitRows = 64;
 struct VocabArgs {
-    const uint16_t *X, *W;              // 16-byte aligned rows for the ring tiles, any for the stream
+    const uint16_t *X, *W;              // 4-byte aligned rows for the tiles, any for the stream
+    int align_x, align_w;               // byte alignment of their rows
     int64_t M, V, K, ldx, ldw;
     int64_t v0, vocab;                  // the piece's first token; all tokens
     float scale;
@@ -299,7 +300,6 @@ struct VocabGrad {
     float *q, *weight, *alpha;          // [M, topk], [M], one
     uint16_t *X2;                       // X with zeros as padding and in rows without targets
     int64_t ldx2;                       // K rounded up to 8
-    int align_x;                        // byte alignment of X's rows
     uint16_t *D;                        // a piece's gradient of the logits
     int64_t ldd;                        // a multiple of 8
     int parts;                          // of D: 1, or 2 behind each other ([2 M, ldd], X2 [2 M, ldx2])

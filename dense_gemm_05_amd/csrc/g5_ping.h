@@ -45,7 +45,11 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
     static_assert(R::LDS_BYTES == 4 * BUF * 2, "two buffers of A and of B");
 
     // Rows of q.A (q.M of them) and columns of q.B (q.N) from the tile's first
-    // on, K summed elements.  The LDS must be free on entry; it is free again
+    // on, K summed elements.  Rows start at any multiple of 4 bytes, which is
+    // what the copies of 16 need (16000 rows in 16 groups by 1540 x 4098 240 us,
+    // 424 with both operands copied to rows of 4104 first); those of an operand
+    // across K have an even length: a copy past the last one's end brings zeros
+    // for the dwords outside.  The LDS must be free on entry; it is free again
     // behind the caller's next barrier.
     __device__ static __forceinline__ void accumulate(const GemmArgs &p, uint16_t *smem, const int64_t K, Acc &acc)
     {
@@ -54,7 +58,7 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
         const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
         const int g = lane >> 4, li = lane & 15;
         const char *A = (const char *)p.A, *B = (const char *)p.B;
-        const uint32_t a_bytes = (uint32_t)((AT ? (p.K - 1) * p.lda + ((p.M + 7) & ~(int64_t)7) : (p.M - 1) * p.lda + p.K) * 2);
+        const uint32_t a_bytes = (uint32_t)((AT ? (p.K - 1) * p.lda + ((p.M + 1) & ~(int64_t)1) : (p.M - 1) * p.lda + p.K) * 2);
         const uint32_t b_bytes = (uint32_t)((BT ? (p.N - 1) * p.ldb + p.K : (p.K - 1) * p.ldb + p.N) * 2);
 
         // Copies: region r of a stage (0: A0, 1: B0, 2: B1, 3: A1) is 16 blocks
@@ -203,8 +207,9 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                     const int q = tid + 512 * i;
                     const uint16_t *src = (const uint16_t *)(o ? B : A);
                     const int64_t ld = o ? p.ldb : p.lda, limit = o ? p.N : p.M;
-                    if (across(!o)) v[o][i] = load_chunk8_bf16(src + (from + (q >> 5)) * ld, 8 * (q & 31), limit, from + (q >> 5) < K, 16);
-                    else v[o][i] = load_chunk8_bf16(src + (q >> 3) * ld, from + 8 * (q & 7), K, (q >> 3) < limit, 16);
+                    const int align = o ? p.align_b : p.align_a;
+                    if (across(!o)) v[o][i] = load_chunk8_bf16(src + (from + (q >> 5)) * ld, 8 * (q & 31), limit, from + (q >> 5) < K, align);
+                    else v[o][i] = load_chunk8_bf16(src + (q >> 3) * ld, from + 8 * (q & 7), K, (q >> 3) < limit, align);
                 }
             __builtin_amdgcn_s_waitcnt(0);
             __syncthreads();

@@ -55,7 +55,8 @@ __device__ __forceinline__ GemmArgs tile_args(const VocabArgs &p, int64_t m0, in
     q.K = p.K;
     q.lda = p.ldx;
     q.ldb = p.ldw;
-    q.align_a = q.align_b = 16;
+    q.align_a = p.align_x;
+    q.align_b = p.align_w;
     return q;
 }
 
@@ -535,7 +536,7 @@ __device__ __forceinline__ float prep_row(const VocabArgs &p, const VocabGrad &b
     if (lane == 0) b.has[m] = some;
     const uint16_t *x = p.X + m * p.ldx;
     for (int64_t col = lane * 8; col < b.ldx2; col += 512) {
-        const u32x4 v = load_chunk8_bf16(x, col, p.K, some, b.align_x);
+        const u32x4 v = load_chunk8_bf16(x, col, p.K, some, p.align_x);
         *(u32x4 *)(b.X2 + m * b.ldx2 + col) = v;
         if (b.parts == 2) *(u32x4 *)(b.X2 + (p.M + m) * b.ldx2 + col) = v;
     }
@@ -772,12 +773,13 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, Vo
     q.B = p.W + k0 * p.ldw + n0;
     q.C = b.sums + (tc.b * rows + m0) * b.ldx2 + n0;
     q.M = rows - m0 < BM ? rows - m0 : BM;
-    q.N = b.ldx2 - n0 < BN ? b.ldx2 - n0 : BN;
+    q.N = p.K - n0 < BN ? p.K - n0 : BN;
     q.K = p.V - k0 < b.per ? p.V - k0 : b.per;
     q.lda = b.ldd;
     q.ldb = p.ldw;
     q.ldc = b.ldx2;
-    q.align_a = q.align_b = q.align_c = 16;
+    q.align_a = q.align_c = 16;
+    q.align_b = p.align_w;
     q.out_f32 = 1;
     f32x4 acc[R::FN][R::FM];
     R::zero(acc);
@@ -793,6 +795,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, Vo
             }
     }
     multiply_tile<R, BM, BN, false, false>(q, smem, q.K, acc);
+    q.N = (q.N + 7) & ~(int64_t)7;                 // whole chunks of the padded rows
     R::store(q, smem, TileCoord{0, 0, 0}, acc);
 }
 

@@ -717,13 +717,13 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t
  * Deterministic, no atomics.
  *
  * E <= 4096, M (rows) < 2^31, other sizes <= 2^30.  With few rows per group in
- * the mean (up to 8, up to 128 where there are few weights or they are not
- * 16-byte aligned) the projection streams the weights past the rows (any
- * alignment); else rows of A or B that are not 16-byte aligned (and
- * those whose length is not a multiple of 8 elements, in the gradients: rows
- * of B and of At) are first copied to padded ones in the workspace
- * (gemm_grouped_workspace_size bytes, 0 where no copy is needed; its first
- * GEMM_WORKSPACE_COUNTER_BYTES are left untouched, so gemm_run's serves).
+ * the mean (up to 8, up to 128 where there are few weights) the projection
+ * streams the weights past the rows, which may have any alignment.  The tiles
+ * take rows that start at multiples of 4 bytes (in the gradients, B's and At's
+ * of an even length besides); others are first copied to padded ones in the
+ * workspace (gemm_grouped_workspace_size bytes, 0 where no copy is needed; its
+ * first GEMM_WORKSPACE_COUNTER_BYTES are left untouched, so gemm_run's
+ * serves).
  * Errors, nothing enqueued: GEMM_ERR_INVALID_ARG for sizes outside these
  * ranges, a c_type other than bf16 and float, strides below the row lengths,
  * negative strides, strideC below C_e's extent, missing or misaligned
@@ -803,8 +803,8 @@ int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, in
  * Deterministic, no atomics; a row's loss does not depend on the other rows'
  * values.  0 <= M <= 2^24, 1 <= V < 2^31 - 256, 1 <= K <= 2^21, topk <= 256.  Up
  * to 32 rows the forward call streams the weight past them.  Rows of any
- * alignment; those that are not 16-byte aligned (gradients: or whose length is
- * not a multiple of 8) are copied, a piece of the vocabulary at a time.  M == 0:
+ * alignment; where that is not a multiple of 4 bytes (gradients: or K is odd)
+ * the weight's are copied, a piece of the vocabulary at a time.  M == 0:
  * dW := 0.  workspace: gemm_linear_loss_workspace_size bytes, 256-byte aligned,
  * as gemm_run's (its counter region zero before and after the call); calls that
  * may overlap in time need workspaces of their own.  Errors, nothing enqueued:

@@ -105,6 +105,34 @@ def test_every_tile_takes_every_size(monkeypatch, kind, config, sizes, n, k):
     _check(_run(kind, a, b, o), *_formula(kind, a, b, o), f"{kind} {config}")
 
 
+def _inside(t, pad, at):
+    """t's rows `pad` elements further apart, `at` elements behind the start of
+    a block that is NaN around them and right behind the last one."""
+    rows, cols = t.reshape(-1, t.shape[-1]).shape
+    block = torch.full((at + rows * (cols + pad) + 64,), NAN, dtype=t.dtype).cuda()
+    strides = (cols + pad, 1) if t.dim() == 2 else (t.shape[1] * (cols + pad), cols + pad, 1)
+    view = block.as_strided(t.shape, strides, at)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("config", ["", "bf16_256x256", "bf16_128x128"])
+@pytest.mark.parametrize("sizes,n,k", [([300, 0, 131, 3], 130, 70), ([90, 257], 268, 196), ([64, 65, 1], 34, 1030), ([200, 70], 93, 71)])
+@pytest.mark.parametrize("pad,at", [(0, 2), (4, 4), (1, 0)])
+def test_rows_of_any_alignment_with_nan_around_them(monkeypatch, kind, config, sizes, n, k, pad, at):
+    """Rows that start at multiples of 2, 4 and 8 bytes and end inside a copy's
+    16 bytes; nothing around them is read into a result."""
+    if config:
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{kind} {config} {sizes} {n} {k} {pad} {at}")
+    a, b, o = _case(kind, sizes, n, k, seed=12)
+    ref, tol = _formula(kind, a, b, o)
+    c = getattr(g5, ENTRY[kind])(_inside(a, pad, at), _inside(b, pad, at), torch.tensor(o, dtype=torch.int32).cuda(),
+                                 workspace=ws())
+    _check(c, ref, tol, f"{kind} {config}")
+
+
 @pytest.mark.parametrize("kind", ["nt", "nn"])
 @pytest.mark.parametrize("sizes,n,k,first,behind", [([3, 0, 4], 40, 64, 2, 5), ([300, 20], 136, 72, 7, 300), ([0, 0], 8, 8, 3, 0)])
 def test_rows_of_no_group_stay(kind, sizes, n, k, first, behind):

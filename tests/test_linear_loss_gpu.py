@@ -161,6 +161,30 @@ def test_every_tile_takes_every_size(monkeypatch, M, V, K, topk, config):
     c.check_backward(lse, *c.backward(lse, workspace=None), config)
 
 
+@pytest.mark.parametrize("topk", [0, 7])
+@pytest.mark.parametrize("config", ["", "bf16_256x256", "bf16_128x128"])
+@pytest.mark.parametrize("M,V,K", [(40, 300, 70), (300, 515, 130), (600, 1001, 1028), (90, 260, 67)])
+@pytest.mark.parametrize("pad,at", [(0, 2), (4, 4), (1, 0)])
+def test_rows_of_any_alignment_with_nan_around_them(monkeypatch, M, V, K, topk, config, pad, at):
+    """Rows that start at multiples of 2, 4 and 8 bytes and end inside a copy's
+    16 bytes; nothing around them is read into a result."""
+    if config:
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{config} {M} {V} {K} {topk} {pad} {at}")
+    c = Case(M, V, K, topk, seed=6)
+
+    def inside(t):
+        block = torch.full((at + t.shape[0] * (K + pad) + 64,), NAN, dtype=t.dtype).cuda()
+        view = block.as_strided(t.shape, (K + pad, 1), at)
+        view.copy_(t)
+        return view
+
+    x, w = inside(c.x), inside(c.w)
+    loss, lse = c.forward(x=x, w=w)
+    c.check_forward(loss, lse, config)
+    c.check_backward(lse, *c.backward(lse, x=x, w=w), config)
+
+
 def test_a_tile_that_does_not_fit_is_refused(monkeypatch):
     c = Case(33, 40, 16)
     for config in ("decode_nt", "bf16_256x192", "f32_64x64", "no such"):

@@ -53,7 +53,8 @@ def test_grouped_refuses(kind, bad, status):
 def test_grouped_refuses_of_one_kind():
     assert grouped(0, K=-1) == INV and grouped(1, sB=-1) == INV and grouped(2, M=-1) == INV
     assert grouped(2, sC=-1) == INV and grouped(2, sC=47 * 64 + 63) == INV
-    assert grouped(1, N=44, ldb=48) == WS and grouped(2, N=60) == WS and grouped(2, M=44) == WS
+    assert grouped(1, N=43, ldb=48) == WS and grouped(2, N=61) == WS and grouped(2, M=45) == WS
+    assert grouped(0, lda=65) == WS and grouped(0, A=A + 4, K=60) == grouped(0, lda=66)        # (dwords suffice)
     # more workgroups than a launch takes
     assert grouped(2, E=4096, M=1 << 20, N=1 << 20, lda=1 << 20, ldb=1 << 20, ldc=1 << 20, sC=1 << 40) == UNS
 
@@ -74,9 +75,12 @@ def test_grouped_workspace_size():
     assert size(0) == size(1) == size(2) == (OK, 0)
     up = lambda b: -(-b // 256) * 256                                      # noqa: E731
     assert size(0, a=A + 2) == (OK, CR + up(600 * 64 * 2))
-    assert size(0, K=60, ldb=60, sB=64 * 60) == (OK, CR + up(4 * 64 * 64 * 2))
-    assert size(1, N=60) == (OK, CR + up(4 * 64 * 64 * 2)) and size(1, N=60, sB=0) == (OK, CR + up(64 * 64 * 2))
-    assert size(2, M=44, N=60) == (OK, CR + up(600 * 48 * 2) + up(600 * 64 * 2))
+    assert size(0, K=61, ldb=61, sB=64 * 61) == (OK, CR + up(4 * 64 * 64 * 2))
+    assert size(1, N=61) == (OK, CR + up(4 * 64 * 64 * 2)) and size(1, N=61, sB=0) == (OK, CR + up(64 * 64 * 2))
+    assert size(2, M=43, N=61) == (OK, CR + up(600 * 48 * 2) + up(600 * 64 * 2))
+    # rows of whole dwords are read where they are
+    assert size(0, K=58, lda=58, ldb=58, sB=64 * 58, a=A + 4, b=B + 8) == (OK, 0)
+    assert size(1, N=58, b=B + 4) == size(2, M=42, N=62, a=A + 12) == (OK, 0)
     # the stream takes rows of any alignment
     assert size(0, rows=512, a=A + 2, b=B + 2) == (OK, 0) and size(0, rows=512, lda=1 << 23, ldb=1 << 25) == (OK, 0)
     assert size(3)[0] == INV and size(0, E=-1)[0] == INV and size(0, rows=0) == (OK, 0)
@@ -201,6 +205,7 @@ def test_loss_workspace_size():
     up = lambda b: -(-b // 256) * 256                                      # noqa: E731
     assert size(0) == (OK, CR + up(8 * 300 * 8) + up(300 * 4))             # 8 column tiles, the targets' logits
     assert size(0, x=A + 2) == (OK, CR + up(300 * 64 * 2) + up(8 * 300 * 8) + up(300 * 4))
+    assert size(0, K=58, x=A + 4, ldx=58, w=B + 8, ldw=62) == size(0)
     assert size(0, M=32, x=A + 2, w=B + 2) == (OK, CR + up(32 * 32 * 8) + up(32 * 4))     # the stream
     assert size(0, M=0) == size(1, M=0) == (OK, 0)
     st, whole = size(1)
