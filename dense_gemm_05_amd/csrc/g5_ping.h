@@ -2,6 +2,8 @@
 // take turns at the matrix cores and at memory.
 #pragma once
 
+#include <type_traits>
+
 #include "g5_device.h"
 
 namespace g5 {
@@ -58,8 +60,10 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
         const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
         const int g = lane >> 4, li = lane & 15;
         const char *A = (const char *)p.A, *B = (const char *)p.B;
-        const uint32_t a_bytes = (uint32_t)((AT ? (p.K - 1) * p.lda + ((p.M + 1) & ~(int64_t)1) : (p.M - 1) * p.lda + p.K) * 2);
-        const uint32_t b_bytes = (uint32_t)((BT ? (p.N - 1) * p.ldb + p.K : (p.K - 1) * p.ldb + p.N) * 2);
+        // (in whole dwords: the range check is per dword)
+        auto even = [](int64_t n) { return (n + 1) & ~(int64_t)1; };
+        const uint32_t a_bytes = (uint32_t)((AT ? (p.K - 1) * p.lda + even(p.M) : (p.M - 1) * p.lda + even(p.K)) * 2);
+        const uint32_t b_bytes = (uint32_t)((BT ? (p.N - 1) * p.ldb + even(p.K) : (p.K - 1) * p.ldb + even(p.N)) * 2);
 
         // Copies: region r of a stage (0: A0, 1: B0, 2: B1, 3: A1) is 16 blocks
         // of 1 KiB, two for each wave: eight rows, or four of the region's k.
@@ -86,10 +90,10 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                     voff[r][i] = row >= limit ? 0x80000000u : (uint32_t)(row * ld * 2 + chunk * 16);
                 }
             }
-        // Both operands across K: rows from K on lie past their descriptors and
-        // arrive as zeros, so the last stage may be a partial one.
-        constexpr bool ZEROS = AT && !BT;
-        const int KT = (int)(ZEROS ? (K + KSTAGE - 1) / KSTAGE : K / KSTAGE);
+        // The last stage may be a partial one.  Of an operand across K the rows
+        // from K on lie past its descriptor and arrive as zeros; one along K
+        // brings what follows its rows, cleared in the fragments.
+        const int KT = (int)((K + KSTAGE - 1) / KSTAGE), KF = AT && !BT ? KT : (int)(K / KSTAGE);
         // (a stage past the last copies the last one again, into a place that
         // is read no more)
         auto copy = [&](int r, int t) {
@@ -148,6 +152,20 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                         acc[hb * 2 + j][ha * 4 + i] =
                             __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][q], a[i][q], acc[hb * 2 + j][ha * 4 + i], 0, 0, 0);
         };
+        // of a lane's fragments the elements from the n-th of step 0 on
+        auto clear = [&](auto &f, int n) {
+            for (auto &row : f)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    u32x4 v = __builtin_bit_cast(u32x4, row[q]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int left = n - 32 * q - 2 * i;
+                        v[i] = left >= 2 ? v[i] : left == 1 ? v[i] & 0xffffu : 0u;
+                    }
+                    row[q] = __builtin_bit_cast(bf16x8, v);
+                }
+        };
         auto barrier = [&]() {
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();
@@ -169,12 +187,19 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
             for (int r = 0; r < 3; ++r) copy(r, 1);
             landed();
             if (wm == 1) barrier();
-            auto stage = [&](int t) {
+            auto stage = [&](int t, auto last) {
+                constexpr bool LAST = decltype(last)::value;
+                const int n = (int)(K - (int64_t)t * KSTAGE) - 8 * g;
                 read_a(a0, t, 0);
                 read_b(b0, t, 0);
                 read_b(b1, t, 1);
                 copy(3, t + 1);
                 landed();
+                if constexpr (LAST && !AT) clear(a0, n);
+                if constexpr (LAST && BT) {
+                    clear(b0, n);
+                    clear(b1, n);
+                }
                 mma(a0, b0, 0, 0);
                 mma(a0, b1, 0, 1);
                 barrier();
@@ -183,60 +208,23 @@ struct PingTile : RingTile<256, 256, 2, 4, 4, 4, 16, true, EPI_NONE, BT, false, 
                 copy(1, t + 2);
                 copy(2, t + 2);
                 landed();
+                if constexpr (LAST && !AT) clear(a1, n);
                 mma(a1, b1, 1, 1);
                 mma(a1, b0, 1, 0);
                 barrier();
             };
+            constexpr std::integral_constant<bool, false> whole{};
+            constexpr std::integral_constant<bool, true> partial{};
             int t = 0;
-            for (; t + 1 < KT; t += 2) {
-                stage(t);
-                stage(t + 1);
+            for (; t + 1 < KF; t += 2) {
+                stage(t, whole);
+                stage(t + 1, whole);
             }
-            if (t < KT) stage(t);
+            if (t < KF) stage(t++, whole);
+            if constexpr (!AT || BT) {
+                if (t < KT) stage(t, partial);
+            }
             if (wm == 0) barrier();
-        }
-        if (!ZEROS && K % KSTAGE != 0) {
-            // what is left of K: chunk by chunk with zeros behind it, all asked
-            // for first, once every copy in flight has landed
-            const int64_t from = (int64_t)KT * KSTAGE;
-            u32x4 v[2][4];
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int q = tid + 512 * i;
-                    const uint16_t *src = (const uint16_t *)(o ? B : A);
-                    const int64_t ld = o ? p.ldb : p.lda, limit = o ? p.N : p.M;
-                    const int align = o ? p.align_b : p.align_a;
-                    if (across(!o)) v[o][i] = load_chunk8_bf16(src + (from + (q >> 5)) * ld, 8 * (q & 31), limit, from + (q >> 5) < K, align);
-                    else v[o][i] = load_chunk8_bf16(src + (q >> 3) * ld, from + 8 * (q & 7), K, (q >> 3) < limit, align);
-                }
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int q = tid + 512 * i;
-                    uint16_t *to = smem + o * 2 * BUF;
-                    if (across(!o)) {
-                        const int k = q >> 5, cc = q & 31;       // chunk of the tile's 32
-                        const int h = o ? (cc >> 2) & 1 : (cc >> 3) & 1;
-                        const int c = o ? (cc >> 3) * 4 + (cc & 3) : (cc >> 4) * 8 + (cc & 7);
-                        *(u32x4 *)(to + h * REGION + k * 128 + ((c ^ swz_bn<128>(k)) * 8)) = v[o][i];
-                    } else {
-                        *(u32x4 *)(to + (q >> 3) * 64 + (((q & 7) ^ ((q >> 3) & 7)) * 8)) = v[o][i];
-                    }
-                }
-            __syncthreads();
-            read_a(a0, 0, 0);
-            read_a(a1, 0, 1);
-            read_b(b0, 0, 0);
-            read_b(b1, 0, 1);
-            mma(a0, b0, 0, 0);
-            mma(a0, b1, 0, 1);
-            mma(a1, b1, 1, 1);
-            mma(a1, b0, 1, 0);
         }
         __builtin_amdgcn_s_waitcnt(0);
     }
