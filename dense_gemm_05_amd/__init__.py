@@ -2,7 +2,8 @@
 accumulation), single and batched, with fused SiLU, SwiGLU and affine
 (alpha, beta, bias) epilogues (SwiGLU also with E4M3FN output), and the
 operators on token rows around them (RMS norm and its gradient, low-rank
-adapters, mixture-of-experts layers),
+adapters, mixture-of-experts layers) and at the ends of a training step
+(products grouped by expert, the loss over a vocabulary with its gradient),
 behind the C ABI of include/gemm05.h."""
 from ._lib import (  # noqa: F401
     GEMM_OK, GEMM_ERR_INVALID_ARG, GEMM_ERR_UNSUPPORTED, GEMM_ERR_LAUNCH, GEMM_ERR_NO_DEVICE, GEMM_ERR_WORKSPACE,

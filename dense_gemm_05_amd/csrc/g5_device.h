@@ -646,8 +646,8 @@ __device__ __forceinline__ void store_tile_via_lds(const f32x4 (&acc)[NFN][NFM],
 //    At + k*lda + m), the layout of the activations in a weight gradient
 //    X^T.dY.  Its slab (BK rows of BM columns m) is copied, swizzled and
 //    read like B's, with the transposing read giving the K-contiguous A
-//    fragments.  Needs 16-byte aligned rows of At and M % 8 == 0 or rows
-//    padded to a multiple of 8 (the masked copy reads whole 16-byte chunks).
+//    fragments.  Needs 4-byte aligned rows of At and an even M or padded rows
+//    (the masked copy reads whole dwords).
 //  * F8: A and Bt hold E4M3FN codes (with BT): the same 64-byte slot rows
 //    then carry 64 values of K per stage.  With an even stage count the
 //    stages go in pairs through the double-rate fp8 instruction (below);

@@ -34,8 +34,9 @@ namespace g5 {
 // the transposing read.
 //
 // Against the ring's 32-deep stages, in which all waves read at once and then
-// multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3150 us (1397
-// TFLOP/s; the platform's library without it 3081) for 3550.  Four phases of 16
+// multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3150 us for
+// 3550 (that epilogue's targets listed by lane since: 2900, 1517 TFLOP/s; the
+// platform's library without any 3081).  Four phases of 16
 // MFMAs 3215, raised wave priority around the MFMAs 1 to 2 % slower, copies
 // ahead of the reads 3 % slower; workgroups that walk over several tiles and
 // copy the next one's first stage under the epilogue 2 to 20 % slower.

@@ -586,8 +586,8 @@ int gemm_rms_norm_workspace_size(int64_t rows, int64_t cols, uint64_t *bytes);
 /* ---- mixture-of-experts layer for a few tokens --------------------------------
  *
  * Everything behind the router's product, for T tokens (0 <= T <= 64;
- * larger batches: gemm_bf16_nt_batched or gemm_fp8_nt_batched per expert and
- * gemm_act_chain).  Per token t, with l = logits[t] (float [T, E], e.g.
+ * larger batches: rows sorted by expert through gemm_bf16_grouped_nt, or
+ * gemm_fp8_nt_batched per expert, and gemm_act_chain).  Per token t, with l = logits[t] (float [T, E], e.g.
  * gemm_bf16_nt with a float output):
  *
  *     ids[t]   = the topk largest of l, in falling order, ties to the lowest
