@@ -2087,7 +2087,6 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.dW = dW;
     b.lddw = lddw;
     b.dw_f32 = ew == 4;
-    b.align_dw = g5::row_alignment((uint64_t)dW, lddw, 0, 1, ew);
     b.ldx2 = (c.K + 7) / 8 * 8;
     b.rows_at_once = b.w_per = 64;
     b.parts = b.w_slices = 1;

@@ -114,7 +114,7 @@ __device__ __forceinline__ void find_group(const GroupedArgs &p, int e, int &fir
 // tile's own first row and column, so that 32-bit offsets span no more than the
 // tile's rows.  Where the summed axis walks rows (B of NN, both of TN), it
 // goes in pieces of p.piece that keep them so.
-template <class R, int KIND, int BM, int BN>
+template <class R, int KIND, int BM, int BN, int WGM, int WGN>
 __device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uint16_t *smem, int64_t K, int n0)
 {
     q.lda = p.lda;
@@ -122,12 +122,10 @@ __device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uin
     q.ldc = p.ldc;
     q.align_a = p.align_a;
     q.align_b = p.align_b;
-    q.align_c = p.align_c;
     q.out_f32 = p.out_f32;
     // (columns of B in whole dwords: even, or padded by the host)
     const int64_t left = p.N - n0;
     q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 1) & ~(int64_t)1) : BN;
-    const TileCoord here{0, 0, 0};
     typename R::Acc acc;
     R::zero(acc);
     for (int64_t done = 0; done < K;) {
@@ -139,7 +137,7 @@ __device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uin
         q.B = (const char *)q.B + q.K * (KIND == GROUPED_NT ? 1 : p.ldb) * 2;
     }
     q.N = left < BN ? left : BN;
-    R::store(q, smem, here, acc);
+    store_rows<R, BM, BN, WGM, WGN>(q, smem, acc);
 }
 
 template <int BM, int BN, int WGM, int WGN, int KIND>
@@ -153,9 +151,8 @@ using GroupedRing = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, KIND ==
 // 32768 rows 395 us (1044 TFLOP/s of the rows that exist; of the multiplied
 // ones a ninth are the tails' padding), the input gradient of 16384 rows 259 us
 // (796 TFLOP/s and 3.8 TB/s: the weights are read once, 805 MB, under tiles of
-// 24 stages), the weight gradient of as many 468 us (3.8 TB/s, nearly all of it
-// FP32 written, of 4.4 that writing alone reaches: a tile has four stages of
-// products before 256 KiB to store).  Workgroups that walk over several tiles were slower (weight gradient
+// 24 stages), the weight gradient of as many 400 us (4.5 TB/s, nearly all of it
+// FP32 written; 460 into outputs that change from call to call).  Workgroups that walk over several tiles were slower (weight gradient
 // 567 for 487, projection 418 for 401), and so were half tiles put last (419).
 template <int BM, int BN, int WGM, int WGN, int KIND, bool HALF>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
@@ -172,7 +169,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
         q.B = p.B + (first * p.ldb + n0);
         q.C = (char *)p.C + (tc.b * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
         q.M = p.M - m0 < BM ? p.M - m0 : BM;
-        ring_tile<R, KIND, BM, BN>(p, q, smem, rows, n0);
+        ring_tile<R, KIND, BM, BN, WGM, WGN>(p, q, smem, rows, n0);
     } else {
         GroupTile t;
         if (!find_tile(p, BM, t)) return;
@@ -183,11 +180,11 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
         q.M = t.rows;
         if constexpr (HALF) {
             if (t.rows <= BM / 2) {
-                ring_tile<GroupedRing<BM / 2, BN, WGM, WGN, KIND>, KIND, BM / 2, BN>(p, q, smem, p.K, n0);
+                ring_tile<GroupedRing<BM / 2, BN, WGM, WGN, KIND>, KIND, BM / 2, BN, WGM, WGN>(p, q, smem, p.K, n0);
                 return;
             }
         }
-        ring_tile<R, KIND, BM, BN>(p, q, smem, p.K, n0);
+        ring_tile<R, KIND, BM, BN, WGM, WGN>(p, q, smem, p.K, n0);
     }
 }
 
@@ -299,6 +296,13 @@ hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream
     a.tiles_n = (a.N + bn - 1) / bn;
     a.tiles_m = (a.M + grouped_tile_m(tile) - 1) / grouped_tile_m(tile);
     a.group_m = a.tiles_m < 8 ? a.tiles_m : 8;
+    // Weight gradients: a run of tiles per XCD gives it whole groups, and the
+    // one with the longest groups is waited for.  So the tiles go round the XCDs
+    // one by one in bands of two (us, run / one by one: 64 groups of 1536 x 4096
+    // FP32, 256 rows each 574 / 461, 78 rows 376 / 311; 8 of them, 2048 rows 262
+    // / 215), but for short groups whose outputs the Infinity Cache holds (32 of
+    // 1024 x 1536, 125 rows 49 / 54; 40 of 700 x 1002, 75 rows 40 / 45).
+    if (kind == GROUPED_TN && (a.rows > 128 * a.E || a.E * a.M * a.N * (a.out_f32 ? 4 : 2) > (int64_t)1 << 28)) a.group_m = -2;
     switch (tile) {
     case GROUPED_STREAM:
     case GROUPED_STREAM_64x32:

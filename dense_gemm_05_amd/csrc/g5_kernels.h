@@ -311,7 +311,7 @@ struct VocabGrad {
     int64_t lddx;
     void *dW;
     int64_t lddw;
-    int dw_f32, align_dw;
+    int dw_f32;
     int64_t rows_at_once;               // a multiple of 64
     int w_slices;                       // of the rows in dW's product
     int64_t w_per;                      // rows in each, a multiple of 64

@@ -240,4 +240,60 @@ __device__ __forceinline__ void multiply_tile(const GemmArgs &q, uint16_t *smem,
     else R::accumulate(q, smem, TileCoord{0, 0, 0}, 0, K, acc);
 }
 
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// A tile's sums to q's rows of C from the tile's first on, of any alignment and
+// length: staged through LDS as C's type, RP rows at a time, then 16 bytes per
+// lane, which a store takes at any address, consecutive lanes on consecutive
+// ones (16 groups' gradients of 1540 x 4101 from 16000 rows 380 us for 630 with
+// rows not aligned stored from the registers, a loss's dW of 32003 x 1028 bf16
+// from 1000 rows 98 for 111).
+template <class R, int BM, int BN, int WGM, int WGN, typename TOut>
+__device__ __forceinline__ void store_rows_as(const GemmArgs &q, uint16_t *smem, const typename R::Acc &acc)
+{
+    constexpr int ESZ = sizeof(TOut), PER = 16 / ESZ, PITCH = BN * ESZ + 16, CPR = BN / PER, NT = WGM * WGN * 64;
+    constexpr int FITS = R::LDS_BYTES / PITCH, RP = FITS >= BM ? BM : FITS >= BM / 2 ? BM / 2 : BM / 4;
+    static_assert(RP % 16 == 0 && RP * PITCH <= R::LDS_BYTES, "staging passes");
+    using at_any = std::conditional_t<ESZ == 4, u32x4_at4, u32x4_at2>;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, wave = tid >> 6, wm = wave / WGN, wn = wave % WGN, g = lane >> 4, li = lane & 15;
+    char *L = (char *)smem;
+#pragma unroll
+    for (int pass = 0; pass < BM / RP; ++pass) {
+        __syncthreads();
+#pragma unroll
+        for (int fm = 0; fm < R::FM; ++fm) {
+            const int row = wm * R::TM + fm * 16;
+            if (row / RP != pass) continue;
+#pragma unroll
+            for (int fn = 0; fn < R::FN; ++fn) {
+                char *to = L + (row - pass * RP + li) * PITCH + (wn * R::TN + fn * 16 + g * 4) * ESZ;
+                const f32x4 v = acc[fn][fm];
+                if constexpr (ESZ == 4) *(f32x4 *)to = v;
+                else *(u32x2 *)to = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < RP * CPR; i += NT) {
+            const int r = i / CPR, c = i % CPR, left = (int)q.N - c * PER;
+            if (pass * RP + r >= q.M || left <= 0) continue;
+            const char *from = L + r * PITCH + c * 16;
+            TOut *to = (TOut *)q.C + (pass * RP + r) * q.ldc + c * PER;
+            if (left >= PER) {
+                __builtin_nontemporal_store(*(const u32x4 *)from, (at_any *)to);      // C is written once
+            } else {
+                for (int j = 0; j < left; ++j) to[j] = ((const TOut *)from)[j];
+            }
+        }
+    }
+}
+template <class R, int BM, int BN, int WGM, int WGN>
+__device__ __forceinline__ void store_rows(const GemmArgs &q, uint16_t *smem, const typename R::Acc &acc)
+{
+    if (q.out_f32) store_rows_as<R, BM, BN, WGM, WGN, float>(q, smem, acc);
+    else store_rows_as<R, BM, BN, WGM, WGN, uint16_t>(q, smem, acc);
+}
+
 }  // namespace g5

@@ -97,7 +97,7 @@ __device__ __forceinline__ uint64_t scan_ids(const T *ids, int tid, int pairs, T
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
             const T col = id[j] - first;
-            found |= (uint32_t)(i + NT * j < pairs & id[j] >= 0 & col >= 0 & col < (T)cols) << j;
+            found |= (uint32_t)((i + NT * j < pairs) & (id[j] >= 0) & (col >= 0) & (col < (T)cols)) << j;
         }
         bits |= (uint64_t)found << (k & 63);
     }
@@ -735,12 +735,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, Voca
     if (b.w_slices == 1) {
         q.C = (char *)b.dW + ((p.v0 + m0) * b.lddw + n0) * (b.dw_f32 ? 4 : 2);
         q.ldc = b.lddw;
-        q.align_c = b.align_dw;
         q.out_f32 = b.dw_f32;
     } else {
         q.C = b.w_sums + (tc.b * p.V + m0) * b.ldx2 + n0;
         q.ldc = b.ldx2;
-        q.align_c = 16;
         q.out_f32 = 1;
     }
     q.lda = b.ldd;
@@ -768,7 +766,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, Voca
                 for (int i = 0; i < 4; ++i) acc[fn][fm][i] *= a;
         q.N = p.K - n0 < BN ? p.K - n0 : BN;
     }
-    R::store(q, smem, TileCoord{0, 0, 0}, acc);
+    store_rows<R, BM, BN, WGM, WGN>(q, smem, acc);
 }
 
 // A piece's share of dX before its factor: sums (+)= D W over one of b.slices
