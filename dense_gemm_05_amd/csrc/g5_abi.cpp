@@ -1578,12 +1578,21 @@ int gemm_bf16_nt_lora(int64_t M, int64_t N, int64_t K, const uint16_t *X, int64_
 }
 
 // ---- products grouped by expert
+// The part of a workspace that a call of `need` bytes may write (a smaller one
+// is refused as such, not as an overlap with what lies behind it).
+static g5::Range scratch_range(const void *workspace, uint64_t bytes, uint64_t need)
+{
+    const __int128 at = (__int128)(uint64_t)workspace;
+    return g5::Range{at, at + (__int128)(bytes < need ? bytes : need)};
+}
+
 namespace {
 struct GroupedPlan {
     int tile = g5::GROUPED_128;
     bool copy_a = false, copy_b = false;
     int64_t lda2 = 0, ldb2 = 0, batch_b = 1, rows_b = 0, cols_a = 0;
-    size_t at_a = 0, at_b = 0, total = 0;
+    int slices = 1;                      // of a group's rows (TN)
+    size_t at_a = 0, at_b = 0, at_sums = 0, total = 0;
 };
 }  // namespace
 
@@ -1643,6 +1652,20 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
         pl.tile = g5::GROUPED_256;
     }
     if (g5::grouped_grid(kind, E, rows, M, N, pl.tile) > (int64_t)1 << 22) return GEMM_ERR_UNSUPPORTED;
+    // A weight gradient with few tiles over many rows: the rows of a group in
+    // slices of at least 512 in the mean, two tiles a CU, as many as 64, whose
+    // planes of FP32 sums stay within 24 MiB (one slice / these, us: one group of
+    // 30000 rows 64 x 64 282 / 19, 512 x 512 290 / 43, 1024 x 1024 290 / 90; 4528
+    // rows 224 x 88 49 / 15; where the rule stays with one, 3000 rows in 4 groups
+    // 1000 x 1000 19 / 27, 600 rows 128 x 128 12 / 14).
+    if (tn && pl.tile == g5::GROUPED_128) {
+        const double plane = 4.0 * E * M * ((N + 3) / 4 * 4);
+        int64_t s = 2 * g5::kNumCU / g5::grouped_grid(kind, E, rows, M, N, pl.tile);
+        if (s > rows / E / 512) s = rows / E / 512;
+        if (s > 64) s = 64;
+        if (plane * s > 3 << 23) s = (int64_t)((3 << 23) / plane);
+        pl.slices = s < 1 ? 1 : (int)s;
+    }
     if (pl.tile != g5::GROUPED_128 && pl.tile != g5::GROUPED_256) {
         pl.copy_a = pl.copy_b = false;
         return GEMM_OK;
@@ -1654,10 +1677,11 @@ static int grouped_plan(int kind, int64_t E, int64_t rows, int64_t M, int64_t N,
     // (32-bit offsets from a tile's own first row: 256 rows, or a piece of 64
     // along the summed axis)
     if (pl.lda2 > (1 << 21) || pl.ldb2 > (1 << 21)) return GEMM_ERR_UNSUPPORTED;
-    if (pl.copy_a || pl.copy_b) {
+    if (pl.copy_a || pl.copy_b || pl.slices > 1) {
         pl.at_a = g5::kCounterBytes;
         pl.at_b = pl.at_a + (pl.copy_a ? g5::round256((size_t)rows * pl.lda2 * 2) : 0);
-        pl.total = pl.at_b + (pl.copy_b ? g5::round256((size_t)pl.batch_b * pl.rows_b * pl.ldb2 * 2) : 0);
+        pl.at_sums = pl.at_b + (pl.copy_b ? g5::round256((size_t)pl.batch_b * pl.rows_b * pl.ldb2 * 2) : 0);
+        pl.total = pl.at_sums + (pl.slices > 1 ? g5::round256((size_t)pl.slices * E * M * ((N + 3) / 4 * 4) * 4) : 0);
     }
     return GEMM_OK;
 }
@@ -1705,7 +1729,7 @@ static int grouped_run(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, 
     }
     const Range out[] = {g5::extent((uint64_t)C, tn ? E : 1, tn ? M : rows, N, ldc, sC, ec),
                          pl.total && workspace
-                             ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                             ? scratch_range(workspace, workspace_bytes, pl.total)
                              : none};
     for (const Range &r : in)
         if (r.hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;
@@ -1734,6 +1758,9 @@ static int grouped_run(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, 
     a.align_c = g5::row_alignment((uint64_t)C, ldc, sC, tn ? E : 1, ec);
     a.out_f32 = ec == 4;
     char *ws = (char *)workspace;
+    a.slices = pl.slices;
+    a.sums = (float *)(ws + pl.at_sums);
+    a.ld_sums = (N + 3) / 4 * 4;
     if (pl.copy_a) {
         uint16_t *A2 = (uint16_t *)(ws + pl.at_a);
         if (g5::launch_realign_rows(A, lda, 0, 1, rows, pl.cols_a, g5::row_alignment((uint64_t)A, lda, 0, 1, 2), A2, pl.lda2,
@@ -2008,7 +2035,7 @@ static int vocab_forward(const VocabCall &c, const uint16_t *X, const uint16_t *
     st = vocab_plan(c, pl);
     if (st != GEMM_OK) return st;
     const Range out[] = {vec_range(loss, c.M, 4), vec_range(lse, c.M, 4),
-                         workspace ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                         workspace ? scratch_range(workspace, workspace_bytes, pl.total)
                                    : Range{0, 0}};
     if (outputs_overlap(out, 3, in, 4)) return GEMM_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < pl.total) return GEMM_ERR_WORKSPACE;
@@ -2069,7 +2096,7 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     const Range out[] = {dX ? g5::extent((uint64_t)dX, 1, c.M, c.K, lddx, 0, 2) : none,
                          dW ? g5::extent((uint64_t)dW, 1, c.V, c.K, lddw, 0, ew) : none,
                          c.M > 0 && workspace
-                             ? Range{(__int128)(uint64_t)workspace, (__int128)(uint64_t)workspace + (__int128)pl.total}
+                             ? scratch_range(workspace, workspace_bytes, pl.total)
                              : none};
     for (const Range &r : out)
         if (r.hi > ((__int128)1 << 63)) return GEMM_ERR_INVALID_ARG;

@@ -119,10 +119,8 @@ __device__ __forceinline__ void ring_tile(const GroupedArgs &p, GemmArgs &q, uin
 {
     q.lda = p.lda;
     q.ldb = p.ldb;
-    q.ldc = p.ldc;
     q.align_a = p.align_a;
     q.align_b = p.align_b;
-    q.out_f32 = p.out_f32;
     // (columns of B in whole dwords: even, or padded by the host)
     const int64_t left = p.N - n0;
     q.N = left < BN ? (KIND == GROUPED_NT ? left : (left + 1) & ~(int64_t)1) : BN;
@@ -160,14 +158,27 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
     using R = GroupedRing<BM, BN, WGM, WGN, KIND>;
     __shared__ __attribute__((aligned(1024))) uint16_t smem[R::LDS_BYTES / 2];
     GemmArgs q{};
+    q.ldc = p.ldc;
+    q.out_f32 = p.out_f32;
     if constexpr (KIND == GROUPED_TN) {
-        const TileCoord tc = tile_map(blockIdx.x, p.E, p.tiles_m, p.tiles_n, p.group_m);
+        const TileCoord tc = tile_map(blockIdx.x, p.E * p.slices, p.tiles_m, p.tiles_n, p.group_m);
+        const int e = (int)tc.b / p.slices, slice = (int)tc.b % p.slices;
         int first, rows;
-        find_group(p, (int)tc.b, first, rows);
+        find_group(p, e, first, rows);
+        if (p.slices > 1) {
+            const int per = ((rows + p.slices - 1) / p.slices + 63) & ~63, from = slice * per < rows ? slice * per : rows;
+            first += from;
+            rows = rows - from < per ? rows - from : per;
+        }
         const int m0 = (int)tc.tm * BM, n0 = (int)tc.tn * BN;
         q.A = p.A + (first * p.lda + m0);
         q.B = p.B + (first * p.ldb + n0);
-        q.C = (char *)p.C + (tc.b * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        q.C = (char *)p.C + (e * p.sC + m0 * p.ldc + n0) * (p.out_f32 ? 4 : 2);
+        if (p.slices > 1) {
+            q.C = p.sums + ((slice * p.E + e) * p.M + m0) * p.ld_sums + n0;
+            q.ldc = p.ld_sums;
+            q.out_f32 = 1;
+        }
         q.M = p.M - m0 < BM ? p.M - m0 : BM;
         ring_tile<R, KIND, BM, BN, WGM, WGN>(p, q, smem, rows, n0);
     } else {
@@ -272,6 +283,20 @@ __global__ void __launch_bounds__(kStreamWaves * 64, 2) k_grouped_stream_many(Gr
     else stream_tile<1, RB, D + 1>(p, t, red);
 }
 
+// The slices' sums of TN added in order.
+__global__ void __launch_bounds__(256) k_grouped_total(GroupedArgs p)
+{
+    const int64_t chunks = p.ld_sums / 4, rows = p.E * p.M, plane = rows * p.ld_sums;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < rows * chunks; at += (int64_t)gridDim.x * 256) {
+        const int64_t row = at / chunks, n = at % chunks * 4, e = row / p.M, m = row % p.M;
+        const float *s = p.sums + row * p.ld_sums + n;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int i = 0; i < p.slices; ++i) v += *(const f32x4 *)(s + i * plane);
+        store4((char *)p.C + e * p.sC * (p.out_f32 ? 4 : 2), p.out_f32 != 0, p.ldc, m, n, v, n + 4 <= p.N, p.M, p.N, p.align_c);
+    }
+}
+
 template <int BM, int BN, int WGM, int WGN>
 hipError_t launch_kind(int kind, const GroupedArgs &a, int64_t grid, hipStream_t s)
 {
@@ -291,7 +316,7 @@ hipError_t launch_kind(int kind, const GroupedArgs &a, int64_t grid, hipStream_t
 hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream_t s)
 {
     GroupedArgs a = args;
-    const int64_t grid = grouped_grid(kind, a.E, a.rows, a.M, a.N, tile);
+    const int64_t grid = grouped_grid(kind, a.E, a.rows, a.M, a.N, tile, a.slices);
     const int64_t bn = grouped_tile_n(tile);
     a.tiles_n = (a.N + bn - 1) / bn;
     a.tiles_m = (a.M + grouped_tile_m(tile) - 1) / grouped_tile_m(tile);
@@ -314,10 +339,15 @@ hipError_t launch_grouped(int kind, const GroupedArgs &args, int tile, hipStream
         else hipLaunchKernelGGL(k_grouped_stream_many<4>, g, b, 0, s, a);
         return hipGetLastError();
     }
-    case GROUPED_128: return launch_kind<128, 128, 4, 2>(kind, a, grid, s);
-    case GROUPED_256: return launch_kind<256, 256, 2, 4>(kind, a, grid, s);
+    case GROUPED_128:
+    case GROUPED_256: break;
     default: return hipErrorInvalidValue;
     }
+    const hipError_t e = tile == GROUPED_256 ? launch_kind<256, 256, 2, 4>(kind, a, grid, s) : launch_kind<128, 128, 4, 2>(kind, a, grid, s);
+    if (e != hipSuccess || a.slices == 1) return e;
+    const int64_t groups = (a.E * a.M * (a.ld_sums / 4) + 255) / 256;
+    hipLaunchKernelGGL(k_grouped_total, dim3((unsigned)(groups < 65536 ? groups : 65536)), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace g5

@@ -247,6 +247,9 @@ struct GroupedArgs {
     int64_t M, N, K;                 // M: TN's output rows; K: the summed axis of NT and NN
     int64_t lda, ldb, sB, ldc, sC;   // sB: B's group stride (NT, NN); sC: C's (TN)
     int64_t piece;                   // NN, TN: elements of the summed axis at a time, a multiple of 64
+    int slices;                      // TN: of a group's rows, each with sums of its own
+    float *sums;                     // slices > 1: [slices, E, M, ld_sums]
+    int64_t ld_sums;                 // N rounded up to 4
     int align_a, align_b, align_c, out_f32;
     int64_t tiles_m, tiles_n, group_m;   // (set by the launch)
 };
@@ -260,10 +263,10 @@ inline int64_t grouped_tile_n(int tile)
     return tile == GROUPED_256 ? 256 : tile == GROUPED_128 ? 128 : tile == GROUPED_STREAM_64x64 ? 64 : 32;
 }
 // Workgroups: the most tiles that E groups of `rows` rows can have.
-inline int64_t grouped_grid(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int tile)
+inline int64_t grouped_grid(int kind, int64_t E, int64_t rows, int64_t M, int64_t N, int tile, int slices = 1)
 {
     const int64_t bm = grouped_tile_m(tile), bn = grouped_tile_n(tile), tn = (N + bn - 1) / bn;
-    if (kind == GROUPED_TN) return E * ((M + bm - 1) / bm) * tn;
+    if (kind == GROUPED_TN) return slices * E * ((M + bm - 1) / bm) * tn;
     const int64_t most = (rows + E * (bm - 1)) / bm;
     return (most < rows ? most : rows) * tn;
 }

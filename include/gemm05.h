@@ -721,9 +721,10 @@ int gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t L, int64_t
  * streams the weights past the rows, which may have any alignment.  The tiles
  * take rows that start at multiples of 4 bytes (in the gradients, B's and At's
  * of an even length besides); others are first copied to padded ones in the
- * workspace (gemm_grouped_workspace_size bytes, 0 where no copy is needed; its
- * first GEMM_WORKSPACE_COUNTER_BYTES are left untouched, so gemm_run's
- * serves).
+ * workspace.  Small weight gradients of many rows are summed in slices of the
+ * rows, whose FP32 sums lie there too (gemm_grouped_workspace_size bytes, 0
+ * where neither is needed; its first GEMM_WORKSPACE_COUNTER_BYTES are left
+ * untouched, so gemm_run's serves).
  * Errors, nothing enqueued: GEMM_ERR_INVALID_ARG for sizes outside these
  * ranges, a c_type other than bf16 and float, strides below the row lengths,
  * negative strides, strideC below C_e's extent, missing or misaligned

@@ -105,6 +105,22 @@ def test_every_tile_takes_every_size(monkeypatch, kind, config, sizes, n, k):
     _check(_run(kind, a, b, o), *_formula(kind, a, b, o), f"{kind} {config}")
 
 
+@pytest.mark.parametrize("sizes,n,k", [([5000], 40, 72), ([2000, 0, 3100], 130, 33), ([1, 6000], 64, 260), ([700, 700, 0, 2900], 128, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_small_weight_gradients_of_many_rows(sizes, n, k, dtype):
+    """Summed in slices of the rows: the same bits in every call, also beside
+    other columns."""
+    _say(f"slices {sizes} {n} {k} {dtype}")
+    a, b, o = _case("tn", sizes, n, k, seed=13)
+    c = _run("tn", a, b, o, out_dtype=dtype)
+    _check(c, *_formula("tn", a, b, o), f"slices {sizes}")
+    wide = torch.full((len(sizes), n + 2, k + 3), 7.0, dtype=dtype).cuda()
+    part = wide[:, 1:n + 1, 1:k + 1]
+    assert _run("tn", a, b, o, C=part) is part and torch.equal(part, c)
+    part.fill_(7.0)
+    assert bool((wide == 7).all())
+
+
 def _inside(t, pad, at):
     """t's rows `pad` elements further apart, `at` elements behind the start of
     a block that is NaN around them and right behind the last one."""

@@ -81,6 +81,9 @@ def test_grouped_workspace_size():
     # rows of whole dwords are read where they are
     assert size(0, K=58, lda=58, ldb=58, sB=64 * 58, a=A + 4, b=B + 8) == (OK, 0)
     assert size(1, N=58, b=B + 4) == size(2, M=42, N=62, a=A + 12) == (OK, 0)
+    # small weight gradients of many rows: slices' sums, one per 512 rows of a group here
+    assert size(2, rows=1 << 13) == (OK, CR + up(4 * 4 * 48 * 64 * 4))
+    assert size(2, rows=1 << 13, M=1024, N=1024, lda=1024, ldb=1024) == (OK, 0)
     # the stream takes rows of any alignment
     assert size(0, rows=512, a=A + 2, b=B + 2) == (OK, 0) and size(0, rows=512, lda=1 << 23, ldb=1 << 25) == (OK, 0)
     assert size(3)[0] == INV and size(0, E=-1)[0] == INV and size(0, rows=0) == (OK, 0)
