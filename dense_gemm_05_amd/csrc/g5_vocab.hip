@@ -43,6 +43,19 @@ __device__ __forceinline__ Stat join_stat(Stat a, Stat b, float c)
     return Stat{top, a.sum * __builtin_amdgcn_exp2f(c * (a.top - base)) + b.sum * __builtin_amdgcn_exp2f(c * (b.top - base))};
 }
 
+// Parts as they are kept: `rest` is the sum without the maximum's own 1 (-1
+// where there are no finite logits), so that a loss near 0, log(1 + rest), does
+// not lose what 1 + rest rounds off.
+struct Part {
+    float top, rest;
+};
+__device__ __forceinline__ Part join_part(Part a, Part b, float c)
+{
+    const Part hi = a.top >= b.top ? a : b, lo = a.top >= b.top ? b : a;
+    const float base = hi.top == -__builtin_inff() ? 0.f : hi.top;
+    return Part{hi.top, hi.rest + (1.f + lo.rest) * __builtin_amdgcn_exp2f(c * (lo.top - base))};
+}
+
 // The tile's operands, bases moved to its first row and column.
 template <int BM, int BN>
 __device__ __forceinline__ GemmArgs tile_args(const VocabArgs &p, int64_t m0, int64_t n0)
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         Stat s = st[tid];
 #pragma unroll
         for (int w = 1; w < WGN; ++w) s = join_stat(s, st[w * BM + tid], c);
-        p.part[(m0 + tid) * p.parts + p.tile0 + tc.tn] = float2{s.top, s.sum};
+        p.part[(m0 + tid) * p.parts + p.tile0 + tc.tn] = float2{s.top, s.sum - 1.f};
     }
     __syncthreads();
     if (!list.over()) {
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
             }
             __builtin_amdgcn_wave_barrier();
         } else {
-            float top = -__builtin_inff(), sum = 0.f;
+            float top = -__builtin_inff(), rest = 0.f, ones = -1.f;
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -365,10 +378,18 @@ __global__ void __launch_bounds__(kVocabWaves * 64, 4) k_vocab_stream(VocabArgs 
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(c * (s[r][i] - base));
-            sum += __shfl_xor(sum, 16, 64);
-            sum += __shfl_xor(sum, 32, 64);
-            if (g == 0 && m < M) p.part[m * p.parts + blockIdx.x] = float2{top, sum};
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(c * (s[r][i] - base));
+                    ones += e == 1.f ? 1.f : 0.f;
+                    rest += e == 1.f ? 0.f : e;
+                }
+            if (g != 0) ones += 1.f;         // (the one taken off once)
+#pragma unroll
+            for (int o = 16; o < 64; o <<= 1) {
+                rest += __shfl_xor(rest, o, 64);
+                ones += __shfl_xor(ones, o, 64);
+            }
+            if (g == 0 && m < M) p.part[m * p.parts + blockIdx.x] = float2{top, ones + rest};
             // (one wave writes and reads the tile: in order)
             __builtin_amdgcn_wave_barrier();
 #pragma unroll 8
@@ -448,31 +469,26 @@ __device__ __forceinline__ bool row_targets(const VocabArgs &p, int64_t m, int l
 constexpr int kJoinWaves = 4;
 __global__ void __launch_bounds__(kJoinWaves * 64) k_vocab_join(VocabArgs p)
 {
-    __shared__ Stat st[kJoinWaves];
+    __shared__ Part st[kJoinWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float c = p.scale * kLog2e;
-    auto base = [](float top) { return top == -__builtin_inff() ? 0.f : top; };
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-        Stat s{-__builtin_inff(), 0.f};
+        Part s{-__builtin_inff(), -1.f};
 #pragma unroll 8
         for (int64_t i = threadIdx.x; i < p.parts; i += kJoinWaves * 64) {
             const float2 v = p.part[m * p.parts + i];
-            s = join_stat(s, Stat{v.x, v.y}, c);
+            s = join_part(s, Part{v.x, v.y}, c);
         }
-        float top = max64(s.top);
-        float sum = sum64(s.sum * __builtin_amdgcn_exp2f(c * (s.top - base(top))));
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) s = join_part(s, Part{__shfl_xor(s.top, o, 64), __shfl_xor(s.rest, o, 64)}, c);
         __syncthreads();                 // (the row before has been read)
-        if (lane == 0) st[wave] = Stat{top, sum};
+        if (lane == 0) st[wave] = s;
         __syncthreads();
         if (wave != 0) continue;
-        s = st[lane % kJoinWaves];
-        top = s.top;
+        s = st[0];
 #pragma unroll
-        for (int o = kJoinWaves / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-        sum = s.sum * __builtin_amdgcn_exp2f(c * (s.top - base(top)));
-#pragma unroll
-        for (int o = kJoinWaves / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-        const float log_sum = logf(sum);
+        for (int w = 1; w < kJoinWaves; ++w) s = join_part(s, st[w], c);
+        const float top = s.top, log_sum = log1pf(s.rest);
         if (lane == 0 && p.lse_out) p.lse_out[m] = p.scale * top + log_sum;
         float loss = 0.f;
         if (!p.teacher) {
