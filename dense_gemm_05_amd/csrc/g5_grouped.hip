@@ -166,9 +166,10 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)
         int first, rows;
         find_group(p, e, first, rows);
         if (p.slices > 1) {
-            const int per = ((rows + p.slices - 1) / p.slices + 63) & ~63, from = slice * per < rows ? slice * per : rows;
+            const int64_t per = (((int64_t)rows + p.slices - 1) / p.slices + 63) & ~(int64_t)63;
+            const int from = slice * per < rows ? (int)(slice * per) : rows;
             first += from;
-            rows = rows - from < per ? rows - from : per;
+            rows = rows - from < per ? rows - from : (int)per;
         }
         const int m0 = (int)tc.tm * BM, n0 = (int)tc.tn * BN;
         q.A = p.A + (first * p.lda + m0);
