@@ -248,7 +248,8 @@ def test_empty_calls():
     assert c[:, 0].tolist() == [3, 0, 0, 3]
 
 
-@pytest.mark.parametrize("sizes,n,k", [([4, 2, 0, 1], 64, 96), ([200, 70, 300], 256, 160)])
+@pytest.mark.parametrize("sizes,n,k", [([4, 2, 0, 1], 64, 96), ([200, 70, 300], 256, 160),
+                                       ([2000, 0, 3100], 40, 72), ([1500, 2600], 43, 71)])
 def test_captured_with_changing_groups(sizes, n, k):
     """A graph reads the offsets when it runs: replays with other groups, the
     program's own eager calls on the same workspace between them."""
