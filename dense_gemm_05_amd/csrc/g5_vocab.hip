@@ -569,14 +569,32 @@ __device__ __forceinline__ float prep_row(const VocabArgs &p, const VocabGrad &b
 __device__ __forceinline__ float weight_factor(float top) { return top > 0.f && top < __builtin_inff() ? top : 1.f; }
 
 constexpr int kPrepWaves = 4;
+template <bool ALPHA>
 __global__ void __launch_bounds__(kPrepWaves * 64) k_vocab_prep(VocabArgs p, VocabGrad b)
 {
     __shared__ PrepRow rows[kPrepWaves];
+    __shared__ float tops[kPrepWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = (int64_t)blockIdx.x * kPrepWaves + wave;
+    float a = 1.f;
+    if constexpr (ALPHA) {
+        float top = 0.f;
+        const int pairs = (int)p.M * p.topk;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < pairs; i += kPrepWaves * 64) {
+            const float d = fabsf(b.dloss[i / p.topk]), t = p.teacher ? p.teacher[i] : 0.f;
+            top = fmaxf(top, has_entry(target_id(p, i), p.vocab, t) ? d : 0.f);
+        }
+        top = max64(top);
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+        for (int w = 0; w < kPrepWaves; ++w) top = fmaxf(top, tops[w]);
+        a = weight_factor(top);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *b.alpha = a;
+    }
     if (m >= p.M) return;                 // (a wave works alone)
     const float w = prep_row(p, b, m, lane, rows[wave]);
-    if (lane == 0) b.weight[m] = w;
+    if (lane == 0) b.weight[m] = w / a;
 }
 
 // The largest |dloss| of the rows with targets into alpha, every row's weight
@@ -601,8 +619,12 @@ __global__ void __launch_bounds__(1024) k_vocab_weights(float *weight, int64_t M
     if (tid == 0) *alpha = a;
 }
 
-// Both for up to 16 rows, a wave each, in one launch (3 rows: 3.6 us for 2.2 +
-// 1.8 and the gap between them).
+// Both in one launch: for up to 16 rows, a wave each (3 rows: 3.6 us for 2.2 +
+// 1.8 and the gap between them), and for up to kPrepScan entries, where every
+// workgroup of k_vocab_prep looks at all of them (262 rows 3.8 us for 3.2 + 1.8
+// and the gap, 1000 rows 5.4 for 3.9 + 1.8; 2000 entries of 100 rows 9.5 for 5.7
+// + 1.6).
+constexpr int kPrepScan = 1024;
 constexpr int kPrepFew = 16;
 __global__ void __launch_bounds__(kPrepFew * 64) k_vocab_prep_few(VocabArgs p, VocabGrad b)
 {
@@ -925,7 +947,12 @@ hipError_t launch_vocab_prep(const VocabArgs &p, const VocabGrad &b, hipStream_t
         hipLaunchKernelGGL(k_vocab_prep_few, dim3(1), dim3((unsigned)p.M * 64), 0, s, p, b);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(k_vocab_prep, dim3((unsigned)((p.M + kPrepWaves - 1) / kPrepWaves)), dim3(kPrepWaves * 64), 0, s, p, b);
+    const dim3 g((unsigned)((p.M + kPrepWaves - 1) / kPrepWaves)), t(kPrepWaves * 64);
+    if (p.M * p.topk <= kPrepScan) {
+        hipLaunchKernelGGL(k_vocab_prep<true>, g, t, 0, s, p, b);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(k_vocab_prep<false>, g, t, 0, s, p, b);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_vocab_weights, dim3(1), dim3(1024), 0, s, b.weight, p.M, b.alpha);
