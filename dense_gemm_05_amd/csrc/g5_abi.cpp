@@ -1896,12 +1896,14 @@ static int vocab_plan(const VocabCall &c, VocabPlan &pl)
         const int64_t ldw = pl.copy_w ? pl.ld2 : c.ldw;
         if (c.ldx > 1 << 21 || ldw > 1 << 21) return GEMM_ERR_UNSUPPORTED;
         // A piece: D of 2^27 elements (256 MiB, the Infinity Cache's size), the
-        // copy of W as many, and W's rows within 32-bit offsets.
+        // copy of W as many, and W's rows and 64 of D's within 32-bit offsets
+        // (each such limit at least 256 tokens, the rounding's).
         int64_t rows = c.V;
         const int64_t cache = (int64_t)1 << 27;
         if (c.grad && c.M > 0 && rows > cache / c.M) rows = cache / c.M;
         if (pl.copy_w && rows > cache / pl.ld2) rows = cache / pl.ld2;
-        if (c.grad && rows > ((int64_t)1 << 29) / ldw) rows = ((int64_t)1 << 29) / ldw;
+        if (c.grad && rows > g5::kVocabReach / ldw) rows = g5::kVocabReach / ldw;
+        if (c.grad && rows > g5::kVocabMaxPiece) rows = g5::kVocabMaxPiece;
         if (rows < c.V) rows = rows < 256 ? 256 : rows / 256 * 256;
         pl.piece = rows < c.V ? rows : c.V;
         pl.parts = pl.tile ? g5::cdiv(c.V, pl.tile) : 0;
@@ -2139,7 +2141,7 @@ static int vocab_backward(const VocabCall &c, const uint16_t *X, const uint16_t 
     b.w_per = pl.w_per;
     b.w_sums = (float *)(ws + pl.w_sums);
     const int64_t widest = b.ldd > b.ldx2 ? b.ldd : b.ldx2;
-    b.rows_at_once = (((int64_t)1 << 29) / widest) / 64 * 64;
+    b.rows_at_once = g5::kVocabReach / widest / 64 * 64;     // (64 at least: neither exceeds kVocabMaxPiece)
     if (g5::launch_vocab_prep(a, b, s) != hipSuccess) return GEMM_ERR_LAUNCH;
     a.X = b.X2;                       // (the stream's rows of X too: at most kVocabStreamRows of them)
     a.ldx = b.ldx2;

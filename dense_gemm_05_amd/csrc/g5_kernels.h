@@ -282,6 +282,10 @@ constexpr int kVocabStreamRows = 32;    // rows of X up to which the weight is s
 // products are bound by reading the weight and writing its gradient, not by
 // twice the rows.
 constexpr int kVocabSplitRows = 64;
+// Elements that 32-bit byte offsets reach, twice over, and so the most tokens of
+// a gradient's piece: 64 rows of its D, the least that dW's product takes at
+// once, end within them.
+constexpr int64_t kVocabReach = (int64_t)1 << 29, kVocabMaxPiece = kVocabReach / 64;
 struct VocabArgs {
     const uint16_t *X, *W;              // 4-byte aligned rows for the tiles, any for the stream
     int align_x, align_w;               // byte alignment of their rows

@@ -474,3 +474,45 @@ def test_gradients_are_the_loss_s(topk):
     # derivative, for 40 rows whose logits move by up to 20 per unit 1e-3
     bound = float(((ex + 2.0 ** -8 * dx.abs()) * ux.abs()).sum() + ((ew + 2.0 ** -24 * dw.abs()) * uw.abs()).sum()) + 1e-4 * abs(want) + 1e-3
     assert abs(got - want) <= bound, (got, want, bound)
+
+
+@pytest.mark.parametrize("M", [4, 15])
+def test_gradients_of_more_tokens_than_a_piece_holds(M):
+    """A vocabulary of 2^23 short rows and some more: two pieces, the first with
+    D's rows 2^23 apart.  Against the formula in 64 bits on the GPU."""
+    V, K = 2 ** 23 + 4096 + 5, 32
+    _say(f"{M} {V} {K}")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((V, K), generator=g, device="cuda") * 3 * K ** -0.5).bfloat16()
+    ids = torch.randint(0, V, (M,), generator=g, device="cuda")
+    ids[:4] = torch.tensor([V - 1, 2 ** 23 - 1, 2 ** 23, 0])
+    dloss = torch.rand((M,), generator=g, device="cuda") + 0.25
+    loss, lse = g5.linear_cross_entropy(x, w, ids, workspace=ws())
+    dx, dw = g5.linear_cross_entropy_backward(dloss, x, w, ids, lse, dw_dtype=torch.float32, workspace=ws())
+    torch.cuda.synchronize()
+    _say("computed")
+    rows = torch.arange(M, device="cuda")
+    xd, wd = x.double(), w.double()
+    l = xd @ wd.t()
+    # FP32 sums of K products; an exponential's argument, of up to |l| + |lse|
+    el = 1.01 * (K + 2) * 2.0 ** -23 * (xd.abs() @ wd.abs().t())
+    want = torch.logsumexp(l, 1)
+    # a part's sum of up to 32, a thread's 1024 parts, and the joins
+    tol = el.max(1).values + 1.01 * 1100 * 2.0 ** -24 + 2.0 ** -16 + 2.0 ** -21 * (l.abs().max(1).values + want)
+    _close(lse, want.cpu(), tol.cpu(), "lse")
+    _close(loss, (want - l[rows, ids]).cpu(), (2 * tol).cpu(), "loss")
+    lse = lse.double()[:, None]
+    p = torch.exp(l - lse)
+    ep = p * torch.expm1(el + 2.0 ** -21 * (l.abs() + lse.abs()) + 2.0 ** -20)
+    d = p
+    d[rows, ids] -= 1
+    d, e = dloss.double()[:, None] * d, dloss.double()[:, None] * ep
+    del l, el, p, ep
+    e += (2.0 ** -16 + 2.0 ** -20) * (d.abs() + e)          # D in two bf16 parts
+    for got, a, ea, b, n, half in ((dx, d, e, wd, 2 * V, 2.0 ** -8), (dw, d.t().contiguous(), e.t().contiguous(), xd, 2 * M, 2.0 ** -24)):
+        ref = a @ b
+        # (dX's sums go in slices of 2^17 tokens, 64 of them and two pieces behind each other)
+        tol = (1 + 2.0 ** -8) * (ea @ b.abs() + 1.01 * min(n, 2 * (2 ** 17 + 66)) * 2.0 ** -23 * (a.abs() @ b.abs())) + half * ref.abs() + 2.0 ** -126
+        bad = ~((got.double() - ref).abs() <= tol)
+        assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist())

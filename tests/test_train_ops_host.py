@@ -220,6 +220,21 @@ def test_loss_workspace_size():
     assert g5.lib().gemm_linear_loss_workspace_size(1, 300, 1000, 64, 1, A, 64, B, 64, None) == OK
 
 
+@pytest.mark.parametrize("M,K", [(1, 2), (4, 32), (8, 32), (15, 32), (15, 31), (4, 56), (40, 2)])
+def test_loss_gradient_pieces_end(M, K):
+    """Few rows and a vocabulary of short rows: a piece holds no more tokens
+    than 64 rows of its D have 32-bit offsets for, so a vocabulary of more needs
+    no more than one of 2^23."""
+    def size(V):
+        n = ctypes.c_uint64(0)
+        assert g5.lib().gemm_linear_loss_workspace_size(1, M, V, K, 1, A, K, B, K, ctypes.byref(n)) == OK
+        return n.value
+
+    most = size(1 << 23)
+    for V in ((1 << 23) + 1, (1 << 23) + 4096, 10_000_000, 1 << 24, 1 << 27, (1 << 31) - 257):
+        assert size(V) == most, V
+
+
 def test_loss_binding_refuses(no_lib):
     x, w, t, f = _bf(30, 64), _bf(100, 64), FakeGpuTensor((30,), torch.int64), _f32(30)
     ids, lg = _i32(30, 4), _f32(30, 4)
