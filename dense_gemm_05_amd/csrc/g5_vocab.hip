@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, Vo
     q.B = p.W + k0 * p.ldw + n0;
     q.C = b.sums + (tc.b * rows + m0) * b.ldx2 + n0;
     q.M = rows - m0 < BM ? rows - m0 : BM;
-    q.N = p.K - n0 < BN ? p.K - n0 : BN;
+    // (in whole dwords, as a copy's range check is: W's rows are padded where K is odd)
+    q.N = p.K - n0 < BN ? (p.K - n0 + 1) & ~(int64_t)1 : BN;
     q.K = p.V - k0 < b.per ? p.V - k0 : b.per;
     q.lda = b.ldd;
     q.ldb = p.ldw;

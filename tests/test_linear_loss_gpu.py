@@ -516,3 +516,24 @@ def test_gradients_of_more_tokens_than_a_piece_holds(M):
         tol = (1 + 2.0 ** -8) * (ea @ b.abs() + 1.01 * min(n, 2 * (2 ** 17 + 66)) * 2.0 ** -23 * (a.abs() @ b.abs())) + half * ref.abs() + 2.0 ** -126
         bad = ~((got.double() - ref).abs() <= tol)
         assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist())
+
+
+@pytest.mark.parametrize("config", ["", "bf16_128x128", "bf16_256x256"])
+@pytest.mark.parametrize("K", [1, 33, 65, 129])
+@pytest.mark.parametrize("V", [32, 64, 512, 2048, 2050])
+@pytest.mark.parametrize("M", [3, 40, 100])
+def test_last_column_of_odd_rows(monkeypatch, M, V, K, config):
+    """An odd K: the weight's last element of dX's summed tokens lies in half a
+    dword of its own.  Targets at the ends of every stage of 32 tokens, so at
+    every slice's end and the vocabulary's."""
+    if config:
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{config} {M} {V} {K}")
+    c = Case(M, V, K, out=0.0, seed=8)
+    c.ids = (V - 1 - 32 * torch.arange(M)) % V
+    if V % 32:
+        c.ids[1::2] = (31 + 32 * torch.arange(M))[1::2] % V
+    c.w[c.ids, -1] = torch.where(torch.arange(M) % 2 == 0, 3.0, -3.0).bfloat16()
+    loss, lse = c.forward()
+    c.check_forward(loss, lse)
+    c.check_backward(lse, *c.backward(lse), config)
