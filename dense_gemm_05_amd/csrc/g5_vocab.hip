@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_vocab_join(VocabArgs p)
             if (row_targets(p, m, lane, q)) {
 #pragma unroll
                 for (int j = 0; j < kTopkPer; ++j)
-                    if (q.id[j] >= 0)
+                    // (a weight of 0 adds nothing, however low its log is; NaN stays)
+                    if (q.id[j] >= 0 && q.q[j] != 0.f)
                         loss += q.q[j] * (q.logq[j] + (p.scale * (top - p.zt[m * p.topk + lane + 64 * j]) + log_sum));
                 loss = sum64(loss);
             }

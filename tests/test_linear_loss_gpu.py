@@ -537,3 +537,23 @@ def test_last_column_of_odd_rows(monkeypatch, M, V, K, config):
     loss, lse = c.forward()
     c.check_forward(loss, lse)
     c.check_backward(lse, *c.backward(lse), config)
+
+
+@pytest.mark.parametrize("scale", [0.5, 1.0, 2.0, 4.0])
+@pytest.mark.parametrize("M", [5, 20, 140])
+def test_teacher_entries_far_below_the_rest(M, scale):
+    """The lowest number as a list's padding, beside ordinary logits, beside the
+    largest and alone: a probability of 0 adds nothing to the loss."""
+    c = Case(M, 90, 48, 6, out=0.1, scale=scale, seed=2)
+    c.ids[:5] = torch.arange(6) * 7
+    low = torch.finfo(torch.float32).min
+    c.t[0, 2:] = low
+    c.t[1, ::2] = low
+    c.t[2, 1:] = low
+    c.t[2, 0] = -low
+    c.t[3] = low
+    c.t[4] = torch.tensor([1e38, -1e38, 3e38, -3e38, 0.0, -INF])
+    loss, lse = c.forward()
+    assert bool(torch.isfinite(loss).all())
+    c.check_forward(loss, lse)
+    c.check_backward(lse, *c.backward(lse))
