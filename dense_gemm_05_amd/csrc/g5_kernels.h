@@ -295,7 +295,7 @@ struct VocabArgs {
     const void *ids;                    // [M, topk], int32 or (ids64) int64
     int ids64, topk;
     const float *teacher;               // [M, topk], or NULL: ids are labels (topk 1)
-    float2 *part;                       // [M, parts]: maximum and sum of a row in a column tile
+    float2 *part;                       // [M, parts]: a row's maximum in a column tile, and the sum without its own 1
     float *zt;                          // [M, topk]: the targets' logits
     int64_t parts, tile0;               // column tiles in all; the piece's first
     float *loss, *lse_out;              // [M]; lse_out or NULL

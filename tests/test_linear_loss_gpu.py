@@ -557,3 +557,38 @@ def test_teacher_entries_far_below_the_rest(M, scale):
     assert bool(torch.isfinite(loss).all())
     c.check_forward(loss, lse)
     c.check_backward(lse, *c.backward(lse))
+
+
+@pytest.mark.parametrize("config", ["", "bf16_128x128", "bf16_256x256"])
+@pytest.mark.parametrize("V", [40, 300, 900])
+@pytest.mark.parametrize("M", [3, 32, 33, 150, 300])
+def test_confident_rows_keep_their_digits(monkeypatch, M, V, config):
+    """Logits that FP32 holds exactly, the target's above the rest by 0 to 84:
+    losses from log V to 1e-34, each to a bound relative to itself."""
+    if config:
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{config} {M} {V}")
+    c = Case(M, V, 16, out=0.0, seed=4)
+    m = torch.arange(M)
+    gap = (7 * m) % 85
+    c.ids = 37 * (m % 8) % V
+    c.x[:], c.w[:] = 0, 0
+    c.x[m, m % 8] = gap.bfloat16()            # the logit above the rest
+    c.w[c.ids[:8], torch.arange(min(M, 8))] = 1
+    c.x[m, 8 + m % 8] = (m % 5).bfloat16()    # and smaller ones below them
+    c.w[::3, 8:] = -1
+    l = c.x.double() @ c.w.double().t()
+    d = l - l.gather(1, c.ids[:, None])
+    d[m, c.ids] = 0
+    others = torch.exp(d)
+    others[m, c.ids] = 0
+    want = torch.log1p(others.sum(1))
+    loss, _ = c.forward()
+    # Relative: an argument's factor, product and difference (twice, where a
+    # part is rescaled) 2^-22 of up to 84 + 2 * 5 each, 2^-22 for either
+    # exponential, V roundings of sums of positive terms, the logarithm.  A
+    # term below 2^-126 may be 0.
+    tol = want * (2 * (94 + 1) * 2.0 ** -22 + 1.01 * (V + 16) * 2.0 ** -24 + 2.0 ** -21) + V * 2.0 ** -126
+    # (where another logit is above the target's, their difference is added)
+    tol = tol + 2.0 ** -22 * d.max(1).values.clamp(min=0)
+    _close(loss, want, tol, f"{config} loss")
