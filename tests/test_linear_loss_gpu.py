@@ -592,3 +592,57 @@ def test_confident_rows_keep_their_digits(monkeypatch, M, V, config):
     # (where another logit is above the target's, their difference is added)
     tol = tol + 2.0 ** -22 * d.max(1).values.clamp(min=0)
     _close(loss, want, tol, f"{config} loss")
+
+
+@pytest.mark.parametrize("topk", [0, 3])
+@pytest.mark.parametrize("config", ["", "bf16_128x128", "bf16_256x256"])
+@pytest.mark.parametrize("M", [3, 40, 140, 1100])
+def test_gradients_of_pieces_in_slices(monkeypatch, M, config, topk):
+    """A weight whose rows lie 2^18 apart goes in pieces of 2048 tokens, dX's
+    product of each in slices of 256, dW's of 1100 rows in two: the last piece,
+    of 52 tokens, leaves all slices but the first empty, and they keep the sums
+    of the piece before."""
+    if config:
+        monkeypatch.setenv("GEMM_FORCE_CONFIG", config)
+    _say(f"{config} {M} {topk}")
+    V, K, apart = 2100, 40, 2 ** 18
+    c = Case(M, V, K, topk, seed=9)
+    if topk == 0:
+        c.ids[:3] = torch.tensor([V - 1, 2047, 2048])
+    big = torch.zeros((V * apart,), dtype=torch.bfloat16, device="cuda")
+    w = big.as_strided((V, K), (apart, 1))
+    w.copy_(c.w)
+    loss, lse = c.forward(w=w)
+    c.check_forward(loss, lse)
+    dx, dw = c.backward(lse, w=w, dw_dtype=torch.float32)
+    c.check_backward(lse, dx, dw, config)
+
+
+class FewColumns(Case):
+    """x is zero but for some columns, so sums over the others are exact."""
+
+    def __init__(self, M, V, K, topk=0, seed=0):
+        super().__init__(M, V, K, topk, seed)
+        self.cols = torch.cat([torch.arange(0, K, K // 30), torch.arange(K - 8, K)]).unique()
+        self.w[:, self.cols] = (self.w[:, self.cols].float() * (K / len(self.cols)) ** 0.5).bfloat16()
+        keep = torch.zeros_like(self.x)
+        keep[:, self.cols] = self.x[:, self.cols]
+        self.x = keep
+
+    def logits(self):
+        x, w = self.x[:, self.cols].double(), self.w[:, self.cols].double()
+        return x @ w.t(), 1.01 * (len(self.cols) + 2) * 2.0 ** -23 * (x.abs() @ w.abs().t())
+
+
+@pytest.mark.parametrize("M", [3, 40, 100])
+def test_gradients_of_a_copied_weight_in_pieces(M):
+    """Rows of 2^18 + 1 elements are copied to padded ones, 256 tokens at a time:
+    D streamed, in two parts and in one, dX's sums carried from piece to piece."""
+    V, K = 600, 2 ** 18 + 1
+    _say(f"{M}")
+    c = FewColumns(M, V, K)
+    c.ids[:3] = torch.tensor([V - 1, 255, 256])
+    loss, lse = c.forward()
+    c.check_forward(loss, lse)
+    dx, dw = c.backward(lse, dw_dtype=torch.float32)
+    c.check_backward(lse, dx, dw)
