@@ -166,9 +166,9 @@ struct TargetList {
 
 // Forward by tiles.  The tile's epilogue is registers but for the join of
 // the four waves side by side, and tiles that hold a target.  Bound by the
-// matrix cores: 4096 rows by 131072 tokens of 4096 2880 us (1527 TFLOP/s), 2048
-// by 32768 with 32 targets a row 380 us (1447); 1000 by 32003 of 1028 70 us
-// (940: two rounds of tiles of 17 stages, a launch and their ends).
+// matrix cores: 4096 rows by 131072 tokens of 4096 2918 us (1507 TFLOP/s), 2048
+// by 32768 with 32 targets a row 384 us (1432); 1000 by 32003 of 1028 72 us
+// (916: two rounds of tiles of 17 stages, a launch and their ends).
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
 {
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
         whole += __shfl_xor(whole, 16, 64);
         whole += __shfl_xor(whole, 32, 64);
         float rest = whole - 1.f;
-        // Where little stands beside the maximum, once more without the terms
-        // that are 1: as many as the whole sum has more than the fractions.
+        // Where little stands beside the maximum, once more without it: the
+        // one term that is 1 has no fraction.
         // (4096 x 32768 x 512 with ordinary logits: none 142 us, so 145; always,
         // 12 us more than none.)
         const bool near = rest < 0.0625f && whole > 0.f;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_stats(VocabArgs p)
                     small += __builtin_amdgcn_fractf(__builtin_amdgcn_exp2f(c * (acc[fn][fm][i] - base)));
             small += __shfl_xor(small, 16, 64);
             small += __shfl_xor(small, 32, 64);
-            if (near) rest = rintf(whole - small) - 1.f + small;
+            if (near) rest = small;
         }
         if (g == 0) st[wn * BM + wm * R::TM + fm * 16 + li] = Part{top, rest};
     }
@@ -471,7 +471,7 @@ __device__ __forceinline__ bool row_targets(const VocabArgs &p, int64_t m, int l
 
 // The tiles' parts of a row joined by a workgroup, then its loss.  Always the
 // same parts in the same order: the same call gives the same bits.  Latency: one
-// row of 1024 parts 4.6 us, 4096 rows of 512 parts 10 us (16 MiB of parts,
+// row of 1024 parts 4.6 us, 4096 rows of 512 parts 11 us (16 MiB of parts,
 // against the 1 GiB of logits in bf16 that are not written).
 constexpr int kJoinWaves = 4;
 __global__ void __launch_bounds__(kJoinWaves * 64) k_vocab_join(VocabArgs p)
@@ -521,8 +521,8 @@ __global__ void __launch_bounds__(kJoinWaves * 64) k_vocab_join(VocabArgs p)
 // (one listed twice has both weights at its first place), their weights,
 // whether there are any, and its row of X with zero padding, all zeros for a
 // row without targets, whose contents must not reach dW (twice with b.parts 2:
-// D's two parts meet it one after the other).  4096 rows of 4096 13 us (67 MB,
-// 5.1 TB/s).
+// D's two parts meet it one after the other).  4096 rows of 4096 13.6 us (67 MB,
+// 4.9 TB/s).
 struct PrepRow {
     int ids[kVocabMaxTopk];
     float qs[kVocabMaxTopk];
@@ -652,9 +652,9 @@ __global__ void __launch_bounds__(kPrepFew * 64) k_vocab_prep_few(VocabArgs p, V
 // they lie, then weighted and rounded to bf16.  Many targets in a tile, and
 // b.parts 2 (few rows: the rounding's rest, as a bf16 of its own, follows in
 // rows M .. 2 M - 1), go through LDS as FP32.  Bound by the matrix cores and the
-// epilogue behind them: 4096 rows by a piece of 32768 tokens of 4096 783 us
-// (1404 TFLOP/s; the same logits alone take 720), 2048 by 50001 of 2048 with 64
-// targets a row 397 us (1056).
+// epilogue behind them: 4096 rows by a piece of 32768 tokens of 4096 780 us
+// (1410 TFLOP/s; the same logits alone take 730), 2048 by 50001 of 2048 with 64
+// targets a row 406 us (1034).
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p, VocabGrad b)
 {
@@ -764,8 +764,8 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dlogits(VocabArgs p,
 // dW rows of a piece: scale alpha D^T X2, summed over the rows in pieces whose
 // 32-bit offsets fit.  Few output tiles over many rows: b.w_slices parts of the
 // rows, each part's sums as FP32 in a plane of its own (k_vocab_total).  A
-// piece of 32768 tokens from 4096 rows of 4096 797 us (1380 TFLOP/s), 50001
-// tokens from 2048 rows of 2048 380 us (1104: a tile's 32 stages, then its 128
+// piece of 32768 tokens from 4096 rows of 4096 804 us (1367 TFLOP/s), 50001
+// tokens from 2048 rows of 2048 388 us (1080: a tile's 32 stages, then its 128
 // KiB stored behind them); few rows are bound by writing dW (131072 x 4096 bf16
 // from two rows 242 us, 4.4 TB/s).
 template <int BM, int BN, int WGM, int WGN>
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_dw(VocabArgs p, Voca
 // A piece's share of dX before its factor: sums (+)= D W over one of b.slices
 // parts of the piece's tokens, each with sums of its own.  Few output tiles
 // would leave CUs idle over a long summed axis.  4096 x 4096 from a piece of
-// 32768 tokens 760 us (1447 TFLOP/s).
+// 32768 tokens 778 us (1414 TFLOP/s).
 template <int BM, int BN, int WGM, int WGN>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_vocab_sums(VocabArgs p, VocabGrad b)
 {
