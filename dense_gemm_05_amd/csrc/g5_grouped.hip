@@ -146,11 +146,11 @@ using GroupedRing = RingTile<BM, BN, WGM, WGN, 4, 4, 16, true, EPI_NONE, KIND ==
 // of the rows for nothing).
 //
 // Measured, 64 groups drawn at random, weights of 1536 x 4096: the projection of
-// 32768 rows 395 us (1044 TFLOP/s of the rows that exist; of the multiplied
-// ones a ninth are the tails' padding), the input gradient of 16384 rows 259 us
-// (796 TFLOP/s and 3.8 TB/s: the weights are read once, 805 MB, under tiles of
-// 24 stages), the weight gradient of as many 400 us (4.5 TB/s, nearly all of it
-// FP32 written; 460 into outputs that change from call to call).  Workgroups that walk over several tiles were slower (weight gradient
+// 32768 rows 394 us (1047 TFLOP/s of the rows that exist; of the multiplied
+// ones a ninth are the tails' padding), the input gradient of 16384 rows 258 us
+// (799 TFLOP/s and 3.8 TB/s: the weights are read once, 805 MB, under tiles of
+// 24 stages), the weight gradient of as many 404 us (4.4 TB/s, nearly all of it
+// FP32 written; 473 into outputs that change from call to call).  Workgroups that walk over several tiles were slower (weight gradient
 // 567 for 487, projection 418 for 401), and so were half tiles put last (419).
 template <int BM, int BN, int WGM, int WGN, int KIND, bool HALF>
 __global__ void __launch_bounds__(WGM *WGN * 64, 2) k_grouped(GroupedArgs p)

@@ -35,7 +35,7 @@ namespace g5 {
 //
 // Against the ring's 32-deep stages, in which all waves read at once and then
 // multiply at once: 4096 x 131072 x 4096 with the loss's epilogue 3150 us for
-// 3550 (that epilogue's targets listed by lane since: 2900, 1517 TFLOP/s; the
+// 3550 (that epilogue's targets listed by lane since: 2918, 1507 TFLOP/s; the
 // platform's library without any 3081).  Four phases of 16
 // MFMAs 3215, raised wave priority around the MFMAs 1 to 2 % slower, copies
 // ahead of the reads 3 % slower; workgroups that walk over several tiles and

@@ -782,7 +782,7 @@ int gemm_grouped_workspace_size(int kind, int64_t E, int64_t rows, int64_t M, in
  * by convention -100 or -1 -- leaves its row out: loss 0, gradients 0, whatever
  * the row holds.  So does a teacher's entry whose id lies outside or whose logit
  * is -inf, and a row that has no entry is left out; an id listed twice counts
- * twice.  lse is written for every row.  NaN in a row of X makes that row's loss
+ * twice; an entry so far below the rest that q_j is 0 adds nothing.  lse is written for every row.  NaN in a row of X makes that row's loss
  * NaN and no other's; an infinite logit may give NaN where the formula gives an
  * infinity.
  *
